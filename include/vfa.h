@@ -1,6 +1,7 @@
 /*
  * vfa.h -- C ABI of libvfa: variable-length FlashAttention forward and paged
- * GQA decode for NVIDIA GB300 (sm_103a).
+ * GQA decode for NVIDIA GB300 (sm_103a), with the operators around them
+ * (query / key norm and rotation, a 4-bit paged cache, page operations).
  *
  * Conventions shared by every entry point:
  *   - Every pointer argument named as a device buffer is a CUDA device
@@ -43,7 +44,8 @@ typedef enum {
     VFA_ERR_BAD_SEQLENS = 5,   /* device: cu_seqlens not a valid prefix sum      */
     VFA_ERR_BAD_BLOCK = 6,     /* device: block id or tile count out of range    */
     VFA_ERR_TIMEOUT = 7,       /* device: a bounded wait inside a kernel expired */
-    VFA_ERR_WORKSPACE = 8      /* device: the work list does not fit the workspace */
+    VFA_ERR_WORKSPACE = 8,     /* device: the work list does not fit the workspace */
+    VFA_ERR_NO_PAGES = 9       /* device: fewer free pages than the call needs     */
 } vfa_status;
 
 /* Message for the last non-OK status returned on the calling host thread. */
@@ -419,6 +421,275 @@ vfa_status vfa_debug_paged_gather(const void *k_pool, const void *v_pool, int nu
  * context stays usable.  device_status: device int32 [1], not NULL.
  */
 vfa_status vfa_debug_bounded_wait(int32_t *device_status, vfa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Query / key norm and position rotation                                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * RMS norm of every query and key head and the rotation of its position, in
+ * one pass: what stands between a projection and vfa_varlen_fwd or a cache.
+ * Per (token, head) vector x of head_dim elements with weight w:
+ *   n = x * (mean(x^2) + eps)^-1/2 * w          (weight NULL: n = x)
+ *   y_a = n_a cos(phi_i) - n_b sin(phi_i)
+ *   y_b = n_b cos(phi_i) + n_a sin(phi_i)       for pair i < rotary_dim / 2
+ *   y_d = n_d                                   for d >= rotary_dim
+ * with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved, and
+ * phi_i = 2 pi * turns_i * positions[axis_i, token].  fp32 arithmetic,
+ * rounded once to bf16.
+ *
+ * q, k         device bf16 [tokens, heads, head_dim]; heads and dims are
+ *              contiguous, tokens q_stride / k_stride elements apart (views of
+ *              a joint projection's output are taken as they are).
+ * q_out, k_out the results, same shape, strides q_out_stride / k_out_stride;
+ *              may be q and k themselves (same pointer and stride), must not
+ *              overlap them otherwise.
+ * positions    device int32 [num_axes, tokens]: each token's position on each
+ *              axis (one for text; time, height and width for video).  Any
+ *              int32 value.
+ * table        device uint64 [rotary_dim / 2][2]: turns per position in units
+ *              of 2^-64 turn (round(inv_freq / (2 pi) * 2^64)), and the axis.
+ *              The angle is position * turns modulo 2^64, exact for every
+ *              position.  An axis >= num_axes reads the last one.
+ * q_weight, k_weight  device f32 [head_dim], each nullable (no norm).
+ * eps          finite, >= 0.
+ *
+ * Supported: head_dim 64, 128 or 256; rotary_dim a multiple of 16 in
+ * [0, head_dim] (0: positions and table are not read); pointers of bf16
+ * tensors 16-byte aligned and strides multiples of 8, at least heads *
+ * head_dim.  With tokens == 0 nothing is enqueued and tensors may be NULL.
+ */
+vfa_status vfa_qk_norm_rope_fwd(const void *q, const void *k, int64_t q_stride, int64_t k_stride,
+                                const int32_t *positions, int num_axes, const uint64_t *table,
+                                int rotary_dim, int interleaved, const float *q_weight,
+                                const float *k_weight, float eps, int tokens, int num_q_heads,
+                                int num_kv_heads, int head_dim, void *q_out, void *k_out,
+                                int64_t q_out_stride, int64_t k_out_stride, vfa_stream_t stream);
+
+/*
+ * Gradients of vfa_qk_norm_rope_fwd: with g the rotation of the upstream
+ * gradient by the opposite angles, r the inverse root mean square and
+ * u = g * w,
+ *   dweight = sum over tokens and heads of g * x * r
+ *   dx = r * (u - x * r^2 * mean(u * x))        (weight NULL: dx = g)
+ * q and k are the forward's inputs (not read where their weight is NULL, but
+ * not NULL).  dq_out and dk_out are the upstream gradients, dq and dk the
+ * results; all have strides as in the forward.  dq and dk may be dq_out and
+ * dk_out themselves.  dq_weight, dk_weight: device f32 [head_dim], required
+ * where the weight is given, ignored where it is NULL; set (not added to).
+ * The sums run in a fixed order: results are bit-identical from run to run
+ * on one device.
+ *
+ * workspace    device scratch of vfa_qk_norm_rope_bwd_workspace_bytes()
+ *              bytes, 16-byte aligned; may be NULL where both weights are.
+ *              Calls sharing it must be stream-ordered.
+ */
+size_t vfa_qk_norm_rope_bwd_workspace_bytes(int head_dim);
+
+vfa_status vfa_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_stride, int64_t k_stride,
+                                const void *dq_out, const void *dk_out, int64_t dq_out_stride,
+                                int64_t dk_out_stride, const int32_t *positions, int num_axes,
+                                const uint64_t *table, int rotary_dim, int interleaved,
+                                const float *q_weight, const float *k_weight, float eps,
+                                int tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                void *dq, void *dk, int64_t dq_stride, int64_t dk_stride,
+                                float *dq_weight, float *dk_weight, void *workspace,
+                                size_t workspace_bytes, vfa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* A paged cache held in 4 bits                                              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Format.  A pool is uint8 [num_blocks, num_kv_heads, 18 * head_dim]: pages of
+ * 16 tokens, K and V of one kv head side by side.  A value is
+ *   descale * scale * code
+ * with code in E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and one E4M3 scale
+ * per 16 consecutive dims of a token.  descale_k and descale_v hold for the
+ * whole pool and are powers of two in [2^-64, 2^64] (VFA_ERR_INVALID_ARG
+ * otherwise): every value then has at most six significant bits and is exact
+ * in bf16.  Bytes of a page's head, t = token in the page, d = dim, D =
+ * head_dim, W = min(16, D / 8), c = d / W (integer divisions):
+ *   K codes   t D/2 + d/2, low nibble for even d
+ *   V codes   8 D + ((t/8) (D/(8 W)) + c/8) 32 W + ((c%8) 4 + (t/2)%4) W +
+ *             (t%2) W/2 + (d%W)/2, low nibble for even d
+ *   K scales  16 D + t D/16 + d/16
+ *   V scales  17 D + ((d/16) 4 + (t/2)%4) 4 + t%2 + 2 (t/8)
+ * No byte holds parts of two tokens.
+ *
+ * tables       device int32 [num_seqs, capacity]: physical page of each
+ *              logical page (as tile_blocks of vfa_paged_decode_step; one
+ *              table serves both kinds of pool).
+ * device_status  nullable device int32 [1]; the first error is kept, so clear
+ *              it before use.
+ * Supported: head_dim 64, 128 or 256; num_blocks <= 2^26; pool, k, v 16-byte
+ * aligned.
+ */
+size_t vfa_kv4_block_bytes(int num_kv_heads, int head_dim);
+
+/*
+ * Writes packed tokens into the cache: token i of sequence s (packed row
+ * cu_seqlens[s] + i) becomes position start_positions[s] + i of its table row.
+ * Per group of 16 dims scale = E4M3(max |x / descale| / 6) and code =
+ * E2M1(x / descale / scale), both to nearest even and saturating; a group
+ * whose scale rounds to zero stores zeros.  Inputs are finite.
+ *
+ * k, v         device bf16 [total, num_kv_heads, head_dim], tokens k_stride /
+ *              v_stride elements apart (multiples of 8).
+ * cu_seqlens   device int32 [num_seqs + 1], from 0, not decreasing, ending at
+ *              or below total: rows past the end are padding and not read.
+ * Nothing but the written tokens' bytes changes.  Two tokens of one call
+ * must not go to one slot (two rows writing a page they share): what that
+ * slot then holds is unspecified.
+ * Device-detected: cu_seqlens that are no prefix sum (VFA_ERR_BAD_SEQLENS),
+ * positions or page ids out of range (VFA_ERR_BAD_BLOCK); the tokens they
+ * leave without a place are skipped.
+ */
+vfa_status vfa_kv4_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                         int total, void *pool, int num_blocks, const int32_t *tables,
+                         int capacity, const int32_t *cu_seqlens, const int32_t *start_positions,
+                         int num_seqs, int num_kv_heads, int head_dim, float descale_k,
+                         float descale_v, int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Reads tokens back as bf16 (exact): the reverse of vfa_kv4_write with the
+ * same arguments, k and v written.  With start_positions 0 and cu_seqlens the
+ * context lengths, k and v are the packed keys and values vfa_varlen_fwd takes
+ * for a prompt that continues them (causal = 2).  Rows without a place in the
+ * cache (padding, errors) are left as they were.
+ */
+vfa_status vfa_kv4_gather(void *k, void *v, int64_t k_stride, int64_t v_stride, int total,
+                          const void *pool, int num_blocks, const int32_t *tables, int capacity,
+                          const int32_t *cu_seqlens, const int32_t *start_positions, int num_seqs,
+                          int num_kv_heads, int head_dim, float descale_k, float descale_v,
+                          int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Attention of one query token per sequence over the cache:
+ *   out[s, h] = sum_j p_j v_j / sum_j p_j, p_j = exp(softmax_scale q.k_j),
+ * over the first token_counts[s] tokens of the sequence's pages, query head h
+ * on kv head h / (num_q_heads / num_kv_heads), and lse = the natural log of
+ * sum_j p_j.  token_counts[s] == 0 gives out = 0 and lse = -FLT_MAX.  What a
+ * page holds past the last token does not matter.  One launch; the work of
+ * the batch is spread over the SMs by page, whatever the lengths.
+ *
+ * q, out       device bf16 [num_seqs, num_q_heads, head_dim].
+ * token_counts device int32 [num_seqs], in [0, capacity * 16].
+ * softmax_scale  <= 0 means 1/sqrt(head_dim); NaN or inf is
+ *              VFA_ERR_INVALID_ARG.
+ * lse          nullable device f32 [num_seqs, num_q_heads].
+ * workspace    device scratch of vfa_kv4_decode_workspace_bytes() bytes,
+ *              256-byte aligned: tickets, then partial states.  It must hold
+ *              zeros before its first use; every call leaves the tickets
+ *              zero.  Calls sharing it must be stream-ordered and have the
+ *              sizes it was made for.
+ * Device-detected: a token count out of range or a listed page id outside
+ * [0, num_blocks) stores VFA_ERR_BAD_BLOCK and leaves that sequence's out and
+ * lse rows (of the kv heads that saw it) as they were.
+ * Supported: any num_q_heads that is a multiple of num_kv_heads;
+ * num_seqs * capacity < 2^31.
+ */
+size_t vfa_kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                      int head_dim);
+
+vfa_status vfa_kv4_decode(const void *q, const void *pool, int num_blocks, const int32_t *tables,
+                          int capacity, const int32_t *token_counts, int num_seqs,
+                          int num_q_heads, int num_kv_heads, int head_dim, float descale_k,
+                          float descale_v, float softmax_scale, void *out, float *lse,
+                          int32_t *device_status, void *workspace, size_t workspace_bytes,
+                          vfa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Pages of a cache                                                          */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Which pages of a pool the sequences hold, kept on the device:
+ *   refcounts     int32 [num_blocks]: rows that list the page, 0 = free;
+ *   tables        int32 [num_seqs, capacity]: physical page of each logical one;
+ *   token_counts  int32 [num_seqs]: tokens; the first ceil(tokens /
+ *                 block_size) entries of a row are live.
+ * One such state serves any number of pools (K and V of every layer, bf16 or
+ * 4-bit): pools is a host array of num_pools device addresses (16-byte
+ * aligned, num_blocks pages each) and page_bytes a host array of their page
+ * sizes (multiples of 16); at most 256 pools, and 0 is allowed.  Nothing is
+ * read back to the host, so the calls can be captured in a graph.
+ *
+ * New pages are the free pages with the lowest ids, handed out in the order
+ * stated, so the results depend on the inputs alone.
+ *
+ * workspace     device scratch of vfa_pages_workspace_bytes() bytes (for at
+ *               least this num_blocks, num_seqs and num_forks; no initial
+ *               value needed), 16-byte aligned.  Calls sharing it must be
+ *               stream-ordered.
+ * device_status nullable device int32 [1]; the first error is kept.
+ */
+size_t vfa_pages_workspace_bytes(int num_blocks, int num_seqs, int num_forks);
+
+/*
+ * token_counts[s] += add_tokens[s], with new pages (refcount 1) for the rows
+ * that need them, in the order of (s, logical page).  VFA_ERR_NO_PAGES (too
+ * few free pages) or VFA_ERR_BAD_BLOCK (a negative addition, a row past its
+ * capacity): nothing changes.
+ */
+vfa_status vfa_pages_extend(int32_t *refcounts, int num_blocks, int32_t *tables, int capacity,
+                            int32_t *token_counts, int num_seqs, const int32_t *add_tokens,
+                            int block_size, void *workspace, size_t workspace_bytes,
+                            int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Row children[i] becomes a copy of row parents[i], i < num_forks: full pages
+ * are shared (their refcounts grow), a partly filled last page is copied in
+ * every pool to a new page of the child's own (in the order of i), so both
+ * rows can be extended and written.  A negative parent skips the entry.  Every
+ * child must have token_counts 0 and be listed once; a parent may be listed
+ * any number of times.  VFA_ERR_NO_PAGES, or VFA_ERR_BAD_BLOCK for rows out of
+ * range, a child in use or listed twice, a bad count or last page: nothing
+ * changes.  A full page that is out of range or not in use is listed in the
+ * child as it is, not counted, and recorded as VFA_ERR_BAD_BLOCK.
+ */
+vfa_status vfa_pages_fork(int32_t *refcounts, int num_blocks, int32_t *tables, int capacity,
+                          int32_t *token_counts, int num_seqs, const int32_t *parents,
+                          const int32_t *children, int num_forks, void *const *pools,
+                          const int *page_bytes, int num_pools, int block_size, void *workspace,
+                          size_t workspace_bytes, int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Rows seqs[i], i < n, give up their pages: refcounts fall by one per live
+ * entry and token_counts become 0.  A row listed twice is freed once; a
+ * negative entry is skipped.  Table entries keep their old values.  A row out
+ * of range, a bad page id or a refcount that is 0 already is recorded as
+ * VFA_ERR_BAD_BLOCK and skipped.
+ */
+vfa_status vfa_pages_free(int32_t *refcounts, int num_blocks, const int32_t *tables, int capacity,
+                          int32_t *token_counts, int num_seqs, const int32_t *seqs, int n,
+                          int block_size, int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Moves the used pages into [0, U), U = their number: those at or above U go,
+ * in ascending order, to the free pages below U, in ascending order, in every
+ * pool.  num_used (device int32 [1]) receives U.  The moved tables and
+ * refcounts go to tables_out (live entries only; the others are left as they
+ * were) and refcounts_out, which may be tables and refcounts themselves.  A
+ * live entry that is out of range or not in use is kept and recorded as
+ * VFA_ERR_BAD_BLOCK; a row with a bad count is skipped.
+ */
+vfa_status vfa_pages_compact(const int32_t *refcounts, int num_blocks, const int32_t *tables,
+                             int capacity, const int32_t *token_counts, int num_seqs,
+                             void *const *pools, const int *page_bytes, int num_pools,
+                             int block_size, int32_t *refcounts_out, int32_t *tables_out,
+                             int32_t *num_used, void *workspace, size_t workspace_bytes,
+                             int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Page src[i] of every pool is copied over page dst[i], i < n (device int32
+ * [n] each).  A negative src skips the entry; other ids out of range are
+ * recorded as VFA_ERR_BAD_BLOCK and skipped.  A page may be the source of any
+ * number of copies, but the target of one only and not a source as well.
+ */
+vfa_status vfa_pages_copy(void *const *pools, const int *page_bytes, int num_pools,
+                          const int32_t *src, const int32_t *dst, int n, int num_blocks,
+                          int32_t *device_status, vfa_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                    */

@@ -1,0 +1,256 @@
+"""GPU page operations against the plain ones: whole numbers and page bytes, all equal."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.serving as O
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vfa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from variable_length_flashattention_gb300 import build, vfa as binding
+    build.build()
+    return binding
+
+
+class State:
+    """One page state on the host (the definition) and on the device."""
+
+    def __init__(self, vfa, blocks, S, cap, bs, page_shapes=((8, 64), (3, 16)), forks=64, seed=0):
+        self.vfa, self.bs = vfa, bs
+        rng = np.random.default_rng(seed)
+        self.refs = np.zeros(blocks, np.int32)
+        self.tables = np.full((S, cap), -7, np.int32)
+        self.counts = np.zeros(S, np.int32)
+        self.pools = [rng.integers(0, 256, (blocks, *s), dtype=np.uint8) for s in page_shapes]
+        self.d_refs, self.d_tables, self.d_counts = (torch.from_numpy(x.copy()).cuda() for x in
+                                                     (self.refs, self.tables, self.counts))
+        self.d_pools = [torch.from_numpy(p.copy()).cuda() for p in self.pools]
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.ws = vfa.alloc_pages_workspace(blocks, S, forks)
+        self.ws.fill_(0xa5)                            # needs no initial value
+
+    def i32(self, x):
+        return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+    def extend(self, add):
+        ok = O.extend(self.refs, self.tables, self.counts, np.asarray(add, np.int32), self.bs)
+        self.vfa.pages_extend(self.d_refs, self.d_tables, self.d_counts, self.i32(add), self.bs,
+                              self.ws, status=self.status)
+        self.check(0 if ok else self.vfa.VFA_ERR_NO_PAGES)
+
+    def fork(self, parents, children):
+        ok = O.fork(self.refs, self.tables, self.counts, parents, children, self.pools, self.bs)
+        self.vfa.pages_fork(self.d_refs, self.d_tables, self.d_counts, self.i32(parents),
+                            self.i32(children), self.d_pools, self.bs, self.ws,
+                            status=self.status)
+        self.check(0 if ok else self.vfa.VFA_ERR_NO_PAGES)
+
+    def free(self, seqs):
+        O.free(self.refs, self.tables, self.counts, seqs, self.bs)
+        self.vfa.pages_free(self.d_refs, self.d_tables, self.d_counts, self.i32(seqs), self.bs,
+                            status=self.status)
+        self.check(0)
+
+    def compact(self):
+        n = O.compact(self.refs, self.tables, self.counts, self.pools, self.bs)
+        got = self.vfa.pages_compact(self.d_refs, self.d_tables, self.d_counts, self.d_pools,
+                                     self.bs, self.ws, status=self.status)
+        assert got.item() == n
+        self.check(0)
+
+    def check(self, status):
+        assert self.vfa.read_status(self.status) == status
+        self.status.zero_()
+        assert np.array_equal(self.d_refs.cpu().numpy(), self.refs)
+        assert np.array_equal(self.d_tables.cpu().numpy(), self.tables)
+        assert np.array_equal(self.d_counts.cpu().numpy(), self.counts)
+        for d, p in zip(self.d_pools, self.pools):
+            assert np.array_equal(d.cpu().numpy(), p)
+
+
+@pytest.mark.parametrize("blocks,S,cap,bs,seed", [
+    (1, 1, 1, 1, 0), (40, 6, 9, 4, 1), (4096, 33, 60, 16, 2), (4097, 70, 40, 16, 3),
+    (9001, 1500, 3, 16, 4), (300, 5, 50, 7, 5)])
+def test_random_histories(vfa, blocks, S, cap, bs, seed):
+    st = State(vfa, blocks, S, cap, bs, seed=seed)
+    rng = np.random.default_rng(seed)
+    for step in range(8):
+        room = cap * bs - st.counts
+        add = np.minimum(room, rng.integers(0, 2 * bs + 1, S)) * (rng.random(S) < 0.7)
+        if step % 2:
+            add = np.minimum(add, 1)
+        st.extend(add)
+        empty = np.flatnonzero(st.counts == 0)[:64]
+        live = np.flatnonzero(st.counts > 0)
+        if len(empty) and len(live):
+            n = rng.integers(1, len(empty) + 1)
+            parents = rng.choice(live, n)
+            parents[rng.random(n) < 0.1] = -1
+            st.fork(parents, rng.permutation(empty)[:n])
+        gone = np.flatnonzero(rng.random(S) < 0.4)
+        st.free(np.concatenate((gone, gone[:1], [-1])))      # one row twice, one padding entry
+        if step % 3 == 2:
+            st.compact()
+        used = (st.refs > 0).sum()
+        assert used <= blocks
+
+
+def test_fork_of_a_row_that_ends_on_a_page_and_of_an_empty_one(vfa):
+    st = State(vfa, 64, 8, 6, 4)
+    st.extend([8, 0, 5, 0, 0, 0, 0, 0])
+    st.fork([0, 1, 2, 2], [3, 4, 5, 6])
+    st.extend([1, 1, 1, 1, 1, 1, 1, 0])
+    st.free([0, 2])
+    st.compact()
+
+
+def test_pages_run_out(vfa):
+    st = State(vfa, 10, 4, 10, 4)
+    st.extend([20, 12, 0, 0])             # 8 pages
+    st.extend([12, 0, 0, 0])              # 3 more: refused, nothing changes
+    st.extend([8, 0, 0, 0])               # exactly all
+    st.free([1])
+    st.extend([0, 12, 0, 0])
+    st.free([0])
+    st.extend([26, 0, 0, 0])              # 7 pages, the last one partly filled: none left
+    st.fork([0], [2])                     # no page for the copy: refused
+
+
+def test_large_requests(vfa):
+    """Thousands of pages in one call, over several chunks of the pool."""
+    st = State(vfa, 30000, 9, 6000, 16, page_shapes=((1, 16),))
+    st.extend([16 * 5000 + 3, 0, 16 * 6000, 1, 0, 16 * 4000 - 1, 0, 0, 0])
+    st.free([2])
+    st.extend([0, 16 * 5999 + 1, 0, 5, 0, 33, 0, 0, 0])
+    st.fork([0, 1, 1, 5], [2, 4, 6, 7])
+    st.free([0, 1])
+    st.compact()
+
+
+def test_refusals_change_nothing(vfa):
+    st = State(vfa, 30, 6, 5, 4)
+    st.extend([9, 4, 0, 0, 0, 0])
+    v = st.vfa
+
+    def refused(call):
+        call()
+        st.check(v.VFA_ERR_BAD_BLOCK)
+
+    ext = lambda add: v.pages_extend(st.d_refs, st.d_tables, st.d_counts, st.i32(add), 4, st.ws,
+                                     status=st.status)
+    fork = lambda p, c: v.pages_fork(st.d_refs, st.d_tables, st.d_counts, st.i32(p), st.i32(c),
+                                     st.d_pools, 4, st.ws, status=st.status)
+    refused(lambda: ext([0, -1, 0, 0, 0, 0]))              # a negative addition
+    refused(lambda: ext([12, 1, 0, 0, 0, 0]))              # past the row's capacity
+    refused(lambda: ext([0, 2 ** 31 - 1, 0, 0, 0, 0]))
+    refused(lambda: fork([0, 0], [2, 2]))                  # a child twice
+    refused(lambda: fork([0], [1]))                        # a child in use
+    refused(lambda: fork([0, 0], [2, 6]))                  # a child out of range
+    refused(lambda: fork([6], [2]))                        # a parent out of range
+    refused(lambda: v.pages_free(st.d_refs, st.d_tables, st.d_counts, st.i32([6]), 4,
+                                 status=st.status))
+    st.fork([0, 1], [2, 3])                                # and the state still works
+
+
+def test_bad_table_entries_are_recorded(vfa):
+    st = State(vfa, 30, 4, 5, 4)
+    st.extend([9, 4, 0, 0])
+    v = st.vfa
+    st.d_tables[0, 0] = 30                                 # a full page out of range
+    v.pages_fork(st.d_refs, st.d_tables, st.d_counts, st.i32([0]), st.i32([2]), st.d_pools, 4,
+                 st.ws, status=st.status)
+    assert v.read_status(st.status) == v.VFA_ERR_BAD_BLOCK
+    assert st.d_tables[2, 0].item() == 30 and st.d_counts[2].item() == 9
+    assert st.d_refs[st.d_tables[0, 1].long()].item() == 2
+    st.status.zero_()
+    v.pages_free(st.d_refs, st.d_tables, st.d_counts, st.i32([0, 2]), 4, status=st.status)
+    assert v.read_status(st.status) == v.VFA_ERR_BAD_BLOCK
+    st.status.zero_()
+    st.d_tables[1, 0] = 29                                 # a page nobody counts
+    v.pages_compact(st.d_refs, st.d_tables, st.d_counts, st.d_pools, 4, st.ws, status=st.status)
+    assert v.read_status(st.status) == v.VFA_ERR_BAD_BLOCK
+    st.status.zero_()
+    v.pages_free(st.d_refs, st.d_tables, st.d_counts, st.i32([1]), 4, status=st.status)
+    assert v.read_status(st.status) == v.VFA_ERR_BAD_BLOCK
+    assert (st.d_refs >= 0).all()
+    # a last page out of range: the fork is refused as a whole
+    st.status.zero_()
+    st.d_counts[3] = 6
+    st.d_tables[3, 1] = -3
+    v.pages_fork(st.d_refs, st.d_tables, st.d_counts, st.i32([3]), st.i32([0]), st.d_pools, 4,
+                 st.ws, status=st.status)
+    assert v.read_status(st.status) == v.VFA_ERR_BAD_BLOCK and st.d_counts[0].item() == 0
+
+
+def test_compact_into_other_tables(vfa):
+    st = State(vfa, 500, 5, 40, 4, seed=9)
+    st.extend([100, 70, 33, 0, 9])
+    st.free([0])
+    st.extend([13, 0, 0, 50, 0])
+    st.free([1])
+    refs, tables, pools = st.d_refs.clone(), st.d_tables.clone(), None
+    r_out, t_out = torch.full_like(st.d_refs, 77), torch.full_like(st.d_tables, 77)
+    n = st.vfa.pages_compact(st.d_refs, st.d_tables, st.d_counts, st.d_pools, 4, st.ws,
+                             refcounts_out=r_out, tables_out=t_out, status=st.status)
+    assert torch.equal(refs, st.d_refs) and torch.equal(tables, st.d_tables)
+    want = O.compact(st.refs, st.tables, st.counts, st.pools, 4)
+    assert n.item() == want and np.array_equal(r_out.cpu().numpy(), st.refs)
+    live = np.arange(40)[None] < -(-st.counts // 4)[:, None]
+    assert np.array_equal(t_out.cpu().numpy(), np.where(live, st.tables, 77))
+    for d, p in zip(st.d_pools, st.pools):
+        assert np.array_equal(d.cpu().numpy(), p)
+
+
+@pytest.mark.parametrize("shape", [(16,), (48,), (4096,), (5, 16), (2304,), (16, 8, 64)])
+def test_copy(vfa, shape):
+    rng = np.random.default_rng(1)
+    pools = [rng.integers(0, 256, (50, *shape), dtype=np.uint8) for _ in range(3)]
+    dev = [torch.from_numpy(p.copy()).cuda() for p in pools]
+    src, dst = [4, 4, -1, 9, 49], [0, 1, 2, 48, 3]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    vfa.pages_copy(dev, i32(src), i32(dst), status=status)
+    for p, d in zip(pools, dev):
+        for a, b in zip(src, dst):
+            if a >= 0:
+                p[b] = p[a]
+        assert np.array_equal(d.cpu().numpy(), p)
+    assert vfa.read_status(status) == 0
+    vfa.pages_copy(dev, i32([50, 3, 5]), i32([0, 50, 6]), status=status)
+    assert vfa.read_status(status) == vfa.VFA_ERR_BAD_BLOCK
+    for p, d in zip(pools, dev):
+        p[6] = p[5]
+        assert np.array_equal(d.cpu().numpy(), p)
+
+
+def test_captured_cycle(vfa):
+    """Fork, extend and free in one graph, replayed: the state after each replay is the same."""
+    st = State(vfa, 200, 12, 10, 4, seed=2)
+    st.extend([13, 8, 30] + [0] * 9)
+    parents, children = st.i32([0, 1, 2, 0]), st.i32([4, 5, 6, 7])
+    add = st.i32([0] * 4 + [1, 1, 1, 1] + [0] * 4)
+    v = st.vfa
+
+    def cycle():
+        v.pages_fork(st.d_refs, st.d_tables, st.d_counts, parents, children, st.d_pools, 4, st.ws)
+        v.pages_extend(st.d_refs, st.d_tables, st.d_counts, add, 4, st.ws)
+        v.pages_free(st.d_refs, st.d_tables, st.d_counts, children, 4)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            cycle()
+        for _ in range(3):
+            g.replay()
+    torch.cuda.synchronize()
+    O.fork(st.refs, st.tables, st.counts, [0, 1, 2, 0], [4, 5, 6, 7], st.pools, 4)
+    O.extend(st.refs, st.tables, st.counts, np.array([0] * 4 + [1] * 4 + [0] * 4, np.int32), 4)
+    O.free(st.refs, st.tables, st.counts, [4, 5, 6, 7], 4)
+    st.check(0)

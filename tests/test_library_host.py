@@ -215,3 +215,144 @@ def test_split_decode_host_checks(vfa):
     need = L.vfa_paged_decode_split_workspace_bytes(4, 32, 8, 128, 4)
     assert step(4, ws, need - 1) == vfa.VFA_ERR_INVALID_ARG
     assert b"too small" in L.vfa_last_error()
+
+
+def test_norm_rotation_host_checks(vfa):
+    L = vfa.lib()
+    f = ctypes.c_void_p(0x100000)              # never dereferenced
+    odd = ctypes.c_void_p(0x100008)
+
+    def fwd(q=f, stride=512, pos=f, axes=1, table=f, rot=64, eps=1e-6, T=4, Hq=4, Hkv=2, D=128,
+            out=f):
+        return L.vfa_qk_norm_rope_fwd(q, f, stride, 256, pos, axes, table, rot, 0, f, f, eps, T,
+                                      Hq, Hkv, D, out, f, 512, 256, None)
+
+    assert fwd(D=96, stride=1024) == vfa.VFA_ERR_UNSUPPORTED
+    assert fwd(rot=24) == vfa.VFA_ERR_UNSUPPORTED and b"rotary_dim" in L.vfa_last_error()
+    for kw in (dict(q=None), dict(out=None), dict(q=odd), dict(stride=508), dict(stride=504),
+               dict(pos=None), dict(table=None), dict(table=odd), dict(axes=0), dict(rot=144),
+               dict(rot=-16), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+               dict(T=-1), dict(Hq=0)):
+        assert fwd(**kw) == vfa.VFA_ERR_INVALID_ARG, kw
+    assert L.vfa_qk_norm_rope_bwd_workspace_bytes(96) == 0
+    need = L.vfa_qk_norm_rope_bwd_workspace_bytes(128)
+    assert need > 0
+
+    def bwd(qw=f, dqw=f, ws=f, n=need, dy=f):
+        return L.vfa_qk_norm_rope_bwd(f, f, 512, 256, dy, f, 512, 256, f, 1, f, 64, 0, qw, None,
+                                      1e-6, 4, 4, 2, 128, f, f, 512, 256, dqw, None, ws, n, None)
+
+    for kw in (dict(dqw=None), dict(ws=None), dict(ws=odd), dict(n=need - 1), dict(dy=None)):
+        assert bwd(**kw) == vfa.VFA_ERR_INVALID_ARG, kw
+
+
+def test_kv4_host_checks(vfa):
+    L = vfa.lib()
+    f, odd = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100008)
+    assert L.vfa_kv4_block_bytes(8, 128) == 8 * 18 * 128
+    assert L.vfa_kv4_block_bytes(8, 96) == 0 and L.vfa_kv4_block_bytes(0, 128) == 0
+
+    def write(k=f, stride=256, total=4, pool=f, blocks=9, tables=f, cap=3, cu=f, start=f, S=2,
+              D=128, dk=1.0, dv=1.0, fn=L.vfa_kv4_write):
+        return fn(k, f, stride, 256, total, pool, blocks, tables, cap, cu, start, S, 2, D, dk, dv,
+                  None, None)
+
+    for fn in (L.vfa_kv4_write, L.vfa_kv4_gather):
+        assert write(fn=fn, D=96) == vfa.VFA_ERR_UNSUPPORTED
+        assert write(fn=fn, blocks=(1 << 26) + 1) == vfa.VFA_ERR_UNSUPPORTED
+        for kw in (dict(k=None), dict(k=odd), dict(pool=None), dict(pool=odd), dict(tables=None),
+                   dict(cu=None), dict(start=None), dict(stride=248), dict(stride=257),
+                   dict(total=-1), dict(cap=-1), dict(S=0), dict(dk=0.0), dict(dk=3.0),
+                   dict(dv=-1.0), dict(dv=float("nan")), dict(dk=float("inf")),
+                   dict(dk=2.0 ** -65), dict(dv=2.0 ** 65)):
+            assert write(fn=fn, **kw) == vfa.VFA_ERR_INVALID_ARG, kw
+    need = L.vfa_kv4_decode_workspace_bytes(4, 32, 8, 128)
+    assert need > 0
+    assert L.vfa_kv4_decode_workspace_bytes(4, 30, 8, 128) == 0
+    assert L.vfa_kv4_decode_workspace_bytes(4, 32, 8, 80) == 0
+    assert L.vfa_kv4_decode_workspace_bytes(0, 32, 8, 128) == 0
+    ws = ctypes.c_void_p(0x200000)
+
+    def decode(q=f, cap=9, counts=f, S=4, Hq=32, D=128, dk=1.0, scale=0.0, out=f, lse=f, w=ws,
+               n=need):
+        return L.vfa_kv4_decode(q, f, 64, f, cap, counts, S, Hq, 8, D, dk, 1.0, scale, out, lse,
+                                None, w, n, None)
+
+    assert decode(D=96) == vfa.VFA_ERR_UNSUPPORTED
+    assert decode(cap=1 << 29, n=1 << 40) == vfa.VFA_ERR_UNSUPPORTED
+    for kw in (dict(q=None), dict(q=odd), dict(counts=None), dict(out=None), dict(Hq=30),
+               dict(Hq=0), dict(dk=0.3), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(w=None), dict(w=odd), dict(n=need - 1), dict(lse=ctypes.c_void_p(0x100002))):
+        assert decode(**kw) == vfa.VFA_ERR_INVALID_ARG, kw
+
+
+def test_page_operation_host_checks(vfa):
+    L = vfa.lib()
+    f, odd = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100002)
+    need = L.vfa_pages_workspace_bytes(100, 4, 8)
+    assert need >= 3 * 100 * 4
+    assert L.vfa_pages_workspace_bytes(0, 4, 8) == 0
+    assert L.vfa_pages_workspace_bytes((1 << 26) + 1, 4, 8) == 0
+    assert L.vfa_pages_workspace_bytes(100, 0, 8) == 0
+    assert L.vfa_pages_workspace_bytes(100, 4, -1) == 0
+    ptrs = (ctypes.c_void_p * 2)(0x100000, 0x200000)
+    sizes = (ctypes.c_int * 2)(64, 128)
+
+    def fork(refs=f, blocks=100, cap=6, S=4, par=f, chi=f, n=8, p=ptrs, sz=sizes, np=2, bs=16,
+             ws=f, nb=need):
+        return L.vfa_pages_fork(refs, blocks, f, cap, f, S, par, chi, n, p, sz, np, bs, ws, nb,
+                                None, None)
+
+    assert fork(blocks=(1 << 26) + 1) == vfa.VFA_ERR_UNSUPPORTED
+    assert fork(np=257) == vfa.VFA_ERR_UNSUPPORTED
+    bad_ptr = (ctypes.c_void_p * 2)(0x100000, 0x200008)
+    null_ptr = (ctypes.c_void_p * 2)(0x100000, None)
+    for kw in (dict(refs=None), dict(refs=odd), dict(blocks=0), dict(cap=0), dict(S=0),
+               dict(par=None), dict(chi=odd), dict(n=-1), dict(p=None), dict(sz=None),
+               dict(np=-1), dict(p=bad_ptr), dict(p=null_ptr),
+               dict(sz=(ctypes.c_int * 2)(64, 24)), dict(sz=(ctypes.c_int * 2)(0, 64)),
+               dict(bs=0), dict(ws=None), dict(nb=need - 1)):
+        assert fork(**kw) == vfa.VFA_ERR_INVALID_ARG, kw
+    ext = lambda add=f, ws=f, nb=need: L.vfa_pages_extend(f, 100, f, 6, f, 4, add, 16, ws, nb, None,
+                                                          None)
+    assert ext(add=None) == vfa.VFA_ERR_INVALID_ARG
+    assert ext(ws=odd) == vfa.VFA_ERR_INVALID_ARG
+    assert ext(nb=64) == vfa.VFA_ERR_INVALID_ARG
+    assert L.vfa_pages_free(f, 100, f, 6, f, 4, None, 1, 16, None, None) == vfa.VFA_ERR_INVALID_ARG
+    assert L.vfa_pages_free(f, 100, f, 6, f, 4, f, -1, 16, None, None) == vfa.VFA_ERR_INVALID_ARG
+    comp = lambda ro=f, to=f, nu=f: L.vfa_pages_compact(f, 100, f, 6, f, 4, ptrs, sizes, 2, 16, ro,
+                                                        to, nu, f, need, None, None)
+    for args in ((None, f, f), (f, None, f), (f, f, None), (odd, f, f)):
+        assert comp(*args) == vfa.VFA_ERR_INVALID_ARG
+    copy = lambda src=f, n=2, nb=9: L.vfa_pages_copy(ptrs, sizes, 2, src, f, n, nb, None, None)
+    assert copy(src=None) == vfa.VFA_ERR_INVALID_ARG
+    assert copy(n=-1) == vfa.VFA_ERR_INVALID_ARG and copy(nb=0) == vfa.VFA_ERR_INVALID_ARG
+
+
+def test_binding_checks_of_the_serving_operators(vfa):
+    """Wrong devices, types and shapes are refused before anything is launched."""
+    import torch
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        vfa.qk_norm_rope(x, x, i, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        vfa.kv4_write(x, x, torch.zeros(1, 2, 1152, dtype=torch.uint8), i[None], i, i)
+    with pytest.raises(ValueError, match="CUDA"):
+        vfa.pages_free(i, i[None], i, i, 16)
+    with pytest.raises(ValueError, match="axis per"):
+        vfa.rope_table([1.0, 0.5], [0], device="cpu")
+    with pytest.raises(ValueError, match="finite"):
+        vfa.rope_table([float("nan")], device="cpu")
+    with pytest.raises(ValueError, match="axes"):
+        vfa.rope_table([1.0], [-1], device="cpu")
+    with pytest.raises(vfa.VfaError):
+        vfa.alloc_kv4_pool(4, 2, 96, device="cpu")
+    assert vfa.alloc_kv4_pool(4, 2, 128, device="cpu").shape == (4, 2, 18 * 128)
+    # the table's steps: exact products of position and step stay within 2^-64 turns a position
+    import math
+    t = vfa.rope_table([1.0, 1e-5, -2.5], [0, 1, 2], device="cpu")
+    assert t[:, 1].tolist() == [0, 1, 2]
+    for step, f in zip(t[:, 0].tolist(), (1.0, 1e-5, -2.5)):
+        turns = (step % 2 ** 64) / 2 ** 64
+        assert abs(turns - f / (2 * math.pi) % 1.0) < 1e-15

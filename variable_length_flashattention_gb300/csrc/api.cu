@@ -170,6 +170,15 @@ vfa_status vfa::set_error(vfa_status st, const char *message)
     return fail(st, "%s", message);
 }
 
+vfa_status vfa::device_sm_count(int *sm_count)
+{
+    DeviceInfo dev;
+    vfa_status st = current_device(&dev);
+    if (st == VFA_OK)
+        *sm_count = dev.sm_count;
+    return st;
+}
+
 extern "C" {
 
 const char *vfa_last_error(void) { return g_err; }

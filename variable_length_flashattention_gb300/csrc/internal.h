@@ -194,6 +194,115 @@ void bwd_workspace_split(void *ws, int batch, int total_q, int num_heads, BwdArg
 cudaError_t launch_bwd(int head_dim, const BwdArgs &a, int key_tile_bound, int q_tile_bound,
                        int sm_count, cudaStream_t stream);
 
+// ------------------------------------------------------------ norm and rotation
+
+// Index 0 is the queries, 1 the keys.
+struct RopeArgs {
+    const void *x[2];                       // bf16 [tokens, heads, D], token stride x_stride
+    const void *dy[2];                      // backward: gradients of the outputs
+    void *y[2];                             // forward: outputs; backward: dx
+    long long x_stride[2], dy_stride[2], y_stride[2];   // elements
+    const float *weight[2];                 // f32 [D], nullable: no norm
+    float *dweight[2];                      // backward: f32 [D], nullable
+    int heads[2];
+    const int32_t *positions;               // [num_axes, tokens]
+    const uint64_t *table;                  // [half][2]: turns per position * 2^64, axis
+    float *partial;                         // backward workspace: [CTAs, D]
+    int tokens, num_axes, half;             // half: rotated dimensions / 2
+    int interleaved;
+    float eps;
+    int segments;                           // set by the launcher: shares a token's heads take
+    int ctas[2];                            // set by the launcher (backward)
+};
+
+// Most CTAs the backward launches: the partial sums of dw in its workspace.
+constexpr int kRopeMaxCtas = 1216;
+
+cudaError_t launch_rope_fwd(int head_dim, RopeArgs &a, int sm_count, cudaStream_t stream);
+cudaError_t launch_rope_bwd(int head_dim, RopeArgs &a, int sm_count, cudaStream_t stream);
+
+// ------------------------------------------------------------ 4-bit cache
+
+// Bytes of one page of 16 tokens for one kv head: K and V codes (8 D each),
+// then K and V scales (D each).
+__host__ __device__ constexpr int kv4_head_page_bytes(int head_dim) { return 18 * head_dim; }
+
+constexpr int kKv4Page = 16;                // tokens per page
+
+// Writing packed tokens into the cache (k, v in) or reading them back (out).
+struct Kv4MoveArgs {
+    void *k, *v;                            // bf16 [total, num_kv_heads, D]
+    long long k_stride, v_stride;           // elements between tokens
+    void *pool;                             // uint8 [num_blocks, num_kv_heads, 18 D]
+    const int32_t *tables;                  // [num_seqs, capacity]
+    const int32_t *cu;                      // [num_seqs + 1]
+    const int32_t *start;                   // [num_seqs] position of each sequence's first token
+    int32_t *status;                        // nullable
+    int total, num_seqs, capacity, num_blocks, num_kv_heads;
+    float k_scale, v_scale;                 // write: 1 / descale; read: descale
+};
+
+cudaError_t launch_kv4_write(int head_dim, const Kv4MoveArgs &a, int sm_count, cudaStream_t stream);
+cudaError_t launch_kv4_gather(int head_dim, const Kv4MoveArgs &a, int sm_count,
+                              cudaStream_t stream);
+
+struct Kv4DecodeArgs {
+    const void *q;                          // bf16 [num_seqs, num_q_heads, D]
+    const uint8_t *pool;
+    const int32_t *tables, *counts;         // [num_seqs, capacity], [num_seqs] tokens
+    void *out;                              // bf16, as q
+    float *lse;                             // [num_seqs, num_q_heads], nullable
+    int32_t *status;                        // nullable
+    int32_t *tickets;                       // workspace: [num_seqs, head chunks], zero between calls
+    float *part;                            // workspace: partial states
+    int num_seqs, capacity, num_blocks, num_q_heads, num_kv_heads;
+    float scale_log2;                       // logit scale * descale_k * log2(e)
+    float descale_v;
+};
+
+size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim);
+cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, int sm_count,
+                              cudaStream_t stream);
+
+// ------------------------------------------------------------ page operations
+
+constexpr int kMaxPagePools = 256;
+
+struct PagePools {
+    uint8_t *ptr[kMaxPagePools];
+    int page_bytes[kMaxPagePools];          // multiples of 16
+    int n;
+};
+
+struct PageArgs {
+    int32_t *refs;                          // [num_blocks]
+    int32_t *refs_out;                      // compact: may equal refs
+    int32_t *tables;                        // [num_seqs, capacity]
+    int32_t *tables_out;                    // compact: may equal tables
+    int32_t *counts;                        // [num_seqs] tokens
+    const int32_t *add;                     // extend: [num_seqs]
+    const int32_t *parents, *children;      // fork: [n]
+    const int32_t *seqs;                    // free: [n]
+    int32_t *num_used;                      // compact: [1]
+    int32_t *status;                        // nullable
+    int32_t *ws;                            // workspace
+    int num_blocks, num_seqs, capacity, block_size, n;
+};
+
+size_t page_workspace_bytes(int num_blocks, int num_seqs, int num_forks);
+cudaError_t launch_pages_extend(const PageArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PageArgs &a, const PagePools &p, int sm_count,
+                              cudaStream_t stream);
+cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_count,
+                                 cudaStream_t stream);
+// pairs of the lists src and dst, n of them.
+cudaError_t launch_pages_copy(const PagePools &p, const int32_t *src, const int32_t *dst, int n,
+                              int num_blocks, int32_t *status, int sm_count, cudaStream_t stream);
+
+// SMs of the current device, which must be the one this library is built for.
+vfa_status device_sm_count(int *sm_count);
+
 // ------------------------------------------------------------ test hooks
 
 cudaError_t launch_debug_bounded_wait(int32_t *status, cudaStream_t stream);

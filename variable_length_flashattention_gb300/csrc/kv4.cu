@@ -1,0 +1,974 @@
+// kv4.cu -- a paged K/V cache held in 4 bits: writing packed tokens into it,
+// reading them back, and one-token grouped-query attention over it.
+//
+// Format.  Pages of 16 tokens; per page and kv head 18 D bytes: K codes
+// (8 D), V codes (8 D), K scales (D), V scales (D).  Codes are E2M1 (0, 0.5,
+// 1, 1.5, 2, 3, 4, 6 and a sign), scales E4M3, one per 16 consecutive
+// dimensions of a token; value = descale * scale * code.  A code has 2
+// significant bits and a scale 4, so with a power of two as descale a value
+// has at most 6: it is exact in bf16 and in f16, and nothing after the
+// quantisation rounds it again.  The order inside a page is the one the
+// decode kernel's lanes read (below); every byte belongs to one token, so
+// tokens are written independently.
+//   K codes   token t, dim d: byte t D/2 + d/2, low nibble for even d
+//   V codes   W = min(16, D/8) dims of a token and of its odd neighbour side by
+//             side: c = d / W, byte ((t/8) (D/8W) + c/8) 32 W +
+//             ((c%8) 4 + (t/2)%4) W + (t%2) W/2 + (d%W)/2
+//   K scales  byte t D/16 + d/16
+//   V scales  byte ((d/16) 4 + (t/2)%4) 4 + t%2 + 2 (t/8)
+#include <cfloat>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace vfa {
+
+namespace {
+
+constexpr int kPage = kKv4Page;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Offset in the V code area of the 16-dim group g of token t; for D = 64 the
+// group is two runs of 4 bytes, 32 bytes apart.
+template <int D>
+__device__ __forceinline__ int v_code_at(int t, int g)
+{
+    if (D == 64)
+        return (t >> 3) * 256 + (2 * g * 4 + ((t >> 1) & 3)) * 8 + (t & 1) * 4;
+    return ((t >> 3) * (D / 128) + (g >> 3)) * 512 + ((g & 7) * 4 + ((t >> 1) & 3)) * 16 +
+           (t & 1) * 8;
+}
+
+__device__ __forceinline__ int v_scale_at(int t, int g)
+{
+    return (g * 4 + ((t >> 1) & 3)) * 4 + (t & 1) + 2 * (t >> 3);
+}
+
+__device__ __forceinline__ void record(int32_t *status, int code)
+{
+    if (status)
+        atomicCAS(status, 0, code);
+}
+
+// ------------------------------------------------------------ number formats
+
+// Four bytes of two E2M1 codes each -> four f16x2 (low nibble in the low half).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Eight floats -> eight E2M1 codes, nearest even, saturating; f[0] in the low nibble.
+__device__ __forceinline__ uint32_t f32_to_e2m1x8(const float *f)
+{
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return w;
+}
+
+// Two E4M3 codes (low byte first) -> f16x2.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two)
+{
+    uint32_t h;
+    asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}"
+        : "=r"(h)
+        : "r"(two));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t f32_to_e4m3(float f)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %1, %2;\n\tcvt.u32.u16 %0, x;\n\t}"
+        : "=r"(r)
+        : "f"(0.f), "f"(f));
+    return r & 0xffu;
+}
+
+__device__ __forceinline__ float f16_lo(uint32_t h)
+{
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffffu)));
+}
+
+__device__ __forceinline__ float f16_hi(uint32_t h)
+{
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h >> 16)));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ------------------------------------------------------------ write, read
+//
+// One warp per packed token, D/16 lanes per head (a lane holds one scale's
+// 16 dims, so nothing is exchanged).  Bound: HBM, 2.5625 bytes per element.
+
+// Page and row of packed token t; false where it has none (a padding row at
+// or past cu[num_seqs], or bad tables, which are recorded).
+__device__ __forceinline__ bool token_slot(const Kv4MoveArgs &a, int t, int *page, int *row)
+{
+    int lo = 0, hi = a.num_seqs;                 // cu[lo] <= t < cu[hi]
+    if (t >= __ldg(a.cu + hi))
+        return false;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.cu + mid) <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int c0 = __ldg(a.cu + lo);
+    if (c0 > t || t >= __ldg(a.cu + lo + 1)) {
+        if ((threadIdx.x & 31) == 0)
+            record(a.status, VFA_ERR_BAD_SEQLENS);
+        return false;
+    }
+    const int st = __ldg(a.start + lo);
+    const long long pos = static_cast<long long>(st) + (t - c0);
+    const bool in = st >= 0 && pos < static_cast<long long>(a.capacity) * kPage;
+    const int p = in ? __ldg(a.tables + static_cast<long long>(lo) * a.capacity + pos / kPage) : -1;
+    if (p < 0 || p >= a.num_blocks) {
+        if ((threadIdx.x & 31) == 0)
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        return false;
+    }
+    *page = p;
+    *row = static_cast<int>(pos % kPage);
+    return true;
+}
+
+// cu must start at 0, not decrease and not pass `total` (CTA 0 checks).
+__device__ __forceinline__ void check_cu(const Kv4MoveArgs &a)
+{
+    bool bad = false;
+    for (int s = threadIdx.x; s <= a.num_seqs; s += blockDim.x) {
+        const int c = a.cu[s];
+        bad |= s == 0 ? c != 0 : c < a.cu[s - 1];
+        bad |= c > a.total;
+    }
+    if (bad)
+        record(a.status, VFA_ERR_BAD_SEQLENS);
+}
+
+// 16 values -> scale byte and two code words.  x / scale decides at most
+// which of two neighbouring codes is nearer.  With a power of two as descale
+// x has 8 significant bits and scale * midpoint 7, so a quotient that is not
+// exactly a midpoint is at least 2^-8 (relative) away from it; x * (1/scale)
+// is within 2^-23, and rounding it to f16 (11 bits) restores exact midpoints
+// and moves the others by at most 2^-11: the codes are those of the exact
+// quotient.  The same holds for max / 6 against the midpoints of E4M3.
+__device__ __forceinline__ void quantise16(const float (&x)[16], uint32_t *scale, uint32_t (&w)[2])
+{
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        m = fmaxf(m, fabsf(x[j]));
+    *scale = f32_to_e4m3(__fdiv_rn(m, 6.f));
+    const float s = f16_lo(e4m3x2_to_f16(*scale));
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t h = pack_f16x2(x[2 * j] * r, x[2 * j + 1] * r);
+        y[2 * j] = f16_lo(h);
+        y[2 * j + 1] = f16_hi(h);
+    }
+    w[0] = f32_to_e2m1x8(y);
+    w[1] = f32_to_e2m1x8(y + 8);
+}
+
+constexpr int kMoveWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMoveWarps * 32) kv4_write_kernel(const Kv4MoveArgs a)
+{
+    constexpr int GR = D / 16, HPW = 32 / GR;
+    const int lane = threadIdx.x & 31;
+    const int g = lane % GR;
+    if (blockIdx.x == 0)
+        check_cu(a);
+    const int nwarps = gridDim.x * kMoveWarps;
+    for (int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); t < a.total; t += nwarps) {
+        int page, row;
+        if (!token_slot(a, t, &page, &row))
+            continue;
+        uint8_t *pg = static_cast<uint8_t *>(a.pool) +
+                      static_cast<long long>(page) * a.num_kv_heads * kv4_head_page_bytes(D);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const __nv_bfloat16 *src =
+                static_cast<const __nv_bfloat16 *>(which ? a.v : a.k) +
+                static_cast<long long>(t) * (which ? a.v_stride : a.k_stride) + g * 16;
+            const float inv = which ? a.v_scale : a.k_scale;
+            for (int h = lane / GR; h < a.num_kv_heads; h += HPW) {
+                const uint4 r0 = __ldcs(reinterpret_cast<const uint4 *>(src + h * D));
+                const uint4 r1 = __ldcs(reinterpret_cast<const uint4 *>(src + h * D) + 1);
+                const uint32_t rw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[2 * j] = __uint_as_float(rw[j] << 16) * inv;
+                    x[2 * j + 1] = __uint_as_float(rw[j] & 0xffff0000u) * inv;
+                }
+                uint32_t scale, w[2];
+                quantise16(x, &scale, w);
+                uint8_t *hp = pg + h * kv4_head_page_bytes(D);
+                if (which == 0) {
+                    *reinterpret_cast<uint2 *>(hp + row * (D / 2) + g * 8) = make_uint2(w[0], w[1]);
+                    hp[16 * D + row * GR + g] = static_cast<uint8_t>(scale);
+                } else {
+                    uint8_t *vp = hp + 8 * D + v_code_at<D>(row, g);
+                    if (D == 64) {
+                        *reinterpret_cast<uint32_t *>(vp) = w[0];
+                        *reinterpret_cast<uint32_t *>(vp + 32) = w[1];
+                    } else {
+                        *reinterpret_cast<uint2 *>(vp) = make_uint2(w[0], w[1]);
+                    }
+                    hp[17 * D + v_scale_at(row, g)] = static_cast<uint8_t>(scale);
+                }
+            }
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4MoveArgs a)
+{
+    constexpr int GR = D / 16, HPW = 32 / GR;
+    const int lane = threadIdx.x & 31;
+    const int g = lane % GR;
+    if (blockIdx.x == 0)
+        check_cu(a);
+    const int nwarps = gridDim.x * kMoveWarps;
+    for (int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); t < a.total; t += nwarps) {
+        int page, row;
+        if (!token_slot(a, t, &page, &row))
+            continue;
+        const uint8_t *pg = static_cast<const uint8_t *>(a.pool) +
+                            static_cast<long long>(page) * a.num_kv_heads * kv4_head_page_bytes(D);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(which ? a.v : a.k) +
+                                 static_cast<long long>(t) * (which ? a.v_stride : a.k_stride) +
+                                 g * 16;
+            const float ds = which ? a.v_scale : a.k_scale;
+            for (int h = lane / GR; h < a.num_kv_heads; h += HPW) {
+                const uint8_t *hp = pg + h * kv4_head_page_bytes(D);
+                uint2 w;
+                uint32_t scale;
+                if (which == 0) {
+                    w = *reinterpret_cast<const uint2 *>(hp + row * (D / 2) + g * 8);
+                    scale = hp[16 * D + row * GR + g];
+                } else {
+                    const uint8_t *vp = hp + 8 * D + v_code_at<D>(row, g);
+                    if (D == 64) {
+                        w.x = *reinterpret_cast<const uint32_t *>(vp);
+                        w.y = *reinterpret_cast<const uint32_t *>(vp + 32);
+                    } else {
+                        w = *reinterpret_cast<const uint2 *>(vp);
+                    }
+                    scale = hp[17 * D + v_scale_at(row, g)];
+                }
+                const float s = f16_lo(e4m3x2_to_f16(scale)) * ds;
+                uint32_t h8[8];
+                {
+                    uint32_t lo[4], hi[4];
+                    e2m1x8_to_f16(w.x, lo);
+                    e2m1x8_to_f16(w.y, hi);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        h8[j] = pack_bf16x2(f16_lo(lo[j]) * s, f16_hi(lo[j]) * s);
+                        h8[4 + j] = pack_bf16x2(f16_lo(hi[j]) * s, f16_hi(hi[j]) * s);
+                    }
+                }
+                uint4 *o = reinterpret_cast<uint4 *>(dst + h * D);
+                o[0] = make_uint4(h8[0], h8[1], h8[2], h8[3]);
+                o[1] = make_uint4(h8[4], h8[5], h8[6], h8[7]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ decode
+//
+// Online softmax over the cached tokens of each sequence, G = Hq / Hkv query
+// heads of a kv head together (eight at most per CTA; more heads are more
+// head chunks, whose pages come from L2).
+//
+// Work.  Every sequence counts ceil(tokens / 16) units (pages; 1 if empty);
+// the batch's units in one row are cut into equal contiguous runs, one per
+// CTA, so long and short contexts load every SM alike.  A run covers any
+// number of sequences; a sequence that lies in one run is finished there, the
+// others leave partial states (m, l, o), merged in a fixed order by the CTA
+// that takes the last ticket.  No CTA waits for another.
+//
+// A producer warp streams the run's head pages (18 D bytes each, contiguous)
+// through a ring of shared-memory stages with bulk copies; unit i is consumed
+// by warp i % 4.  Per page and warp, two products on mma.sync m16n8k16 (f16
+// in, fp32 accumulate):
+//   S[16 tokens x 8 heads] = K Q^T    O^T[D x 8 heads] += V^T P
+// The page's order gives every lane its A operands in whole 16-byte words: a
+// lane of K's operand holds 32 consecutive dims of two tokens (two scales
+// each), one of V's 16 dims of four tokens, whose codes are paired by token
+// with two logic operations per eight codes.  Which dim is which k index of
+// a product is free as long as Q agrees.
+//
+// Numbers.  K, V as f16: exact (see the format).  q is multiplied by a power
+// of two per head that puts its largest element at 2^14: f16 then holds every
+// bf16 bit of elements down to 2^-21 of the largest and is within 2^-39 of
+// the largest below.  p is held as 2^14 p in f16 (2^-12 relative for p above
+// 2^-28), l sums the fp32 values, and m, l, o are fp32.
+constexpr int kConsumers = 4;
+constexpr int kDecThreads = (kConsumers + 1) * 32;
+constexpr int kHeads = 8;               // query heads of a kv head per CTA
+constexpr int kMinRun = 8;              // units per CTA at least
+constexpr int kMaxParts = 608;          // CTAs at most, where there are fewer head chunks
+constexpr float kPShift = 14.f;
+
+template <int D>
+struct DecCfg {
+    static constexpr int STAGE = 18 * D;
+    static constexpr int NS = 36864 / STAGE;        // 32, 16, 8 stages: a multiple of kConsumers
+    static constexpr int MT = D / 16;
+    static constexpr int KW = D / 32;               // code words of one token per lane
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t movm_t(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void consumers_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+
+// Units of a sequence, and its token count (0 and *bad for an invalid one).
+__device__ __forceinline__ int seq_units(const Kv4DecodeArgs &a, int s, int *tokens, bool *bad)
+{
+    const int n = __ldg(a.counts + s);
+    *bad = n < 0 || n > static_cast<long long>(a.capacity) * kPage;
+    *tokens = *bad ? 0 : n;
+    const int u = (*tokens + kPage - 1) / kPage;
+    return u < 1 ? 1 : u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4DecodeArgs a)
+{
+    using C = DecCfg<D>;
+    constexpr int NS = C::NS, MT = C::MT, KW = C::KW;
+    extern __shared__ __align__(128) uint8_t dsm[];
+    __shared__ uint64_t s_full[NS], s_empty[NS];
+    __shared__ int s_stage_bad[NS];
+    __shared__ float s_m[kConsumers][kHeads], s_l[kConsumers][kHeads];
+    __shared__ int s_bad[kConsumers];
+    __shared__ int s_scan[kDecThreads / 32];
+    __shared__ int s_first, s_first_unit, s_abort, s_last;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = a.num_q_heads / a.num_kv_heads;
+    const int chunks = (group + kHeads - 1) / kHeads;
+    const int kh = blockIdx.y / chunks;
+    const int h0 = kh * group + (blockIdx.y % chunks) * kHeads;     // first query head
+    const int G = min(kHeads, (kh + 1) * group - h0);
+
+    // Units before each thread's share of the sequences.
+    const int per = (a.num_seqs + kDecThreads - 1) / kDecThreads;
+    const int sa = min(a.num_seqs, tid * per), sb = min(a.num_seqs, sa + per);
+    int mine = 0;
+    for (int s = sa; s < sb; ++s) {
+        int n;
+        bool bad;
+        mine += seq_units(a, s, &n, &bad);
+    }
+    int x = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off)
+            x += y;
+    }
+    if (lane == 31)
+        s_scan[warp] = x;
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&s_empty[i]), 1);
+            s_stage_bad[i] = 0;
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    int before = x - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kDecThreads / 32; ++i) {
+        before += i < warp ? s_scan[i] : 0;
+        total += s_scan[i];
+    }
+    // This CTA's run [u0, u1) of the row of units.
+    int run = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    run = run < kMinRun ? kMinRun : run;
+    const long long u0l = static_cast<long long>(blockIdx.x) * run;
+    if (u0l >= total)
+        return;
+    const int u0 = static_cast<int>(u0l), u1 = min(total, u0 + run);
+    if (u0 >= before && u0 < before + mine) {
+        int at = before;
+        for (int s = sa; s < sb; ++s) {
+            int n;
+            bool bad;
+            const int u = seq_units(a, s, &n, &bad);
+            if (u0 < at + u) {
+                s_first = s;
+                s_first_unit = at;
+                break;
+            }
+            at += u;
+        }
+    }
+    __syncthreads();
+    volatile int *abort = &s_abort;
+    const uint32_t ring = smem_u32(dsm);
+    const size_t page_bytes = static_cast<size_t>(a.num_kv_heads) * C::STAGE;
+    const uint8_t *pool = a.pool + static_cast<size_t>(kh) * C::STAGE;
+
+    if (warp == kConsumers) {
+        // ------------------------------------------------ producer
+        int s = s_first, at = s_first_unit, i = 0;
+        bool ok = true;
+        while (ok && at < u1) {
+            int n;
+            bool bad;
+            const int units = seq_units(a, s, &n, &bad);
+            if (bad && lane == 0)
+                record(a.status, VFA_ERR_BAD_BLOCK);
+            const int j0 = max(0, u0 - at), j1 = min(units, u1 - at);
+            const int32_t *row = a.tables + static_cast<long long>(s) * a.capacity;
+            for (int jb = j0; ok && jb < j1; jb += 32) {
+                const int id = jb + lane < j1 && n > 0 ? __ldg(row + jb + lane) : -1;
+                const int m = min(32, j1 - jb);
+                for (int k = 0; k < m; ++k, ++i) {
+                    const int blk = __shfl_sync(0xffffffffu, id, k);
+                    const int st = i % NS, f = i / NS;
+                    if (lane == 0) {
+                        if (f > 0)
+                            ok = mbar_wait(smem_u32(&s_empty[st]), (f - 1) & 1, abort);
+                        if (ok && blk >= 0 && blk < a.num_blocks) {
+                            s_stage_bad[st] = 0;
+                            mbar_arrive_expect_tx(smem_u32(&s_full[st]), C::STAGE);
+                            bulk_load(ring + st * C::STAGE, pool + blk * page_bytes, C::STAGE,
+                                      smem_u32(&s_full[st]));
+                        } else if (ok) {
+                            // an empty sequence's one unit, or a bad id
+                            s_stage_bad[st] = n > 0;
+                            if (n > 0)
+                                record(a.status, VFA_ERR_BAD_BLOCK);
+                            mbar_arrive(smem_u32(&s_full[st]));
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok)
+                        break;
+                }
+            }
+            at += units;
+            ++s;
+        }
+        // every copy issued has landed before the CTA can end, also after a
+        // consumer gave up: the last of the i units issued into each stage
+        if (lane == 0)
+            for (int st = 0; st < NS && st < i; ++st)
+                mbar_wait_drain(smem_u32(&s_full[st]), ((i - 1 - (i - 1 - st) % NS) / NS) & 1);
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    const int r = lane >> 2, t4 = lane & 3;
+    float *s_o = reinterpret_cast<float *>(dsm + NS * C::STAGE);    // [kConsumers][G][D]
+    int s = s_first, at = s_first_unit;
+    int i = warp;                                   // this warp's next unit, from the run's start
+    bool first_segment = true;
+    while (at < u1) {
+        int n;
+        bool seq_bad;
+        const int units = seq_units(a, s, &n, &seq_bad);
+        const int j0 = max(0, u0 - at), j1 = min(units, u1 - at);
+        const int end = at + j1 - u0;               // run-local index of the segment's end
+
+        // Q^T operand: head r, dims as K's lanes hold them.
+        uint32_t qb[MT][2];
+        float sc;
+        {
+            const uint2 *qrow = reinterpret_cast<const uint2 *>(
+                static_cast<const __nv_bfloat16 *>(a.q) +
+                (static_cast<long long>(s) * a.num_q_heads + h0 + (r < G ? r : 0)) * D);
+            uint2 raw[MT];
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                // dims of product j: piece j / 8 (128 dims), 4 dims from t4 * 32 (D = 64: t4 * 16)
+                const int d = D == 64 ? t4 * 16 + 4 * j : (j >> 3) * 128 + t4 * 32 + 4 * (j & 7);
+                raw[j] = __ldg(qrow + d / 4);
+                const uint32_t w[2] = {raw[j].x, raw[j].y};
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                                       fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+            }
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // exponent of the largest element, kept where 2^(14 - e) is a normal float
+            int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+            e = m > 0.f ? max(-100, min(127, e)) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+            const float down = ldexpf(1.f, e - 14);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const uint32_t w[2] = {raw[j].x, raw[j].y};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    qb[j][c] = r < G ? pack_f16x2(__uint_as_float(w[c] << 16) * up,
+                                                  __uint_as_float(w[c] & 0xffff0000u) * up)
+                                     : 0u;
+            }
+            sc = a.scale_log2 * down;               // of head r; the accumulators hold 2 t4, + 1
+        }
+        const float sc0 = __shfl_sync(0xffffffffu, sc, (2 * t4) * 4);
+        const float sc1 = __shfl_sync(0xffffffffu, sc, (2 * t4 + 1) * 4);
+
+        float m_run[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
+        float o[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[mt][e] = 0.f;
+        bool bad = seq_bad;
+
+        for (; i < end; i += kConsumers) {
+            const int st = i % NS;
+            if (!mbar_wait_warp(smem_u32(&s_full[st]), (i / NS) & 1, abort)) {
+                bad = true;
+                continue;
+            }
+            const uint32_t page = ring + st * C::STAGE;
+            const int valid = n - (u0 + i - at) * kPage;        // tokens of this page that count
+            bad |= s_stage_bad[st] != 0;
+            if (valid > 0 && !bad) {
+                // S = K Q^T
+                float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t kw[2][KW], ks[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int tok = r + 8 * half;
+                    const uint32_t row = page + tok * (D / 2);
+                    if constexpr (D == 64) {
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                     : "=r"(kw[half][0]), "=r"(kw[half][1])
+                                     : "r"(row + t4 * 8));
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < KW / 4; ++p) {
+                            const uint4 v = ld_shared_v4(row + p * 64 + t4 * 16);
+                            kw[half][4 * p] = v.x;
+                            kw[half][4 * p + 1] = v.y;
+                            kw[half][4 * p + 2] = v.z;
+                            kw[half][4 * p + 3] = v.w;
+                        }
+                    }
+                    // the token's scales for this lane's dims, in order
+                    const uint8_t *sp = dsm + st * C::STAGE + 16 * D + tok * (D / 16);
+                    if constexpr (D == 64) {
+                        ks[half] = sp[t4] * 0x101u;
+                    } else if constexpr (D == 128) {
+                        ks[half] = *reinterpret_cast<const uint16_t *>(sp + 2 * t4);
+                    } else {
+                        ks[half] = *reinterpret_cast<const uint16_t *>(sp + 2 * t4) |
+                                   (static_cast<uint32_t>(
+                                        *reinterpret_cast<const uint16_t *>(sp + 8 + 2 * t4))
+                                    << 16);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    // one word: eight codes of 8 dims = products 2w, 2w + 1; one scale
+                    uint32_t c0[4], c1[4];
+                    e2m1x8_to_f16(kw[0][w], c0);
+                    e2m1x8_to_f16(kw[1][w], c1);
+                    const int si = D == 64 ? 0 : w / 2;         // index of the word's scale
+                    const uint32_t p0 = e4m3x2_to_f16(ks[0] >> (16 * (si / 2)));
+                    const uint32_t p1 = e4m3x2_to_f16(ks[1] >> (16 * (si / 2)));
+                    const uint32_t f0 = __byte_perm(p0, p0, si & 1 ? 0x3232 : 0x1010);
+                    const uint32_t f1 = __byte_perm(p1, p1, si & 1 ? 0x3232 : 0x1010);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t af[4] = {hmul2(c0[2 * q], f0), hmul2(c1[2 * q], f1),
+                                                hmul2(c0[2 * q + 1], f0), hmul2(c1[2 * q + 1], f1)};
+                        mma_f16(sacc, af, qb[2 * w + q][0], qb[2 * w + q][1]);
+                    }
+                }
+                // tokens r (0, 1) and r + 8 (2, 3); heads 2 t4 (0, 2) and 2 t4 + 1 (1, 3)
+                float xs[4] = {sacc[0] * sc0, sacc[1] * sc1, sacc[2] * sc0, sacc[3] * sc1};
+                if (valid < kPage) {
+                    if (r >= valid)
+                        xs[0] = xs[1] = -INFINITY;
+                    if (r + 8 >= valid)
+                        xs[2] = xs[3] = -INFINITY;
+                }
+                float bm[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float y = fmaxf(xs[h], xs[h + 2]);
+#pragma unroll
+                    for (int off = 4; off <= 16; off <<= 1)
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+                    bm[h] = y;
+                }
+                if (__any_sync(0xffffffffu, bm[0] > m_run[0] || bm[1] > m_run[1])) {
+                    float f[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float mnew = fmaxf(m_run[h], bm[h]);
+                        f[h] = mnew == m_run[h] ? 1.f : ex2_approx(m_run[h] - mnew);
+                        m_run[h] = mnew;
+                        l_part[h] *= f[h];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        o[mt][0] *= f[0];
+                        o[mt][1] *= f[1];
+                        o[mt][2] *= f[0];
+                        o[mt][3] *= f[1];
+                    }
+                }
+                const float e0 = kPShift - m_run[0], e1 = kPShift - m_run[1];
+                const float p0 = ex2_approx(xs[0] + e0), p1 = ex2_approx(xs[1] + e1);
+                const float p2 = ex2_approx(xs[2] + e0), p3 = ex2_approx(xs[3] + e1);
+                l_part[0] += p0 + p2;
+                l_part[1] += p1 + p3;
+                const uint32_t pb0 = movm_t(pack_f16x2(p0, p1));
+                const uint32_t pb1 = movm_t(pack_f16x2(p2, p3));
+
+                // O^T += V^T P
+#pragma unroll
+                for (int p = 0; p < (D == 256 ? 2 : 1); ++p) {
+                    const int grp = D == 64 ? r >> 1 : r + 8 * p;
+                    uint32_t vs;
+                    asm volatile("ld.shared.b32 %0, [%1];"
+                                 : "=r"(vs)
+                                 : "r"(page + 17 * D + (grp * 4 + t4) * 4));
+                    if (valid < kPage) {
+                        // a page's unused rows may hold any bytes: their scales count as zero
+                        vs &= (2 * t4 < valid ? 0x000000ffu : 0u) |
+                              (2 * t4 + 1 < valid ? 0x0000ff00u : 0u) |
+                              (2 * t4 + 8 < valid ? 0x00ff0000u : 0u) |
+                              (2 * t4 + 9 < valid ? 0xff000000u : 0u);
+                    }
+                    const uint32_t f0 = e4m3x2_to_f16(vs & 0xffffu), f1 = e4m3x2_to_f16(vs >> 16);
+                    uint32_t even[2][2], odd[2][2];         // [token half][code word]
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if constexpr (D == 64) {
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                         : "=r"(even[half][0]), "=r"(odd[half][0])
+                                         : "r"(page + 8 * D + half * 256 + lane * 8));
+                        } else {
+                            const uint4 v =
+                                ld_shared_v4(page + 8 * D + (half * (D / 128) + p) * 512 + lane * 16);
+                            even[half][0] = v.x;
+                            even[half][1] = v.y;
+                            odd[half][0] = v.z;
+                            odd[half][1] = v.w;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < (D == 64 ? 1 : 2); ++w) {
+                        // codes of eight dims paired by token: (even, odd) per byte
+                        uint32_t a0[4], a1[4], a2[4], a3[4];
+                        const uint32_t M = 0x0f0f0f0fu;
+                        e2m1x8_to_f16((even[0][w] & M) | ((odd[0][w] << 4) & ~M), a0);
+                        e2m1x8_to_f16(((even[0][w] >> 4) & M) | (odd[0][w] & ~M), a1);
+                        e2m1x8_to_f16((even[1][w] & M) | ((odd[1][w] << 4) & ~M), a2);
+                        e2m1x8_to_f16(((even[1][w] >> 4) & M) | (odd[1][w] & ~M), a3);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint32_t af[4] = {hmul2(a0[b], f0), hmul2(a1[b], f0),
+                                                    hmul2(a2[b], f1), hmul2(a3[b], f1)};
+                            mma_f16(o[8 * p + 4 * w + b], af, pb0, pb1);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&s_empty[st]));
+        }
+
+        // ------------------------------------------------ end of the segment
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1)
+                l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], off);
+        }
+        bad = __any_sync(0xffffffffu, bad || *abort != 0);
+        if (lane < 4) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s_m[warp][2 * lane + h] = m_run[h];
+                s_l[warp][2 * lane + h] = l_part[h];
+            }
+        }
+        if (lane == 0)
+            s_bad[warp] = bad;
+        // o[mt]: dims of run r: 16 (r + 8 p) + 2 b (D = 64: 8 r + 2 b) in c0, c1, the next in c2, c3
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int d = D == 64 ? r * 8 + 2 * mt : (r + 8 * (mt >> 3)) * 16 + 2 * (mt & 7);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (2 * t4 + h < G)
+                    *reinterpret_cast<float2 *>(&s_o[(warp * G + 2 * t4 + h) * D + d]) =
+                        make_float2(o[mt][h], o[mt][2 + h]);
+        }
+        consumers_sync();
+        bad = s_bad[0] || s_bad[1] || s_bad[2] || s_bad[3];
+        const bool whole = j0 == 0 && j1 == units;
+        float *part = a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 *
+                                   kHeads * (D + 2) +
+                      (first_segment ? 0 : kHeads * (D + 2));
+        if (tid == 0 && *abort)
+            record(a.status, VFA_ERR_TIMEOUT);
+        for (int e = tid; e < G * D; e += kConsumers * 32) {
+            const int g = e / D, d = e % D;
+            float mt = s_m[0][g];
+#pragma unroll
+            for (int w = 1; w < kConsumers; ++w)
+                mt = fmaxf(mt, s_m[w][g]);
+            float acc_o = 0.f, acc_l = 0.f;
+            if (mt != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w) {
+                    const float f = ex2_approx(s_m[w][g] - mt);
+                    acc_o = fmaf(s_o[(w * G + g) * D + d], f, acc_o);
+                    acc_l = fmaf(s_l[w][g], f, acc_l);
+                }
+            }
+            if (whole) {
+                if (!bad) {
+                    const long long row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
+                    static_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(
+                        mt == -INFINITY ? 0.f : acc_o / acc_l * a.descale_v);
+                    if (d == 0 && a.lse)
+                        a.lse[row] = mt == -INFINITY ? -FLT_MAX
+                                                     : (mt - kPShift + __log2f(acc_l)) * kLn2;
+                }
+            } else {
+                part[g * (D + 2) + 2 + d] = acc_o;
+                if (d == 0) {
+                    part[g * (D + 2)] = mt;
+                    part[g * (D + 2) + 1] = bad ? -1.f : acc_l;     // a sum is never negative
+                }
+            }
+        }
+        if (!whole) {
+            // runs of this sequence: the first may start inside it, as a later segment
+            const int xa = at / run, xb = (at + units - 1) / run;
+            int32_t *ticket = a.tickets + static_cast<long long>(s) * gridDim.y + blockIdx.y;
+            __threadfence();
+            consumers_sync();
+            if (tid == 0)
+                s_last = atomicAdd(ticket, 1) == xb - xa;
+            consumers_sync();
+            if (s_last) {
+                __threadfence();
+                const float *base = a.part + static_cast<long long>(blockIdx.y) * gridDim.x * 2 *
+                                                 kHeads * (D + 2);
+                const int late = at % run != 0;     // run xa holds it in its second slot
+                for (int e = tid; e < G * D; e += kConsumers * 32) {
+                    const int g = e / D, d = e % D;
+                    auto slot = [&](int xx) {
+                        return base + (static_cast<long long>(xx) * 2 + (xx == xa ? late : 0)) *
+                                          kHeads * (D + 2) + g * (D + 2);
+                    };
+                    float mt = -INFINITY;
+                    bool any_bad = false;
+                    for (int xx = xa; xx <= xb; ++xx) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot(xx)));
+                        mt = fmaxf(mt, ml.x);
+                        any_bad |= ml.y < 0.f;
+                    }
+                    float acc_o = 0.f, acc_l = 0.f;
+                    for (int xx = xa; xx <= xb; ++xx) {
+                        const float *q = slot(xx);
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q));
+                        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mt);
+                        acc_l = fmaf(ml.y, f, acc_l);
+                        acc_o = fmaf(__ldcg(q + 2 + d), f, acc_o);
+                    }
+                    if (!any_bad) {
+                        const long long row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
+                        static_cast<__nv_bfloat16 *>(a.out)[row * D + d] =
+                            __float2bfloat16_rn(acc_o / acc_l * a.descale_v);
+                        if (d == 0 && a.lse)
+                            a.lse[row] = (mt - kPShift + __log2f(acc_l)) * kLn2;
+                    }
+                }
+                if (tid == 0)
+                    *ticket = 0;                    // ready for the next call
+            }
+        }
+        consumers_sync();                           // s_o, s_m, s_l, s_bad are free again
+        at += units;
+        ++s;
+        first_segment = false;
+    }
+}
+
+template <int D>
+cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
+{
+    using C = DecCfg<D>;
+    const int group = a.num_q_heads / a.num_kv_heads;
+    const int chunks = (group + kHeads - 1) / kHeads;
+    const int rows = a.num_kv_heads * chunks;
+    const int heads = group < kHeads ? group : kHeads;
+    const size_t smem = static_cast<size_t>(C::NS) * C::STAGE +
+                        static_cast<size_t>(kConsumers) * heads * D * sizeof(float);
+    // the largest size any call needs, once per device
+    static int attr_done[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !attr_done[dev]) {
+        e = cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::NS * C::STAGE +
+                                     kConsumers * kHeads * D * static_cast<int>(sizeof(float)));
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            attr_done[dev] = 1;
+    }
+    // three CTAs fit on an SM; runs of at least kMinRun pages
+    long long parts = (3LL * sm_count < kMaxParts ? 3LL * sm_count : kMaxParts) / rows;
+    const long long most = (static_cast<long long>(a.num_seqs) * (a.capacity > 0 ? a.capacity : 1) +
+                            kMinRun - 1) / kMinRun;
+    parts = parts < most ? parts : most;
+    parts = parts < 1 ? 1 : parts;
+    kv4_decode_kernel<D><<<dim3(static_cast<int>(parts), rows), kDecThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+int move_grid(int total, int sm_count)
+{
+    const long long g = (static_cast<long long>(total) + kMoveWarps - 1) / kMoveWarps;
+    const long long most = 64LL * sm_count;
+    return static_cast<int>(g < most ? g : most);
+}
+
+size_t ticket_bytes(int num_seqs, int rows)
+{
+    const size_t n = static_cast<size_t>(num_seqs) * rows * sizeof(int32_t);
+    return (n + 255) & ~static_cast<size_t>(255);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(int head_dim, const Kv4MoveArgs &a, int sm_count, cudaStream_t stream)
+{
+    const int grid = move_grid(a.total, sm_count);
+    switch (head_dim) {
+    case 64: kv4_write_kernel<64><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    case 128: kv4_write_kernel<128><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    case 256: kv4_write_kernel<256><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_gather(int head_dim, const Kv4MoveArgs &a, int sm_count,
+                              cudaStream_t stream)
+{
+    const int grid = move_grid(a.total, sm_count);
+    switch (head_dim) {
+    case 64: kv4_gather_kernel<64><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    case 128: kv4_gather_kernel<128><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    case 256: kv4_gather_kernel<256><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim)
+{
+    const int group = num_q_heads / num_kv_heads;
+    const int rows = num_kv_heads * ((group + kHeads - 1) / kHeads);
+    // at most kMaxParts runs in all, or one per row where there are more rows
+    const size_t runs = rows > kMaxParts ? rows : kMaxParts;
+    return ticket_bytes(num_seqs, rows) + runs * 2 * kHeads * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, int sm_count,
+                              cudaStream_t stream)
+{
+    const int group = a.num_q_heads / a.num_kv_heads;
+    const int rows = a.num_kv_heads * ((group + kHeads - 1) / kHeads);
+    a.tickets = static_cast<int32_t *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                       ticket_bytes(a.num_seqs, rows));
+    switch (head_dim) {
+    case 64: return launch_decode_d<64>(a, sm_count, stream);
+    case 128: return launch_decode_d<128>(a, sm_count, stream);
+    case 256: return launch_decode_d<256>(a, sm_count, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace vfa

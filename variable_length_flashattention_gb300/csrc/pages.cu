@@ -1,0 +1,601 @@
+// pages.cu -- the pages of paged K/V pools: extend, fork, free, compact, copy.
+//
+// State: refs[num_blocks] (users of a page, 0 = free), tables[num_seqs,
+// capacity] (physical page of each logical page), counts[num_seqs] (tokens).
+// A sequence of n tokens holds its first ceil(n / block_size) table entries.
+// New pages are the free ones with the lowest ids, so every result is a
+// function of the inputs alone, whatever order the threads run in.
+//
+// Extend, fork and compact need ranks among the free (or used) pages:
+//   count    one CTA per chunk of 4096 pages counts its used pages;
+//   plan     one CTA checks the request and gives every new page its rank
+//            (extend, fork); it is the only step that can refuse, before
+//            anything but the workspace is written;
+//   assign   one CTA per chunk: the chunk's first free rank is a sum over the
+//            earlier chunks' counts, so the free pages of rank < N go to
+//            their tables without a pass over the pool in one CTA;
+//   copy     page data, 4 KB per warp and turn, every pool in one launch.
+// Consecutive steps are launched with programmatic serialisation.
+//
+// Bound: HBM for the copied pages (2 bytes moved per byte), launch latency
+// for the rest.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace vfa {
+
+namespace {
+
+constexpr int kChunk = 4096;
+constexpr int kPlanThreads = 1024;
+constexpr int kPer = kChunk / kPlanThreads;
+constexpr int kPiece = 4096;            // bytes a warp copies per turn
+
+enum { H_N = 0, H_USED = 1 };
+
+struct PageWs {
+    int32_t *head;      // [64]: [H_N] pages to assign / move, [H_USED] used pages
+    int32_t *chunk;     // [chunks] used pages per chunk
+    int32_t *src, *dst; // [num_blocks] page copies
+    int32_t *rank;      // [num_blocks] compact: index of the page's move, -1 none
+    int32_t *offs;      // [max(num_seqs, forks) + 1] first rank per sequence; fork: entry per rank
+    int32_t *plan;      // [forks][4] parent, child, tokens, 0
+    int32_t *mark;      // [num_seqs] fork: entry that claimed the child
+};
+
+__host__ __device__ inline int chunks_of(int num_blocks) { return (num_blocks + kChunk - 1) / kChunk; }
+
+size_t carve(int32_t *ws, int num_blocks, int num_seqs, int forks, PageWs *w)
+{
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += (n + 63) & ~static_cast<size_t>(63);
+        return ws ? ws + o : nullptr;
+    };
+    PageWs r;
+    r.head = take(64);
+    r.chunk = take(chunks_of(num_blocks));
+    r.src = take(num_blocks);
+    r.dst = take(num_blocks);
+    r.rank = take(num_blocks);
+    r.offs = take(static_cast<size_t>(num_seqs > forks ? num_seqs : forks) + 1);
+    r.plan = take(static_cast<size_t>(forks) * 4);
+    r.mark = take(num_seqs);
+    if (w)
+        *w = r;
+    return at * sizeof(int32_t);
+}
+
+__device__ __forceinline__ void pdl_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void record(int32_t *status, int code)
+{
+    if (status)
+        atomicCAS(status, 0, code);
+}
+
+// Exclusive sum of v over the CTA's 1024 threads; *total gets the sum.
+__device__ __forceinline__ int block_scan(int v, int *total, int *s_warp)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off)
+            x += y;
+    }
+    __syncthreads();                    // s_warp's readers of the previous call are done
+    if (lane == 31)
+        s_warp[warp] = x;
+    __syncthreads();
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+        const int w = s_warp[i];
+        before += i < warp ? w : 0;
+        sum += w;
+    }
+    *total = sum;
+    return before + x - v;
+}
+
+// Sum over chunks [0, n) of the used counts.
+__device__ __forceinline__ int used_before(const int32_t *chunk, int n, int *s_warp)
+{
+    int v = 0, total;
+    for (int i = threadIdx.x; i < n; i += kPlanThreads)
+        v += chunk[i];
+    block_scan(v, &total, s_warp);
+    return total;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) count_kernel(const int32_t *refs, int num_blocks,
+                                                             int32_t *chunk)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ int s_warp[kPlanThreads / 32];
+    int v = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const long long id = static_cast<long long>(blockIdx.x) * kChunk + k * kPlanThreads + threadIdx.x;
+        v += id < num_blocks && refs[id] > 0;
+    }
+    block_scan(v, &total, s_warp);
+    if (threadIdx.x == 0)
+        chunk[blockIdx.x] = total;
+}
+
+// ------------------------------------------------------------ extend, fork
+
+__global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PageArgs a, const PageWs w)
+{
+    pdl_start();
+    __shared__ int s_warp[kPlanThreads / 32];
+    const long long room = static_cast<long long>(a.capacity) * a.block_size;
+    const int used = used_before(w.chunk, chunks_of(a.num_blocks), s_warp);
+    long long carry = 0;
+    bool bad = false;
+    for (int s0 = 0; s0 < a.num_seqs; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        int need = 0;
+        if (s < a.num_seqs) {
+            const long long n = a.counts[s], add = a.add[s];
+            if (n < 0 || add < 0 || n + add > room)
+                bad = true;
+            else
+                need = static_cast<int>((n + add + a.block_size - 1) / a.block_size -
+                                        (n + a.block_size - 1) / a.block_size);
+        }
+        // a row needs at most `capacity` pages; past num_blocks the request fails anyway
+        need = min(need, a.num_blocks + 1);
+        // 1024 rows' needs can pass 32 bits: sum in two parts
+        int lo, hi, tl, th;
+        lo = block_scan(need & 0xffff, &tl, s_warp);
+        hi = block_scan(need >> 16, &th, s_warp);
+        const long long at = carry + lo + (static_cast<long long>(hi) << 16);
+        if (s < a.num_seqs)
+            w.offs[s] = at > a.num_blocks ? a.num_blocks : static_cast<int>(at);
+        carry += tl + (static_cast<long long>(th) << 16);
+    }
+    bad = __syncthreads_or(bad);
+    const bool room_ok = carry <= a.num_blocks - used;
+    const bool ok = !bad && room_ok;
+    if (threadIdx.x == 0) {
+        w.head[H_N] = ok ? static_cast<int>(carry) : 0;
+        w.offs[a.num_seqs] = ok ? static_cast<int>(carry) : 0;
+        if (!ok)
+            record(a.status, bad ? VFA_ERR_BAD_BLOCK : VFA_ERR_NO_PAGES);
+    }
+    if (ok)
+        for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads)
+            a.counts[s] += a.add[s];
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs a, const PageWs w)
+{
+    pdl_start();
+    __shared__ int s_warp[kPlanThreads / 32];
+    const long long room = static_cast<long long>(a.capacity) * a.block_size;
+    const int used = used_before(w.chunk, chunks_of(a.num_blocks), s_warp);
+    bool bad = false;
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        const int c = a.children[i];
+        if (a.parents[i] >= 0 && c >= 0 && c < a.num_seqs)
+            w.mark[c] = -1;
+    }
+    __syncthreads();
+    int carry = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
+        const int i = i0 + threadIdx.x;
+        int take = 0, total, tail = 0, p = -1, c = 0, n = 0;
+        if (i < a.n) {
+            p = a.parents[i];
+            c = a.children[i];
+            if (p >= 0) {
+                if (p >= a.num_seqs || c < 0 || c >= a.num_seqs || a.counts[c] != 0 ||
+                    atomicExch(&w.mark[c], i) != -1) {
+                    bad = true;
+                } else {
+                    n = a.counts[p];
+                    if (n < 0 || n > room) {
+                        bad = true;
+                    } else if (n % a.block_size) {
+                        tail = a.tables[static_cast<long long>(p) * a.capacity + n / a.block_size];
+                        if (tail < 0 || tail >= a.num_blocks || a.refs[tail] <= 0)
+                            bad = true;
+                        else
+                            take = 1;
+                    }
+                }
+            }
+            w.plan[4 * i] = bad ? -1 : p;
+            w.plan[4 * i + 1] = c;
+            w.plan[4 * i + 2] = n;
+        }
+        const int r = carry + block_scan(take, &total, s_warp);
+        if (take && r < a.num_blocks) {
+            w.offs[r] = i;
+            w.src[r] = tail;
+        }
+        carry += total;
+    }
+    bad = __syncthreads_or(bad);
+    const bool ok = !bad && carry <= a.num_blocks - used;
+    if (threadIdx.x == 0) {
+        w.head[H_N] = ok ? carry : 0;
+        if (!ok)
+            record(a.status, bad ? VFA_ERR_BAD_BLOCK : VFA_ERR_NO_PAGES);
+    }
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        if (!ok)
+            w.plan[4 * i] = -1;
+        else if (w.plan[4 * i] >= 0)
+            a.counts[w.plan[4 * i + 1]] = w.plan[4 * i + 2];
+    }
+}
+
+// CTAs [0, chunks): the chunk's free pages of rank < N go to their rows.
+// FORK: CTA chunks + i shares the full pages of entry i's parent.
+template <bool FORK>
+__global__ void __launch_bounds__(kPlanThreads) assign_kernel(const PageArgs a, const PageWs w)
+{
+    pdl_start();
+    __shared__ int s_warp[kPlanThreads / 32];
+    const int chunks = chunks_of(a.num_blocks);
+    if (FORK && static_cast<int>(blockIdx.x) >= chunks) {
+        const int i = blockIdx.x - chunks;
+        const int p = w.plan[4 * i];
+        if (p < 0)
+            return;
+        const int full = w.plan[4 * i + 2] / a.block_size;
+        const int32_t *from = a.tables + static_cast<long long>(p) * a.capacity;
+        int32_t *to = a.tables + static_cast<long long>(w.plan[4 * i + 1]) * a.capacity;
+        for (int j = threadIdx.x; j < full; j += kPlanThreads) {
+            const int id = from[j];
+            to[j] = id;
+            if (id < 0 || id >= a.num_blocks || a.refs[id] <= 0)
+                record(a.status, VFA_ERR_BAD_BLOCK);        // not a page in use: not counted
+            else
+                atomicAdd(&a.refs[id], 1);
+        }
+        return;
+    }
+    const int n = w.head[H_N];
+    if (n == 0)
+        return;
+    const int base = blockIdx.x * kChunk;
+    const int first = base - used_before(w.chunk, blockIdx.x, s_warp);   // free pages below
+    if (first >= n)
+        return;
+    const int id0 = base + threadIdx.x * kPer;
+    bool is_free[kPer];
+    int mine = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        is_free[k] = id0 + k < a.num_blocks && a.refs[id0 + k] <= 0;
+        mine += is_free[k];
+    }
+    int r = first + block_scan(mine, &total, s_warp);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        if (!is_free[k])
+            continue;
+        if (r < n) {
+            const int id = id0 + k;
+            a.refs[id] = 1;
+            if (FORK) {
+                const int i = w.offs[r];
+                w.dst[r] = id;
+                a.tables[static_cast<long long>(w.plan[4 * i + 1]) * a.capacity +
+                         w.plan[4 * i + 2] / a.block_size] = id;
+            } else {
+                int lo = 0, hi = a.num_seqs;         // the row s with offs[s] <= r < offs[s + 1]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (w.offs[mid] <= r)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                const int pages = static_cast<int>(
+                    (static_cast<long long>(a.counts[lo]) + a.block_size - 1) / a.block_size);
+                a.tables[static_cast<long long>(lo) * a.capacity + pages - w.offs[lo + 1] + r] = id;
+            }
+        }
+        ++r;
+    }
+}
+
+// ------------------------------------------------------------ free
+
+__global__ void __launch_bounds__(256) free_kernel(const PageArgs a)
+{
+    __shared__ int s_n;
+    const int s = a.seqs[blockIdx.x];
+    if (s < 0)
+        return;                                     // a padding entry
+    if (s >= a.num_seqs) {
+        if (threadIdx.x == 0)
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        // the exchange makes a sequence listed twice release its pages once
+        int n = atomicExch(&a.counts[s], 0);
+        if (n < 0 || n > static_cast<long long>(a.capacity) * a.block_size) {
+            record(a.status, VFA_ERR_BAD_BLOCK);
+            a.counts[s] = n;
+            n = 0;
+        }
+        s_n = n;
+    }
+    __syncthreads();
+    const int pages = static_cast<int>((static_cast<long long>(s_n) + a.block_size - 1) / a.block_size);
+    for (int j = threadIdx.x; j < pages; j += blockDim.x) {
+        const int id = a.tables[static_cast<long long>(s) * a.capacity + j];
+        if (id < 0 || id >= a.num_blocks) {
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        } else if (atomicSub(&a.refs[id], 1) <= 0) {
+            atomicAdd(&a.refs[id], 1);
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        }
+    }
+}
+
+// ------------------------------------------------------------ compact
+//
+// With U used pages, the used pages at or above U move, in ascending order,
+// to the free pages below U: as many, and no page is both source and target.
+
+__global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const PageArgs a, const PageWs w)
+{
+    pdl_start();
+    __shared__ int s_warp[kPlanThreads / 32];
+    const int chunks = chunks_of(a.num_blocks);
+    const int U = used_before(w.chunk, chunks, s_warp);
+    // used pages below U: whole chunks, then the chunk that holds U
+    const int cu = U / kChunk;
+    int below = used_before(w.chunk, min(cu, chunks), s_warp);
+    {
+        int v = 0, total;
+        for (int id = cu * kChunk + threadIdx.x; id < U; id += kPlanThreads)
+            v += a.refs[id] > 0;
+        block_scan(v, &total, s_warp);
+        below += total;
+    }
+    const int id0 = blockIdx.x * kChunk + threadIdx.x * kPer;
+    bool is_used[kPer];
+    int mine = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        is_used[k] = id0 + k < a.num_blocks && a.refs[id0 + k] > 0;
+        mine += is_used[k];
+    }
+    int before = used_before(w.chunk, blockIdx.x, s_warp);
+    before += block_scan(mine, &total, s_warp);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int id = id0 + k;
+        if (id < a.num_blocks) {
+            int r = -1;
+            if (is_used[k] && id >= U) {
+                r = before - below;
+                w.src[r] = id;
+            } else if (!is_used[k] && id < U) {
+                r = id - before;
+                w.dst[r] = id;
+            }
+            w.rank[id] = r;
+        }
+        before += is_used[k];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        w.head[H_N] = U - below;
+        w.head[H_USED] = U;
+        *a.num_used = U;
+    }
+}
+
+// Tables and reference counts after the moves (part, parts: this CTA's share).
+__device__ __forceinline__ void compact_apply(const PageArgs &a, const PageWs &w, int part,
+                                              int parts)
+{
+    const int U = w.head[H_USED];
+    const long long stride = static_cast<long long>(parts) * blockDim.x;
+    const long long t0 = static_cast<long long>(part) * blockDim.x + threadIdx.x;
+    for (long long id = t0; id < a.num_blocks; id += stride) {
+        const int r = w.rank[id];
+        if (id < U && r >= 0) {                     // takes over a moved page's users
+            const int from = w.src[r];
+            a.refs_out[id] = a.refs[from];
+            a.refs_out[from] = 0;
+        } else if (r < 0) {
+            a.refs_out[id] = a.refs[id];
+        }
+    }
+    const long long entries = static_cast<long long>(a.num_seqs) * a.capacity;
+    for (long long e = t0; e < entries; e += stride) {
+        const int s = static_cast<int>(e / a.capacity);
+        const long long n = a.counts[s];
+        if (n < 0 || n > static_cast<long long>(a.capacity) * a.block_size) {
+            record(a.status, VFA_ERR_BAD_BLOCK);
+            continue;
+        }
+        if (e % a.capacity >= (n + a.block_size - 1) / a.block_size)
+            continue;
+        int id = a.tables[e];
+        if (id < 0 || id >= a.num_blocks) {
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        } else {
+            const int r = w.rank[id];
+            if ((id < U) == (r >= 0))               // listed, but nobody counts as its user
+                record(a.status, VFA_ERR_BAD_BLOCK);
+            else if (r >= 0)
+                id = w.dst[r];
+        }
+        a.tables_out[e] = id;
+    }
+}
+
+// ------------------------------------------------------------ copy
+//
+// blockIdx.y < pools: warps copy pieces of that pool's pages; COMPACT:
+// blockIdx.y == pools rewrites tables and counts meanwhile.
+template <bool COMPACT>
+__global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ PagePools p,
+                                                   const int32_t *src, const int32_t *dst,
+                                                   const int32_t *n_dev, int n_host, int num_blocks,
+                                                   int32_t *status, const PageArgs a,
+                                                   const PageWs w)
+{
+    pdl_start();
+    if (COMPACT && static_cast<int>(blockIdx.y) == p.n) {
+        compact_apply(a, w, blockIdx.x, gridDim.x);
+        return;
+    }
+    const int n = n_dev ? *n_dev : n_host;
+    const int bytes = p.page_bytes[blockIdx.y];
+    uint8_t *base = p.ptr[blockIdx.y];
+    const int pieces = (bytes + kPiece - 1) / kPiece;
+    const int lane = threadIdx.x & 31;
+    const long long items = static_cast<long long>(n) * pieces;
+    const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
+    for (long long it = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+         it < items; it += nwarps) {
+        const int pair = static_cast<int>(it / pieces), piece = static_cast<int>(it % pieces);
+        const int from = src[pair], to = dst[pair];
+        if (!n_dev && from < 0)
+            continue;                               // a padding entry of the caller's list
+        if (from < 0 || from >= num_blocks || to < 0 || to >= num_blocks) {
+            if (lane == 0)
+                record(status, VFA_ERR_BAD_BLOCK);
+            continue;
+        }
+        const uint8_t *s = base + static_cast<long long>(from) * bytes;
+        uint8_t *d = base + static_cast<long long>(to) * bytes;
+        uint4 v[kPiece / 512];
+#pragma unroll
+        for (int k = 0; k < kPiece / 512; ++k) {
+            const int o = piece * kPiece + k * 512 + lane * 16;
+            if (o < bytes)
+                v[k] = __ldcs(reinterpret_cast<const uint4 *>(s + o));
+        }
+#pragma unroll
+        for (int k = 0; k < kPiece / 512; ++k) {
+            const int o = piece * kPiece + k * 512 + lane * 16;
+            if (o < bytes)
+                __stcs(reinterpret_cast<uint4 *>(d + o), v[k]);
+        }
+    }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, int threads, cudaStream_t stream,
+                         bool dependent, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// CTAs per pool: about eight CTAs of eight warps on every SM in all, and no
+// more warps than `max_pairs` pages have pieces.
+int copy_ctas(const PagePools &p, long long max_pairs, int sm_count)
+{
+    int pieces = 1;
+    for (int i = 0; i < p.n; ++i)
+        pieces = pieces > (p.page_bytes[i] + kPiece - 1) / kPiece
+                     ? pieces
+                     : (p.page_bytes[i] + kPiece - 1) / kPiece;
+    long long g = (8LL * sm_count + p.n - 1) / (p.n > 0 ? p.n : 1);
+    const long long need = (max_pairs * pieces + 7) / 8;
+    g = g < need ? g : need;
+    return static_cast<int>(g < 1 ? 1 : g);
+}
+
+}  // namespace
+
+size_t page_workspace_bytes(int num_blocks, int num_seqs, int num_forks)
+{
+    return carve(nullptr, num_blocks, num_seqs, num_forks, nullptr);
+}
+
+cudaError_t launch_pages_extend(const PageArgs &a, cudaStream_t stream)
+{
+    PageWs w;
+    carve(a.ws, a.num_blocks, a.num_seqs, 0, &w);
+    const int chunks = chunks_of(a.num_blocks);
+    cudaError_t e;
+    if ((e = launch_after(count_kernel, chunks, kPlanThreads, stream, false, a.refs, a.num_blocks,
+                          w.chunk)) ||
+        (e = launch_after(extend_plan_kernel, 1, kPlanThreads, stream, true, a, w)) ||
+        (e = launch_after(assign_kernel<false>, chunks, kPlanThreads, stream, true, a, w)))
+        return e;
+    return cudaSuccess;
+}
+
+cudaError_t launch_pages_fork(const PageArgs &a, const PagePools &p, int sm_count,
+                              cudaStream_t stream)
+{
+    PageWs w;
+    carve(a.ws, a.num_blocks, a.num_seqs, a.n, &w);
+    const int chunks = chunks_of(a.num_blocks);
+    cudaError_t e;
+    if ((e = launch_after(count_kernel, chunks, kPlanThreads, stream, false, a.refs, a.num_blocks,
+                          w.chunk)) ||
+        (e = launch_after(fork_plan_kernel, 1, kPlanThreads, stream, true, a, w)) ||
+        (e = launch_after(assign_kernel<true>, chunks + a.n, kPlanThreads, stream, true, a, w)))
+        return e;
+    if (p.n == 0)
+        return cudaSuccess;
+    return launch_after(copy_kernel<false>, dim3(copy_ctas(p, a.n, sm_count), p.n), 256, stream,
+                        true, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a, w);
+}
+
+cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t stream)
+{
+    free_kernel<<<a.n, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_count,
+                                 cudaStream_t stream)
+{
+    PageWs w;
+    carve(a.ws, a.num_blocks, a.num_seqs, 0, &w);
+    const int chunks = chunks_of(a.num_blocks);
+    cudaError_t e;
+    if ((e = launch_after(count_kernel, chunks, kPlanThreads, stream, false, a.refs, a.num_blocks,
+                          w.chunk)) ||
+        (e = launch_after(compact_rank_kernel, chunks, kPlanThreads, stream, true, a, w)))
+        return e;
+    return launch_after(copy_kernel<true>, dim3(copy_ctas(p, a.num_blocks / 2 + 1, sm_count), p.n + 1), 256,
+                        stream, true, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a,
+                        w);
+}
+
+cudaError_t launch_pages_copy(const PagePools &p, const int32_t *src, const int32_t *dst, int n,
+                              int num_blocks, int32_t *status, int sm_count, cudaStream_t stream)
+{
+    PageArgs a = {};
+    PageWs w = {};
+    return launch_after(copy_kernel<false>, dim3(copy_ctas(p, n, sm_count), p.n), 256, stream,
+                        false, p, src, dst, static_cast<const int32_t *>(nullptr), n, num_blocks,
+                        status, a, w);
+}
+
+}  // namespace vfa

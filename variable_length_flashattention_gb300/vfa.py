@@ -9,9 +9,12 @@ first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
+from fractions import Fraction
 from typing import Optional, Tuple
 
 import torch
@@ -30,12 +33,15 @@ STATUS_NAMES = {
     6: "VFA_ERR_BAD_BLOCK",
     7: "VFA_ERR_TIMEOUT",
     8: "VFA_ERR_WORKSPACE",
+    9: "VFA_ERR_NO_PAGES",
 }
 VFA_OK, VFA_ERR_INVALID_ARG, VFA_ERR_UNSUPPORTED, VFA_ERR_ARCH, VFA_ERR_CUDA = 0, 1, 2, 3, 4
 VFA_ERR_BAD_SEQLENS, VFA_ERR_BAD_BLOCK, VFA_ERR_TIMEOUT, VFA_ERR_WORKSPACE = 5, 6, 7, 8
+VFA_ERR_NO_PAGES = 9
 
 # Every symbol include/vfa.h declares: (name, restype, argtypes).
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_int64
 SIGNATURES = [
     ("vfa_last_error", ctypes.c_char_p, []),
     ("vfa_version", ctypes.c_char_p, []),
@@ -62,6 +68,26 @@ SIGNATURES = [
     ("vfa_paged_decode_finalize", _I, [_P, _P, _I, _I, _I, _P, _P]),
     ("vfa_debug_paged_gather", _I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
     ("vfa_debug_bounded_wait", _I, [_P, _P]),
+    ("vfa_qk_norm_rope_fwd", _I, [_P, _P, _L, _L, _P, _I, _P, _I, _I, _P, _P, _F, _I, _I, _I, _I,
+                                  _P, _P, _L, _L, _P]),
+    ("vfa_qk_norm_rope_bwd_workspace_bytes", _S, [_I]),
+    ("vfa_qk_norm_rope_bwd", _I, [_P, _P, _L, _L, _P, _P, _L, _L, _P, _I, _P, _I, _I, _P, _P, _F,
+                                  _I, _I, _I, _I, _P, _P, _L, _L, _P, _P, _P, _S, _P]),
+    ("vfa_kv4_block_bytes", _S, [_I, _I]),
+    ("vfa_kv4_write", _I, [_P, _P, _L, _L, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _F, _F, _P,
+                           _P]),
+    ("vfa_kv4_gather", _I, [_P, _P, _L, _L, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _F, _F, _P,
+                            _P]),
+    ("vfa_kv4_decode_workspace_bytes", _S, [_I, _I, _I, _I]),
+    ("vfa_kv4_decode", _I, [_P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _F, _F, _F, _P, _P, _P, _P,
+                            _S, _P]),
+    ("vfa_pages_workspace_bytes", _S, [_I, _I, _I]),
+    ("vfa_pages_extend", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _S, _P, _P]),
+    ("vfa_pages_fork", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _P, _I, _I, _P, _S, _P, _P]),
+    ("vfa_pages_free", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P]),
+    ("vfa_pages_compact", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _S, _P,
+                               _P]),
+    ("vfa_pages_copy", _I, [_P, _P, _I, _P, _P, _I, _I, _P, _P]),
     ("vfa_read_status", _I, [_P, _P, _P]),
 ]
 
@@ -410,6 +436,450 @@ def decode_finalize(l: torch.Tensor, o: torch.Tensor, out: Optional[torch.Tensor
     _check(lib().vfa_paged_decode_finalize(_ptr(l), _ptr(o), S, Hq, D, _ptr(out),
                                            _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------- norm and rotation
+
+# 1 / (2 pi) to 60 digits: the table's steps are rounded once, from this.
+_INV_2PI = Fraction("0.159154943091895335768883763372514362034459645740456448747667")
+
+
+def _on_stream(stream):
+    """Allocations of a call belong to the stream its kernels run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _here(*tensors):
+    """Every tensor lives on the current device (where the kernels are launched)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _need_rows(t: torch.Tensor, name: str):
+    """bf16 [tokens, heads, head_dim], heads and dims contiguous, any token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must have contiguous heads and dims")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between tokens (one or no token has no neighbour: the packed distance)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_table(inv_freq, axes=None, device="cuda") -> torch.Tensor:
+    """The table of vfa_qk_norm_rope_fwd: int64 [len(inv_freq), 2].
+
+    inv_freq: radians per position of each rotated pair (rotary_dim / 2 finite
+    numbers); axes: the position axis each pair follows (default: all 0)."""
+    inv_freq = [float(f) for f in inv_freq]
+    axes = [0] * len(inv_freq) if axes is None else [int(a) for a in axes]
+    if len(axes) != len(inv_freq):
+        raise ValueError("axes must give one axis per frequency")
+    if any(a < 0 for a in axes):
+        raise ValueError("axes must be >= 0")
+    rows = []
+    for f, a in zip(inv_freq, axes):
+        if not math.isfinite(f):
+            raise ValueError("inv_freq must be finite")
+        step = round(Fraction(f) * _INV_2PI * 2 ** 64) % 2 ** 64
+        rows.append((step - 2 ** 64 if step >= 2 ** 63 else step, a))
+    return torch.tensor(rows, dtype=torch.int64, device=device).reshape(len(rows), 2)
+
+
+def _rope_inputs(q, k, positions, table, q_weight, k_weight):
+    for t, n in ((q, "q"), (k, "k")):
+        _need_rows(t, n)
+    if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q [T, Hq, D] and k [T, Hkv, D] must agree in tokens and head_dim")
+    axes = rot = 0
+    if table is not None:
+        _need(table, torch.int64, "table")
+        if table.dim() != 2 or table.shape[1] != 2:
+            raise ValueError("table must be [rotary_dim / 2, 2], as rope_table makes it")
+        rot = 2 * table.shape[0]
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _need(positions, torch.int32, "positions")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.dim() > 2 or positions.shape[-1] != q.shape[0]:
+            raise ValueError("positions must be [tokens] or [axes, tokens]")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, torch.float32, n)
+            if w.shape != (q.shape[2],):
+                raise ValueError(f"{n} must be [head_dim]")
+    _here(q, k, positions if rot else None, table, q_weight, k_weight)
+    return axes, rot
+
+
+def _outputs(like, given, name, stream):
+    if given is None:
+        with _on_stream(stream):
+            return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _need_rows(given, name)
+    if given.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    _here(given)
+    return given
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
+                 table: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+    """(q_out, k_out) bf16 = per-head RMS norm and position rotation (vfa_qk_norm_rope_fwd).
+
+    q [T, Hq, D], k [T, Hkv, D] bf16, views with a token stride included;
+    positions int32 [T] or [axes, T]; table from rope_table (None: no rotation);
+    weights f32 [D] (None: no norm); q_out / k_out may be q / k."""
+    axes, rot = _rope_inputs(q, k, positions, table, q_weight, k_weight)
+    q_out = _outputs(q, q_out, "q_out", stream)
+    k_out = _outputs(k, k_out, "k_out", stream)
+    _check(lib().vfa_qk_norm_rope_fwd(
+        _ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(positions), axes, _ptr(table), rot,
+        int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), float(eps), q.shape[0], q.shape[1],
+        k.shape[1], q.shape[2], _ptr(q_out), _ptr(k_out), _row_stride(q_out), _row_stride(k_out),
+        _stream(stream)))
+    return q_out, k_out
+
+
+def alloc_qk_norm_rope_bwd_workspace(head_dim: int, device="cuda") -> torch.Tensor:
+    n = lib().vfa_qk_norm_rope_bwd_workspace_bytes(head_dim)
+    if n == 0:
+        raise VfaError(VFA_ERR_UNSUPPORTED, f"no workspace size for head_dim {head_dim}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                     positions: Optional[torch.Tensor], table: Optional[torch.Tensor],
+                     q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     interleaved: bool = False, dq: Optional[torch.Tensor] = None,
+                     dk: Optional[torch.Tensor] = None, dq_weight: Optional[torch.Tensor] = None,
+                     dk_weight: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) = gradients of qk_norm_rope (vfa_qk_norm_rope_bwd).
+
+    dq_out, dk_out: upstream gradients; dq / dk may be dq_out / dk_out.  The
+    weight gradients are f32 [D], None where there is no weight."""
+    axes, rot = _rope_inputs(q, k, positions, table, q_weight, k_weight)
+    for t, x, n in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
+        _need_rows(t, n)
+        if t.shape != x.shape:
+            raise ValueError(f"{n} must have shape {tuple(x.shape)}")
+    _here(dq_out, dk_out, workspace)
+    dq = _outputs(q, dq, "dq", stream)
+    dk = _outputs(k, dk, "dk", stream)
+    grads = []
+    for w, g, n in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None:
+            grads.append(None)
+            continue
+        if g is None:
+            with _on_stream(stream):
+                g = torch.empty_like(w)
+        _need(g, torch.float32, n)
+        if g.shape != w.shape:
+            raise ValueError(f"{n} must be [head_dim]")
+        _here(g)
+        grads.append(g)
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        with _on_stream(stream):
+            workspace = alloc_qk_norm_rope_bwd_workspace(q.shape[2], device=q.device)
+    _check(lib().vfa_qk_norm_rope_bwd(
+        _ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(dq_out), _ptr(dk_out),
+        _row_stride(dq_out), _row_stride(dk_out), _ptr(positions), axes, _ptr(table), rot,
+        int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), float(eps), q.shape[0], q.shape[1],
+        k.shape[1], q.shape[2], _ptr(dq), _ptr(dk), _row_stride(dq), _row_stride(dk),
+        _ptr(grads[0]), _ptr(grads[1]), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    return dq, dk, grads[0], grads[1]
+
+
+# ----------------------------------------------------------------- 4-bit cache
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def kv4_block_bytes(num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of 16 tokens (vfa_kv4_block_bytes)."""
+    n = lib().vfa_kv4_block_bytes(num_kv_heads, head_dim)
+    if n == 0:
+        raise VfaError(VFA_ERR_UNSUPPORTED, "no 4-bit page size for these arguments")
+    return int(n)
+
+
+def alloc_kv4_pool(num_blocks: int, num_kv_heads: int, head_dim: int,
+                   device="cuda") -> torch.Tensor:
+    """A zero-filled 4-bit pool, uint8 [num_blocks, num_kv_heads, 18 * head_dim]."""
+    kv4_block_bytes(num_kv_heads, head_dim)
+    return torch.zeros(num_blocks, num_kv_heads, 18 * head_dim, dtype=torch.uint8, device=device)
+
+
+def _need_kv4(pool, tables, status):
+    _need(pool, torch.uint8, "pool")
+    _need(tables, torch.int32, "tables")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    if pool.dim() != 3 or tables.dim() != 2:
+        raise ValueError("pool must be [num_blocks, num_kv_heads, 18 * head_dim], tables "
+                         "[num_seqs, capacity]")
+    if pool.shape[2] % 18:
+        raise ValueError("pool pages must hold 18 * head_dim bytes per kv head")
+    _here(pool, tables, status)
+    return pool.shape[2] // 18
+
+
+def _need_seqs(cu_seqlens, start_positions, tables):
+    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    _need(start_positions, torch.int32, "start_positions")
+    _here(cu_seqlens, start_positions)
+    if cu_seqlens.numel() != tables.shape[0] + 1 or start_positions.numel() != tables.shape[0]:
+        raise ValueError("cu_seqlens [num_seqs + 1] and start_positions [num_seqs] must match "
+                         "tables")
+
+
+def kv4_write(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
+              cu_seqlens: torch.Tensor, start_positions: torch.Tensor, descale_k: float = 1.0,
+              descale_v: float = 1.0, status: Optional[torch.Tensor] = None, stream=None):
+    """Quantises packed k, v bf16 [T, Hkv, D] into a 4-bit pool (vfa_kv4_write).
+
+    Token i of sequence s (row cu_seqlens[s] + i) becomes position
+    start_positions[s] + i of its table row; rows past cu_seqlens[-1] are padding."""
+    D = _need_kv4(pool, tables, status)
+    for t, n in ((k, "k"), (v, "v")):
+        _need_rows(t, n)
+        if t.shape != (k.shape[0], pool.shape[1], D):
+            raise ValueError(f"{n} must be [tokens, {pool.shape[1]}, {D}]")
+    _need_seqs(cu_seqlens, start_positions, tables)
+    _here(k, v)
+    _check(lib().vfa_kv4_write(_ptr(k), _ptr(v), _row_stride(k), _row_stride(v), k.shape[0],
+                               _ptr(pool), pool.shape[0], _ptr(tables), tables.shape[1],
+                               _ptr(cu_seqlens), _ptr(start_positions), tables.shape[0],
+                               pool.shape[1], D, float(descale_k), float(descale_v), _ptr(status),
+                               _stream(stream)))
+
+
+def kv4_gather(pool: torch.Tensor, tables: torch.Tensor, cu_seqlens: torch.Tensor,
+               start_positions: torch.Tensor, total_tokens: int, descale_k: float = 1.0,
+               descale_v: float = 1.0, k_out: Optional[torch.Tensor] = None,
+               v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+               stream=None):
+    """(k, v) bf16 [total_tokens, Hkv, D] read back from a 4-bit pool, exactly (vfa_kv4_gather).
+
+    Rows without a place in the cache are left as they were (unset if allocated here)."""
+    D = _need_kv4(pool, tables, status)
+    _need_seqs(cu_seqlens, start_positions, tables)
+    outs = []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            with _on_stream(stream):
+                t = torch.empty(total_tokens, pool.shape[1], D, dtype=torch.bfloat16,
+                                device=pool.device)
+        _need_rows(t, n)
+        if t.shape != (total_tokens, pool.shape[1], D):
+            raise ValueError(f"{n} must be [{total_tokens}, {pool.shape[1]}, {D}]")
+        _here(t)
+        outs.append(t)
+    k, v = outs
+    _check(lib().vfa_kv4_gather(_ptr(k), _ptr(v), _row_stride(k), _row_stride(v), k.shape[0],
+                                _ptr(pool), pool.shape[0], _ptr(tables), tables.shape[1],
+                                _ptr(cu_seqlens), _ptr(start_positions), tables.shape[0],
+                                pool.shape[1], D, float(descale_k), float(descale_v),
+                                _ptr(status), _stream(stream)))
+    return k, v
+
+
+def alloc_kv4_decode_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                               device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for kv4_decode (its tickets start at zero)."""
+    n = lib().vfa_kv4_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise VfaError(VFA_ERR_UNSUPPORTED, "no 4-bit decode workspace for these sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
+               token_counts: torch.Tensor, descale_k: float = 1.0, descale_v: float = 1.0,
+               softmax_scale: float = 0.0, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, stream=None):
+    """(out bf16 [S, Hq, D], lse f32 [S, Hq]): one query token per sequence over a 4-bit cache
+    (vfa_kv4_decode).  Keep a workspace from alloc_kv4_decode_workspace between calls;
+    without one, each call allocates and clears its own."""
+    D = _need_kv4(pool, tables, status)
+    _need(q, torch.bfloat16, "q")
+    _need(token_counts, torch.int32, "token_counts")
+    if q.dim() != 3 or q.shape[0] != tables.shape[0] or q.shape[2] != D:
+        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
+    if token_counts.numel() != q.shape[0]:
+        raise ValueError("token_counts must be [num_seqs]")
+    S, Hq, _ = q.shape
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = alloc_kv4_decode_workspace(S, Hq, pool.shape[1], D, device=q.device)
+    _need(out, torch.bfloat16, "out")
+    _need(lse, torch.float32, "lse")
+    _need(workspace, torch.uint8, "workspace")
+    if out.shape != q.shape or lse.shape != (S, Hq):
+        raise ValueError("out must have q's shape and lse [num_seqs, num_q_heads]")
+    _here(q, token_counts, out, lse, workspace)
+    _check(lib().vfa_kv4_decode(_ptr(q), _ptr(pool), pool.shape[0], _ptr(tables), tables.shape[1],
+                                _ptr(token_counts), S, Hq, pool.shape[1], D, float(descale_k),
+                                float(descale_v), float(softmax_scale), _ptr(out), _ptr(lse),
+                                _ptr(status), _ptr(workspace), workspace.numel(),
+                                _stream(stream)))
+    return out, lse
+
+
+# ----------------------------------------------------------------- pages
+
+def alloc_pages_workspace(num_blocks: int, num_seqs: int, num_forks: int = 0,
+                          device="cuda") -> torch.Tensor:
+    """Scratch of the page operations for at least these sizes."""
+    n = lib().vfa_pages_workspace_bytes(num_blocks, num_seqs, num_forks)
+    if n == 0:
+        raise VfaError(VFA_ERR_INVALID_ARG, "no page workspace for these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _need_pages(refcounts, tables, token_counts, status, workspace=None):
+    for t, n in ((refcounts, "refcounts"), (tables, "tables"), (token_counts, "token_counts")):
+        _need(t, torch.int32, n)
+    if status is not None:
+        _need(status, torch.int32, "status")
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    if refcounts.dim() != 1 or tables.dim() != 2 or token_counts.shape != (tables.shape[0],):
+        raise ValueError("refcounts [num_blocks], tables [num_seqs, capacity] and token_counts "
+                         "[num_seqs]")
+    _here(refcounts, tables, token_counts, status, workspace)
+
+
+def _pool_list(pools, num_blocks):
+    """Host arrays of the pools' addresses and page sizes."""
+    for i, p in enumerate(pools):
+        if not p.is_cuda or not p.is_contiguous():
+            raise ValueError(f"pools[{i}] must be a contiguous CUDA tensor")
+        if p.dim() < 2 or p.shape[0] != num_blocks:
+            raise ValueError(f"pools[{i}] must hold {num_blocks} pages")
+        _here(p)
+    n = len(pools)
+    ptrs = (ctypes.c_void_p * max(n, 1))(*[p.data_ptr() for p in pools])
+    sizes = (ctypes.c_int * max(n, 1))(*[p.stride(0) * p.element_size() for p in pools])
+    return ptrs, sizes, n
+
+
+def pages_extend(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
+                 add_tokens: torch.Tensor, block_size: int, workspace: torch.Tensor,
+                 status: Optional[torch.Tensor] = None, stream=None):
+    """token_counts += add_tokens, with new pages where rows need them (vfa_pages_extend)."""
+    _need_pages(refcounts, tables, token_counts, status, workspace)
+    _need(add_tokens, torch.int32, "add_tokens")
+    if add_tokens.shape != token_counts.shape:
+        raise ValueError("add_tokens must be [num_seqs]")
+    _here(add_tokens)
+    _check(lib().vfa_pages_extend(_ptr(refcounts), refcounts.numel(), _ptr(tables),
+                                  tables.shape[1], _ptr(token_counts), tables.shape[0],
+                                  _ptr(add_tokens), int(block_size), _ptr(workspace),
+                                  workspace.numel(), _ptr(status), _stream(stream)))
+
+
+def pages_fork(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
+               parents: torch.Tensor, children: torch.Tensor, pools, block_size: int,
+               workspace: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None):
+    """Rows children[i] become copies of rows parents[i]: full pages shared, a partly filled
+    last page copied in every pool (vfa_pages_fork)."""
+    _need_pages(refcounts, tables, token_counts, status, workspace)
+    _need(parents, torch.int32, "parents")
+    _need(children, torch.int32, "children")
+    if parents.dim() != 1 or parents.shape != children.shape:
+        raise ValueError("parents and children must be [num_forks]")
+    _here(parents, children)
+    ptrs, sizes, n = _pool_list(pools, refcounts.numel())
+    if parents.numel() == 0:
+        return
+    _check(lib().vfa_pages_fork(_ptr(refcounts), refcounts.numel(), _ptr(tables), tables.shape[1],
+                                _ptr(token_counts), tables.shape[0], _ptr(parents),
+                                _ptr(children), parents.numel(), ptrs, sizes, n, int(block_size),
+                                _ptr(workspace), workspace.numel(), _ptr(status),
+                                _stream(stream)))
+
+
+def pages_free(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
+               seqs: torch.Tensor, block_size: int, status: Optional[torch.Tensor] = None,
+               stream=None):
+    """Rows seqs[i] give up their pages (vfa_pages_free)."""
+    _need_pages(refcounts, tables, token_counts, status)
+    _need(seqs, torch.int32, "seqs")
+    _here(seqs)
+    if seqs.numel() == 0:
+        return
+    _check(lib().vfa_pages_free(_ptr(refcounts), refcounts.numel(), _ptr(tables), tables.shape[1],
+                                _ptr(token_counts), tables.shape[0], _ptr(seqs), seqs.numel(),
+                                int(block_size), _ptr(status), _stream(stream)))
+
+
+def pages_compact(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
+                  pools, block_size: int, workspace: torch.Tensor,
+                  refcounts_out: Optional[torch.Tensor] = None,
+                  tables_out: Optional[torch.Tensor] = None,
+                  num_used: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Moves the used pages to the low end of every pool (vfa_pages_compact); refcounts and
+    tables are rewritten in place unless outputs are given.  Returns int32 [1]: used pages."""
+    _need_pages(refcounts, tables, token_counts, status, workspace)
+    refcounts_out = refcounts if refcounts_out is None else refcounts_out
+    tables_out = tables if tables_out is None else tables_out
+    if num_used is None:
+        with _on_stream(stream):
+            num_used = torch.empty(1, dtype=torch.int32, device=refcounts.device)
+    for t, x, n in ((refcounts_out, refcounts, "refcounts_out"), (tables_out, tables, "tables_out")):
+        _need(t, torch.int32, n)
+        if t.shape != x.shape:
+            raise ValueError(f"{n} must have shape {tuple(x.shape)}")
+    _need(num_used, torch.int32, "num_used")
+    _here(refcounts_out, tables_out, num_used)
+    ptrs, sizes, n = _pool_list(pools, refcounts.numel())
+    _check(lib().vfa_pages_compact(_ptr(refcounts), refcounts.numel(), _ptr(tables),
+                                   tables.shape[1], _ptr(token_counts), tables.shape[0], ptrs,
+                                   sizes, n, int(block_size), _ptr(refcounts_out),
+                                   _ptr(tables_out), _ptr(num_used), _ptr(workspace),
+                                   workspace.numel(), _ptr(status), _stream(stream)))
+    return num_used
+
+
+def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
+               status: Optional[torch.Tensor] = None, stream=None):
+    """Page src[i] of every pool over page dst[i] (vfa_pages_copy)."""
+    if not pools:
+        return
+    _need(src, torch.int32, "src")
+    _need(dst, torch.int32, "dst")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be [n]")
+    _here(src, dst, status)
+    num_blocks = pools[0].shape[0]
+    ptrs, sizes, n = _pool_list(pools, num_blocks)
+    if src.numel() == 0:
+        return
+    _check(lib().vfa_pages_copy(ptrs, sizes, n, _ptr(src), _ptr(dst), src.numel(), num_blocks,
+                                _ptr(status), _stream(stream)))
 
 
 def debug_bounded_wait(status: torch.Tensor, stream=None):
