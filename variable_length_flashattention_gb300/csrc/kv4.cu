@@ -330,9 +330,10 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // that takes the last ticket.  No CTA waits for another.
 //
 // A producer warp streams the run's head pages (18 D bytes each, contiguous)
-// through a ring of shared-memory stages with bulk copies; unit i is consumed
-// by warp i % 4.  Per page and warp, two products on mma.sync m16n8k16 (f16
-// in, fp32 accumulate):
+// two by two through a ring of shared-memory stages with bulk copies; pair i
+// is consumed by warp i % 4 (two pages at a time give a warp two independent
+// chains of products and halve the exchanges of the maximum).  Per page, two
+// products on mma.sync m16n8k16 (f16 in, fp32 accumulate):
 //   S[16 tokens x 8 heads] = K Q^T    O^T[D x 8 heads] += V^T P
 // The page's order gives every lane its A operands in whole 16-byte words: a
 // lane of K's operand holds 32 consecutive dims of two tokens (two scales
@@ -354,8 +355,10 @@ constexpr float kPShift = 14.f;
 
 template <int D>
 struct DecCfg {
-    static constexpr int STAGE = 18 * D;
-    static constexpr int NS = 36864 / STAGE;        // 32, 16, 8 stages: a multiple of kConsumers
+    static constexpr int PAGE = 18 * D;                         // bytes of a head page
+    static constexpr int STAGE = 2 * PAGE;                      // a stage holds two pages
+    static constexpr int NS = D == 64 ? 16 : D == 128 ? 12 : 8; // stages: a multiple of kConsumers
+    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : 2; // resident per SM
     static constexpr int MT = D / 16;
     static constexpr int KW = D / 32;               // code words of one token per lane
 };
@@ -398,7 +401,7 @@ __device__ __forceinline__ int seq_units(const Kv4DecodeArgs &a, int s, int *tok
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4DecodeArgs a)
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kernel(const Kv4DecodeArgs a)
 {
     using C = DecCfg<D>;
     constexpr int NS = C::NS, MT = C::MT, KW = C::KW;
@@ -475,12 +478,12 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4Dec
     __syncthreads();
     volatile int *abort = &s_abort;
     const uint32_t ring = smem_u32(dsm);
-    const size_t page_bytes = static_cast<size_t>(a.num_kv_heads) * C::STAGE;
-    const uint8_t *pool = a.pool + static_cast<size_t>(kh) * C::STAGE;
+    const size_t page_bytes = static_cast<size_t>(a.num_kv_heads) * C::PAGE;
+    const uint8_t *pool = a.pool + static_cast<size_t>(kh) * C::PAGE;
 
     if (warp == kConsumers) {
         // ------------------------------------------------ producer
-        int s = s_first, at = s_first_unit, i = 0;
+        int s = s_first, at = s_first_unit, issued = 0, st = 0, phase = 1;
         bool ok = true;
         while (ok && at < u1) {
             int n;
@@ -493,38 +496,52 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4Dec
             for (int jb = j0; ok && jb < j1; jb += 32) {
                 const int id = jb + lane < j1 && n > 0 ? __ldg(row + jb + lane) : -1;
                 const int m = min(32, j1 - jb);
-                for (int k = 0; k < m; ++k, ++i) {
-                    const int blk = __shfl_sync(0xffffffffu, id, k);
-                    const int st = i % NS, f = i / NS;
+                for (int k = 0; k < m; k += 2) {
+                    const int blk[2] = {__shfl_sync(0xffffffffu, id, k),
+                                        __shfl_sync(0xffffffffu, id, k + 1)};
                     if (lane == 0) {
-                        if (f > 0)
-                            ok = mbar_wait(smem_u32(&s_empty[st]), (f - 1) & 1, abort);
-                        if (ok && blk >= 0 && blk < a.num_blocks) {
-                            s_stage_bad[st] = 0;
-                            mbar_arrive_expect_tx(smem_u32(&s_full[st]), C::STAGE);
-                            bulk_load(ring + st * C::STAGE, pool + blk * page_bytes, C::STAGE,
-                                      smem_u32(&s_full[st]));
-                        } else if (ok) {
-                            // an empty sequence's one unit, or a bad id
-                            s_stage_bad[st] = n > 0;
-                            if (n > 0)
+                        // (a fresh barrier counts as having completed the phase before its first)
+                        ok = mbar_wait(smem_u32(&s_empty[st]), phase, abort);
+                        if (ok) {
+                            int good = 0;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                good += blk[c] >= 0 && blk[c] < a.num_blocks;
+                            // an empty sequence's one unit has no page; every other listed one has
+                            const bool bad_id = n > 0 && good != min(2, m - k);
+                            s_stage_bad[st] = bad_id;
+                            if (bad_id)
                                 record(a.status, VFA_ERR_BAD_BLOCK);
-                            mbar_arrive(smem_u32(&s_full[st]));
+                            if (good)
+                                mbar_arrive_expect_tx(smem_u32(&s_full[st]), good * C::PAGE);
+                            else
+                                mbar_arrive(smem_u32(&s_full[st]));
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (blk[c] >= 0 && blk[c] < a.num_blocks)
+                                    bulk_load(ring + st * C::STAGE + c * C::PAGE,
+                                              pool + blk[c] * page_bytes, C::PAGE,
+                                              smem_u32(&s_full[st]));
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok)
                         break;
+                    ++issued;
+                    if (++st == NS) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             at += units;
             ++s;
         }
         // every copy issued has landed before the CTA can end, also after a
-        // consumer gave up: the last of the i units issued into each stage
+        // consumer gave up: the last fill issued into each stage
         if (lane == 0)
-            for (int st = 0; st < NS && st < i; ++st)
-                mbar_wait_drain(smem_u32(&s_full[st]), ((i - 1 - (i - 1 - st) % NS) / NS) & 1);
+            for (int q = 0; q < NS && q < issued; ++q)
+                mbar_wait_drain(smem_u32(&s_full[q]), ((issued - 1 - q) / NS) & 1);
         return;
     }
 
@@ -532,14 +549,16 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4Dec
     const int r = lane >> 2, t4 = lane & 3;
     float *s_o = reinterpret_cast<float *>(dsm + NS * C::STAGE);    // [kConsumers][G][D]
     int s = s_first, at = s_first_unit;
-    int i = warp;                                   // this warp's next unit, from the run's start
+    int i = warp;                                   // this warp's next pair of the run
+    int base_pair = 0;                              // pairs of the earlier segments
+    int st = warp, phase = 0;
     bool first_segment = true;
     while (at < u1) {
         int n;
         bool seq_bad;
         const int units = seq_units(a, s, &n, &seq_bad);
         const int j0 = max(0, u0 - at), j1 = min(units, u1 - at);
-        const int end = at + j1 - u0;               // run-local index of the segment's end
+        const int end = base_pair + (j1 - j0 + 1) / 2;
 
         // Q^T operand: head r, dims as K's lanes hold them.
         uint32_t qb[MT][2];
@@ -592,79 +611,97 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4Dec
         bool bad = seq_bad;
 
         for (; i < end; i += kConsumers) {
-            const int st = i % NS;
-            if (!mbar_wait_warp(smem_u32(&s_full[st]), (i / NS) & 1, abort)) {
+            if (!mbar_wait_warp(smem_u32(&s_full[st]), phase, abort)) {
                 bad = true;
                 continue;
             }
-            const uint32_t page = ring + st * C::STAGE;
-            const int valid = n - (u0 + i - at) * kPage;        // tokens of this page that count
+            const uint32_t pair = ring + st * C::STAGE;
+            // tokens of the two pages that count, those of the run's pages
+            const int j = j0 + 2 * (i - base_pair);
+            const int valid = min(n - j * kPage, j + 1 < j1 ? 2 * kPage : kPage);
             bad |= s_stage_bad[st] != 0;
             if (valid > 0 && !bad) {
-                // S = K Q^T
-                float sacc[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t kw[2][KW], ks[2];
+                // S = K Q^T: two pages, two independent accumulators
+                float sacc[2][4];
+                uint32_t kw[2][2][KW], ks[2][2];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int tok = r + 8 * half;
-                    const uint32_t row = page + tok * (D / 2);
-                    if constexpr (D == 64) {
-                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                     : "=r"(kw[half][0]), "=r"(kw[half][1])
-                                     : "r"(row + t4 * 8));
-                    } else {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                        for (int p = 0; p < KW / 4; ++p) {
-                            const uint4 v = ld_shared_v4(row + p * 64 + t4 * 16);
-                            kw[half][4 * p] = v.x;
-                            kw[half][4 * p + 1] = v.y;
-                            kw[half][4 * p + 2] = v.z;
-                            kw[half][4 * p + 3] = v.w;
+                    for (int e = 0; e < 4; ++e)
+                        sacc[c][e] = 0.f;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int tok = r + 8 * half;
+                        const uint32_t row = pair + c * C::PAGE + tok * (D / 2);
+                        if constexpr (D == 64) {
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                         : "=r"(kw[c][half][0]), "=r"(kw[c][half][1])
+                                         : "r"(row + t4 * 8));
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < KW / 4; ++p) {
+                                const uint4 v = ld_shared_v4(row + p * 64 + t4 * 16);
+                                kw[c][half][4 * p] = v.x;
+                                kw[c][half][4 * p + 1] = v.y;
+                                kw[c][half][4 * p + 2] = v.z;
+                                kw[c][half][4 * p + 3] = v.w;
+                            }
                         }
-                    }
-                    // the token's scales for this lane's dims, in order
-                    const uint8_t *sp = dsm + st * C::STAGE + 16 * D + tok * (D / 16);
-                    if constexpr (D == 64) {
-                        ks[half] = sp[t4] * 0x101u;
-                    } else if constexpr (D == 128) {
-                        ks[half] = *reinterpret_cast<const uint16_t *>(sp + 2 * t4);
-                    } else {
-                        ks[half] = *reinterpret_cast<const uint16_t *>(sp + 2 * t4) |
-                                   (static_cast<uint32_t>(
-                                        *reinterpret_cast<const uint16_t *>(sp + 8 + 2 * t4))
-                                    << 16);
+                        // the token's scales for this lane's dims, in order
+                        const uint8_t *sp = dsm + st * C::STAGE + c * C::PAGE + 16 * D + tok * (D / 16);
+                        if constexpr (D == 64) {
+                            ks[c][half] = sp[t4] * 0x101u;
+                        } else if constexpr (D == 128) {
+                            ks[c][half] = *reinterpret_cast<const uint16_t *>(sp + 2 * t4);
+                        } else {
+                            ks[c][half] = *reinterpret_cast<const uint16_t *>(sp + 2 * t4) |
+                                          (static_cast<uint32_t>(
+                                               *reinterpret_cast<const uint16_t *>(sp + 8 + 2 * t4))
+                                           << 16);
+                        }
                     }
                 }
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
                     // one word: eight codes of 8 dims = products 2w, 2w + 1; one scale
-                    uint32_t c0[4], c1[4];
-                    e2m1x8_to_f16(kw[0][w], c0);
-                    e2m1x8_to_f16(kw[1][w], c1);
                     const int si = D == 64 ? 0 : w / 2;         // index of the word's scale
-                    const uint32_t p0 = e4m3x2_to_f16(ks[0] >> (16 * (si / 2)));
-                    const uint32_t p1 = e4m3x2_to_f16(ks[1] >> (16 * (si / 2)));
-                    const uint32_t f0 = __byte_perm(p0, p0, si & 1 ? 0x3232 : 0x1010);
-                    const uint32_t f1 = __byte_perm(p1, p1, si & 1 ? 0x3232 : 0x1010);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t af[4] = {hmul2(c0[2 * q], f0), hmul2(c1[2 * q], f1),
-                                                hmul2(c0[2 * q + 1], f0), hmul2(c1[2 * q + 1], f1)};
-                        mma_f16(sacc, af, qb[2 * w + q][0], qb[2 * w + q][1]);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t c0[4], c1[4];
+                        e2m1x8_to_f16(kw[c][0][w], c0);
+                        e2m1x8_to_f16(kw[c][1][w], c1);
+                        const uint32_t p0 = e4m3x2_to_f16(ks[c][0] >> (16 * (si / 2)));
+                        const uint32_t p1 = e4m3x2_to_f16(ks[c][1] >> (16 * (si / 2)));
+                        const uint32_t f0 = __byte_perm(p0, p0, si & 1 ? 0x3232 : 0x1010);
+                        const uint32_t f1 = __byte_perm(p1, p1, si & 1 ? 0x3232 : 0x1010);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t af[4] = {hmul2(c0[2 * q], f0), hmul2(c1[2 * q], f1),
+                                                    hmul2(c0[2 * q + 1], f0),
+                                                    hmul2(c1[2 * q + 1], f1)};
+                            mma_f16(sacc[c], af, qb[2 * w + q][0], qb[2 * w + q][1]);
+                        }
                     }
                 }
                 // tokens r (0, 1) and r + 8 (2, 3); heads 2 t4 (0, 2) and 2 t4 + 1 (1, 3)
-                float xs[4] = {sacc[0] * sc0, sacc[1] * sc1, sacc[2] * sc0, sacc[3] * sc1};
-                if (valid < kPage) {
-                    if (r >= valid)
-                        xs[0] = xs[1] = -INFINITY;
-                    if (r + 8 >= valid)
-                        xs[2] = xs[3] = -INFINITY;
+                float xs[2][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        xs[c][e] = sacc[c][e] * (e & 1 ? sc1 : sc0);
+                if (valid < 2 * kPage) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (c * kPage + r + 8 * (e >> 1) >= valid)
+                                xs[c][e] = -INFINITY;
                 }
                 float bm[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float y = fmaxf(xs[h], xs[h + 2]);
+                    float y = fmaxf(fmaxf(xs[0][h], xs[0][h + 2]), fmaxf(xs[1][h], xs[1][h + 2]));
 #pragma unroll
                     for (int off = 4; off <= 16; off <<= 1)
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
@@ -688,59 +725,68 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4Dec
                     }
                 }
                 const float e0 = kPShift - m_run[0], e1 = kPShift - m_run[1];
-                const float p0 = ex2_approx(xs[0] + e0), p1 = ex2_approx(xs[1] + e1);
-                const float p2 = ex2_approx(xs[2] + e0), p3 = ex2_approx(xs[3] + e1);
-                l_part[0] += p0 + p2;
-                l_part[1] += p1 + p3;
-                const uint32_t pb0 = movm_t(pack_f16x2(p0, p1));
-                const uint32_t pb1 = movm_t(pack_f16x2(p2, p3));
+                uint32_t pb[2][2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float p0 = ex2_approx(xs[c][0] + e0), p1 = ex2_approx(xs[c][1] + e1);
+                    const float p2 = ex2_approx(xs[c][2] + e0), p3 = ex2_approx(xs[c][3] + e1);
+                    l_part[0] += p0 + p2;
+                    l_part[1] += p1 + p3;
+                    pb[c][0] = movm_t(pack_f16x2(p0, p1));
+                    pb[c][1] = movm_t(pack_f16x2(p2, p3));
+                }
 
                 // O^T += V^T P
 #pragma unroll
-                for (int p = 0; p < (D == 256 ? 2 : 1); ++p) {
-                    const int grp = D == 64 ? r >> 1 : r + 8 * p;
-                    uint32_t vs;
-                    asm volatile("ld.shared.b32 %0, [%1];"
-                                 : "=r"(vs)
-                                 : "r"(page + 17 * D + (grp * 4 + t4) * 4));
-                    if (valid < kPage) {
-                        // a page's unused rows may hold any bytes: their scales count as zero
-                        vs &= (2 * t4 < valid ? 0x000000ffu : 0u) |
-                              (2 * t4 + 1 < valid ? 0x0000ff00u : 0u) |
-                              (2 * t4 + 8 < valid ? 0x00ff0000u : 0u) |
-                              (2 * t4 + 9 < valid ? 0xff000000u : 0u);
-                    }
-                    const uint32_t f0 = e4m3x2_to_f16(vs & 0xffffu), f1 = e4m3x2_to_f16(vs >> 16);
-                    uint32_t even[2][2], odd[2][2];         // [token half][code word]
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t page = pair + c * C::PAGE;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if constexpr (D == 64) {
-                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                         : "=r"(even[half][0]), "=r"(odd[half][0])
-                                         : "r"(page + 8 * D + half * 256 + lane * 8));
-                        } else {
-                            const uint4 v =
-                                ld_shared_v4(page + 8 * D + (half * (D / 128) + p) * 512 + lane * 16);
-                            even[half][0] = v.x;
-                            even[half][1] = v.y;
-                            odd[half][0] = v.z;
-                            odd[half][1] = v.w;
+                    for (int p = 0; p < (D == 256 ? 2 : 1); ++p) {
+                        const int grp = D == 64 ? r >> 1 : r + 8 * p;
+                        uint32_t vs;
+                        asm volatile("ld.shared.b32 %0, [%1];"
+                                     : "=r"(vs)
+                                     : "r"(page + 17 * D + (grp * 4 + t4) * 4));
+                        if (valid < 2 * kPage) {
+                            // unused rows may hold any bytes: their scales count as zero
+                            const int left = valid - c * kPage;
+                            vs &= (2 * t4 < left ? 0x000000ffu : 0u) |
+                                  (2 * t4 + 1 < left ? 0x0000ff00u : 0u) |
+                                  (2 * t4 + 8 < left ? 0x00ff0000u : 0u) |
+                                  (2 * t4 + 9 < left ? 0xff000000u : 0u);
                         }
-                    }
+                        const uint32_t f0 = e4m3x2_to_f16(vs & 0xffffu), f1 = e4m3x2_to_f16(vs >> 16);
+                        uint32_t even[2][2], odd[2][2];         // [token half][code word]
 #pragma unroll
-                    for (int w = 0; w < (D == 64 ? 1 : 2); ++w) {
-                        // codes of eight dims paired by token: (even, odd) per byte
-                        uint32_t a0[4], a1[4], a2[4], a3[4];
-                        const uint32_t M = 0x0f0f0f0fu;
-                        e2m1x8_to_f16((even[0][w] & M) | ((odd[0][w] << 4) & ~M), a0);
-                        e2m1x8_to_f16(((even[0][w] >> 4) & M) | (odd[0][w] & ~M), a1);
-                        e2m1x8_to_f16((even[1][w] & M) | ((odd[1][w] << 4) & ~M), a2);
-                        e2m1x8_to_f16(((even[1][w] >> 4) & M) | (odd[1][w] & ~M), a3);
+                        for (int half = 0; half < 2; ++half) {
+                            if constexpr (D == 64) {
+                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                             : "=r"(even[half][0]), "=r"(odd[half][0])
+                                             : "r"(page + 8 * D + half * 256 + lane * 8));
+                            } else {
+                                const uint4 v = ld_shared_v4(
+                                    page + 8 * D + (half * (D / 128) + p) * 512 + lane * 16);
+                                even[half][0] = v.x;
+                                even[half][1] = v.y;
+                                odd[half][0] = v.z;
+                                odd[half][1] = v.w;
+                            }
+                        }
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint32_t af[4] = {hmul2(a0[b], f0), hmul2(a1[b], f0),
-                                                    hmul2(a2[b], f1), hmul2(a3[b], f1)};
-                            mma_f16(o[8 * p + 4 * w + b], af, pb0, pb1);
+                        for (int w = 0; w < (D == 64 ? 1 : 2); ++w) {
+                            // codes of eight dims paired by token: (even, odd) per byte
+                            uint32_t a0[4], a1[4], a2[4], a3[4];
+                            const uint32_t M = 0x0f0f0f0fu;
+                            e2m1x8_to_f16((even[0][w] & M) | ((odd[0][w] << 4) & ~M), a0);
+                            e2m1x8_to_f16(((even[0][w] >> 4) & M) | (odd[0][w] & ~M), a1);
+                            e2m1x8_to_f16((even[1][w] & M) | ((odd[1][w] << 4) & ~M), a2);
+                            e2m1x8_to_f16(((even[1][w] >> 4) & M) | (odd[1][w] & ~M), a3);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const uint32_t af[4] = {hmul2(a0[b], f0), hmul2(a1[b], f0),
+                                                        hmul2(a2[b], f1), hmul2(a3[b], f1)};
+                                mma_f16(o[8 * p + 4 * w + b], af, pb[c][0], pb[c][1]);
+                            }
                         }
                     }
                 }
@@ -748,7 +794,13 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv4_decode_kernel(const Kv4Dec
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_u32(&s_empty[st]));
+            st += kConsumers;
+            if (st >= NS) {
+                st -= NS;
+                phase ^= 1;
+            }
         }
+        base_pair = end;
 
         // ------------------------------------------------ end of the segment
 #pragma unroll
@@ -896,8 +948,9 @@ cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
         if (dev < 64)
             attr_done[dev] = 1;
     }
-    // three CTAs fit on an SM; runs of at least kMinRun pages
-    long long parts = (3LL * sm_count < kMaxParts ? 3LL * sm_count : kMaxParts) / rows;
+    // as many CTAs as fit on the SMs; runs of at least kMinRun pages
+    const long long ctas = static_cast<long long>(C::CTAS) * sm_count;
+    long long parts = (ctas < kMaxParts ? ctas : kMaxParts) / rows;
     const long long most = (static_cast<long long>(a.num_seqs) * (a.capacity > 0 ? a.capacity : 1) +
                             kMinRun - 1) / kMinRun;
     parts = parts < most ? parts : most;
