@@ -322,17 +322,22 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // heads of a kv head together (eight at most per CTA; more heads are more
 // head chunks, whose pages come from L2).
 //
-// Work.  Every sequence counts ceil(tokens / 16) units (pages; 1 if empty);
-// the batch's units in one row are cut into equal contiguous runs, one per
-// CTA, so long and short contexts load every SM alike.  A run covers any
-// number of sequences; a sequence that lies in one run is finished there, the
-// others leave partial states (m, l, o), merged in a fixed order by the CTA
-// that takes the last ticket.  No CTA waits for another.
+// Work.  Every sequence counts its pages (1 if empty) and kSeqUnits for its
+// start and end (a query load, a merge of the warps, an output: about as long
+// as kSeqUnits pages take a CTA); the batch's units in one row are cut into
+// equal contiguous runs, one per CTA, so long and short contexts load every SM
+// alike.  A run covers any number of sequences; a sequence whose pages lie in
+// one run is finished there, the others leave partial states (m, l, o), merged
+// in a fixed order by the CTA that takes the last ticket.  No CTA waits for
+// another.
 //
-// A producer warp streams the run's head pages (18 D bytes each, contiguous)
-// two by two through a ring of shared-memory stages with bulk copies; pair i
-// is consumed by warp i % 4 (two pages at a time give a warp two independent
-// chains of products and halve the exchanges of the maximum).  Per page, two
+// Warp w takes every fourth pair of the run's pages (two at a time give a warp
+// two independent chains of products and halve the exchanges of the maximum)
+// and copies them ahead into its own ring of shared-memory stages with 16-byte
+// asynchronous copies; it alone reads what it copied, so the ring needs no
+// barrier, only its copy groups.  (Bulk copies held the issuing warp for about
+// 500 cycles each: four 49k-65k-token contexts took 72 us with every warp
+// issuing its own and 87 us from one producer warp.)  Per page, two
 // products on mma.sync m16n8k16 (f16 in, fp32 accumulate):
 //   S[16 tokens x 8 heads] = K Q^T    O^T[D x 8 heads] += V^T P
 // The page's order gives every lane its A operands in whole 16-byte words: a
@@ -347,27 +352,38 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // the largest below.  p is held as 2^14 p in f16 (2^-12 relative for p above
 // 2^-28), l sums the fp32 values, and m, l, o are fp32.
 constexpr int kConsumers = 4;
-constexpr int kDecThreads = (kConsumers + 1) * 32;
+constexpr int kDecThreads = kConsumers * 32;
 constexpr int kHeads = 8;               // query heads of a kv head per CTA
-constexpr int kMinRun = 8;              // units per CTA at least
-constexpr int kMaxParts = 608;          // CTAs at most, where there are fewer head chunks
+constexpr int kSeqUnits = 8;            // units of a sequence besides its pages
+constexpr int kMinRun = 16;             // units per CTA at least
+constexpr int kMaxParts = 256;          // runs of one row of units at most (their weights in a merge
+                                        // take the place of the warps' outputs: 256 <= 4 D)
+constexpr int kMaxCtas = 1024;          // in all rows, where there are fewer rows
 constexpr float kPShift = 14.f;
 
 template <int D>
 struct DecCfg {
     static constexpr int PAGE = 18 * D;                         // bytes of a head page
     static constexpr int STAGE = 2 * PAGE;                      // a stage holds two pages
-    static constexpr int NS = D == 64 ? 16 : D == 128 ? 12 : 8; // stages: a multiple of kConsumers
-    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : 2; // resident per SM
+    static constexpr int NS = D == 64 ? 16 : 8;                 // stages of the CTA
+    static constexpr int WS = NS / kConsumers;                  // stages of a warp
+    static constexpr int CTAS = D == 64 ? 5 : D == 128 ? 4 : 2; // resident per SM
     static constexpr int MT = D / 16;
     static constexpr int KW = D / 32;               // code words of one token per lane
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until all but the newest N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t movm_t(uint32_t x)
@@ -385,13 +401,9 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void consumers_sync()
-{
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
-}
-
-// Units of a sequence, and its token count (0 and *bad for an invalid one).
-__device__ __forceinline__ int seq_units(const Kv4DecodeArgs &a, int s, int *tokens, bool *bad)
+// Pages of a sequence (1 if empty), and its token count (0 and *bad for an
+// invalid one).
+__device__ __forceinline__ int seq_pages(const Kv4DecodeArgs &a, int s, int *tokens, bool *bad)
 {
     const int n = __ldg(a.counts + s);
     *bad = n < 0 || n > static_cast<long long>(a.capacity) * kPage;
@@ -400,18 +412,53 @@ __device__ __forceinline__ int seq_units(const Kv4DecodeArgs &a, int s, int *tok
     return u < 1 ? 1 : u;
 }
 
+// A place in the CTA's run [u0, u1): the segment of sequence s whose units
+// start at `at` in the row (kSeqUnits, then its pages), the run's pages [j0,
+// j1) of it, and (modulo 4) the pairs of the earlier segments, which decide
+// the warp that takes its first pair.
+struct RunCursor {
+    int s, at, pages, tokens, j0, j1, base;
+    bool bad;
+
+    // The first segment with pages in the run from sequence s on; false if none.
+    __device__ __forceinline__ bool enter(const Kv4DecodeArgs &a, int u0, int u1)
+    {
+        for (; at + kSeqUnits < u1; ++s) {
+            pages = seq_pages(a, s, &tokens, &bad);
+            const int p0 = at + kSeqUnits;
+            j0 = max(0, u0 - p0);
+            j1 = min(pages, u1 - p0);
+            if (j0 < j1)
+                return true;
+            at = p0 + pages;
+        }
+        return false;
+    }
+    // First page of `warp`'s first pair of the segment (at or past j1: none).
+    __device__ __forceinline__ int first(int warp) const
+    {
+        return j0 + 2 * ((warp - base) & (kConsumers - 1));
+    }
+    // The next segment; false at the end of the run.
+    __device__ __forceinline__ bool next(const Kv4DecodeArgs &a, int u0, int u1)
+    {
+        base += (j1 - j0 + 1) / 2;
+        at += kSeqUnits + pages;
+        ++s;
+        return enter(a, u0, u1);
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kernel(const Kv4DecodeArgs a)
 {
     using C = DecCfg<D>;
     constexpr int NS = C::NS, MT = C::MT, KW = C::KW;
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ uint64_t s_full[NS], s_empty[NS];
-    __shared__ int s_stage_bad[NS];
     __shared__ float s_m[kConsumers][kHeads], s_l[kConsumers][kHeads];
     __shared__ int s_bad[kConsumers];
     __shared__ int s_scan[kDecThreads / 32];
-    __shared__ int s_first, s_first_unit, s_abort, s_last;
+    __shared__ int s_first, s_first_unit, s_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.num_q_heads / a.num_kv_heads;
@@ -427,7 +474,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     for (int s = sa; s < sb; ++s) {
         int n;
         bool bad;
-        mine += seq_units(a, s, &n, &bad);
+        mine += kSeqUnits + seq_pages(a, s, &n, &bad);
     }
     int x = mine;
 #pragma unroll
@@ -438,15 +485,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     }
     if (lane == 31)
         s_scan[warp] = x;
-    if (tid == 0) {
-        s_abort = 0;
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(smem_u32(&s_full[i]), 1);
-            mbar_init(smem_u32(&s_empty[i]), 1);
-            s_stage_bad[i] = 0;
-        }
-        fence_barrier_init();
-    }
     __syncthreads();
     int before = x - mine, total = 0;
 #pragma unroll
@@ -466,7 +504,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
         for (int s = sa; s < sb; ++s) {
             int n;
             bool bad;
-            const int u = seq_units(a, s, &n, &bad);
+            const int u = kSeqUnits + seq_pages(a, s, &n, &bad);
             if (u0 < at + u) {
                 s_first = s;
                 s_first_unit = at;
@@ -476,89 +514,92 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
         }
     }
     __syncthreads();
-    volatile int *abort = &s_abort;
-    const uint32_t ring = smem_u32(dsm);
-    const size_t page_bytes = static_cast<size_t>(a.num_kv_heads) * C::PAGE;
+    const uint32_t page_bytes = static_cast<uint32_t>(a.num_kv_heads) * C::PAGE;
     const uint8_t *pool = a.pool + static_cast<size_t>(kh) * C::PAGE;
 
-    if (warp == kConsumers) {
-        // ------------------------------------------------ producer
-        int s = s_first, at = s_first_unit, issued = 0, st = 0, phase = 1;
-        bool ok = true;
-        while (ok && at < u1) {
-            int n;
-            bool bad;
-            const int units = seq_units(a, s, &n, &bad);
-            if (bad && lane == 0)
-                record(a.status, VFA_ERR_BAD_BLOCK);
-            const int j0 = max(0, u0 - at), j1 = min(units, u1 - at);
-            const int32_t *row = a.tables + static_cast<long long>(s) * a.capacity;
-            for (int jb = j0; ok && jb < j1; jb += 32) {
-                const int id = jb + lane < j1 && n > 0 ? __ldg(row + jb + lane) : -1;
-                const int m = min(32, j1 - jb);
-                for (int k = 0; k < m; k += 2) {
-                    const int blk[2] = {__shfl_sync(0xffffffffu, id, k),
-                                        __shfl_sync(0xffffffffu, id, k + 1)};
-                    if (lane == 0) {
-                        // (a fresh barrier counts as having completed the phase before its first)
-                        ok = mbar_wait(smem_u32(&s_empty[st]), phase, abort);
-                        if (ok) {
-                            int good = 0;
+    // ---------------------------------------------------- copies
+    // Fills of this warp's stages, WS pairs ahead: the pair at page `ahead` of
+    // segment `fill` next, its page ids already loaded.  Every turn commits one
+    // group of copies, also where there is nothing left to copy.
+    RunCursor fill;
+    fill.s = s_first;
+    fill.at = s_first_unit;
+    fill.base = 0;
+    if (!fill.enter(a, u0, u1))
+        return;                                     // (the whole CTA) no page in this run
+    RunCursor seg = fill;
+    int ahead = fill.first(warp), id0 = 0, id1 = 0;
+    const int32_t *row = a.tables + static_cast<long long>(fill.s) * a.capacity;
+    uint32_t bad_stages = 0;
+    bool more = true;
+    auto load_ids = [&]() {
+        while (ahead >= fill.j1) {
+            more = fill.next(a, u0, u1);
+            if (!more)
+                return;
+            ahead = fill.first(warp);
+            row = a.tables + static_cast<long long>(fill.s) * a.capacity;
+        }
+        if (fill.tokens > 0) {                      // an empty sequence has no page
+            id0 = __ldg(row + ahead);
+            if (ahead + 1 < fill.j1)
+                id1 = __ldg(row + ahead + 1);
+        }
+    };
+    const uint32_t my_ring = smem_u32(dsm) + warp * C::WS * C::STAGE + lane * 16;
+    const uint8_t *my_pool = pool + lane * 16;
+    auto issue = [&](int ws) {
+        if (more) {
+            constexpr int PIECES = C::PAGE / 16;    // 16-byte pieces of a page
+            const bool two = ahead + 1 < fill.j1, one = fill.tokens > 0;
+            const bool good = !one || (static_cast<unsigned>(id0) < static_cast<unsigned>(a.num_blocks) &&
+                                       (!two || static_cast<unsigned>(id1) <
+                                                    static_cast<unsigned>(a.num_blocks)));
+            if (good && one) {
+                // the pair's pieces in order, 32 per turn: those of page 0, then page 1
+                const uint8_t *p0 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * page_bytes;
+                const uint8_t *p1 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id1)) * page_bytes -
+                                    C::PAGE;
+                const uint32_t dst = my_ring + ws * C::STAGE;
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                good += blk[c] >= 0 && blk[c] < a.num_blocks;
-                            // an empty sequence's one unit has no page; every other listed one has
-                            const bool bad_id = n > 0 && good != min(2, m - k);
-                            s_stage_bad[st] = bad_id;
-                            if (bad_id)
-                                record(a.status, VFA_ERR_BAD_BLOCK);
-                            if (good)
-                                mbar_arrive_expect_tx(smem_u32(&s_full[st]), good * C::PAGE);
-                            else
-                                mbar_arrive(smem_u32(&s_full[st]));
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                if (blk[c] >= 0 && blk[c] < a.num_blocks)
-                                    bulk_load(ring + st * C::STAGE + c * C::PAGE,
-                                              pool + blk[c] * page_bytes, C::PAGE,
-                                              smem_u32(&s_full[st]));
-                        }
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok)
-                        break;
-                    ++issued;
-                    if (++st == NS) {
-                        st = 0;
-                        phase ^= 1;
+                for (int k = 0; k < 2 * PIECES; k += 32) {
+                    if (k + 32 <= PIECES) {
+                        copy16_async(dst + k * 16, p0 + k * 16);
+                    } else if (k >= PIECES) {
+                        if (two && (k + 32 <= 2 * PIECES || k + lane < 2 * PIECES))
+                            copy16_async(dst + k * 16, p1 + k * 16);
+                    } else {
+                        const bool second = lane >= PIECES - k;
+                        if (two || !second)
+                            copy16_async(dst + k * 16, (second ? p1 : p0) + k * 16);
                     }
                 }
             }
-            at += units;
-            ++s;
+            bad_stages &= ~(1u << ws);
+            if (!good) {
+                bad_stages |= 1u << ws;
+                if (lane == 0)
+                    record(a.status, VFA_ERR_BAD_BLOCK);
+            }
+            ahead += 2 * kConsumers;
+            load_ids();
         }
-        // every copy issued has landed before the CTA can end, also after a
-        // consumer gave up: the last fill issued into each stage
-        if (lane == 0)
-            for (int q = 0; q < NS && q < issued; ++q)
-                mbar_wait_drain(smem_u32(&s_full[q]), ((issued - 1 - q) / NS) & 1);
-        return;
-    }
+        copy_commit();
+    };
+    load_ids();
+#pragma unroll 1
+    for (int k = 0; k < C::WS; ++k)
+        issue(k);
 
-    // ---------------------------------------------------- consumers
+    // ---------------------------------------------------- attention
     const int r = lane >> 2, t4 = lane & 3;
     float *s_o = reinterpret_cast<float *>(dsm + NS * C::STAGE);    // [kConsumers][G][D]
-    int s = s_first, at = s_first_unit;
-    int i = warp;                                   // this warp's next pair of the run
-    int base_pair = 0;                              // pairs of the earlier segments
-    int st = warp, phase = 0;
+    int ws = 0;                                     // stage of this warp's next pair
     bool first_segment = true;
-    while (at < u1) {
-        int n;
-        bool seq_bad;
-        const int units = seq_units(a, s, &n, &seq_bad);
-        const int j0 = max(0, u0 - at), j1 = min(units, u1 - at);
-        const int end = base_pair + (j1 - j0 + 1) / 2;
+    do {
+        const int s = seg.s, n = seg.tokens, j0 = seg.j0, j1 = seg.j1;
+        if (seg.bad && tid == 0)
+            record(a.status, VFA_ERR_BAD_BLOCK);
 
         // Q^T operand: head r, dims as K's lanes hold them.
         uint32_t qb[MT][2];
@@ -596,7 +637,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                                                   __uint_as_float(w[c] & 0xffff0000u) * up)
                                      : 0u;
             }
-            sc = a.scale_log2 * down;               // of head r; the accumulators hold 2 t4, + 1
+            // of head r (the accumulators hold 2 t4, + 1); positive, or a masked -inf times it
+            // would be no number
+            sc = fmaxf(a.scale_log2 * down, FLT_MIN);
         }
         const float sc0 = __shfl_sync(0xffffffffu, sc, (2 * t4) * 4);
         const float sc1 = __shfl_sync(0xffffffffu, sc, (2 * t4 + 1) * 4);
@@ -608,18 +651,15 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 o[mt][e] = 0.f;
-        bool bad = seq_bad;
+        bool bad = seg.bad;
 
-        for (; i < end; i += kConsumers) {
-            if (!mbar_wait_warp(smem_u32(&s_full[st]), phase, abort)) {
-                bad = true;
-                continue;
-            }
-            const uint32_t pair = ring + st * C::STAGE;
+        for (int j = seg.first(warp); j < j1; j += 2 * kConsumers) {
+            copy_wait<C::WS - 1>();
+            __syncwarp();                           // every lane's copies are there for every lane
+            const uint32_t pair = my_ring - lane * 16 + ws * C::STAGE;
             // tokens of the two pages that count, those of the run's pages
-            const int j = j0 + 2 * (i - base_pair);
             const int valid = min(n - j * kPage, j + 1 < j1 ? 2 * kPage : kPage);
-            bad |= s_stage_bad[st] != 0;
+            bad |= (bad_stages >> ws) & 1u;
             if (valid > 0 && !bad) {
                 // S = K Q^T: two pages, two independent accumulators
                 float sacc[2][4];
@@ -648,7 +688,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                             }
                         }
                         // the token's scales for this lane's dims, in order
-                        const uint8_t *sp = dsm + st * C::STAGE + c * C::PAGE + 16 * D + tok * (D / 16);
+                        const uint8_t *sp = dsm + (warp * C::WS + ws) * C::STAGE + c * C::PAGE +
+                                            16 * D + tok * (D / 16);
                         if constexpr (D == 64) {
                             ks[c][half] = sp[t4] * 0x101u;
                         } else if constexpr (D == 128) {
@@ -684,28 +725,22 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                     }
                 }
                 // tokens r (0, 1) and r + 8 (2, 3); heads 2 t4 (0, 2) and 2 t4 + 1 (1, 3)
-                float xs[2][4];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        xs[c][e] = sacc[c][e] * (e & 1 ? sc1 : sc0);
                 if (valid < 2 * kPage) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (c * kPage + r + 8 * (e >> 1) >= valid)
-                                xs[c][e] = -INFINITY;
+                                sacc[c][e] = -INFINITY;
                 }
                 float bm[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float y = fmaxf(fmaxf(xs[0][h], xs[0][h + 2]), fmaxf(xs[1][h], xs[1][h + 2]));
+                    float y = fmax3(fmaxf(sacc[0][h], sacc[0][h + 2]), sacc[1][h], sacc[1][h + 2]);
 #pragma unroll
                     for (int off = 4; off <= 16; off <<= 1)
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                    bm[h] = y;
+                    bm[h] = y * (h ? sc1 : sc0);    // the scales are positive
                 }
                 if (__any_sync(0xffffffffu, bm[0] > m_run[0] || bm[1] > m_run[1])) {
                     float f[2];
@@ -728,8 +763,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                 uint32_t pb[2][2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float p0 = ex2_approx(xs[c][0] + e0), p1 = ex2_approx(xs[c][1] + e1);
-                    const float p2 = ex2_approx(xs[c][2] + e0), p3 = ex2_approx(xs[c][3] + e1);
+                    const float p0 = ex2_approx(fmaf(sacc[c][0], sc0, e0));
+                    const float p1 = ex2_approx(fmaf(sacc[c][1], sc1, e1));
+                    const float p2 = ex2_approx(fmaf(sacc[c][2], sc0, e0));
+                    const float p3 = ex2_approx(fmaf(sacc[c][3], sc1, e1));
                     l_part[0] += p0 + p2;
                     l_part[1] += p1 + p3;
                     pb[c][0] = movm_t(pack_f16x2(p0, p1));
@@ -791,16 +828,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&s_empty[st]));
-            st += kConsumers;
-            if (st >= NS) {
-                st -= NS;
-                phase ^= 1;
-            }
+            __syncwarp();                           // every lane is done with the stage: refill it
+            issue(ws);
+            ws = ws + 1 == C::WS ? 0 : ws + 1;
         }
-        base_pair = end;
 
         // ------------------------------------------------ end of the segment
 #pragma unroll
@@ -809,7 +840,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
             for (int off = 4; off <= 16; off <<= 1)
                 l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], off);
         }
-        bad = __any_sync(0xffffffffu, bad || *abort != 0);
         if (lane < 4) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -829,14 +859,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                     *reinterpret_cast<float2 *>(&s_o[(warp * G + 2 * t4 + h) * D + d]) =
                         make_float2(o[mt][h], o[mt][2 + h]);
         }
-        consumers_sync();
+        __syncthreads();
         bad = s_bad[0] || s_bad[1] || s_bad[2] || s_bad[3];
-        const bool whole = j0 == 0 && j1 == units;
+        const bool whole = j0 == 0 && j1 == seg.pages;
         float *part = a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 *
                                    kHeads * (D + 2) +
                       (first_segment ? 0 : kHeads * (D + 2));
-        if (tid == 0 && *abort)
-            record(a.status, VFA_ERR_TIMEOUT);
         for (int e = tid; e < G * D; e += kConsumers * 32) {
             const int g = e / D, d = e % D;
             float mt = s_m[0][g];
@@ -870,57 +898,81 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
             }
         }
         if (!whole) {
-            // runs of this sequence: the first may start inside it, as a later segment
-            const int xa = at / run, xb = (at + units - 1) / run;
+            // runs with pages of this sequence
+            const int p0 = seg.at + kSeqUnits;
+            const int xa = p0 / run, parts = (p0 + seg.pages - 1) / run - xa + 1;
             int32_t *ticket = a.tickets + static_cast<long long>(s) * gridDim.y + blockIdx.y;
             __threadfence();
-            consumers_sync();
+            __syncthreads();
             if (tid == 0)
-                s_last = atomicAdd(ticket, 1) == xb - xa;
-            consumers_sync();
+                s_last = atomicAdd(ticket, 1) == parts - 1;
+            __syncthreads();
             if (s_last) {
                 __threadfence();
                 const float *base = a.part + static_cast<long long>(blockIdx.y) * gridDim.x * 2 *
                                                  kHeads * (D + 2);
-                const int late = at % run != 0;     // run xa holds it in its second slot
-                for (int e = tid; e < G * D; e += kConsumers * 32) {
-                    const int g = e / D, d = e % D;
-                    auto slot = [&](int xx) {
-                        return base + (static_cast<long long>(xx) * 2 + (xx == xa ? late : 0)) *
-                                          kHeads * (D + 2) + g * (D + 2);
-                    };
-                    float mt = -INFINITY;
+                // run xa holds it in its second slot if it has pages of an earlier one
+                const int late = seg.at > xa * run;
+                auto slot = [&](int x, int g) {
+                    return base + (static_cast<long long>(xa + x) * 2 + (x == 0 ? late : 0)) *
+                                      kHeads * (D + 2) + g * (D + 2);
+                };
+                // weights of the parts, a warp per head: s_o[g][x], free by now
+                for (int g = warp; g < G; g += kConsumers) {
+                    float *w = s_o + g * parts;
+                    float mt = -INFINITY, l = 0.f;
                     bool any_bad = false;
-                    for (int xx = xa; xx <= xb; ++xx) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot(xx)));
-                        mt = fmaxf(mt, ml.x);
-                        any_bad |= ml.y < 0.f;
+                    for (int x = lane; x < parts; x += 32) {
+                        const float m = __ldcg(slot(x, g));
+                        w[x] = m;
+                        mt = fmaxf(mt, m);
                     }
-                    float acc_o = 0.f, acc_l = 0.f;
-                    for (int xx = xa; xx <= xb; ++xx) {
-                        const float *q = slot(xx);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q));
-                        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mt);
-                        acc_l = fmaf(ml.y, f, acc_l);
-                        acc_o = fmaf(__ldcg(q + 2 + d), f, acc_o);
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1)
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+                    for (int x = lane; x < parts; x += 32) {
+                        const float lx = __ldcg(slot(x, g) + 1);
+                        const float f = w[x] == -INFINITY ? 0.f : ex2_approx(w[x] - mt);
+                        any_bad |= lx < 0.f;
+                        l = fmaf(lx, f, l);
+                        w[x] = f;
                     }
-                    if (!any_bad) {
-                        const long long row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
-                        static_cast<__nv_bfloat16 *>(a.out)[row * D + d] =
-                            __float2bfloat16_rn(acc_o / acc_l * a.descale_v);
-                        if (d == 0 && a.lse)
-                            a.lse[row] = (mt - kPShift + __log2f(acc_l)) * kLn2;
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1)
+                        l += __shfl_xor_sync(0xffffffffu, l, off);
+                    any_bad = __any_sync(0xffffffffu, any_bad);
+                    if (lane == 0) {
+                        s_m[0][g] = mt;
+                        s_l[0][g] = any_bad ? -1.f : l;
                     }
+                }
+                __syncthreads();
+                for (int e = 2 * tid; e < G * D; e += 2 * kDecThreads) {
+                    const int g = e / D, d = e % D;
+                    const float l = s_l[0][g];
+                    if (l < 0.f)
+                        continue;
+                    const float *w = s_o + g * parts;
+                    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 8
+                    for (int x = 0; x < parts; ++x) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(slot(x, g) + 2 + d));
+                        acc.x = fmaf(v.x, w[x], acc.x);
+                        acc.y = fmaf(v.y, w[x], acc.y);
+                    }
+                    const long long row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
+                    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) =
+                        pack_bf16x2(acc.x / l * a.descale_v, acc.y / l * a.descale_v);
+                    if (d == 0 && a.lse)
+                        a.lse[row] = (s_m[0][g] - kPShift + __log2f(l)) * kLn2;
                 }
                 if (tid == 0)
                     *ticket = 0;                    // ready for the next call
             }
         }
-        consumers_sync();                           // s_o, s_m, s_l, s_bad are free again
-        at += units;
-        ++s;
+        __syncthreads();                            // s_o, s_m, s_l, s_bad are free again
         first_segment = false;
-    }
+    } while (seg.next(a, u0, u1));
 }
 
 template <int D>
@@ -949,12 +1001,16 @@ cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
             attr_done[dev] = 1;
     }
     // as many CTAs as fit on the SMs; runs of at least kMinRun pages
-    const long long ctas = static_cast<long long>(C::CTAS) * sm_count;
-    long long parts = (ctas < kMaxParts ? ctas : kMaxParts) / rows;
-    const long long most = (static_cast<long long>(a.num_seqs) * (a.capacity > 0 ? a.capacity : 1) +
+    // (228 KB per SM; 2 KB covers a CTA's static and reserved shared memory)
+    const long long by_smem = (228 * 1024) / (static_cast<long long>(smem) + 2048);
+    const long long fit = (by_smem < C::CTAS ? by_smem : C::CTAS) * sm_count;
+    const long long ctas = fit < kMaxCtas ? fit : kMaxCtas;
+    long long parts = ctas / rows;
+    const long long most = (static_cast<long long>(a.num_seqs) *
+                                (kSeqUnits + (a.capacity > 0 ? a.capacity : 1)) +
                             kMinRun - 1) / kMinRun;
     parts = parts < most ? parts : most;
-    parts = parts < 1 ? 1 : parts;
+    parts = parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts);
     kv4_decode_kernel<D><<<dim3(static_cast<int>(parts), rows), kDecThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
@@ -1003,8 +1059,10 @@ size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_head
 {
     const int group = num_q_heads / num_kv_heads;
     const int rows = num_kv_heads * ((group + kHeads - 1) / kHeads);
-    // at most kMaxParts runs in all, or one per row where there are more rows
-    const size_t runs = rows > kMaxParts ? rows : kMaxParts;
+    // runs: kMaxParts for one row, kMaxCtas in all rows or one per row
+    const long long all = rows > kMaxCtas ? rows : kMaxCtas;
+    const size_t runs = all < static_cast<long long>(rows) * kMaxParts
+                            ? static_cast<size_t>(all) : static_cast<size_t>(rows) * kMaxParts;
     return ticket_bytes(num_seqs, rows) + runs * 2 * kHeads * (head_dim + 2) * sizeof(float);
 }
 
