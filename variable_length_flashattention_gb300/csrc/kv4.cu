@@ -21,6 +21,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace vfa {
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_write_kernel(const Kv4Mov
     constexpr int GR = D / 16, HPW = 32 / GR;
     const int lane = threadIdx.x & 31;
     const int g = lane % GR;
+    grid_dependency();
     if (blockIdx.x == 0)
         check_cu(a);
     const int nwarps = gridDim.x * kMoveWarps;
@@ -264,6 +266,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
     constexpr int GR = D / 16, HPW = 32 / GR;
     const int lane = threadIdx.x & 31;
     const int g = lane % GR;
+    grid_dependency();
     if (blockIdx.x == 0)
         check_cu(a);
     const int nwarps = gridDim.x * kMoveWarps;
@@ -356,8 +359,7 @@ constexpr int kDecThreads = kConsumers * 32;
 constexpr int kHeads = 8;               // query heads of a kv head per CTA
 constexpr int kSeqUnits = 8;            // units of a sequence besides its pages
 constexpr int kMinRun = 16;             // units per CTA at least
-constexpr int kMaxParts = 256;          // runs of one row of units at most (their weights in a merge
-                                        // take the place of the warps' outputs: 256 <= 4 D)
+constexpr int kMaxParts = 256;          // runs of one row of units at most (what one CTA merges)
 constexpr int kMaxCtas = 1024;          // in all rows, where there are fewer rows
 constexpr float kPShift = 14.f;
 
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     __shared__ int s_scan[kDecThreads / 32];
     __shared__ int s_first, s_first_unit, s_last;
 
+    grid_dependency();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.num_q_heads / a.num_kv_heads;
     const int chunks = (group + kHeads - 1) / kHeads;
@@ -551,36 +554,31 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     auto issue = [&](int ws) {
         if (more) {
             constexpr int PIECES = C::PAGE / 16;    // 16-byte pieces of a page
-            const bool two = ahead + 1 < fill.j1, one = fill.tokens > 0;
-            const bool good = !one || (static_cast<unsigned>(id0) < static_cast<unsigned>(a.num_blocks) &&
-                                       (!two || static_cast<unsigned>(id1) <
-                                                    static_cast<unsigned>(a.num_blocks)));
-            if (good && one) {
+            const unsigned blocks = static_cast<unsigned>(a.num_blocks);
+            const bool two = ahead + 1 < fill.j1;
+            // (an empty sequence's one page is not there to be copied)
+            const bool bad = fill.tokens > 0 && (static_cast<unsigned>(id0) >= blocks ||
+                                                 (two && static_cast<unsigned>(id1) >= blocks));
+            const uint8_t *p0 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * page_bytes;
+            const uint32_t dst = my_ring + ws * C::STAGE;
+            if (two && !bad) {
                 // the pair's pieces in order, 32 per turn: those of page 0, then page 1
-                const uint8_t *p0 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * page_bytes;
                 const uint8_t *p1 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id1)) * page_bytes -
                                     C::PAGE;
-                const uint32_t dst = my_ring + ws * C::STAGE;
+                const uint8_t *mid = lane >= PIECES % 32 ? p1 : p0;     // the turn with both
 #pragma unroll
-                for (int k = 0; k < 2 * PIECES; k += 32) {
-                    if (k + 32 <= PIECES) {
+                for (int k = 0; k < 2 * PIECES; k += 32)
+                    if (k + 32 <= 2 * PIECES || k + lane < 2 * PIECES)
+                        copy16_async(dst + k * 16, (k + 32 <= PIECES ? p0 : k >= PIECES ? p1 : mid) + k * 16);
+            } else if (fill.tokens > 0 && !bad) {
+#pragma unroll 1
+                for (int k = 0; k < PIECES; k += 32)
+                    if (k + lane < PIECES)
                         copy16_async(dst + k * 16, p0 + k * 16);
-                    } else if (k >= PIECES) {
-                        if (two && (k + 32 <= 2 * PIECES || k + lane < 2 * PIECES))
-                            copy16_async(dst + k * 16, p1 + k * 16);
-                    } else {
-                        const bool second = lane >= PIECES - k;
-                        if (two || !second)
-                            copy16_async(dst + k * 16, (second ? p1 : p0) + k * 16);
-                    }
-                }
             }
-            bad_stages &= ~(1u << ws);
-            if (!good) {
-                bad_stages |= 1u << ws;
-                if (lane == 0)
-                    record(a.status, VFA_ERR_BAD_BLOCK);
-            }
+            bad_stages = (bad_stages & ~(1u << ws)) | (static_cast<uint32_t>(bad) << ws);
+            if (bad && lane == 0)
+                record(a.status, VFA_ERR_BAD_BLOCK);
             ahead += 2 * kConsumers;
             load_ids();
         }
@@ -862,39 +860,42 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
         __syncthreads();
         bad = s_bad[0] || s_bad[1] || s_bad[2] || s_bad[3];
         const bool whole = j0 == 0 && j1 == seg.pages;
-        float *part = a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 *
-                                   kHeads * (D + 2) +
-                      (first_segment ? 0 : kHeads * (D + 2));
-        for (int e = tid; e < G * D; e += kConsumers * 32) {
+        // The warps' states merged: four dims per thread and turn.
+        constexpr int PART = kHeads * (D + 4);      // floats of a part: per head o, m, l
+        float *part = a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * PART +
+                      (first_segment ? 0 : PART);
+        auto finish = [&](int g, int d, float4 v, float m, float l) {
+            const long long out_row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
+            const float f = m == -INFINITY ? 0.f : a.descale_v / l;
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D + d) =
+                make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+            if (d == 0 && a.lse)
+                a.lse[out_row] = m == -INFINITY ? -FLT_MAX : (m - kPShift + __log2f(l)) * kLn2;
+        };
+        for (int e = 4 * tid; e < G * D; e += 4 * kDecThreads) {
             const int g = e / D, d = e % D;
-            float mt = s_m[0][g];
-#pragma unroll
-            for (int w = 1; w < kConsumers; ++w)
-                mt = fmaxf(mt, s_m[w][g]);
-            float acc_o = 0.f, acc_l = 0.f;
+            const float mt = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
             if (mt != -INFINITY) {
 #pragma unroll
                 for (int w = 0; w < kConsumers; ++w) {
                     const float f = ex2_approx(s_m[w][g] - mt);
-                    acc_o = fmaf(s_o[(w * G + g) * D + d], f, acc_o);
-                    acc_l = fmaf(s_l[w][g], f, acc_l);
+                    const float4 v = *reinterpret_cast<const float4 *>(&s_o[(w * G + g) * D + d]);
+                    acc.x = fmaf(v.x, f, acc.x);
+                    acc.y = fmaf(v.y, f, acc.y);
+                    acc.z = fmaf(v.z, f, acc.z);
+                    acc.w = fmaf(v.w, f, acc.w);
+                    l = fmaf(s_l[w][g], f, l);
                 }
             }
-            if (whole) {
-                if (!bad) {
-                    const long long row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
-                    static_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(
-                        mt == -INFINITY ? 0.f : acc_o / acc_l * a.descale_v);
-                    if (d == 0 && a.lse)
-                        a.lse[row] = mt == -INFINITY ? -FLT_MAX
-                                                     : (mt - kPShift + __log2f(acc_l)) * kLn2;
-                }
-            } else {
-                part[g * (D + 2) + 2 + d] = acc_o;
-                if (d == 0) {
-                    part[g * (D + 2)] = mt;
-                    part[g * (D + 2) + 1] = bad ? -1.f : acc_l;     // a sum is never negative
-                }
+            if (!whole) {
+                float *q = part + g * (D + 4);
+                __stcg(reinterpret_cast<float4 *>(q + d), acc);
+                if (d == 0)                         // a sum is never negative
+                    __stcg(reinterpret_cast<float2 *>(q + D), make_float2(mt, bad ? -1.f : l));
+            } else if (!bad) {
+                finish(g, d, acc, mt, l);
             }
         }
         if (!whole) {
@@ -902,69 +903,58 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
             const int p0 = seg.at + kSeqUnits;
             const int xa = p0 / run, parts = (p0 + seg.pages - 1) / run - xa + 1;
             int32_t *ticket = a.tickets + static_cast<long long>(s) * gridDim.y + blockIdx.y;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0)
+            __syncthreads();                        // every thread's part is written
+            if (tid == 0) {
+                __threadfence();
                 s_last = atomicAdd(ticket, 1) == parts - 1;
+                __threadfence();
+            }
             __syncthreads();
             if (s_last) {
-                __threadfence();
-                const float *base = a.part + static_cast<long long>(blockIdx.y) * gridDim.x * 2 *
-                                                 kHeads * (D + 2);
                 // run xa holds it in its second slot if it has pages of an earlier one
+                const float *base = a.part + static_cast<long long>(blockIdx.y) * gridDim.x * 2 * PART;
                 const int late = seg.at > xa * run;
-                auto slot = [&](int x, int g) {
-                    return base + (static_cast<long long>(xa + x) * 2 + (x == 0 ? late : 0)) *
-                                      kHeads * (D + 2) + g * (D + 2);
-                };
-                // weights of the parts, a warp per head: s_o[g][x], free by now
-                for (int g = warp; g < G; g += kConsumers) {
-                    float *w = s_o + g * parts;
-                    float mt = -INFINITY, l = 0.f;
-                    bool any_bad = false;
-                    for (int x = lane; x < parts; x += 32) {
-                        const float m = __ldcg(slot(x, g));
-                        w[x] = m;
-                        mt = fmaxf(mt, m);
-                    }
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1)
-                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-                    for (int x = lane; x < parts; x += 32) {
-                        const float lx = __ldcg(slot(x, g) + 1);
-                        const float f = w[x] == -INFINITY ? 0.f : ex2_approx(w[x] - mt);
-                        any_bad |= lx < 0.f;
-                        l = fmaf(lx, f, l);
-                        w[x] = f;
-                    }
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1)
-                        l += __shfl_xor_sync(0xffffffffu, l, off);
-                    any_bad = __any_sync(0xffffffffu, any_bad);
-                    if (lane == 0) {
-                        s_m[0][g] = mt;
-                        s_l[0][g] = any_bad ? -1.f : l;
-                    }
-                }
-                __syncthreads();
-                for (int e = 2 * tid; e < G * D; e += 2 * kDecThreads) {
+                for (int e = 4 * tid; e < G * D; e += 4 * kDecThreads) {
                     const int g = e / D, d = e % D;
-                    const float l = s_l[0][g];
-                    if (l < 0.f)
-                        continue;
-                    const float *w = s_o + g * parts;
-                    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 8
-                    for (int x = 0; x < parts; ++x) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(slot(x, g) + 2 + d));
-                        acc.x = fmaf(v.x, w[x], acc.x);
-                        acc.y = fmaf(v.y, w[x], acc.y);
+                    float mt = -INFINITY, l = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    bool any_bad = false;
+                    constexpr int B = 8;            // parts whose loads are in flight together
+                    for (int x0 = 0; x0 < parts; x0 += B) {
+                        float4 v[B];
+                        float2 ml[B];
+#pragma unroll
+                        for (int x = 0; x < B; ++x) {
+                            ml[x] = make_float2(-INFINITY, 0.f);
+                            v[x] = acc;
+                            if (x0 + x < parts) {
+                                const float *q = base + (static_cast<long long>(xa + x0 + x) * 2 +
+                                                         (x0 + x == 0 ? late : 0)) * PART + g * (D + 4);
+                                v[x] = __ldcg(reinterpret_cast<const float4 *>(q + d));
+                                ml[x] = __ldcg(reinterpret_cast<const float2 *>(q + D));
+                            }
+                        }
+                        float mn = mt;
+#pragma unroll
+                        for (int x = 0; x < B; ++x)
+                            mn = fmaxf(mn, ml[x].x);
+                        const float keep = mt == -INFINITY ? 0.f : ex2_approx(mt - mn);
+                        mt = mn;
+                        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+                        l *= keep;
+#pragma unroll
+                        for (int x = 0; x < B; ++x) {
+                            const float f = ml[x].x == -INFINITY ? 0.f : ex2_approx(ml[x].x - mn);
+                            any_bad |= ml[x].y < 0.f;
+                            acc.x = fmaf(v[x].x, f, acc.x);
+                            acc.y = fmaf(v[x].y, f, acc.y);
+                            acc.z = fmaf(v[x].z, f, acc.z);
+                            acc.w = fmaf(v[x].w, f, acc.w);
+                            l = fmaf(ml[x].y, f, l);
+                        }
                     }
-                    const long long row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
-                    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) =
-                        pack_bf16x2(acc.x / l * a.descale_v, acc.y / l * a.descale_v);
-                    if (d == 0 && a.lse)
-                        a.lse[row] = (s_m[0][g] - kPShift + __log2f(l)) * kLn2;
+                    if (!any_bad)
+                        finish(g, d, acc, mt, l);
                 }
                 if (tid == 0)
                     *ticket = 0;                    // ready for the next call
@@ -1011,8 +1001,8 @@ cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
                             kMinRun - 1) / kMinRun;
     parts = parts < most ? parts : most;
     parts = parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts);
-    kv4_decode_kernel<D><<<dim3(static_cast<int>(parts), rows), kDecThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kv4_decode_kernel<D>, dim3(static_cast<int>(parts), rows), kDecThreads, smem,
+                            stream, a);
 }
 
 int move_grid(int total, int sm_count)
@@ -1034,12 +1024,11 @@ cudaError_t launch_kv4_write(int head_dim, const Kv4MoveArgs &a, int sm_count, c
 {
     const int grid = move_grid(a.total, sm_count);
     switch (head_dim) {
-    case 64: kv4_write_kernel<64><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
-    case 128: kv4_write_kernel<128><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
-    case 256: kv4_write_kernel<256><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    case 64: return launch_dependent(kv4_write_kernel<64>, dim3(grid), kMoveWarps * 32, 0, stream, a);
+    case 128: return launch_dependent(kv4_write_kernel<128>, dim3(grid), kMoveWarps * 32, 0, stream, a);
+    case 256: return launch_dependent(kv4_write_kernel<256>, dim3(grid), kMoveWarps * 32, 0, stream, a);
     default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_gather(int head_dim, const Kv4MoveArgs &a, int sm_count,
@@ -1047,12 +1036,11 @@ cudaError_t launch_kv4_gather(int head_dim, const Kv4MoveArgs &a, int sm_count,
 {
     const int grid = move_grid(a.total, sm_count);
     switch (head_dim) {
-    case 64: kv4_gather_kernel<64><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
-    case 128: kv4_gather_kernel<128><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
-    case 256: kv4_gather_kernel<256><<<grid, kMoveWarps * 32, 0, stream>>>(a); break;
+    case 64: return launch_dependent(kv4_gather_kernel<64>, dim3(grid), kMoveWarps * 32, 0, stream, a);
+    case 128: return launch_dependent(kv4_gather_kernel<128>, dim3(grid), kMoveWarps * 32, 0, stream, a);
+    case 256: return launch_dependent(kv4_gather_kernel<256>, dim3(grid), kMoveWarps * 32, 0, stream, a);
     default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim)
@@ -1063,7 +1051,7 @@ size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_head
     const long long all = rows > kMaxCtas ? rows : kMaxCtas;
     const size_t runs = all < static_cast<long long>(rows) * kMaxParts
                             ? static_cast<size_t>(all) : static_cast<size_t>(rows) * kMaxParts;
-    return ticket_bytes(num_seqs, rows) + runs * 2 * kHeads * (head_dim + 2) * sizeof(float);
+    return ticket_bytes(num_seqs, rows) + runs * 2 * kHeads * (head_dim + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, int sm_count,

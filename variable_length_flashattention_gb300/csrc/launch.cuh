@@ -1,0 +1,36 @@
+// launch.cuh -- launches that may start while the kernel before them in the
+// stream is still running (programmatic stream serialisation).
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace vfa {
+
+// First statement of a kernel launched this way: the next kernel of the
+// stream may be scheduled from here on, and nothing after this line runs
+// before the kernels ahead of this one have completed.
+__device__ __forceinline__ void grid_dependency()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace vfa
