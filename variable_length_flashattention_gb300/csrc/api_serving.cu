@@ -250,7 +250,7 @@ size_t vfa_qk_norm_rope_bwd_workspace_bytes(int head_dim)
 {
     if (!supported_head_dim(head_dim))
         return 0;
-    return static_cast<size_t>(vfa::kRopeMaxCtas) * head_dim * sizeof(float);
+    return static_cast<size_t>(vfa::kRopeMaxCtas) * 2 * head_dim * sizeof(float);
 }
 
 vfa_status vfa_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_stride, int64_t k_stride,

@@ -207,12 +207,12 @@ struct RopeArgs {
     int heads[2];
     const int32_t *positions;               // [num_axes, tokens]
     const uint64_t *table;                  // [half][2]: turns per position * 2^64, axis
-    float *partial;                         // backward workspace: [CTAs, D]
+    float *partial;                         // backward workspace: [CTAs, 2, D]
     int tokens, num_axes, half;             // half: rotated dimensions / 2
     int interleaved;
     float eps;
     int segments;                           // set by the launcher: shares a token's heads take
-    int ctas[2];                            // set by the launcher (backward)
+    int ctas;                               // set by the launcher (backward)
 };
 
 // Most CTAs the backward launches: the partial sums of dw in its workspace.
@@ -287,6 +287,7 @@ struct PageArgs {
     int32_t *status;                        // nullable
     int32_t *ws;                            // workspace
     int num_blocks, num_seqs, capacity, block_size, n;
+    int copies;                             // set by the launcher: a copy kernel follows
 };
 
 size_t page_workspace_bytes(int num_blocks, int num_seqs, int num_forks);

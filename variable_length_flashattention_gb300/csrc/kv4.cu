@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_write_kernel(const Kv4Mov
     constexpr int GR = D / 16, HPW = 32 / GR;
     const int lane = threadIdx.x & 31;
     const int g = lane % GR;
-    grid_dependency();
+    grid_wait();
     if (blockIdx.x == 0)
         check_cu(a);
     const int nwarps = gridDim.x * kMoveWarps;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
     constexpr int GR = D / 16, HPW = 32 / GR;
     const int lane = threadIdx.x & 31;
     const int g = lane % GR;
-    grid_dependency();
+    grid_wait();
     if (blockIdx.x == 0)
         check_cu(a);
     const int nwarps = gridDim.x * kMoveWarps;
@@ -374,9 +374,27 @@ struct DecCfg {
     static constexpr int KW = D / 32;               // code words of one token per lane
 };
 
+// 16 bytes from src + OFF to shared memory at dst + OFF.
+template <int OFF>
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0 + %2], [%1 + %2], 16;" ::"r"(dst), "l"(src),
+                 "n"(OFF)
+                 : "memory");
+}
+
+// The 16-byte pieces of two pages in a row, 32 per turn and one per lane:
+// those of the first at p0, then those of the second at p1 (less the first
+// one's size), `mid` the lane's choice in the turn that has both.
+template <int PIECES, int K = 0>
+__device__ __forceinline__ void copy_pair(uint32_t dst, const uint8_t *p0, const uint8_t *mid,
+                                          const uint8_t *p1, int lane)
+{
+    if constexpr (K < 2 * PIECES) {
+        if (K + 32 <= 2 * PIECES || K + lane < 2 * PIECES)
+            copy16_async<K * 16>(dst, K + 32 <= PIECES ? p0 : K >= PIECES ? p1 : mid);
+        copy_pair<PIECES, K + 32>(dst, p0, mid, p1, lane);
+    }
 }
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -462,7 +480,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     __shared__ int s_scan[kDecThreads / 32];
     __shared__ int s_first, s_first_unit, s_last;
 
-    grid_dependency();
+    grid_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.num_q_heads / a.num_kv_heads;
     const int chunks = (group + kHeads - 1) / kHeads;
@@ -522,8 +540,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
 
     // ---------------------------------------------------- copies
     // Fills of this warp's stages, WS pairs ahead: the pair at page `ahead` of
-    // segment `fill` next, its page ids already loaded.  Every turn commits one
-    // group of copies, also where there is nothing left to copy.
+    // segment `fill` next.  The ids of the warp's next 16 pairs are loaded
+    // together, lane l page l % 2 of pair l / 2.  Every turn commits one group
+    // of copies, also where there is nothing left to copy.
     RunCursor fill;
     fill.s = s_first;
     fill.at = s_first_unit;
@@ -531,8 +550,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     if (!fill.enter(a, u0, u1))
         return;                                     // (the whole CTA) no page in this run
     RunCursor seg = fill;
-    int ahead = fill.first(warp), id0 = 0, id1 = 0;
-    const int32_t *row = a.tables + static_cast<long long>(fill.s) * a.capacity;
+    int ahead = fill.first(warp), ids = 0, id_lane = 0;
     uint32_t bad_stages = 0;
     bool more = true;
     auto load_ids = [&]() {
@@ -541,13 +559,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
             if (!more)
                 return;
             ahead = fill.first(warp);
-            row = a.tables + static_cast<long long>(fill.s) * a.capacity;
         }
-        if (fill.tokens > 0) {                      // an empty sequence has no page
-            id0 = __ldg(row + ahead);
-            if (ahead + 1 < fill.j1)
-                id1 = __ldg(row + ahead + 1);
-        }
+        const int j = ahead + (lane >> 1) * (2 * kConsumers) + (lane & 1);
+        ids = j < fill.j1 && fill.tokens > 0        // an empty sequence has no page
+                  ? __ldg(a.tables + static_cast<long long>(fill.s) * a.capacity + j)
+                  : -1;
+        id_lane = 0;
     };
     const uint32_t my_ring = smem_u32(dsm) + warp * C::WS * C::STAGE + lane * 16;
     const uint8_t *my_pool = pool + lane * 16;
@@ -555,6 +572,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
         if (more) {
             constexpr int PIECES = C::PAGE / 16;    // 16-byte pieces of a page
             const unsigned blocks = static_cast<unsigned>(a.num_blocks);
+            const int id0 = __shfl_sync(0xffffffffu, ids, id_lane);
+            const int id1 = __shfl_sync(0xffffffffu, ids, id_lane + 1);
             const bool two = ahead + 1 < fill.j1;
             // (an empty sequence's one page is not there to be copied)
             const bool bad = fill.tokens > 0 && (static_cast<unsigned>(id0) >= blocks ||
@@ -562,25 +581,24 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
             const uint8_t *p0 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * page_bytes;
             const uint32_t dst = my_ring + ws * C::STAGE;
             if (two && !bad) {
-                // the pair's pieces in order, 32 per turn: those of page 0, then page 1
                 const uint8_t *p1 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id1)) * page_bytes -
                                     C::PAGE;
-                const uint8_t *mid = lane >= PIECES % 32 ? p1 : p0;     // the turn with both
-#pragma unroll
-                for (int k = 0; k < 2 * PIECES; k += 32)
-                    if (k + 32 <= 2 * PIECES || k + lane < 2 * PIECES)
-                        copy16_async(dst + k * 16, (k + 32 <= PIECES ? p0 : k >= PIECES ? p1 : mid) + k * 16);
+                copy_pair<PIECES>(dst, p0, lane >= PIECES % 32 ? p1 : p0, p1, lane);
             } else if (fill.tokens > 0 && !bad) {
 #pragma unroll 1
                 for (int k = 0; k < PIECES; k += 32)
                     if (k + lane < PIECES)
-                        copy16_async(dst + k * 16, p0 + k * 16);
+                        copy16_async<0>(dst + k * 16, p0 + k * 16);
             }
-            bad_stages = (bad_stages & ~(1u << ws)) | (static_cast<uint32_t>(bad) << ws);
-            if (bad && lane == 0)
-                record(a.status, VFA_ERR_BAD_BLOCK);
+            if (bad) {
+                bad_stages |= 1u << ws;
+                if (lane == 0)
+                    record(a.status, VFA_ERR_BAD_BLOCK);
+            }
             ahead += 2 * kConsumers;
-            load_ids();
+            id_lane += 2;
+            if (ahead >= fill.j1 || id_lane == 32)
+                load_ids();
         }
         copy_commit();
     };
@@ -654,10 +672,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
         for (int j = seg.first(warp); j < j1; j += 2 * kConsumers) {
             copy_wait<C::WS - 1>();
             __syncwarp();                           // every lane's copies are there for every lane
-            const uint32_t pair = my_ring - lane * 16 + ws * C::STAGE;
+            const uint8_t *pair = dsm + (warp * C::WS + ws) * C::STAGE;
             // tokens of the two pages that count, those of the run's pages
             const int valid = min(n - j * kPage, j + 1 < j1 ? 2 * kPage : kPage);
-            bad |= (bad_stages >> ws) & 1u;
+            if (bad_stages) {
+                bad |= (bad_stages >> ws) & 1u;
+                bad_stages &= ~(1u << ws);
+            }
             if (valid > 0 && !bad) {
                 // S = K Q^T: two pages, two independent accumulators
                 float sacc[2][4];
@@ -670,15 +691,15 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int tok = r + 8 * half;
-                        const uint32_t row = pair + c * C::PAGE + tok * (D / 2);
+                        const uint8_t *row = pair + c * C::PAGE + tok * (D / 2);
                         if constexpr (D == 64) {
-                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                         : "=r"(kw[c][half][0]), "=r"(kw[c][half][1])
-                                         : "r"(row + t4 * 8));
+                            const uint2 v = *reinterpret_cast<const uint2 *>(row + t4 * 8);
+                            kw[c][half][0] = v.x;
+                            kw[c][half][1] = v.y;
                         } else {
 #pragma unroll
                             for (int p = 0; p < KW / 4; ++p) {
-                                const uint4 v = ld_shared_v4(row + p * 64 + t4 * 16);
+                                const uint4 v = *reinterpret_cast<const uint4 *>(row + p * 64 + t4 * 16);
                                 kw[c][half][4 * p] = v.x;
                                 kw[c][half][4 * p + 1] = v.y;
                                 kw[c][half][4 * p + 2] = v.z;
@@ -686,8 +707,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                             }
                         }
                         // the token's scales for this lane's dims, in order
-                        const uint8_t *sp = dsm + (warp * C::WS + ws) * C::STAGE + c * C::PAGE +
-                                            16 * D + tok * (D / 16);
+                        const uint8_t *sp = pair + c * C::PAGE + 16 * D + tok * (D / 16);
                         if constexpr (D == 64) {
                             ks[c][half] = sp[t4] * 0x101u;
                         } else if constexpr (D == 128) {
@@ -774,14 +794,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                 // O^T += V^T P
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint32_t page = pair + c * C::PAGE;
+                    const uint8_t *page = pair + c * C::PAGE;
 #pragma unroll
                     for (int p = 0; p < (D == 256 ? 2 : 1); ++p) {
                         const int grp = D == 64 ? r >> 1 : r + 8 * p;
-                        uint32_t vs;
-                        asm volatile("ld.shared.b32 %0, [%1];"
-                                     : "=r"(vs)
-                                     : "r"(page + 17 * D + (grp * 4 + t4) * 4));
+                        uint32_t vs = *reinterpret_cast<const uint32_t *>(page + 17 * D + (grp * 4 + t4) * 4);
                         if (valid < 2 * kPage) {
                             // unused rows may hold any bytes: their scales count as zero
                             const int left = valid - c * kPage;
@@ -795,11 +812,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             if constexpr (D == 64) {
-                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                             : "=r"(even[half][0]), "=r"(odd[half][0])
-                                             : "r"(page + 8 * D + half * 256 + lane * 8));
+                                const uint2 v =
+                                    *reinterpret_cast<const uint2 *>(page + 8 * D + half * 256 + lane * 8);
+                                even[half][0] = v.x;
+                                odd[half][0] = v.y;
                             } else {
-                                const uint4 v = ld_shared_v4(
+                                const uint4 v = *reinterpret_cast<const uint4 *>(
                                     page + 8 * D + (half * (D / 128) + p) * 512 + lane * 16);
                                 even[half][0] = v.x;
                                 even[half][1] = v.y;

@@ -6,13 +6,20 @@
 
 namespace vfa {
 
-// First statement of a kernel launched this way: the next kernel of the
-// stream may be scheduled from here on, and nothing after this line runs
-// before the kernels ahead of this one have completed.
-__device__ __forceinline__ void grid_dependency()
+// First statement of a kernel launched this way: nothing after it runs before
+// the kernels ahead in the stream have completed.
+__device__ __forceinline__ void grid_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The next kernel of the stream may be scheduled from here on.  Only for a
+// kernel whose successor is known to begin with grid_wait(): the last kernel
+// of a call must not say this, since a decode step behind it reads its pools,
+// tables and queries before it waits.
+__device__ __forceinline__ void grid_release()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <typename... KArgs, typename... Args>

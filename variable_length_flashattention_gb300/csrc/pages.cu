@@ -6,7 +6,9 @@
 // New pages are the free ones with the lowest ids, so every result is a
 // function of the inputs alone, whatever order the threads run in.
 //
-// Extend, fork and compact need ranks among the free (or used) pages:
+// Extend, fork and compact need ranks among the free (or used) pages.  A pool
+// of at most 32768 pages fits one CTA, a 32-page word of its use bits per
+// thread: one kernel does all but the page data.  Larger pools take three:
 //   count    one CTA per chunk of 4096 pages counts its used pages;
 //   plan     one CTA checks the request and gives every new page its rank
 //            (extend, fork); it is the only step that can refuse, before
@@ -18,9 +20,10 @@
 // Consecutive steps are launched with programmatic serialisation.
 //
 // Bound: HBM for the copied pages (2 bytes moved per byte), launch latency
-// for the rest.
+// for the rest: with 1024 pages the one-CTA form takes an extension from three
+// launches (9.9 us) to one, a fork from four to two.
 #include "internal.h"
-#include "ptx.cuh"
+#include "launch.cuh"
 
 namespace vfa {
 
@@ -30,6 +33,8 @@ constexpr int kChunk = 4096;
 constexpr int kPlanThreads = 1024;
 constexpr int kPer = kChunk / kPlanThreads;
 constexpr int kPiece = 4096;            // bytes a warp copies per turn
+constexpr int kSmallPool = 32 * kPlanThreads;   // pages one CTA ranks
+constexpr int kSmallRows = 4096;        // rows (ranks) whose places one CTA keeps in shared memory
 
 enum { H_N = 0, H_USED = 1 };
 
@@ -65,12 +70,6 @@ size_t carve(int32_t *ws, int num_blocks, int num_seqs, int forks, PageWs *w)
     if (w)
         *w = r;
     return at * sizeof(int32_t);
-}
-
-__device__ __forceinline__ void pdl_start()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ void record(int32_t *status, int code)
@@ -118,7 +117,8 @@ __device__ __forceinline__ int used_before(const int32_t *chunk, int n, int *s_w
 __global__ void __launch_bounds__(kPlanThreads) count_kernel(const int32_t *refs, int num_blocks,
                                                              int32_t *chunk)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();
+    grid_release();
     __shared__ int s_warp[kPlanThreads / 32];
     int v = 0, total;
 #pragma unroll
@@ -133,12 +133,11 @@ __global__ void __launch_bounds__(kPlanThreads) count_kernel(const int32_t *refs
 
 // ------------------------------------------------------------ extend, fork
 
-__global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PageArgs a, const PageWs w)
+// The pages every row needs (offs[s]: before row s) and the verdict; token
+// counts grow if there are enough.  Returns the pages to assign, 0 if refused.
+__device__ __forceinline__ int plan_extend(const PageArgs &a, int used, int32_t *offs, int *s_warp)
 {
-    pdl_start();
-    __shared__ int s_warp[kPlanThreads / 32];
     const long long room = static_cast<long long>(a.capacity) * a.block_size;
-    const int used = used_before(w.chunk, chunks_of(a.num_blocks), s_warp);
     long long carry = 0;
     bool bad = false;
     for (int s0 = 0; s0 < a.num_seqs; s0 += kPlanThreads) {
@@ -160,29 +159,58 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PageArg
         hi = block_scan(need >> 16, &th, s_warp);
         const long long at = carry + lo + (static_cast<long long>(hi) << 16);
         if (s < a.num_seqs)
-            w.offs[s] = at > a.num_blocks ? a.num_blocks : static_cast<int>(at);
+            offs[s] = at > a.num_blocks ? a.num_blocks : static_cast<int>(at);
         carry += tl + (static_cast<long long>(th) << 16);
     }
     bad = __syncthreads_or(bad);
     const bool room_ok = carry <= a.num_blocks - used;
     const bool ok = !bad && room_ok;
     if (threadIdx.x == 0) {
-        w.head[H_N] = ok ? static_cast<int>(carry) : 0;
-        w.offs[a.num_seqs] = ok ? static_cast<int>(carry) : 0;
+        offs[a.num_seqs] = ok ? static_cast<int>(carry) : 0;
         if (!ok)
             record(a.status, bad ? VFA_ERR_BAD_BLOCK : VFA_ERR_NO_PAGES);
     }
     if (ok)
         for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads)
             a.counts[s] += a.add[s];
+    __syncthreads();
+    return ok ? static_cast<int>(carry) : 0;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs a, const PageWs w)
+// Page `id` becomes the r-th new page.
+__device__ __forceinline__ void place_extend(const PageArgs &a, const int32_t *offs, int r, int id)
 {
-    pdl_start();
+    int lo = 0, hi = a.num_seqs;                    // the row s with offs[s] <= r < offs[s + 1]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (offs[mid] <= r)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int pages = static_cast<int>((static_cast<long long>(a.counts[lo]) + a.block_size - 1) /
+                                       a.block_size);
+    a.tables[static_cast<long long>(lo) * a.capacity + pages - offs[lo + 1] + r] = id;
+    a.refs[id] = 1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PageArgs a, const PageWs w)
+{
+    grid_wait();
+    grid_release();
     __shared__ int s_warp[kPlanThreads / 32];
-    const long long room = static_cast<long long>(a.capacity) * a.block_size;
     const int used = used_before(w.chunk, chunks_of(a.num_blocks), s_warp);
+    const int n = plan_extend(a, used, w.offs, s_warp);
+    if (threadIdx.x == 0)
+        w.head[H_N] = n;
+}
+
+// The entries' plan (parent -1: nothing to do), the entry and the source page
+// of every copy in order, and the verdict; children's token counts are set if
+// there are enough pages.  Returns the copies, 0 if refused.
+__device__ __forceinline__ int plan_fork(const PageArgs &a, const PageWs &w, int used, int *s_warp)
+{
+    const long long room = static_cast<long long>(a.capacity) * a.block_size;
     bool bad = false;
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
         const int c = a.children[i];
@@ -238,6 +266,45 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
         else if (w.plan[4 * i] >= 0)
             a.counts[w.plan[4 * i + 1]] = w.plan[4 * i + 2];
     }
+    __syncthreads();
+    return ok ? carry : 0;
+}
+
+// Page `id` becomes the target of the r-th copy.
+__device__ __forceinline__ void place_fork(const PageArgs &a, const PageWs &w, int r, int id)
+{
+    const int i = w.offs[r];
+    w.dst[r] = id;
+    a.tables[static_cast<long long>(w.plan[4 * i + 1]) * a.capacity +
+             w.plan[4 * i + 2] / a.block_size] = id;
+    a.refs[id] = 1;
+}
+
+// The full pages of entry i's parent are shared with its child.
+__device__ __forceinline__ void share_pages(const PageArgs &a, const PageWs &w, int i)
+{
+    const int p = w.plan[4 * i];
+    if (p < 0)
+        return;
+    const int full = w.plan[4 * i + 2] / a.block_size;
+    const int32_t *from = a.tables + static_cast<long long>(p) * a.capacity;
+    int32_t *to = a.tables + static_cast<long long>(w.plan[4 * i + 1]) * a.capacity;
+    for (int j = threadIdx.x; j < full; j += blockDim.x) {
+        const int id = from[j];
+        to[j] = id;
+        if (id < 0 || id >= a.num_blocks || a.refs[id] <= 0)
+            record(a.status, VFA_ERR_BAD_BLOCK);        // not a page in use: not counted
+        else
+            atomicAdd(&a.refs[id], 1);
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs a, const PageWs w)
+{
+    grid_wait();
+    grid_release();
+    __shared__ int s_warp[kPlanThreads / 32];
+    plan_fork(a, w, used_before(w.chunk, chunks_of(a.num_blocks), s_warp), s_warp);
 }
 
 // CTAs [0, chunks): the chunk's free pages of rank < N go to their rows.
@@ -245,25 +312,13 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) assign_kernel(const PageArgs a, const PageWs w)
 {
-    pdl_start();
+    grid_wait();
+    if (FORK && a.copies)
+        grid_release();
     __shared__ int s_warp[kPlanThreads / 32];
     const int chunks = chunks_of(a.num_blocks);
     if (FORK && static_cast<int>(blockIdx.x) >= chunks) {
-        const int i = blockIdx.x - chunks;
-        const int p = w.plan[4 * i];
-        if (p < 0)
-            return;
-        const int full = w.plan[4 * i + 2] / a.block_size;
-        const int32_t *from = a.tables + static_cast<long long>(p) * a.capacity;
-        int32_t *to = a.tables + static_cast<long long>(w.plan[4 * i + 1]) * a.capacity;
-        for (int j = threadIdx.x; j < full; j += kPlanThreads) {
-            const int id = from[j];
-            to[j] = id;
-            if (id < 0 || id >= a.num_blocks || a.refs[id] <= 0)
-                record(a.status, VFA_ERR_BAD_BLOCK);        // not a page in use: not counted
-            else
-                atomicAdd(&a.refs[id], 1);
-        }
+        share_pages(a, w, blockIdx.x - chunks);
         return;
     }
     const int n = w.head[H_N];
@@ -287,35 +342,82 @@ __global__ void __launch_bounds__(kPlanThreads) assign_kernel(const PageArgs a, 
         if (!is_free[k])
             continue;
         if (r < n) {
-            const int id = id0 + k;
-            a.refs[id] = 1;
-            if (FORK) {
-                const int i = w.offs[r];
-                w.dst[r] = id;
-                a.tables[static_cast<long long>(w.plan[4 * i + 1]) * a.capacity +
-                         w.plan[4 * i + 2] / a.block_size] = id;
-            } else {
-                int lo = 0, hi = a.num_seqs;         // the row s with offs[s] <= r < offs[s + 1]
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    if (w.offs[mid] <= r)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
-                const int pages = static_cast<int>(
-                    (static_cast<long long>(a.counts[lo]) + a.block_size - 1) / a.block_size);
-                a.tables[static_cast<long long>(lo) * a.capacity + pages - w.offs[lo + 1] + r] = id;
-            }
+            if (FORK)
+                place_fork(a, w, r, id0 + k);
+            else
+                place_extend(a, w.offs, r, id0 + k);
         }
         ++r;
     }
+}
+
+// ------------------------------------------------------------ small pools
+//
+// Thread t's word of the pool's use bits (pages [32 t, 32 t + 32), past the end
+// counted as used) and the number of used pages.
+__device__ __forceinline__ uint32_t use_word(const PageArgs &a, uint32_t *s_bits, int *used, int *s_warp)
+{
+    const int lane = threadIdx.x & 31;
+    const int words = (a.num_blocks + 31) / 32;
+    for (int w = threadIdx.x >> 5; w < words; w += kPlanThreads / 32) {
+        const int id = w * 32 + lane;
+        const uint32_t bits = __ballot_sync(0xffffffffu, id >= a.num_blocks || a.refs[id] > 0);
+        if (lane == 0)
+            s_bits[w] = bits;
+    }
+    __syncthreads();
+    const uint32_t word = static_cast<int>(threadIdx.x) < words ? s_bits[threadIdx.x] : 0xffffffffu;
+    int free;
+    block_scan(__popc(~word), &free, s_warp);
+    *used = a.num_blocks - free;
+    return word;
+}
+
+// list[r] = the r-th free page, r < n.
+__device__ __forceinline__ void list_free(uint32_t word, int n, int32_t *list, int *s_warp)
+{
+    int total;
+    int r = block_scan(__popc(~word), &total, s_warp);
+    for (uint32_t left = ~word; left && r < n; left &= left - 1, ++r)
+        list[r] = threadIdx.x * 32 + __ffs(left) - 1;
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPlanThreads) extend_small_kernel(const PageArgs a, const PageWs w)
+{
+    grid_wait();
+    __shared__ uint32_t s_bits[kPlanThreads];
+    __shared__ int s_warp[kPlanThreads / 32];
+    __shared__ int32_t s_offs[kSmallRows + 1], s_list[kSmallRows];
+    int used;
+    const uint32_t word = use_word(a, s_bits, &used, s_warp);
+    int32_t *offs = a.num_seqs <= kSmallRows ? s_offs : w.offs;
+    const int n = plan_extend(a, used, offs, s_warp);
+    int32_t *list = n <= kSmallRows ? s_list : w.dst;
+    list_free(word, n, list, s_warp);
+    for (int r = threadIdx.x; r < n; r += kPlanThreads)
+        place_extend(a, offs, r, list[r]);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PageArgs a, const PageWs w)
+{
+    grid_wait();
+    grid_release();
+    __shared__ uint32_t s_bits[kPlanThreads];
+    __shared__ int s_warp[kPlanThreads / 32];
+    int used;
+    const uint32_t word = use_word(a, s_bits, &used, s_warp);
+    const int n = plan_fork(a, w, used, s_warp);
+    list_free(word, n, w.dst, s_warp);
+    for (int r = threadIdx.x; r < n; r += kPlanThreads)
+        place_fork(a, w, r, w.dst[r]);
 }
 
 // ------------------------------------------------------------ free
 
 __global__ void __launch_bounds__(256) free_kernel(const PageArgs a)
 {
+    grid_wait();
     __shared__ int s_n;
     const int s = a.seqs[blockIdx.x];
     if (s < 0)
@@ -355,7 +457,8 @@ __global__ void __launch_bounds__(256) free_kernel(const PageArgs a)
 
 __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const PageArgs a, const PageWs w)
 {
-    pdl_start();
+    grid_wait();
+    grid_release();
     __shared__ int s_warp[kPlanThreads / 32];
     const int chunks = chunks_of(a.num_blocks);
     const int U = used_before(w.chunk, chunks, s_warp);
@@ -396,6 +499,43 @@ __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const PageAr
         before += is_used[k];
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
+        w.head[H_N] = U - below;
+        w.head[H_USED] = U;
+        *a.num_used = U;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PageArgs a, const PageWs w)
+{
+    grid_wait();
+    grid_release();
+    __shared__ uint32_t s_bits[kPlanThreads];
+    __shared__ int s_warp[kPlanThreads / 32];
+    int U, total, below;
+    const uint32_t word = use_word(a, s_bits, &U, s_warp);
+    const int id0 = threadIdx.x * 32;
+    // pages past the pool's end have set bits, but no page of the pool is above them
+    int before = block_scan(__popc(word), &total, s_warp);
+    {
+        const int part = U - id0;                   // pages of this word below U
+        const uint32_t mask = part <= 0 ? 0u : part >= 32 ? 0xffffffffu : (1u << part) - 1;
+        block_scan(__popc(word & mask), &below, s_warp);
+    }
+    for (int k = 0; k < 32 && id0 + k < a.num_blocks; ++k) {
+        const int id = id0 + k;
+        const bool is_used = word >> k & 1;
+        int r = -1;
+        if (is_used && id >= U) {
+            r = before - below;
+            w.src[r] = id;
+        } else if (!is_used && id < U) {
+            r = id - before;
+            w.dst[r] = id;
+        }
+        w.rank[id] = r;
+        before += is_used;
+    }
+    if (threadIdx.x == 0) {
         w.head[H_N] = U - below;
         w.head[H_USED] = U;
         *a.num_used = U;
@@ -445,18 +585,25 @@ __device__ __forceinline__ void compact_apply(const PageArgs &a, const PageWs &w
 
 // ------------------------------------------------------------ copy
 //
-// blockIdx.y < pools: warps copy pieces of that pool's pages; COMPACT:
-// blockIdx.y == pools rewrites tables and counts meanwhile.
-template <bool COMPACT>
+// blockIdx.y < pools: warps copy pieces of that pool's pages.  blockIdx.y ==
+// pools, meanwhile: COMPACT rewrites tables and counts, SHARE shares a fork's
+// full pages.
+enum { COPY_ONLY, COPY_COMPACT, COPY_SHARE };
+
+template <int ROLE>
 __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ PagePools p,
                                                    const int32_t *src, const int32_t *dst,
                                                    const int32_t *n_dev, int n_host, int num_blocks,
                                                    int32_t *status, const PageArgs a,
                                                    const PageWs w)
 {
-    pdl_start();
-    if (COMPACT && static_cast<int>(blockIdx.y) == p.n) {
-        compact_apply(a, w, blockIdx.x, gridDim.x);
+    grid_wait();
+    if (ROLE != COPY_ONLY && static_cast<int>(blockIdx.y) == p.n) {
+        if (ROLE == COPY_COMPACT)
+            compact_apply(a, w, blockIdx.x, gridDim.x);
+        else
+            for (int i = blockIdx.x; i < a.n; i += gridDim.x)
+                share_pages(a, w, i);
         return;
     }
     const int n = n_dev ? *n_dev : n_host;
@@ -495,23 +642,6 @@ __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ PageP
     }
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, int threads, cudaStream_t stream,
-                         bool dependent, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // CTAs per pool: about eight CTAs of eight warps on every SM in all, and no
 // more warps than `max_pairs` pages have pieces.
 int copy_ctas(const PagePools &p, long long max_pairs, int sm_count)
@@ -538,12 +668,14 @@ cudaError_t launch_pages_extend(const PageArgs &a, cudaStream_t stream)
 {
     PageWs w;
     carve(a.ws, a.num_blocks, a.num_seqs, 0, &w);
+    if (a.num_blocks <= kSmallPool)
+        return launch_dependent(extend_small_kernel, dim3(1), kPlanThreads, 0, stream, a, w);
     const int chunks = chunks_of(a.num_blocks);
     cudaError_t e;
-    if ((e = launch_after(count_kernel, chunks, kPlanThreads, stream, false, a.refs, a.num_blocks,
-                          w.chunk)) ||
-        (e = launch_after(extend_plan_kernel, 1, kPlanThreads, stream, true, a, w)) ||
-        (e = launch_after(assign_kernel<false>, chunks, kPlanThreads, stream, true, a, w)))
+    if ((e = launch_dependent(count_kernel, dim3(chunks), kPlanThreads, 0, stream, a.refs,
+                              a.num_blocks, w.chunk)) ||
+        (e = launch_dependent(extend_plan_kernel, dim3(1), kPlanThreads, 0, stream, a, w)) ||
+        (e = launch_dependent(assign_kernel<false>, dim3(chunks), kPlanThreads, 0, stream, a, w)))
         return e;
     return cudaSuccess;
 }
@@ -553,23 +685,32 @@ cudaError_t launch_pages_fork(const PageArgs &a, const PagePools &p, int sm_coun
 {
     PageWs w;
     carve(a.ws, a.num_blocks, a.num_seqs, a.n, &w);
-    const int chunks = chunks_of(a.num_blocks);
     cudaError_t e;
-    if ((e = launch_after(count_kernel, chunks, kPlanThreads, stream, false, a.refs, a.num_blocks,
-                          w.chunk)) ||
-        (e = launch_after(fork_plan_kernel, 1, kPlanThreads, stream, true, a, w)) ||
-        (e = launch_after(assign_kernel<true>, chunks + a.n, kPlanThreads, stream, true, a, w)))
+    if (a.num_blocks <= kSmallPool) {
+        if ((e = launch_dependent(fork_small_kernel, dim3(1), kPlanThreads, 0, stream, a, w)))
+            return e;
+        const int ctas = copy_ctas(p, a.n, sm_count);
+        return launch_dependent(copy_kernel<COPY_SHARE>, dim3(ctas > a.n ? ctas : a.n, p.n + 1), 256, 0,
+                                stream, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a,
+                                w);
+    }
+    const int chunks = chunks_of(a.num_blocks);
+    PageArgs b = a;
+    b.copies = p.n > 0;
+    if ((e = launch_dependent(count_kernel, dim3(chunks), kPlanThreads, 0, stream, a.refs,
+                              a.num_blocks, w.chunk)) ||
+        (e = launch_dependent(fork_plan_kernel, dim3(1), kPlanThreads, 0, stream, a, w)) ||
+        (e = launch_dependent(assign_kernel<true>, dim3(chunks + a.n), kPlanThreads, 0, stream, b, w)))
         return e;
     if (p.n == 0)
         return cudaSuccess;
-    return launch_after(copy_kernel<false>, dim3(copy_ctas(p, a.n, sm_count), p.n), 256, stream,
-                        true, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a, w);
+    return launch_dependent(copy_kernel<COPY_ONLY>, dim3(copy_ctas(p, a.n, sm_count), p.n), 256, 0,
+                            stream, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a, w);
 }
 
 cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t stream)
 {
-    free_kernel<<<a.n, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(free_kernel, dim3(a.n), 256, 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_count,
@@ -579,13 +720,18 @@ cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_c
     carve(a.ws, a.num_blocks, a.num_seqs, 0, &w);
     const int chunks = chunks_of(a.num_blocks);
     cudaError_t e;
-    if ((e = launch_after(count_kernel, chunks, kPlanThreads, stream, false, a.refs, a.num_blocks,
-                          w.chunk)) ||
-        (e = launch_after(compact_rank_kernel, chunks, kPlanThreads, stream, true, a, w)))
+    if (a.num_blocks <= kSmallPool) {
+        if ((e = launch_dependent(compact_small_kernel, dim3(1), kPlanThreads, 0, stream, a, w)))
+            return e;
+    } else if ((e = launch_dependent(count_kernel, dim3(chunks), kPlanThreads, 0, stream, a.refs,
+                                     a.num_blocks, w.chunk)) ||
+               (e = launch_dependent(compact_rank_kernel, dim3(chunks), kPlanThreads, 0, stream, a,
+                                     w))) {
         return e;
-    return launch_after(copy_kernel<true>, dim3(copy_ctas(p, a.num_blocks / 2 + 1, sm_count), p.n + 1), 256,
-                        stream, true, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a,
-                        w);
+    }
+    return launch_dependent(copy_kernel<COPY_COMPACT>,
+                            dim3(copy_ctas(p, a.num_blocks / 2 + 1, sm_count), p.n + 1), 256, 0,
+                            stream, p, w.src, w.dst, w.head + H_N, 0, a.num_blocks, a.status, a, w);
 }
 
 cudaError_t launch_pages_copy(const PagePools &p, const int32_t *src, const int32_t *dst, int n,
@@ -593,9 +739,9 @@ cudaError_t launch_pages_copy(const PagePools &p, const int32_t *src, const int3
 {
     PageArgs a = {};
     PageWs w = {};
-    return launch_after(copy_kernel<false>, dim3(copy_ctas(p, n, sm_count), p.n), 256, stream,
-                        false, p, src, dst, static_cast<const int32_t *>(nullptr), n, num_blocks,
-                        status, a, w);
+    return launch_dependent(copy_kernel<COPY_ONLY>, dim3(copy_ctas(p, n, sm_count), p.n), 256, 0,
+                            stream, p, src, dst, static_cast<const int32_t *>(nullptr), n,
+                            num_blocks, status, a, w);
 }
 
 }  // namespace vfa

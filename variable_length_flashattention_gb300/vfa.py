@@ -105,6 +105,8 @@ def library_path() -> str:
 def lib():
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -444,34 +446,67 @@ def decode_finalize(l: torch.Tensor, o: torch.Tensor, out: Optional[torch.Tensor
 _INV_2PI = Fraction("0.159154943091895335768883763372514362034459645740456448747667")
 
 
-def _on_stream(stream):
-    """Allocations of a call belong to the stream its kernels run on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+# The operators below are called once per layer of a step, often on little
+# data, so their checks are one expression per tensor and the messages are
+# worked out only where one fails.
 
-
-def _here(*tensors):
-    """Every tensor lives on the current device (where the kernels are launched)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
-
-
-def _need_rows(t: torch.Tensor, name: str):
-    """bf16 [tokens, heads, head_dim], heads and dims contiguous, any token stride."""
+def _refuse(t, dtype, name, dev):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if t.get_device() != dev or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device (cuda:{torch.cuda.current_device()}), "
+                         f"like the other tensors; got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The current device, which must be t's: kernels are launched there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse(t, t.dtype, name, dev)
+    return dev
+
+
+def _dense(t: torch.Tensor, dtype, name: str, dev: int):
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        _refuse(t, dtype, name, dev)
+
+
+def _rows(t: torch.Tensor, shape, name: str, dev: int) -> int:
+    """t: bf16 [tokens, heads, head_dim], heads and dims contiguous; returns the token stride
+    in elements (one or no token has no neighbour: the packed distance)."""
+    if t.get_device() != dev or t.dtype != torch.bfloat16:
+        _refuse(t, torch.bfloat16, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] = {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    T, H, D = shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name} must have contiguous heads and dims")
+    return st if T > 1 else H * D
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements between tokens (one or no token has no neighbour: the packed distance)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An allocation that belongs to the stream the call's kernels run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def rope_table(inv_freq, axes=None, device="cuda") -> torch.Tensor:
@@ -495,40 +530,37 @@ def rope_table(inv_freq, axes=None, device="cuda") -> torch.Tensor:
 
 
 def _rope_inputs(q, k, positions, table, q_weight, k_weight):
-    for t, n in ((q, "q"), (k, "k")):
-        _need_rows(t, n)
-    if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    """Checks; (device, q's and k's token strides, position axes, rotated dims)."""
+    dev = _device(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError("q [T, Hq, D] and k [T, Hkv, D] must agree in tokens and head_dim")
+    qs, ks = _rows(q, q.shape, "q", dev), _rows(k, k.shape, "k", dev)
     axes = rot = 0
     if table is not None:
-        _need(table, torch.int64, "table")
+        _dense(table, torch.int64, "table", dev)
         if table.dim() != 2 or table.shape[1] != 2:
             raise ValueError("table must be [rotary_dim / 2, 2], as rope_table makes it")
         rot = 2 * table.shape[0]
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _need(positions, torch.int32, "positions")
+        _dense(positions, torch.int32, "positions", dev)
         axes = 1 if positions.dim() == 1 else positions.shape[0]
         if positions.dim() > 2 or positions.shape[-1] != q.shape[0]:
             raise ValueError("positions must be [tokens] or [axes, tokens]")
     for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            _need(w, torch.float32, n)
-            if w.shape != (q.shape[2],):
+            _dense(w, torch.float32, n, dev)
+            if w.dim() != 1 or w.shape[0] != q.shape[2]:
                 raise ValueError(f"{n} must be [head_dim]")
-    _here(q, k, positions if rot else None, table, q_weight, k_weight)
-    return axes, rot
+    return dev, qs, ks, axes, rot
 
 
-def _outputs(like, given, name, stream):
+def _row_output(given, like, name, dev, stream):
+    """(the output, its token stride): the given one checked, or a new one shaped like `like`."""
     if given is None:
-        with _on_stream(stream):
-            return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _need_rows(given, name)
-    if given.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    _here(given)
-    return given
+        given = _empty(like.shape, torch.bfloat16, like.device, stream)
+        return given, like.shape[1] * like.shape[2]
+    return given, _rows(given, like.shape, name, dev)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
@@ -541,14 +573,16 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     q [T, Hq, D], k [T, Hkv, D] bf16, views with a token stride included;
     positions int32 [T] or [axes, T]; table from rope_table (None: no rotation);
     weights f32 [D] (None: no norm); q_out / k_out may be q / k."""
-    axes, rot = _rope_inputs(q, k, positions, table, q_weight, k_weight)
-    q_out = _outputs(q, q_out, "q_out", stream)
-    k_out = _outputs(k, k_out, "k_out", stream)
-    _check(lib().vfa_qk_norm_rope_fwd(
-        _ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(positions), axes, _ptr(table), rot,
-        int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), float(eps), q.shape[0], q.shape[1],
-        k.shape[1], q.shape[2], _ptr(q_out), _ptr(k_out), _row_stride(q_out), _row_stride(k_out),
-        _stream(stream)))
+    dev, qs, ks, axes, rot = _rope_inputs(q, k, positions, table, q_weight, k_weight)
+    q_out, qos = _row_output(q_out, q, "q_out", dev, stream)
+    k_out, kos = _row_output(k_out, k, "k_out", dev, stream)
+    T, Hq, D = q.shape
+    st = lib().vfa_qk_norm_rope_fwd(
+        q.data_ptr(), k.data_ptr(), qs, ks, _address(positions), axes, _address(table), rot,
+        1 if interleaved else 0, _address(q_weight), _address(k_weight), eps, T, Hq, k.shape[1], D,
+        q_out.data_ptr(), k_out.data_ptr(), qos, kos, _raw_stream(stream, dev))
+    if st:
+        _check(st)
     return q_out, k_out
 
 
@@ -571,44 +605,40 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
 
     dq_out, dk_out: upstream gradients; dq / dk may be dq_out / dk_out.  The
     weight gradients are f32 [D], None where there is no weight."""
-    axes, rot = _rope_inputs(q, k, positions, table, q_weight, k_weight)
-    for t, x, n in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        _need_rows(t, n)
-        if t.shape != x.shape:
-            raise ValueError(f"{n} must have shape {tuple(x.shape)}")
-    _here(dq_out, dk_out, workspace)
-    dq = _outputs(q, dq, "dq", stream)
-    dk = _outputs(k, dk, "dk", stream)
-    grads = []
-    for w, g, n in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+    dev, qs, ks, axes, rot = _rope_inputs(q, k, positions, table, q_weight, k_weight)
+    dqos, dkos = _rows(dq_out, q.shape, "dq_out", dev), _rows(dk_out, k.shape, "dk_out", dev)
+    dq, dqs = _row_output(dq, q, "dq", dev, stream)
+    dk, dks = _row_output(dk, k, "dk", dev, stream)
+    grads = [None, None]
+    for i, (w, g, n) in enumerate(((q_weight, dq_weight, "dq_weight"),
+                                   (k_weight, dk_weight, "dk_weight"))):
         if w is None:
-            grads.append(None)
             continue
         if g is None:
-            with _on_stream(stream):
-                g = torch.empty_like(w)
-        _need(g, torch.float32, n)
-        if g.shape != w.shape:
-            raise ValueError(f"{n} must be [head_dim]")
-        _here(g)
-        grads.append(g)
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        with _on_stream(stream):
-            workspace = alloc_qk_norm_rope_bwd_workspace(q.shape[2], device=q.device)
-    _check(lib().vfa_qk_norm_rope_bwd(
-        _ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(dq_out), _ptr(dk_out),
-        _row_stride(dq_out), _row_stride(dk_out), _ptr(positions), axes, _ptr(table), rot,
-        int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), float(eps), q.shape[0], q.shape[1],
-        k.shape[1], q.shape[2], _ptr(dq), _ptr(dk), _row_stride(dq), _row_stride(dk),
-        _ptr(grads[0]), _ptr(grads[1]), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+            g = _empty(w.shape, torch.float32, w.device, stream)
+        else:
+            _dense(g, torch.float32, n, dev)
+            if g.shape != w.shape:
+                raise ValueError(f"{n} must be [head_dim]")
+        grads[i] = g
+    if workspace is not None:
+        _dense(workspace, workspace.dtype, "workspace", dev)
+    elif q_weight is not None or k_weight is not None:
+        n = lib().vfa_qk_norm_rope_bwd_workspace_bytes(q.shape[2])
+        workspace = _empty(n, torch.uint8, q.device, stream)
+    T, Hq, D = q.shape
+    st = lib().vfa_qk_norm_rope_bwd(
+        q.data_ptr(), k.data_ptr(), qs, ks, dq_out.data_ptr(), dk_out.data_ptr(), dqos, dkos,
+        _address(positions), axes, _address(table), rot, 1 if interleaved else 0,
+        _address(q_weight), _address(k_weight), eps, T, Hq, k.shape[1], D, dq.data_ptr(),
+        dk.data_ptr(), dqs, dks, _address(grads[0]), _address(grads[1]), _address(workspace),
+        _nbytes(workspace), _raw_stream(stream, dev))
+    if st:
+        _check(st)
     return dq, dk, grads[0], grads[1]
 
 
 # ----------------------------------------------------------------- 4-bit cache
-
-def _nbytes(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
-
 
 def kv4_block_bytes(num_kv_heads: int, head_dim: int) -> int:
     """Bytes of one page of 16 tokens (vfa_kv4_block_bytes)."""
@@ -625,25 +655,27 @@ def alloc_kv4_pool(num_blocks: int, num_kv_heads: int, head_dim: int,
     return torch.zeros(num_blocks, num_kv_heads, 18 * head_dim, dtype=torch.uint8, device=device)
 
 
-def _need_kv4(pool, tables, status):
-    _need(pool, torch.uint8, "pool")
-    _need(tables, torch.int32, "tables")
+def _kv4_pool(pool, tables, status):
+    """Checks; (device, head_dim)."""
+    dev = _device(pool, "pool")
+    _dense(pool, torch.uint8, "pool", dev)
+    _dense(tables, torch.int32, "tables", dev)
     if status is not None:
-        _need(status, torch.int32, "status")
+        _dense(status, torch.int32, "status", dev)
     if pool.dim() != 3 or tables.dim() != 2:
         raise ValueError("pool must be [num_blocks, num_kv_heads, 18 * head_dim], tables "
                          "[num_seqs, capacity]")
-    if pool.shape[2] % 18:
+    D, rest = divmod(pool.shape[2], 18)
+    if rest:
         raise ValueError("pool pages must hold 18 * head_dim bytes per kv head")
-    _here(pool, tables, status)
-    return pool.shape[2] // 18
+    return dev, D
 
 
-def _need_seqs(cu_seqlens, start_positions, tables):
-    _need(cu_seqlens, torch.int32, "cu_seqlens")
-    _need(start_positions, torch.int32, "start_positions")
-    _here(cu_seqlens, start_positions)
-    if cu_seqlens.numel() != tables.shape[0] + 1 or start_positions.numel() != tables.shape[0]:
+def _token_map(cu_seqlens, start_positions, tables, dev):
+    _dense(cu_seqlens, torch.int32, "cu_seqlens", dev)
+    _dense(start_positions, torch.int32, "start_positions", dev)
+    S = tables.shape[0]
+    if cu_seqlens.numel() != S + 1 or start_positions.numel() != S:
         raise ValueError("cu_seqlens [num_seqs + 1] and start_positions [num_seqs] must match "
                          "tables")
 
@@ -655,18 +687,17 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, tables: torc
 
     Token i of sequence s (row cu_seqlens[s] + i) becomes position
     start_positions[s] + i of its table row; rows past cu_seqlens[-1] are padding."""
-    D = _need_kv4(pool, tables, status)
-    for t, n in ((k, "k"), (v, "v")):
-        _need_rows(t, n)
-        if t.shape != (k.shape[0], pool.shape[1], D):
-            raise ValueError(f"{n} must be [tokens, {pool.shape[1]}, {D}]")
-    _need_seqs(cu_seqlens, start_positions, tables)
-    _here(k, v)
-    _check(lib().vfa_kv4_write(_ptr(k), _ptr(v), _row_stride(k), _row_stride(v), k.shape[0],
-                               _ptr(pool), pool.shape[0], _ptr(tables), tables.shape[1],
-                               _ptr(cu_seqlens), _ptr(start_positions), tables.shape[0],
-                               pool.shape[1], D, float(descale_k), float(descale_v), _ptr(status),
-                               _stream(stream)))
+    dev, D = _kv4_pool(pool, tables, status)
+    _token_map(cu_seqlens, start_positions, tables, dev)
+    blocks, Hkv, _ = pool.shape
+    T = k.shape[0]
+    ks, vs = _rows(k, (T, Hkv, D), "k", dev), _rows(v, (T, Hkv, D), "v", dev)
+    st = lib().vfa_kv4_write(k.data_ptr(), v.data_ptr(), ks, vs, T, pool.data_ptr(), blocks,
+                             tables.data_ptr(), tables.shape[1], cu_seqlens.data_ptr(),
+                             start_positions.data_ptr(), tables.shape[0], Hkv, D, descale_k,
+                             descale_v, _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def kv4_gather(pool: torch.Tensor, tables: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -677,26 +708,26 @@ def kv4_gather(pool: torch.Tensor, tables: torch.Tensor, cu_seqlens: torch.Tenso
     """(k, v) bf16 [total_tokens, Hkv, D] read back from a 4-bit pool, exactly (vfa_kv4_gather).
 
     Rows without a place in the cache are left as they were (unset if allocated here)."""
-    D = _need_kv4(pool, tables, status)
-    _need_seqs(cu_seqlens, start_positions, tables)
-    outs = []
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            with _on_stream(stream):
-                t = torch.empty(total_tokens, pool.shape[1], D, dtype=torch.bfloat16,
-                                device=pool.device)
-        _need_rows(t, n)
-        if t.shape != (total_tokens, pool.shape[1], D):
-            raise ValueError(f"{n} must be [{total_tokens}, {pool.shape[1]}, {D}]")
-        _here(t)
-        outs.append(t)
-    k, v = outs
-    _check(lib().vfa_kv4_gather(_ptr(k), _ptr(v), _row_stride(k), _row_stride(v), k.shape[0],
-                                _ptr(pool), pool.shape[0], _ptr(tables), tables.shape[1],
-                                _ptr(cu_seqlens), _ptr(start_positions), tables.shape[0],
-                                pool.shape[1], D, float(descale_k), float(descale_v),
-                                _ptr(status), _stream(stream)))
-    return k, v
+    dev, D = _kv4_pool(pool, tables, status)
+    _token_map(cu_seqlens, start_positions, tables, dev)
+    blocks, Hkv, _ = pool.shape
+    shape = (total_tokens, Hkv, D)
+    if k_out is None:
+        k_out, ks = _empty(shape, torch.bfloat16, pool.device, stream), Hkv * D
+    else:
+        ks = _rows(k_out, shape, "k_out", dev)
+    if v_out is None:
+        v_out, vs = _empty(shape, torch.bfloat16, pool.device, stream), Hkv * D
+    else:
+        vs = _rows(v_out, shape, "v_out", dev)
+    st = lib().vfa_kv4_gather(k_out.data_ptr(), v_out.data_ptr(), ks, vs, total_tokens,
+                              pool.data_ptr(), blocks, tables.data_ptr(), tables.shape[1],
+                              cu_seqlens.data_ptr(), start_positions.data_ptr(), tables.shape[0],
+                              Hkv, D, descale_k, descale_v, _address(status),
+                              _raw_stream(stream, dev))
+    if st:
+        _check(st)
+    return k_out, v_out
 
 
 def alloc_kv4_decode_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -716,32 +747,37 @@ def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
     """(out bf16 [S, Hq, D], lse f32 [S, Hq]): one query token per sequence over a 4-bit cache
     (vfa_kv4_decode).  Keep a workspace from alloc_kv4_decode_workspace between calls;
     without one, each call allocates and clears its own."""
-    D = _need_kv4(pool, tables, status)
-    _need(q, torch.bfloat16, "q")
-    _need(token_counts, torch.int32, "token_counts")
+    dev, D = _kv4_pool(pool, tables, status)
+    _dense(q, torch.bfloat16, "q", dev)
+    _dense(token_counts, torch.int32, "token_counts", dev)
     if q.dim() != 3 or q.shape[0] != tables.shape[0] or q.shape[2] != D:
         raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
-    if token_counts.numel() != q.shape[0]:
-        raise ValueError("token_counts must be [num_seqs]")
     S, Hq, _ = q.shape
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = alloc_kv4_decode_workspace(S, Hq, pool.shape[1], D, device=q.device)
-    _need(out, torch.bfloat16, "out")
-    _need(lse, torch.float32, "lse")
-    _need(workspace, torch.uint8, "workspace")
+    blocks, Hkv, _ = pool.shape
+    if token_counts.numel() != S:
+        raise ValueError("token_counts must be [num_seqs]")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+    else:
+        _dense(out, torch.bfloat16, "out", dev)
+    if lse is None:
+        lse = _empty((S, Hq), torch.float32, q.device, stream)
+    else:
+        _dense(lse, torch.float32, "lse", dev)
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = alloc_kv4_decode_workspace(S, Hq, Hkv, D, device=q.device)
+    else:
+        _dense(workspace, torch.uint8, "workspace", dev)
     if out.shape != q.shape or lse.shape != (S, Hq):
         raise ValueError("out must have q's shape and lse [num_seqs, num_q_heads]")
-    _here(q, token_counts, out, lse, workspace)
-    _check(lib().vfa_kv4_decode(_ptr(q), _ptr(pool), pool.shape[0], _ptr(tables), tables.shape[1],
-                                _ptr(token_counts), S, Hq, pool.shape[1], D, float(descale_k),
-                                float(descale_v), float(softmax_scale), _ptr(out), _ptr(lse),
-                                _ptr(status), _ptr(workspace), workspace.numel(),
-                                _stream(stream)))
+    st = lib().vfa_kv4_decode(q.data_ptr(), pool.data_ptr(), blocks, tables.data_ptr(),
+                              tables.shape[1], token_counts.data_ptr(), S, Hq, Hkv, D, descale_k,
+                              descale_v, softmax_scale, out.data_ptr(), lse.data_ptr(),
+                              _address(status), workspace.data_ptr(), workspace.numel(),
+                              _raw_stream(stream, dev))
+    if st:
+        _check(st)
     return out, lse
 
 
@@ -756,81 +792,89 @@ def alloc_pages_workspace(num_blocks: int, num_seqs: int, num_forks: int = 0,
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _need_pages(refcounts, tables, token_counts, status, workspace=None):
-    for t, n in ((refcounts, "refcounts"), (tables, "tables"), (token_counts, "token_counts")):
-        _need(t, torch.int32, n)
+def _page_state(refcounts, tables, token_counts, status):
+    """Checks; (device, num_blocks, capacity, num_seqs)."""
+    dev = _device(refcounts, "refcounts")
+    _dense(refcounts, torch.int32, "refcounts", dev)
+    _dense(tables, torch.int32, "tables", dev)
+    _dense(token_counts, torch.int32, "token_counts", dev)
     if status is not None:
-        _need(status, torch.int32, "status")
-    if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
-    if refcounts.dim() != 1 or tables.dim() != 2 or token_counts.shape != (tables.shape[0],):
+        _dense(status, torch.int32, "status", dev)
+    if refcounts.dim() != 1 or tables.dim() != 2 or token_counts.dim() != 1 or \
+            token_counts.shape[0] != tables.shape[0]:
         raise ValueError("refcounts [num_blocks], tables [num_seqs, capacity] and token_counts "
                          "[num_seqs]")
-    _here(refcounts, tables, token_counts, status, workspace)
+    S, cap = tables.shape
+    return dev, refcounts.shape[0], cap, S
 
 
-def _pool_list(pools, num_blocks):
+def _pool_list(pools, num_blocks, dev):
     """Host arrays of the pools' addresses and page sizes."""
+    n = len(pools)
+    ptrs, sizes = [], []
     for i, p in enumerate(pools):
-        if not p.is_cuda or not p.is_contiguous():
-            raise ValueError(f"pools[{i}] must be a contiguous CUDA tensor")
+        if p.get_device() != dev or not p.is_contiguous():
+            _refuse(p, p.dtype, f"pools[{i}]", dev)
         if p.dim() < 2 or p.shape[0] != num_blocks:
             raise ValueError(f"pools[{i}] must hold {num_blocks} pages")
-        _here(p)
-    n = len(pools)
-    ptrs = (ctypes.c_void_p * max(n, 1))(*[p.data_ptr() for p in pools])
-    sizes = (ctypes.c_int * max(n, 1))(*[p.stride(0) * p.element_size() for p in pools])
-    return ptrs, sizes, n
+        ptrs.append(p.data_ptr())
+        sizes.append(p.nbytes // max(num_blocks, 1))
+    return (_P * n)(*ptrs), (_I * n)(*sizes), n
 
 
 def pages_extend(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
                  add_tokens: torch.Tensor, block_size: int, workspace: torch.Tensor,
                  status: Optional[torch.Tensor] = None, stream=None):
     """token_counts += add_tokens, with new pages where rows need them (vfa_pages_extend)."""
-    _need_pages(refcounts, tables, token_counts, status, workspace)
-    _need(add_tokens, torch.int32, "add_tokens")
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    _dense(workspace, torch.uint8, "workspace", dev)
+    _dense(add_tokens, torch.int32, "add_tokens", dev)
     if add_tokens.shape != token_counts.shape:
         raise ValueError("add_tokens must be [num_seqs]")
-    _here(add_tokens)
-    _check(lib().vfa_pages_extend(_ptr(refcounts), refcounts.numel(), _ptr(tables),
-                                  tables.shape[1], _ptr(token_counts), tables.shape[0],
-                                  _ptr(add_tokens), int(block_size), _ptr(workspace),
-                                  workspace.numel(), _ptr(status), _stream(stream)))
+    st = lib().vfa_pages_extend(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+                                token_counts.data_ptr(), S, add_tokens.data_ptr(), block_size,
+                                workspace.data_ptr(), workspace.numel(), _address(status),
+                                _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def pages_fork(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
                parents: torch.Tensor, children: torch.Tensor, pools, block_size: int,
                workspace: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None):
     """Rows children[i] become copies of rows parents[i]: full pages shared, a partly filled
-    last page copied in every pool (vfa_pages_fork)."""
-    _need_pages(refcounts, tables, token_counts, status, workspace)
-    _need(parents, torch.int32, "parents")
-    _need(children, torch.int32, "children")
+    last page copied in every pool (vfa_pages_fork).  A negative parent skips the entry."""
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    _dense(workspace, torch.uint8, "workspace", dev)
+    _dense(parents, torch.int32, "parents", dev)
+    _dense(children, torch.int32, "children", dev)
     if parents.dim() != 1 or parents.shape != children.shape:
         raise ValueError("parents and children must be [num_forks]")
-    _here(parents, children)
-    ptrs, sizes, n = _pool_list(pools, refcounts.numel())
-    if parents.numel() == 0:
+    ptrs, sizes, n = _pool_list(pools, blocks, dev)
+    if parents.shape[0] == 0:
         return
-    _check(lib().vfa_pages_fork(_ptr(refcounts), refcounts.numel(), _ptr(tables), tables.shape[1],
-                                _ptr(token_counts), tables.shape[0], _ptr(parents),
-                                _ptr(children), parents.numel(), ptrs, sizes, n, int(block_size),
-                                _ptr(workspace), workspace.numel(), _ptr(status),
-                                _stream(stream)))
+    st = lib().vfa_pages_fork(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+                              token_counts.data_ptr(), S, parents.data_ptr(), children.data_ptr(),
+                              parents.shape[0], ptrs, sizes, n, block_size, workspace.data_ptr(),
+                              workspace.numel(), _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def pages_free(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
                seqs: torch.Tensor, block_size: int, status: Optional[torch.Tensor] = None,
                stream=None):
-    """Rows seqs[i] give up their pages (vfa_pages_free)."""
-    _need_pages(refcounts, tables, token_counts, status)
-    _need(seqs, torch.int32, "seqs")
-    _here(seqs)
-    if seqs.numel() == 0:
+    """Rows seqs[i] give up their pages (vfa_pages_free).  A negative entry is skipped."""
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    _dense(seqs, torch.int32, "seqs", dev)
+    n = seqs.numel()
+    if n == 0:
         return
-    _check(lib().vfa_pages_free(_ptr(refcounts), refcounts.numel(), _ptr(tables), tables.shape[1],
-                                _ptr(token_counts), tables.shape[0], _ptr(seqs), seqs.numel(),
-                                int(block_size), _ptr(status), _stream(stream)))
+    st = lib().vfa_pages_free(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+                              token_counts.data_ptr(), S, seqs.data_ptr(), n, block_size,
+                              _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def pages_compact(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
@@ -841,24 +885,25 @@ def pages_compact(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: t
                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the used pages to the low end of every pool (vfa_pages_compact); refcounts and
     tables are rewritten in place unless outputs are given.  Returns int32 [1]: used pages."""
-    _need_pages(refcounts, tables, token_counts, status, workspace)
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    _dense(workspace, torch.uint8, "workspace", dev)
     refcounts_out = refcounts if refcounts_out is None else refcounts_out
     tables_out = tables if tables_out is None else tables_out
     if num_used is None:
-        with _on_stream(stream):
-            num_used = torch.empty(1, dtype=torch.int32, device=refcounts.device)
+        num_used = _empty(1, torch.int32, refcounts.device, stream)
     for t, x, n in ((refcounts_out, refcounts, "refcounts_out"), (tables_out, tables, "tables_out")):
-        _need(t, torch.int32, n)
+        _dense(t, torch.int32, n, dev)
         if t.shape != x.shape:
             raise ValueError(f"{n} must have shape {tuple(x.shape)}")
-    _need(num_used, torch.int32, "num_used")
-    _here(refcounts_out, tables_out, num_used)
-    ptrs, sizes, n = _pool_list(pools, refcounts.numel())
-    _check(lib().vfa_pages_compact(_ptr(refcounts), refcounts.numel(), _ptr(tables),
-                                   tables.shape[1], _ptr(token_counts), tables.shape[0], ptrs,
-                                   sizes, n, int(block_size), _ptr(refcounts_out),
-                                   _ptr(tables_out), _ptr(num_used), _ptr(workspace),
-                                   workspace.numel(), _ptr(status), _stream(stream)))
+    _dense(num_used, torch.int32, "num_used", dev)
+    ptrs, sizes, n = _pool_list(pools, blocks, dev)
+    st = lib().vfa_pages_compact(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+                                 token_counts.data_ptr(), S, ptrs, sizes, n, block_size,
+                                 refcounts_out.data_ptr(), tables_out.data_ptr(),
+                                 num_used.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
     return num_used
 
 
@@ -867,19 +912,21 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
     """Page src[i] of every pool over page dst[i] (vfa_pages_copy)."""
     if not pools:
         return
-    _need(src, torch.int32, "src")
-    _need(dst, torch.int32, "dst")
+    dev = _device(src, "src")
+    _dense(src, torch.int32, "src", dev)
+    _dense(dst, torch.int32, "dst", dev)
     if status is not None:
-        _need(status, torch.int32, "status")
+        _dense(status, torch.int32, "status", dev)
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be [n]")
-    _here(src, dst, status)
-    num_blocks = pools[0].shape[0]
-    ptrs, sizes, n = _pool_list(pools, num_blocks)
-    if src.numel() == 0:
+    blocks = pools[0].shape[0]
+    ptrs, sizes, n = _pool_list(pools, blocks, dev)
+    if src.shape[0] == 0:
         return
-    _check(lib().vfa_pages_copy(ptrs, sizes, n, _ptr(src), _ptr(dst), src.numel(), num_blocks,
-                                _ptr(status), _stream(stream)))
+    st = lib().vfa_pages_copy(ptrs, sizes, n, src.data_ptr(), dst.data_ptr(), src.shape[0], blocks,
+                              _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def debug_bounded_wait(status: torch.Tensor, stream=None):
