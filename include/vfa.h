@@ -537,7 +537,7 @@ size_t vfa_kv4_block_bytes(int num_kv_heads, int head_dim);
  * k, v         device bf16 [total, num_kv_heads, head_dim], tokens k_stride /
  *              v_stride elements apart (multiples of 8).
  * cu_seqlens   device int32 [num_seqs + 1], from 0, not decreasing, ending at
- *              or below total: rows past the end are padding and not read.
+ *              or below total: rows past the end are padding, whatever they hold.
  * Nothing but the written tokens' bytes changes.  Two tokens of one call
  * must not go to one slot (two rows writing a page they share): what that
  * slot then holds is unspecified.

@@ -128,15 +128,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 
 // ------------------------------------------------------------ write, read
 //
-// One warp per packed token, D/16 lanes per head (a lane holds one scale's
-// 16 dims, so nothing is exchanged).  Bound: HBM, 2.5625 bytes per element.
+// A warp takes 32 / (D/16) consecutive packed tokens, D/16 lanes each (a lane
+// holds one scale's 16 dims, so nothing is exchanged), and goes over the kv
+// heads: the tokens' places are found side by side, and the V codes of
+// neighbouring tokens, 8 bytes each, fill whole 32-byte sectors.  Bound: HBM,
+// 2.5625 bytes per element.  85k tokens of 8 heads of 128: 75 us to write, 72
+// to read back (89 and 89 with one token per warp).
 
 // Page and row of packed token t; false where it has none (a padding row at
 // or past cu[num_seqs], or bad tables, which are recorded).
 __device__ __forceinline__ bool token_slot(const Kv4MoveArgs &a, int t, int *page, int *row)
 {
     int lo = 0, hi = a.num_seqs;                 // cu[lo] <= t < cu[hi]
-    if (t >= __ldg(a.cu + hi))
+    if (t >= a.total || t >= __ldg(a.cu + hi))
         return false;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -147,8 +151,7 @@ __device__ __forceinline__ bool token_slot(const Kv4MoveArgs &a, int t, int *pag
     }
     const int c0 = __ldg(a.cu + lo);
     if (c0 > t || t >= __ldg(a.cu + lo + 1)) {
-        if ((threadIdx.x & 31) == 0)
-            record(a.status, VFA_ERR_BAD_SEQLENS);
+        record(a.status, VFA_ERR_BAD_SEQLENS);
         return false;
     }
     const int st = __ldg(a.start + lo);
@@ -156,8 +159,7 @@ __device__ __forceinline__ bool token_slot(const Kv4MoveArgs &a, int t, int *pag
     const bool in = st >= 0 && pos < static_cast<long long>(a.capacity) * kPage;
     const int p = in ? __ldg(a.tables + static_cast<long long>(lo) * a.capacity + pos / kPage) : -1;
     if (p < 0 || p >= a.num_blocks) {
-        if ((threadIdx.x & 31) == 0)
-            record(a.status, VFA_ERR_BAD_BLOCK);
+        record(a.status, VFA_ERR_BAD_BLOCK);
         return false;
     }
     *page = p;
@@ -206,56 +208,108 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], uint32_t *scale
 }
 
 constexpr int kMoveWarps = 8;
+constexpr int kMoveAhead = 2;           // kv heads of K and V loaded together
+
+// A lane's 32 bytes as two 16-byte words, read or written by pairs of lanes so
+// that every instruction touches whole 32-byte sectors: even lanes move the
+// first halves of the pair's two runs, odd lanes the second halves.
+struct PairBytes {
+    uint4 lo, hi;                       // the lane's own 32 bytes
+
+    // before a write, after a read: even lanes trade their neighbour's first
+    // half for their own second half
+    __device__ __forceinline__ void exchange(int lane)
+    {
+        const bool odd = lane & 1;
+        uint4 give = odd ? lo : hi;
+        give.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+        give.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+        give.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+        give.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+        if (odd)
+            lo = give;
+        else
+            hi = give;
+    }
+};
+
+// Byte offset, from the lane's own run, of the word it moves first; the other
+// is 32 bytes on.
+__device__ __forceinline__ int pair_offset(int lane) { return lane & 1 ? -16 : 0; }
 
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) kv4_write_kernel(const Kv4MoveArgs a)
 {
-    constexpr int GR = D / 16, HPW = 32 / GR;
+    constexpr int GR = D / 16, TPW = 32 / GR;
     const int lane = threadIdx.x & 31;
     const int g = lane % GR;
     grid_wait();
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0)
         check_cu(a);
-    const int nwarps = gridDim.x * kMoveWarps;
-    for (int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); t < a.total; t += nwarps) {
-        int page, row;
-        if (!token_slot(a, t, &page, &row))
-            continue;
+    // this CTA's share of the kv heads (all of them but where tokens are few)
+    const int per = (a.num_kv_heads + gridDim.y - 1) / gridDim.y;
+    const int first_head = blockIdx.y * per, heads = min(a.num_kv_heads, first_head + per);
+    const int po = pair_offset(lane);
+    const long long warps = static_cast<long long>(gridDim.x) * kMoveWarps;
+    for (long long t0 = (static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5)) * TPW;
+         t0 < a.total; t0 += warps * TPW) {
+        const int t = static_cast<int>(t0) + lane / GR;
+        int page = 0, row = 0;
+        const bool has = token_slot(a, t, &page, &row);
         uint8_t *pg = static_cast<uint8_t *>(a.pool) +
                       static_cast<long long>(page) * a.num_kv_heads * kv4_head_page_bytes(D);
+        const uint8_t *src[2] = {
+            reinterpret_cast<const uint8_t *>(static_cast<const __nv_bfloat16 *>(a.k) +
+                                              static_cast<long long>(t) * a.k_stride + g * 16) + po,
+            reinterpret_cast<const uint8_t *>(static_cast<const __nv_bfloat16 *>(a.v) +
+                                              static_cast<long long>(t) * a.v_stride + g * 16) + po};
+        for (int h0 = first_head; h0 < heads; h0 += kMoveAhead) {
+            PairBytes in[2][kMoveAhead];
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const __nv_bfloat16 *src =
-                static_cast<const __nv_bfloat16 *>(which ? a.v : a.k) +
-                static_cast<long long>(t) * (which ? a.v_stride : a.k_stride) + g * 16;
-            const float inv = which ? a.v_scale : a.k_scale;
-            for (int h = lane / GR; h < a.num_kv_heads; h += HPW) {
-                const uint4 r0 = __ldcs(reinterpret_cast<const uint4 *>(src + h * D));
-                const uint4 r1 = __ldcs(reinterpret_cast<const uint4 *>(src + h * D) + 1);
-                const uint32_t rw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-                float x[16];
+            for (int i = 0; i < kMoveAhead; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[2 * j] = __uint_as_float(rw[j] << 16) * inv;
-                    x[2 * j + 1] = __uint_as_float(rw[j] & 0xffff0000u) * inv;
-                }
-                uint32_t scale, w[2];
-                quantise16(x, &scale, w);
-                uint8_t *hp = pg + h * kv4_head_page_bytes(D);
-                if (which == 0) {
-                    *reinterpret_cast<uint2 *>(hp + row * (D / 2) + g * 8) = make_uint2(w[0], w[1]);
-                    hp[16 * D + row * GR + g] = static_cast<uint8_t>(scale);
-                } else {
-                    uint8_t *vp = hp + 8 * D + v_code_at<D>(row, g);
-                    if (D == 64) {
-                        *reinterpret_cast<uint32_t *>(vp) = w[0];
-                        *reinterpret_cast<uint32_t *>(vp + 32) = w[1];
-                    } else {
-                        *reinterpret_cast<uint2 *>(vp) = make_uint2(w[0], w[1]);
+                for (int which = 0; which < 2; ++which) {
+                    in[which][i].lo = in[which][i].hi = make_uint4(0, 0, 0, 0);
+                    if (has && h0 + i < heads) {
+                        const uint8_t *q = src[which] + (h0 + i) * (2 * D);
+                        in[which][i].lo = __ldcs(reinterpret_cast<const uint4 *>(q));
+                        in[which][i].hi = __ldcs(reinterpret_cast<const uint4 *>(q + 32));
                     }
-                    hp[17 * D + v_scale_at(row, g)] = static_cast<uint8_t>(scale);
                 }
-            }
+#pragma unroll
+            for (int i = 0; i < kMoveAhead; ++i)
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    PairBytes &r = in[which][i];
+                    r.exchange(lane);
+                    if (!has || h0 + i >= heads)
+                        continue;
+                    const float inv = which ? a.v_scale : a.k_scale;
+                    const uint32_t rw[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w,
+                                            r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+                    float x[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[2 * j] = __uint_as_float(rw[j] << 16) * inv;
+                        x[2 * j + 1] = __uint_as_float(rw[j] & 0xffff0000u) * inv;
+                    }
+                    uint32_t scale, w[2];
+                    quantise16(x, &scale, w);
+                    uint8_t *hp = pg + (h0 + i) * kv4_head_page_bytes(D);
+                    if (which == 0) {
+                        *reinterpret_cast<uint2 *>(hp + row * (D / 2) + g * 8) = make_uint2(w[0], w[1]);
+                        hp[16 * D + row * GR + g] = static_cast<uint8_t>(scale);
+                    } else {
+                        uint8_t *vp = hp + 8 * D + v_code_at<D>(row, g);
+                        if (D == 64) {
+                            *reinterpret_cast<uint32_t *>(vp) = w[0];
+                            *reinterpret_cast<uint32_t *>(vp + 32) = w[1];
+                        } else {
+                            *reinterpret_cast<uint2 *>(vp) = make_uint2(w[0], w[1]);
+                        }
+                        hp[17 * D + v_scale_at(row, g)] = static_cast<uint8_t>(scale);
+                    }
+                }
         }
     }
 }
@@ -263,58 +317,78 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_write_kernel(const Kv4Mov
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4MoveArgs a)
 {
-    constexpr int GR = D / 16, HPW = 32 / GR;
+    constexpr int GR = D / 16, TPW = 32 / GR;
     const int lane = threadIdx.x & 31;
     const int g = lane % GR;
     grid_wait();
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0)
         check_cu(a);
-    const int nwarps = gridDim.x * kMoveWarps;
-    for (int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); t < a.total; t += nwarps) {
-        int page, row;
-        if (!token_slot(a, t, &page, &row))
-            continue;
+    // this CTA's share of the kv heads (all of them but where tokens are few)
+    const int per = (a.num_kv_heads + gridDim.y - 1) / gridDim.y;
+    const int first_head = blockIdx.y * per, heads = min(a.num_kv_heads, first_head + per);
+    const int po = pair_offset(lane);
+    const long long warps = static_cast<long long>(gridDim.x) * kMoveWarps;
+    for (long long t0 = (static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5)) * TPW;
+         t0 < a.total; t0 += warps * TPW) {
+        const int t = static_cast<int>(t0) + lane / GR;
+        int page = 0, row = 0;
+        const bool has = token_slot(a, t, &page, &row);
         const uint8_t *pg = static_cast<const uint8_t *>(a.pool) +
                             static_cast<long long>(page) * a.num_kv_heads * kv4_head_page_bytes(D);
+        uint8_t *dst[2] = {
+            reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.k) +
+                                        static_cast<long long>(t) * a.k_stride + g * 16) + po,
+            reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.v) +
+                                        static_cast<long long>(t) * a.v_stride + g * 16) + po};
+        for (int h0 = first_head; h0 < heads; h0 += kMoveAhead) {
+            uint2 code[2][kMoveAhead];
+            uint32_t scale[2][kMoveAhead];
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(which ? a.v : a.k) +
-                                 static_cast<long long>(t) * (which ? a.v_stride : a.k_stride) +
-                                 g * 16;
-            const float ds = which ? a.v_scale : a.k_scale;
-            for (int h = lane / GR; h < a.num_kv_heads; h += HPW) {
-                const uint8_t *hp = pg + h * kv4_head_page_bytes(D);
-                uint2 w;
-                uint32_t scale;
-                if (which == 0) {
-                    w = *reinterpret_cast<const uint2 *>(hp + row * (D / 2) + g * 8);
-                    scale = hp[16 * D + row * GR + g];
-                } else {
-                    const uint8_t *vp = hp + 8 * D + v_code_at<D>(row, g);
-                    if (D == 64) {
-                        w.x = *reinterpret_cast<const uint32_t *>(vp);
-                        w.y = *reinterpret_cast<const uint32_t *>(vp + 32);
-                    } else {
-                        w = *reinterpret_cast<const uint2 *>(vp);
+            for (int i = 0; i < kMoveAhead; ++i)
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    code[which][i] = make_uint2(0, 0);
+                    scale[which][i] = 0;
+                    if (has && h0 + i < heads) {
+                        const uint8_t *hp = pg + (h0 + i) * kv4_head_page_bytes(D);
+                        if (which == 0) {
+                            code[0][i] = *reinterpret_cast<const uint2 *>(hp + row * (D / 2) + g * 8);
+                            scale[0][i] = hp[16 * D + row * GR + g];
+                        } else {
+                            const uint8_t *vp = hp + 8 * D + v_code_at<D>(row, g);
+                            if (D == 64) {
+                                code[1][i].x = *reinterpret_cast<const uint32_t *>(vp);
+                                code[1][i].y = *reinterpret_cast<const uint32_t *>(vp + 32);
+                            } else {
+                                code[1][i] = *reinterpret_cast<const uint2 *>(vp);
+                            }
+                            scale[1][i] = hp[17 * D + v_scale_at(row, g)];
+                        }
                     }
-                    scale = hp[17 * D + v_scale_at(row, g)];
                 }
-                const float s = f16_lo(e4m3x2_to_f16(scale)) * ds;
-                uint32_t h8[8];
-                {
-                    uint32_t lo[4], hi[4];
-                    e2m1x8_to_f16(w.x, lo);
-                    e2m1x8_to_f16(w.y, hi);
+#pragma unroll
+            for (int i = 0; i < kMoveAhead; ++i)
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    const float s = f16_lo(e4m3x2_to_f16(scale[which][i])) * (which ? a.v_scale : a.k_scale);
+                    uint32_t lo[4], hi[4], o[8];
+                    e2m1x8_to_f16(code[which][i].x, lo);
+                    e2m1x8_to_f16(code[which][i].y, hi);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        h8[j] = pack_bf16x2(f16_lo(lo[j]) * s, f16_hi(lo[j]) * s);
-                        h8[4 + j] = pack_bf16x2(f16_lo(hi[j]) * s, f16_hi(hi[j]) * s);
+                        o[j] = pack_bf16x2(f16_lo(lo[j]) * s, f16_hi(lo[j]) * s);
+                        o[4 + j] = pack_bf16x2(f16_lo(hi[j]) * s, f16_hi(hi[j]) * s);
+                    }
+                    PairBytes out;
+                    out.lo = make_uint4(o[0], o[1], o[2], o[3]);
+                    out.hi = make_uint4(o[4], o[5], o[6], o[7]);
+                    out.exchange(lane);
+                    if (has && h0 + i < heads) {
+                        uint8_t *q = dst[which] + (h0 + i) * (2 * D);
+                        *reinterpret_cast<uint4 *>(q) = out.lo;
+                        *reinterpret_cast<uint4 *>(q + 32) = out.hi;
                     }
                 }
-                uint4 *o = reinterpret_cast<uint4 *>(dst + h * D);
-                o[0] = make_uint4(h8[0], h8[1], h8[2], h8[3]);
-                o[1] = make_uint4(h8[4], h8[5], h8[6], h8[7]);
-            }
         }
     }
 }
@@ -1023,11 +1097,18 @@ cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
                             stream, a);
 }
 
-int move_grid(int total, int sm_count)
+// CTAs over the tokens; with too few tokens for every SM, CTAs share the kv
+// heads too, kMoveAhead of them each at least.
+dim3 move_grid(const Kv4MoveArgs &a, int head_dim, int sm_count)
 {
-    const long long g = (static_cast<long long>(total) + kMoveWarps - 1) / kMoveWarps;
+    const int tokens = 32 / (head_dim / 16) * kMoveWarps;       // of a CTA
+    long long x = (static_cast<long long>(a.total) + tokens - 1) / tokens;
     const long long most = 64LL * sm_count;
-    return static_cast<int>(g < most ? g : most);
+    x = x < most ? x : most;
+    long long y = sm_count / x;
+    const long long shares = (a.num_kv_heads + kMoveAhead - 1) / kMoveAhead;
+    y = y < 1 ? 1 : (y < shares ? y : shares);
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
 
 size_t ticket_bytes(int num_seqs, int rows)
@@ -1040,11 +1121,11 @@ size_t ticket_bytes(int num_seqs, int rows)
 
 cudaError_t launch_kv4_write(int head_dim, const Kv4MoveArgs &a, int sm_count, cudaStream_t stream)
 {
-    const int grid = move_grid(a.total, sm_count);
+    const dim3 grid = move_grid(a, head_dim, sm_count);
     switch (head_dim) {
-    case 64: return launch_dependent(kv4_write_kernel<64>, dim3(grid), kMoveWarps * 32, 0, stream, a);
-    case 128: return launch_dependent(kv4_write_kernel<128>, dim3(grid), kMoveWarps * 32, 0, stream, a);
-    case 256: return launch_dependent(kv4_write_kernel<256>, dim3(grid), kMoveWarps * 32, 0, stream, a);
+    case 64: return launch_dependent(kv4_write_kernel<64>, grid, kMoveWarps * 32, 0, stream, a);
+    case 128: return launch_dependent(kv4_write_kernel<128>, grid, kMoveWarps * 32, 0, stream, a);
+    case 256: return launch_dependent(kv4_write_kernel<256>, grid, kMoveWarps * 32, 0, stream, a);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -1052,11 +1133,11 @@ cudaError_t launch_kv4_write(int head_dim, const Kv4MoveArgs &a, int sm_count, c
 cudaError_t launch_kv4_gather(int head_dim, const Kv4MoveArgs &a, int sm_count,
                               cudaStream_t stream)
 {
-    const int grid = move_grid(a.total, sm_count);
+    const dim3 grid = move_grid(a, head_dim, sm_count);
     switch (head_dim) {
-    case 64: return launch_dependent(kv4_gather_kernel<64>, dim3(grid), kMoveWarps * 32, 0, stream, a);
-    case 128: return launch_dependent(kv4_gather_kernel<128>, dim3(grid), kMoveWarps * 32, 0, stream, a);
-    case 256: return launch_dependent(kv4_gather_kernel<256>, dim3(grid), kMoveWarps * 32, 0, stream, a);
+    case 64: return launch_dependent(kv4_gather_kernel<64>, grid, kMoveWarps * 32, 0, stream, a);
+    case 128: return launch_dependent(kv4_gather_kernel<128>, grid, kMoveWarps * 32, 0, stream, a);
+    case 256: return launch_dependent(kv4_gather_kernel<256>, grid, kMoveWarps * 32, 0, stream, a);
     default: return cudaErrorInvalidValue;
     }
 }

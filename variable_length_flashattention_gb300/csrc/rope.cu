@@ -15,14 +15,20 @@
 // a turn with no rounding, so position 2^30 is as accurate as position 1 (a
 // 32-bit product would have lost the angle near position 2^20).
 //
-// Bound: HBM.  Forward 4 bytes per element, backward 6, about 10 and 20
-// flops.  A lane holds 8 dimensions of a head as two 8-byte pieces that
-// contain both members of its four pairs, so D/8 lanes hold a head and the
-// only exchange is the sum of the norm.  (16 dimensions per lane halve the
-// load instructions but double the weights, sines and sums of dw a lane keeps:
-// 150 registers and 8 warps per SM in the backward, 265 us where this takes
-// 202.)  A warp takes one token (or, when there are few, a share of its
-// heads) and works out the token's sines and cosines once for all its heads.
+// Bound: HBM (forward 4 bytes per element, backward 6), with the issue of
+// instructions next: at the copy rate an SM has 350 issue slots per KB read
+// forward.  A warp's turn is 1 KB of a tensor: 32 / (D/16) heads, 16
+// dimensions per lane in two 16-byte pieces that contain both members of the
+// lane's eight pairs, so the only exchange is the sum of the norm.  A warp
+// takes one token after the other (or, when there are few, a share of a
+// token's heads) and works out a token's sines and cosines once for all its
+// heads.  Its turns are copied ahead into its own ring in shared memory with
+// 16-byte asynchronous copies, across tokens, so the bytes in flight do not
+// depend on registers.  32768 tokens of 40 heads of 128, forward and backward:
+// 109 and 189 us; without the ring (loads into registers) 131 and 265 us at 16
+// dimensions per lane and 113 and 188 us at 8, which halves what a lane keeps;
+// with the ring at 8 dimensions, whose turns are too short for their
+// instructions, 167 and 250 us.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -35,63 +41,121 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFwdUnroll = 4;           // head iterations whose loads are in flight together
-constexpr int kBwdUnroll = 2;
-constexpr int kBwdCtas = 3;             // resident per SM
+constexpr int kFwdAhead = 6;            // turns copied ahead, CTAs per SM
+constexpr int kFwdCtas = 3;
+constexpr int kBwdAhead = 5;
+constexpr int kBwdCtas = 2;
+constexpr int kTurn = 1024;             // bytes of a turn of one tensor
 
-__device__ __forceinline__ void unpack4(const uint2 v, float *f)
+// Two floats in a 64-bit register, for the packed fp32 instructions.
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 f2_pack(float lo, float hi)
 {
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
 
-__device__ __forceinline__ uint2 pack4(const float *f)
+__device__ __forceinline__ float2 f2_unpack(f2 v)
 {
-    return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
 
-// The 8 dimensions of lane piece p of a head: [a, a + 4) and [b, b + 4).
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ float f2_sum(f2 v)
+{
+    const float2 x = f2_unpack(v);
+    return x.x + x.y;
+}
+
+// The 16 dimensions of lane piece p of a head: [a, a + 8) and [b, b + 8).
 template <bool INTER>
 __device__ __forceinline__ void lane_dims(int p, int half, int *a, int *b)
 {
-    if (!INTER && 4 * p < half) {
-        *a = 4 * p;
-        *b = half + 4 * p;
+    if (!INTER && 8 * p < half) {
+        *a = 8 * p;
+        *b = half + 8 * p;
     } else {
-        *a = 8 * p;                     // interleaved pairs, or dimensions past the rotated ones
-        *b = 8 * p + 4;
+        *a = 16 * p;                    // interleaved pairs, or dimensions past the rotated ones
+        *b = 16 * p + 8;
     }
 }
 
-// x[0..3] = dims [a, a+4), x[4..7] = dims [b, b+4); pair j is (x[j], x[4+j])
-// for halves and (x[2j], x[2j+1]) for interleaved pairs.
+// Eight pairs of dimensions: the first members at v[0..3], the second at
+// v[4..7], two pairs per word.  Pair j is dims (a + j, b + j) for halves, (a +
+// 2j, a + 2j + 1) for interleaved pairs (b = a + 8).
 template <bool INTER>
-__device__ __forceinline__ void rotate(float (&x)[8], const float (&c)[4], const float (&s)[4])
+__device__ __forceinline__ void unpack_pairs(const uint4 ra, const uint4 rb, f2 (&v)[8])
+{
+    const uint32_t w[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+    auto lo = [&](int i) { return __uint_as_float(w[i] << 16); };
+    auto hi = [&](int i) { return __uint_as_float(w[i] & 0xffff0000u); };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = INTER ? f2_pack(lo(2 * j), lo(2 * j + 1)) : f2_pack(lo(j), hi(j));
+        v[4 + j] = INTER ? f2_pack(hi(2 * j), hi(2 * j + 1)) : f2_pack(lo(4 + j), hi(4 + j));
+    }
+}
+
+template <bool INTER>
+__device__ __forceinline__ void store_pairs(__nv_bfloat16 *pa, __nv_bfloat16 *pb, const f2 (&v)[8])
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = f2_unpack(v[j]), y = f2_unpack(v[4 + j]);
+        if (INTER) {
+            w[2 * j] = pack_bf16x2(x.x, y.x);
+            w[2 * j + 1] = pack_bf16x2(x.y, y.y);
+        } else {
+            w[j] = pack_bf16x2(x.x, x.y);
+            w[4 + j] = pack_bf16x2(y.x, y.y);
+        }
+    }
+    *reinterpret_cast<uint4 *>(pa) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(pb) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// ns: the negated sines.
+__device__ __forceinline__ void rotate(f2 (&v)[8], const f2 (&c)[4], const f2 (&s)[4], const f2 (&ns)[4])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : 4 + j;
-        const float xa = x[ia], xb = x[ib];
-        x[ia] = xa * c[j] - xb * s[j];
-        x[ib] = xb * c[j] + xa * s[j];
+        const f2 a = v[j], b = v[4 + j];
+        v[j] = f2_fma(a, c[j], f2_mul(b, ns[j]));
+        v[4 + j] = f2_fma(b, c[j], f2_mul(a, s[j]));
     }
 }
 
-// Cosines and sines of token t for frequencies 4p .. 4p + 3 (1 and 0 past the
+// Cosines and sines of token t for frequencies 8p .. 8p + 7 (1 and 0 past the
 // rotated ones).  The warp's lane groups (one per head it holds) work out a
 // share each and exchange.
 template <int D>
-__device__ __forceinline__ void angles(const RopeArgs &a, int t, int lane, float (&c)[4],
-                                       float (&s)[4])
+__device__ __forceinline__ void angles(const RopeArgs &a, int t, int lane, float (&c)[8],
+                                       float (&s)[8])
 {
-    constexpr int LPH = D / 8, GROUPS = 32 / LPH, PER = 4 / GROUPS;
+    constexpr int LPH = D / 16, GROUPS = 32 / LPH, PER = 8 / GROUPS;
     const int p = lane % LPH, g = lane / LPH;
     float mc[PER], ms[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        const int i = 4 * p + g * PER + e;
+        const int i = 8 * p + g * PER + e;
         mc[e] = 1.f;
         ms[e] = 0.f;
         if (i < a.half) {
@@ -107,7 +171,7 @@ __device__ __forceinline__ void angles(const RopeArgs &a, int t, int lane, float
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
         const int src = (j / PER) * LPH + p;
         c[j] = __shfl_sync(0xffffffffu, mc[j % PER], src);
         s[j] = __shfl_sync(0xffffffffu, ms[j % PER], src);
@@ -118,236 +182,246 @@ template <int D>
 __device__ __forceinline__ float head_sum(float v)
 {
 #pragma unroll
-    for (int off = 1; off < D / 8; off <<= 1)
+    for (int off = 1; off < D / 16; off <<= 1)
         v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
 
-__device__ __forceinline__ void load_weight(const float *w, int da, int db, float (&o)[8])
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src)
 {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        o[j] = w ? __ldg(w + da + j) : 1.f;
-        o[4 + j] = w ? __ldg(w + db + j) : 1.f;
-    }
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ uint2 load_piece(const __nv_bfloat16 *p)
-{
-    return __ldcs(reinterpret_cast<const uint2 *>(p));
-}
+// A warp's place in its work: turn e of token t (the query heads' turns first).
+// Unit u covers turns [e, end) of a token; the warp takes units u, u + warps, ...
+struct Turn {
+    unsigned u;
+    int t, e, end;
 
-__device__ __forceinline__ void store_piece(__nv_bfloat16 *p, const float *f)
-{
-    *reinterpret_cast<uint2 *>(p) = pack4(f);
-}
-
-// A unit of work: head iterations [i0, i1) of token t, the query heads first.
-struct Unit {
-    int t, i0, i1;
-
-    __device__ __forceinline__ Unit(const RopeArgs &a, long long u, int iters)
+    __device__ __forceinline__ void unit(unsigned units, unsigned warps, unsigned segments, int per,
+                                         int turns)
     {
-        const int per = (iters + a.segments - 1) / a.segments;
-        t = static_cast<int>(u / a.segments);
-        i0 = static_cast<int>(u % a.segments) * per;
-        i1 = min(iters, i0 + per);
+        for (; u < units; u += warps) {
+            t = static_cast<int>(u / segments);
+            e = static_cast<int>(u % segments) * per;
+            end = min(turns, e + per);
+            if (e < end)
+                return;
+        }
     }
 };
 
-// ------------------------------------------------------------ forward
-
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) rope_fwd_kernel(const RopeArgs a)
+// Both directions.  Backward: a persistent grid whose warps take fixed units,
+// so the sums of dw run in a fixed order: per lane over its turns, then over
+// the warp's lane groups, the CTA's warps, and (second kernel) the CTAs.  No
+// atomics.
+template <int D, bool INTER, bool BWD>
+__global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kernel(const RopeArgs a)
 {
-    constexpr int LPH = D / 8, HPW = 32 / LPH, U = kFwdUnroll;
+    constexpr int LPH = D / 16, HPW = 32 / LPH;
+    constexpr int AHEAD = BWD ? kBwdAhead : kFwdAhead, STAGE = BWD ? 2 * kTurn : kTurn;
+    extern __shared__ __align__(16) uint8_t ring[];     // [kWarps][AHEAD][STAGE]
+    __shared__ __align__(16) float s_w[2][D];         // [which][quarter of a lane's 16][lane piece][4]
     grid_wait();
-    const int lane = threadIdx.x & 31;
-    const int p = lane % LPH, g = lane / LPH;
-    int da, db;
-    lane_dims<INTER>(p, a.half, &da, &db);
-    const bool turns = 4 * p < a.half;
-    const int iq = (a.heads[0] + HPW - 1) / HPW, ik = (a.heads[1] + HPW - 1) / HPW;
-    const long long units = static_cast<long long>(a.tokens) * a.segments;
-    const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
-    for (long long u = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
-         u += nwarps) {
-        const Unit un(a, u, iq + ik);
-        float c[4], s[4];
-        bool have_angles = false;
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-            const int base = which ? iq : 0;
-            const int e0 = max(un.i0 - base, 0), e1 = min(un.i1 - base, which ? ik : iq);
-            const int H = a.heads[which];
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.x[which]) +
-                                       un.t * a.x_stride[which];
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.y[which]) + un.t * a.y_stride[which];
-            const bool norm = a.weight[which] != nullptr;
-            float w[8];
-            if (e0 < e1)
-                load_weight(a.weight[which], da, db, w);
-            for (int e = e0; e < e1; e += U) {
-                uint2 ra[U], rb[U];
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int h = (e + k) * HPW + g;
-                    ra[k] = rb[k] = make_uint2(0, 0);
-                    if (e + k < e1 && h < H) {
-                        ra[k] = load_piece(src + h * D + da);
-                        rb[k] = load_piece(src + h * D + db);
-                    }
-                }
-                if (!have_angles) {                 // behind the first loads
-                    angles<D>(a, un.t, lane, c, s);
-                    have_angles = true;
-                }
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int h = (e + k) * HPW + g;
-                    float x[8];
-                    unpack4(ra[k], x);
-                    unpack4(rb[k], x + 4);
-                    if (norm) {
-                        float q = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            q = fmaf(x[j], x[j], q);
-                        const float r = rsqrtf(head_sum<D>(q) * (1.f / D) + a.eps);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            x[j] = x[j] * r * w[j];
-                    }
-                    if (turns)
-                        rotate<INTER>(x, c, s);
-                    if (e + k < e1 && h < H) {
-                        store_piece(dst + h * D + da, x);
-                        store_piece(dst + h * D + db, x + 4);
-                    }
-                }
-            }
-        }
-    }
-}
-
-// ------------------------------------------------------------ backward
-//
-// A persistent grid whose warps take fixed units, so the sums of dw run in a
-// fixed order: per lane over its units, then over the warp's lane groups, the
-// CTA's warps, and (second kernel) the CTAs.  No atomics.
-
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const RopeArgs a)
-{
-    constexpr int LPH = D / 8, HPW = 32 / LPH, U = kBwdUnroll;
-    __shared__ float s_dw[kWarps][D];
-    grid_wait();
-    if (a.dweight[0] || a.dweight[1])
+    if (BWD && (a.dweight[0] || a.dweight[1]))
         grid_release();                             // the sums of dw follow
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int p = lane % LPH, g = lane / LPH;
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+        const float *w = a.weight[i / D];
+        const int quarter = i % D / (4 * LPH), q = i / 4 % LPH, j = quarter % 2 * 4 + i % 4;
+        int da, db;
+        lane_dims<INTER>(q, a.half, &da, &db);
+        const int d = INTER ? da + 2 * j + quarter / 2 : (quarter < 2 ? da : db) + j;
+        s_w[i / D][i % D] = w ? w[d] : 1.f;
+    }
+    __syncthreads();
     int da, db;
     lane_dims<INTER>(p, a.half, &da, &db);
-    const bool turns = 4 * p < a.half;
-    const int iq = (a.heads[0] + HPW - 1) / HPW, ik = (a.heads[1] + HPW - 1) / HPW;
-    float dw[2][8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        dw[0][j] = dw[1][j] = 0.f;
-    const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
-    const long long units = static_cast<long long>(a.tokens) * a.segments;
-    for (long long u = static_cast<long long>(blockIdx.x) * kWarps + warp; u < units; u += nwarps) {
-        const Unit un(a, u, iq + ik);
-        float c[4], s[4];
-        bool have_angles = false;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const int base = which ? iq : 0;
-            const int e0 = max(un.i0 - base, 0), e1 = min(un.i1 - base, which ? ik : iq);
-            const int H = a.heads[which];
-            const bool norm = a.weight[which] != nullptr;
-            const __nv_bfloat16 *px = static_cast<const __nv_bfloat16 *>(a.x[which]) +
-                                      un.t * a.x_stride[which];
-            const __nv_bfloat16 *pdy = static_cast<const __nv_bfloat16 *>(a.dy[which]) +
-                                       un.t * a.dy_stride[which];
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.y[which]) + un.t * a.y_stride[which];
-            float w[8];
-            if (e0 < e1)
-                load_weight(a.weight[which], da, db, w);
-#pragma unroll 1
-            for (int e = e0; e < e1; e += U) {
-                uint2 xa[U], xb[U], ya[U], yb[U];
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int h = (e + k) * HPW + g;
-                    xa[k] = xb[k] = ya[k] = yb[k] = make_uint2(0, 0);
-                    if (e + k < e1 && h < H) {
-                        ya[k] = load_piece(pdy + h * D + da);
-                        yb[k] = load_piece(pdy + h * D + db);
-                        if (norm) {
-                            xa[k] = load_piece(px + h * D + da);
-                            xb[k] = load_piece(px + h * D + db);
-                        }
-                    }
-                }
-                if (!have_angles) {                 // behind the first loads
-                    angles<D>(a, un.t, lane, c, s);
-                    have_angles = true;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[j] = -s[j];
-                }
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int h = (e + k) * HPW + g;
-                    float y[8];
-                    unpack4(ya[k], y);
-                    unpack4(yb[k], y + 4);
-                    if (turns)
-                        rotate<INTER>(y, c, s);
-                    if (norm) {
-                        float x[8];
-                        unpack4(xa[k], x);
-                        unpack4(xb[k], x + 4);
-                        float q = 0.f, d = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            q = fmaf(x[j], x[j], q);
-                            d = fmaf(y[j] * w[j], x[j], d);
-                        }
-                        const float r = rsqrtf(head_sum<D>(q) * (1.f / D) + a.eps);
-                        const float m = head_sum<D>(d) * (1.f / D) * r * r;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            dw[which][j] = fmaf(y[j] * r, x[j], dw[which][j]);
-                            y[j] = r * (y[j] * w[j] - x[j] * m);
-                        }
-                    }
-                    if (e + k < e1 && h < H) {
-                        store_piece(dst + h * D + da, y);
-                        store_piece(dst + h * D + db, y + 4);
-                    }
-                }
+    const bool turns_dims = 8 * p < a.half;
+    const int iq = (a.heads[0] + HPW - 1) / HPW, turns = iq + (a.heads[1] + HPW - 1) / HPW;
+    const unsigned segments = a.segments, units = static_cast<unsigned>(a.tokens) * segments;
+    const unsigned warps = gridDim.x * kWarps;
+    const int per = (turns + a.segments - 1) / a.segments;
+    uint8_t *mine = ring + warp * AHEAD * STAGE;
+    const uint32_t mine_u32 = smem_u32(mine) + lane * 16;
+
+    Turn fill;
+    fill.u = blockIdx.x * kWarps + warp;
+    fill.unit(units, warps, segments, per, turns);
+    Turn cur = fill;
+    // Copies the next turn (or nothing, at the end) as one group.
+    auto copy_turn = [&](int stage) {
+        if (fill.u < units) {
+            const int which = fill.e >= iq;
+            const int first = (fill.e - (which ? iq : 0)) * (HPW * D) + lane * 8;
+            const int left = a.heads[which] * D - first;        // elements of the row from here on
+            const uint32_t dst = mine_u32 + stage * STAGE;
+            if (!BWD || a.weight[which]) {          // a plain rotation's gradient needs no x
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.x[which]) +
+                                           fill.t * a.x_stride[which] + first;
+                if (left > 0)
+                    copy16_async(dst, src);
+                if (left > 256)
+                    copy16_async(dst + 512, src + 256);
+            }
+            if (BWD) {
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.dy[which]) +
+                                           fill.t * a.dy_stride[which] + first;
+                if (left > 0)
+                    copy16_async(dst + kTurn, src);
+                if (left > 256)
+                    copy16_async(dst + kTurn + 512, src + 256);
+            }
+            if (++fill.e == fill.end) {
+                fill.u += warps;
+                fill.unit(units, warps, segments, per, turns);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int k = 0; k < AHEAD; ++k)
+        copy_turn(k);
+
+    f2 dw[2][8];
+    if (BWD) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            dw[0][j] = dw[1][j] = 0;
     }
-    // partial[cta][which][d]
+    f2 c2[4], s2[4], ns2[4];
+    int stage = 0, t = -1;
+    while (cur.u < units) {
+        if (cur.t != t) {
+            t = cur.t;
+            float c[8], s[8];
+            angles<D>(a, t, lane, c, s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c2[j] = f2_pack(c[2 * j], c[2 * j + 1]);
+                s2[j] = f2_pack(BWD ? -s[2 * j] : s[2 * j], BWD ? -s[2 * j + 1] : s[2 * j + 1]);
+                ns2[j] = f2_pack(BWD ? s[2 * j] : -s[2 * j], BWD ? s[2 * j + 1] : -s[2 * j + 1]);
+            }
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+        __syncwarp();
+        const int which = cur.e >= iq;
+        const int h = (cur.e - (which ? iq : 0)) * HPW + g;
+        const bool live = h < a.heads[which];
+        const bool norm = a.weight[which] != nullptr;
+        const __nv_bfloat16 *sx = reinterpret_cast<const __nv_bfloat16 *>(mine + stage * STAGE) + g * D;
+        f2 x[8], y[8];
+        if (!BWD || norm)
+            unpack_pairs<INTER>(*reinterpret_cast<const uint4 *>(sx + da),
+                                *reinterpret_cast<const uint4 *>(sx + db), x);
+        if (BWD) {
+            const __nv_bfloat16 *sy = sx + kTurn / 2;
+            unpack_pairs<INTER>(*reinterpret_cast<const uint4 *>(sy + da),
+                                *reinterpret_cast<const uint4 *>(sy + db), y);
+        }
+        __syncwarp();                               // every lane has read the stage: refill it
+        copy_turn(stage);
+        stage = stage + 1 == AHEAD ? 0 : stage + 1;
+
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.y[which]) + t * a.y_stride[which] + h * D;
+        // words 2i, 2i + 1 of the weights, in the order of the pairs
+        auto weights = [&](int i) {
+            const float4 v = *reinterpret_cast<const float4 *>(&s_w[which][(i * LPH + p) * 4]);
+            return make_ulonglong2(f2_pack(v.x, v.y), f2_pack(v.z, v.w));
+        };
+        if (!BWD) {
+            if (norm) {
+                f2 q = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    q = f2_fma(x[j], x[j], q);
+                const float r = rsqrtf(head_sum<D>(f2_sum(q)) * (1.f / D) + a.eps);
+                const f2 r2 = f2_pack(r, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const ulonglong2 w = weights(i);
+                    x[2 * i] = f2_mul(f2_mul(x[2 * i], r2), w.x);
+                    x[2 * i + 1] = f2_mul(f2_mul(x[2 * i + 1], r2), w.y);
+                }
+            }
+            if (turns_dims)
+                rotate(x, c2, s2, ns2);
+            if (live)
+                store_pairs<INTER>(dst + da, dst + db, x);
+        } else {
+            if (turns_dims)
+                rotate(y, c2, s2, ns2);
+            if (norm) {
+                if (h - g + HPW > a.heads[which] && !live) {
+                    // lanes past the heads hold whatever was there
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = y[j] = 0;
+                }
+                f2 q = 0, d = 0, g2[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const ulonglong2 w = weights(i);
+                    q = f2_fma(x[2 * i], x[2 * i], q);
+                    q = f2_fma(x[2 * i + 1], x[2 * i + 1], q);
+                    g2[2 * i] = f2_mul(y[2 * i], w.x);              // u = g w
+                    g2[2 * i + 1] = f2_mul(y[2 * i + 1], w.y);
+                    d = f2_fma(g2[2 * i], x[2 * i], d);
+                    d = f2_fma(g2[2 * i + 1], x[2 * i + 1], d);
+                }
+                const float r = rsqrtf(head_sum<D>(f2_sum(q)) * (1.f / D) + a.eps);
+                const float m = -head_sum<D>(f2_sum(d)) * (1.f / D) * r * r;
+                const f2 r2 = f2_pack(r, r), m2 = f2_pack(m, m);
+                if (which) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dw[1][j] = f2_fma(f2_mul(y[j], r2), x[j], dw[1][j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dw[0][j] = f2_fma(f2_mul(y[j], r2), x[j], dw[0][j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = f2_mul(r2, f2_fma(x[j], m2, g2[j]));
+            }
+            if (live)
+                store_pairs<INTER>(dst + da, dst + db, y);
+        }
+        if (++cur.e == cur.end) {
+            cur.u += warps;
+            cur.unit(units, warps, segments, per, turns);
+        }
+    }
+    if (!BWD)
+        return;
+    // partial[cta][which][d], the warps' sums over the ring (no copy is in flight)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float *s_dw = reinterpret_cast<float *>(ring);      // [kWarps][D]
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         if (!a.dweight[which])
             continue;
+        float sum[16];                              // first members, then second members
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            const float2 v = f2_unpack(dw[which][j]);
+            sum[2 * j] = v.x;
+            sum[2 * j + 1] = v.y;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
 #pragma unroll
             for (int off = LPH; off < 32; off <<= 1)
-                dw[which][j] += __shfl_xor_sync(0xffffffffu, dw[which][j], off);
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], off);
         }
-        __syncthreads();                            // s_dw's readers of the queries' turn
+        __syncthreads();                            // the ring, or the queries' sums, have been read
         if (g == 0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s_dw[warp][da + j] = dw[which][j];
-                s_dw[warp][db + j] = dw[which][4 + j];
+            for (int j = 0; j < 8; ++j) {
+                s_dw[warp * D + (INTER ? da + 2 * j : da + j)] = sum[j];
+                s_dw[warp * D + (INTER ? da + 2 * j + 1 : db + j)] = sum[8 + j];
             }
         }
         __syncthreads();
@@ -355,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const Rope
             float v = 0.f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k)
-                v += s_dw[k][d];
+                v += s_dw[k * D + d];
             a.partial[(static_cast<long long>(blockIdx.x) * 2 + which) * D + d] = v;
         }
     }
@@ -394,34 +468,36 @@ int head_segments(const RopeArgs &a, int iters, int sm_count)
     return static_cast<int>(seg < 1 ? 1 : (seg > iters ? iters : seg));
 }
 
-template <int D>
-cudaError_t launch_fwd_d(RopeArgs &a, int sm_count, cudaStream_t stream)
+template <int D, bool BWD>
+cudaError_t launch_d(RopeArgs &a, int sm_count, cudaStream_t stream)
 {
-    constexpr int HPW = 32 / (D / 8);
-    a.segments = head_segments(a, (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW,
-                               sm_count);
-    const long long units = static_cast<long long>(a.tokens) * a.segments;
-    long long grid = (units + kWarps - 1) / kWarps;
-    if (grid > (1 << 20))
-        grid = 1 << 20;
-    const auto kernel = a.interleaved ? rope_fwd_kernel<D, true> : rope_fwd_kernel<D, false>;
-    return launch_dependent(kernel, dim3(static_cast<int>(grid)), kThreads, 0, stream, a);
-}
-
-template <int D>
-cudaError_t launch_bwd_d(RopeArgs &a, int sm_count, cudaStream_t stream)
-{
-    constexpr int HPW = 32 / (D / 8);
+    constexpr int HPW = 32 / (D / 16);
+    constexpr int SMEM = kWarps * (BWD ? kBwdAhead * 2 : kFwdAhead) * kTurn;
+    static_assert(SMEM >= kWarps * D * static_cast<int>(sizeof(float)), "the ring holds the warps' dw");
     a.segments = head_segments(a, (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW,
                                sm_count);
     const long long need = (static_cast<long long>(a.tokens) * a.segments + kWarps - 1) / kWarps;
-    long long grid = static_cast<long long>(sm_count) * kBwdCtas;
+    long long grid = static_cast<long long>(sm_count) * (BWD ? kBwdCtas : kFwdCtas);
     grid = grid < need ? grid : need;
     grid = grid < kRopeMaxCtas ? grid : kRopeMaxCtas;
     a.ctas = static_cast<int>(grid);
-    const auto kernel = a.interleaved ? rope_bwd_kernel<D, true> : rope_bwd_kernel<D, false>;
-    const cudaError_t e = launch_dependent(kernel, dim3(a.ctas), kThreads, 0, stream, a);
-    if (e != cudaSuccess || (!a.dweight[0] && !a.dweight[1]))
+    const auto kernel = a.interleaved ? rope_kernel<D, true, BWD> : rope_kernel<D, false, BWD>;
+    if (SMEM + 2 * D * sizeof(float) > 48 * 1024) {
+        static int attr_done[2][64] = {{0}};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return e;
+        if (dev >= 64 || !attr_done[a.interleaved][dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            if (e != cudaSuccess)
+                return e;
+            if (dev < 64)
+                attr_done[a.interleaved][dev] = 1;
+        }
+    }
+    const cudaError_t e = launch_dependent(kernel, dim3(a.ctas), kThreads, SMEM, stream, a);
+    if (e != cudaSuccess || !BWD || (!a.dweight[0] && !a.dweight[1]))
         return e;
     return launch_dependent(rope_dw_kernel, dim3(D / 32, 2), 1024, 0, stream, a, D);
 }
@@ -433,9 +509,9 @@ cudaError_t launch_rope_fwd(int head_dim, RopeArgs &a, int sm_count, cudaStream_
     if (a.tokens == 0)
         return cudaSuccess;
     switch (head_dim) {
-    case 64: return launch_fwd_d<64>(a, sm_count, stream);
-    case 128: return launch_fwd_d<128>(a, sm_count, stream);
-    case 256: return launch_fwd_d<256>(a, sm_count, stream);
+    case 64: return launch_d<64, false>(a, sm_count, stream);
+    case 128: return launch_d<128, false>(a, sm_count, stream);
+    case 256: return launch_d<256, false>(a, sm_count, stream);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -449,9 +525,9 @@ cudaError_t launch_rope_bwd(int head_dim, RopeArgs &a, int sm_count, cudaStream_
         return cudaSuccess;
     }
     switch (head_dim) {
-    case 64: return launch_bwd_d<64>(a, sm_count, stream);
-    case 128: return launch_bwd_d<128>(a, sm_count, stream);
-    case 256: return launch_bwd_d<256>(a, sm_count, stream);
+    case 64: return launch_d<64, true>(a, sm_count, stream);
+    case 128: return launch_d<128, true>(a, sm_count, stream);
+    case 256: return launch_d<256, true>(a, sm_count, stream);
     default: return cudaErrorInvalidValue;
     }
 }
