@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 constexpr int kConsumers = 4;
 constexpr int kDecThreads = kConsumers * 32;
 constexpr int kHeads = 8;               // query heads of a kv head per CTA
-constexpr int kSeqUnits = 8;            // units of a sequence besides its pages
-constexpr int kMinRun = 16;             // units per CTA at least
+constexpr int kSeqUnits = 20;           // units of a sequence besides its pages
+constexpr int kMinRun = 24;             // units per CTA at least
 constexpr int kMaxParts = 256;          // runs of one row of units at most (what one CTA merges)
 constexpr int kMaxCtas = 1024;          // in all rows, where there are fewer rows
 constexpr float kPShift = 14.f;
@@ -443,7 +443,7 @@ struct DecCfg {
     static constexpr int STAGE = 2 * PAGE;                      // a stage holds two pages
     static constexpr int NS = D == 64 ? 16 : 8;                 // stages of the CTA
     static constexpr int WS = NS / kConsumers;                  // stages of a warp
-    static constexpr int CTAS = D == 64 ? 5 : D == 128 ? 4 : 2; // resident per SM
+    static constexpr int CTAS = D == 64 ? 5 : D == 128 ? 3 : 2; // resident per SM
     static constexpr int MT = D / 16;
     static constexpr int KW = D / 32;               // code words of one token per lane
 };
@@ -613,10 +613,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     const uint8_t *pool = a.pool + static_cast<size_t>(kh) * C::PAGE;
 
     // ---------------------------------------------------- copies
-    // Fills of this warp's stages, WS pairs ahead: the pair at page `ahead` of
-    // segment `fill` next.  The ids of the warp's next 16 pairs are loaded
-    // together, lane l page l % 2 of pair l / 2.  Every turn commits one group
-    // of copies, also where there is nothing left to copy.
+    // Fills of this warp's stages, WS pairs ahead.  The ids of its next pairs
+    // in segment `fill`, up to 16, are loaded and checked together: lane l
+    // holds page l % 2 of pair l / 2.  Where there is no page (a lone last
+    // page's neighbour, an empty sequence) or the id is bad, page 0 is copied in
+    // its place and not used.  Every turn commits one group of copies, also
+    // where there is nothing left to copy.
     RunCursor fill;
     fill.s = s_first;
     fill.at = s_first_unit;
@@ -624,54 +626,43 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     if (!fill.enter(a, u0, u1))
         return;                                     // (the whole CTA) no page in this run
     RunCursor seg = fill;
-    int ahead = fill.first(warp), ids = 0, id_lane = 0;
-    uint32_t bad_stages = 0;
-    bool more = true;
+    int ahead = fill.first(warp), ids = 0, id_lane = 0, left = 0;
+    uint32_t bad_ids = 0, bad_stages = 0;
     auto load_ids = [&]() {
         while (ahead >= fill.j1) {
-            more = fill.next(a, u0, u1);
-            if (!more)
+            if (!fill.next(a, u0, u1))
                 return;
             ahead = fill.first(warp);
         }
+        left = min(16, (fill.j1 - ahead + 2 * kConsumers - 1) / (2 * kConsumers));
         const int j = ahead + (lane >> 1) * (2 * kConsumers) + (lane & 1);
-        ids = j < fill.j1 && fill.tokens > 0        // an empty sequence has no page
-                  ? __ldg(a.tables + static_cast<long long>(fill.s) * a.capacity + j)
-                  : -1;
+        const bool listed = j < fill.j1 && fill.tokens > 0;
+        ids = listed ? __ldg(a.tables + static_cast<long long>(fill.s) * a.capacity + j) : 0;
+        const bool bad = static_cast<unsigned>(ids) >= static_cast<unsigned>(a.num_blocks);
+        bad_ids = __ballot_sync(0xffffffffu, bad && listed);
+        ids = bad ? 0 : ids;
         id_lane = 0;
+        ahead += 32 * kConsumers;
     };
     const uint32_t my_ring = smem_u32(dsm) + warp * C::WS * C::STAGE + lane * 16;
     const uint8_t *my_pool = pool + lane * 16;
+    const bool pages_exist = a.num_blocks > 0;
     auto issue = [&](int ws) {
-        if (more) {
+        if (left > 0) {
             constexpr int PIECES = C::PAGE / 16;    // 16-byte pieces of a page
-            const unsigned blocks = static_cast<unsigned>(a.num_blocks);
-            const int id0 = __shfl_sync(0xffffffffu, ids, id_lane);
-            const int id1 = __shfl_sync(0xffffffffu, ids, id_lane + 1);
-            const bool two = ahead + 1 < fill.j1;
-            // (an empty sequence's one page is not there to be copied)
-            const bool bad = fill.tokens > 0 && (static_cast<unsigned>(id0) >= blocks ||
-                                                 (two && static_cast<unsigned>(id1) >= blocks));
-            const uint8_t *p0 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * page_bytes;
-            const uint32_t dst = my_ring + ws * C::STAGE;
-            if (two && !bad) {
-                const uint8_t *p1 = my_pool + static_cast<uint64_t>(static_cast<uint32_t>(id1)) * page_bytes -
-                                    C::PAGE;
-                copy_pair<PIECES>(dst, p0, lane >= PIECES % 32 ? p1 : p0, p1, lane);
-            } else if (fill.tokens > 0 && !bad) {
-#pragma unroll 1
-                for (int k = 0; k < PIECES; k += 32)
-                    if (k + lane < PIECES)
-                        copy16_async<0>(dst + k * 16, p0 + k * 16);
-            }
-            if (bad) {
+            const uint32_t id0 = __shfl_sync(0xffffffffu, ids, id_lane);
+            const uint32_t id1 = __shfl_sync(0xffffffffu, ids, id_lane + 1);
+            const uint8_t *p0 = my_pool + static_cast<uint64_t>(id0) * page_bytes;
+            const uint8_t *p1 = my_pool + static_cast<uint64_t>(id1) * page_bytes - C::PAGE;
+            if (pages_exist)
+                copy_pair<PIECES>(my_ring + ws * C::STAGE, p0, lane >= PIECES % 32 ? p1 : p0, p1, lane);
+            if (bad_ids >> id_lane & 3u) {
                 bad_stages |= 1u << ws;
                 if (lane == 0)
                     record(a.status, VFA_ERR_BAD_BLOCK);
             }
-            ahead += 2 * kConsumers;
             id_lane += 2;
-            if (ahead >= fill.j1 || id_lane == 32)
+            if (--left == 0)
                 load_ids();
         }
         copy_commit();
