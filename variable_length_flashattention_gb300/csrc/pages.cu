@@ -359,11 +359,20 @@ __device__ __forceinline__ uint32_t use_word(const PageArgs &a, uint32_t *s_bits
 {
     const int lane = threadIdx.x & 31;
     const int words = (a.num_blocks + 31) / 32;
-    for (int w = threadIdx.x >> 5; w < words; w += kPlanThreads / 32) {
-        const int id = w * 32 + lane;
-        const uint32_t bits = __ballot_sync(0xffffffffu, id >= a.num_blocks || a.refs[id] > 0);
-        if (lane == 0)
-            s_bits[w] = bits;
+    constexpr int STEP = kPlanThreads / 32, U = 8;  // loads in flight per warp
+    for (int w0 = threadIdx.x >> 5; w0 < words; w0 += U * STEP) {
+        int ref[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int id = (w0 + u * STEP) * 32 + lane;
+            ref[u] = id < a.num_blocks ? a.refs[id] : 1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, ref[u] > 0);
+            if (lane == 0 && w0 + u * STEP < words)
+                s_bits[w0 + u * STEP] = bits;
+        }
     }
     __syncthreads();
     const uint32_t word = static_cast<int>(threadIdx.x) < words ? s_bits[threadIdx.x] : 0xffffffffu;
@@ -514,16 +523,18 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PageA
     int U, total, below;
     const uint32_t word = use_word(a, s_bits, &U, s_warp);
     const int id0 = threadIdx.x * 32;
-    // pages past the pool's end have set bits, but no page of the pool is above them
-    int before = block_scan(__popc(word), &total, s_warp);
+    // (pages past the pool's end have set bits, but no page of the pool is above them)
+    __shared__ int s_before[kPlanThreads];              // used pages below the word
+    s_before[threadIdx.x] = block_scan(__popc(word), &total, s_warp);
     {
         const int part = U - id0;                   // pages of this word below U
         const uint32_t mask = part <= 0 ? 0u : part >= 32 ? 0xffffffffu : (1u << part) - 1;
         block_scan(__popc(word & mask), &below, s_warp);
     }
-    for (int k = 0; k < 32 && id0 + k < a.num_blocks; ++k) {
-        const int id = id0 + k;
-        const bool is_used = word >> k & 1;
+    for (int id = threadIdx.x; id < a.num_blocks; id += kPlanThreads) {
+        const uint32_t bits = s_bits[id >> 5];
+        const int before = s_before[id >> 5] + __popc(bits & ((1u << (id & 31)) - 1));
+        const bool is_used = bits >> (id & 31) & 1;
         int r = -1;
         if (is_used && id >= U) {
             r = before - below;
@@ -533,7 +544,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(const PageA
             w.dst[r] = id;
         }
         w.rank[id] = r;
-        before += is_used;
     }
     if (threadIdx.x == 0) {
         w.head[H_N] = U - below;
