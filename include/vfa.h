@@ -579,10 +579,11 @@ vfa_status vfa_kv4_gather(void *k, void *v, int64_t k_stride, int64_t v_stride, 
  *              VFA_ERR_INVALID_ARG.
  * lse          nullable device f32 [num_seqs, num_q_heads].
  * workspace    device scratch of vfa_kv4_decode_workspace_bytes() bytes,
- *              256-byte aligned: tickets, then partial states.  It must hold
- *              zeros before its first use; every call leaves the tickets
- *              zero.  Calls sharing it must be stream-ordered and have the
- *              sizes it was made for.
+ *              256-byte aligned: partial states, then tickets.  It must hold
+ *              zeros before its first use; every call leaves the tickets zero.
+ *              A workspace made for num_seqs sequences serves any smaller
+ *              number with the same heads and head_dim.  Calls sharing it
+ *              must be stream-ordered.
  * Device-detected: a token count out of range or a listed page id outside
  * [0, num_blocks) stores VFA_ERR_BAD_BLOCK and leaves that sequence's out and
  * lse rows (of the kv heads that saw it) as they were.

@@ -203,8 +203,7 @@ def test_decode_lengths(vfa, lens):
     ws = vfa.alloc_kv4_decode_workspace(len(lens), 4, 2, 64)
     first = _run(vfa, case, workspace=ws)
     _check_decode(first, case)
-    tickets = (len(lens) * 2 * 4 + 255) // 256 * 256
-    assert (ws[:tickets] == 0).all()
+    assert (ws[-len(lens) * 2 * 4:] == 0).all()           # the tickets
     second = _run(vfa, case, workspace=ws)                # the workspace serves again
     assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
 
@@ -308,6 +307,16 @@ def test_decode_captured_twice_with_one_workspace(vfa):
     torch.cuda.synchronize()
     _check_decode(outs[0], a)
     _check_decode(outs[1], b)
+
+
+def test_one_workspace_for_smaller_batches(vfa):
+    """A workspace made for the largest batch serves the smaller ones between."""
+    big = _decode_case([3000, 1, 77, 900, 2500, 40, 0, 129, 4000], 8, 2, 128, seed=6)
+    ws = vfa.alloc_kv4_decode_workspace(9, 8, 2, 128)
+    for n in (9, 2, 5, 1, 9, 3, 9):
+        q, pool, tables, lens, dk, dv = big
+        case = (q[:n], pool, tables[:n], lens[:n], dk, dv)
+        _check_decode(_run(vfa, case, workspace=ws), case)
 
 
 def test_offsets_past_32_bits(vfa):

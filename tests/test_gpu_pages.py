@@ -157,6 +157,17 @@ def test_refusals_change_nothing(vfa):
     st.fork([0, 1], [2, 3])                                # and the state still works
 
 
+def test_token_counts_stay_within_32_bits(vfa):
+    st = State(vfa, 8, 2, 4, 2 ** 30)
+    st.extend([2 ** 30 + 5, 0])
+    v = st.vfa
+    v.pages_extend(st.d_refs, st.d_tables, st.d_counts, st.i32([2 ** 30, 1]), st.bs, st.ws,
+                   status=st.status)
+    st.check(v.VFA_ERR_BAD_BLOCK)                          # 2^31 + 5 tokens: nothing changes
+    st.extend([2 ** 30 - 6, 2 ** 30])
+    st.free([0])
+
+
 def test_bad_table_entries_are_recorded(vfa):
     st = State(vfa, 30, 4, 5, 4)
     st.extend([9, 4, 0, 0])

@@ -253,8 +253,8 @@ struct Kv4DecodeArgs {
     void *out;                              // bf16, as q
     float *lse;                             // [num_seqs, num_q_heads], nullable
     int32_t *status;                        // nullable
-    int32_t *tickets;                       // workspace: [num_seqs, head chunks], zero between calls
     float *part;                            // workspace: partial states
+    int32_t *tickets;                       // workspace: [num_seqs, head chunks], zero between calls
     int num_seqs, capacity, num_blocks, num_q_heads, num_kv_heads;
     float scale_log2;                       // logit scale * descale_k * log2(e)
     float descale_v;

@@ -1102,9 +1102,16 @@ dim3 move_grid(const Kv4MoveArgs &a, int head_dim, int sm_count)
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
 
-size_t ticket_bytes(int num_seqs, int rows)
+// The workspace: partial states, then the tickets.  Where the tickets start
+// does not depend on the number of sequences, so a workspace made for a batch
+// serves smaller ones too.
+size_t part_bytes(int rows, int head_dim)
 {
-    const size_t n = static_cast<size_t>(num_seqs) * rows * sizeof(int32_t);
+    // runs: kMaxParts for one row, kMaxCtas in all rows or one per row
+    const long long all = rows > kMaxCtas ? rows : kMaxCtas;
+    const size_t runs = all < static_cast<long long>(rows) * kMaxParts
+                            ? static_cast<size_t>(all) : static_cast<size_t>(rows) * kMaxParts;
+    const size_t n = runs * 2 * kHeads * (head_dim + 4) * sizeof(float);
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
@@ -1137,11 +1144,7 @@ size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_head
 {
     const int group = num_q_heads / num_kv_heads;
     const int rows = num_kv_heads * ((group + kHeads - 1) / kHeads);
-    // runs: kMaxParts for one row, kMaxCtas in all rows or one per row
-    const long long all = rows > kMaxCtas ? rows : kMaxCtas;
-    const size_t runs = all < static_cast<long long>(rows) * kMaxParts
-                            ? static_cast<size_t>(all) : static_cast<size_t>(rows) * kMaxParts;
-    return ticket_bytes(num_seqs, rows) + runs * 2 * kHeads * (head_dim + 4) * sizeof(float);
+    return part_bytes(rows, head_dim) + static_cast<size_t>(num_seqs) * rows * sizeof(int32_t);
 }
 
 cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, int sm_count,
@@ -1149,9 +1152,9 @@ cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, i
 {
     const int group = a.num_q_heads / a.num_kv_heads;
     const int rows = a.num_kv_heads * ((group + kHeads - 1) / kHeads);
-    a.tickets = static_cast<int32_t *>(workspace);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                       ticket_bytes(a.num_seqs, rows));
+    a.part = static_cast<float *>(workspace);
+    a.tickets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
+                                            part_bytes(rows, head_dim));
     switch (head_dim) {
     case 64: return launch_decode_d<64>(a, sm_count, stream);
     case 128: return launch_decode_d<128>(a, sm_count, stream);

@@ -22,6 +22,8 @@
 // Bound: HBM for the copied pages (2 bytes moved per byte), launch latency
 // for the rest: with 1024 pages the one-CTA form takes an extension from three
 // launches (9.9 us) to one, a fork from four to two.
+#include <climits>
+
 #include "internal.h"
 #include "launch.cuh"
 
@@ -145,7 +147,7 @@ __device__ __forceinline__ int plan_extend(const PageArgs &a, int used, int32_t 
         int need = 0;
         if (s < a.num_seqs) {
             const long long n = a.counts[s], add = a.add[s];
-            if (n < 0 || add < 0 || n + add > room)
+            if (n < 0 || add < 0 || n + add > room || n + add > INT_MAX)
                 bad = true;
             else
                 need = static_cast<int>((n + add + a.block_size - 1) / a.block_size -
