@@ -447,8 +447,12 @@ _INV_2PI = Fraction("0.159154943091895335768883763372514362034459645740456448747
 
 
 # The operators below are called once per layer of a step, often on little
-# data, so their checks are one expression per tensor and the messages are
-# worked out only where one fails.
+# data, where the host's time is the call's time: a check is one expression per
+# tensor, and the message is worked out only where it fails.
+
+_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.uint8)
+
 
 def _refuse(t, dtype, name, dev):
     if not t.is_cuda:
@@ -470,15 +474,15 @@ def _device(t: torch.Tensor, name: str) -> int:
 
 
 def _dense(t: torch.Tensor, dtype, name: str, dev: int):
-    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
         _refuse(t, dtype, name, dev)
 
 
 def _rows(t: torch.Tensor, shape, name: str, dev: int) -> int:
     """t: bf16 [tokens, heads, head_dim], heads and dims contiguous; returns the token stride
     in elements (one or no token has no neighbour: the packed distance)."""
-    if t.get_device() != dev or t.dtype != torch.bfloat16:
-        _refuse(t, torch.bfloat16, name, dev)
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _refuse(t, _BF16, name, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must be [tokens, heads, head_dim] = {tuple(shape)}, got "
                          f"{tuple(t.shape)}")
@@ -499,6 +503,14 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_rows(like, stream) -> torch.Tensor:
+    """A packed tensor shaped like `like`, whose token stride is its largest."""
+    if stream is None:
+        return torch.empty_like(like)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like)
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -531,35 +543,50 @@ def rope_table(inv_freq, axes=None, device="cuda") -> torch.Tensor:
 
 def _rope_inputs(q, k, positions, table, q_weight, k_weight):
     """Checks; (device, q's and k's token strides, position axes, rotated dims)."""
-    dev = _device(q, "q")
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    dev = q.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse(q, _BF16, "q", dev)
+    qshape, kshape = q.shape, k.shape
+    if len(qshape) != 3 or len(kshape) != 3 or qshape[0] != kshape[0] or qshape[2] != kshape[2]:
         raise ValueError("q [T, Hq, D] and k [T, Hkv, D] must agree in tokens and head_dim")
-    qs, ks = _rows(q, q.shape, "q", dev), _rows(k, k.shape, "k", dev)
+    qs, ks = _rows(q, qshape, "q", dev), _rows(k, kshape, "k", dev)
+    T, _, D = qshape
     axes = rot = 0
     if table is not None:
-        _dense(table, torch.int64, "table", dev)
-        if table.dim() != 2 or table.shape[1] != 2:
+        tshape = table.shape
+        if table.get_device() != dev or table.dtype is not _I64 or not table.is_contiguous():
+            _refuse(table, _I64, "table", dev)
+        if len(tshape) != 2 or tshape[1] != 2:
             raise ValueError("table must be [rotary_dim / 2, 2], as rope_table makes it")
-        rot = 2 * table.shape[0]
+        rot = 2 * tshape[0]
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _dense(positions, torch.int32, "positions", dev)
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.dim() > 2 or positions.shape[-1] != q.shape[0]:
+        if positions.get_device() != dev or positions.dtype is not _I32 or \
+                not positions.is_contiguous():
+            _refuse(positions, _I32, "positions", dev)
+        pshape = positions.shape
+        axes = 1 if len(pshape) == 1 else pshape[0]
+        if not 1 <= len(pshape) <= 2 or pshape[-1] != T:
             raise ValueError("positions must be [tokens] or [axes, tokens]")
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _dense(w, torch.float32, n, dev)
-            if w.dim() != 1 or w.shape[0] != q.shape[2]:
-                raise ValueError(f"{n} must be [head_dim]")
+    if q_weight is not None:
+        _rope_weight(q_weight, "q_weight", D, dev)
+    if k_weight is not None:
+        _rope_weight(k_weight, "k_weight", D, dev)
     return dev, qs, ks, axes, rot
+
+
+def _rope_weight(w, name, D, dev):
+    if w.get_device() != dev or w.dtype is not _F32 or not w.is_contiguous():
+        _refuse(w, _F32, name, dev)
+    if w.shape != (D,):
+        raise ValueError(f"{name} must be [head_dim]")
 
 
 def _row_output(given, like, name, dev, stream):
     """(the output, its token stride): the given one checked, or a new one shaped like `like`."""
     if given is None:
-        given = _empty(like.shape, torch.bfloat16, like.device, stream)
-        return given, like.shape[1] * like.shape[2]
+        shape = like.shape
+        return _empty_rows(like, stream), shape[1] * shape[2]
     return given, _rows(given, like.shape, name, dev)
 
 
@@ -577,7 +604,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     q_out, qos = _row_output(q_out, q, "q_out", dev, stream)
     k_out, kos = _row_output(k_out, k, "k_out", dev, stream)
     T, Hq, D = q.shape
-    st = lib().vfa_qk_norm_rope_fwd(
+    st = (_lib or lib()).vfa_qk_norm_rope_fwd(
         q.data_ptr(), k.data_ptr(), qs, ks, _address(positions), axes, _address(table), rot,
         1 if interleaved else 0, _address(q_weight), _address(k_weight), eps, T, Hq, k.shape[1], D,
         q_out.data_ptr(), k_out.data_ptr(), qos, kos, _raw_stream(stream, dev))
@@ -587,7 +614,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
 
 
 def alloc_qk_norm_rope_bwd_workspace(head_dim: int, device="cuda") -> torch.Tensor:
-    n = lib().vfa_qk_norm_rope_bwd_workspace_bytes(head_dim)
+    n = (_lib or lib()).vfa_qk_norm_rope_bwd_workspace_bytes(head_dim)
     if n == 0:
         raise VfaError(VFA_ERR_UNSUPPORTED, f"no workspace size for head_dim {head_dim}")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -617,17 +644,17 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
         if g is None:
             g = _empty(w.shape, torch.float32, w.device, stream)
         else:
-            _dense(g, torch.float32, n, dev)
+            _dense(g, _F32, n, dev)
             if g.shape != w.shape:
                 raise ValueError(f"{n} must be [head_dim]")
         grads[i] = g
     if workspace is not None:
         _dense(workspace, workspace.dtype, "workspace", dev)
     elif q_weight is not None or k_weight is not None:
-        n = lib().vfa_qk_norm_rope_bwd_workspace_bytes(q.shape[2])
+        n = (_lib or lib()).vfa_qk_norm_rope_bwd_workspace_bytes(q.shape[2])
         workspace = _empty(n, torch.uint8, q.device, stream)
     T, Hq, D = q.shape
-    st = lib().vfa_qk_norm_rope_bwd(
+    st = (_lib or lib()).vfa_qk_norm_rope_bwd(
         q.data_ptr(), k.data_ptr(), qs, ks, dq_out.data_ptr(), dk_out.data_ptr(), dqos, dkos,
         _address(positions), axes, _address(table), rot, 1 if interleaved else 0,
         _address(q_weight), _address(k_weight), eps, T, Hq, k.shape[1], D, dq.data_ptr(),
@@ -642,7 +669,7 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
 
 def kv4_block_bytes(num_kv_heads: int, head_dim: int) -> int:
     """Bytes of one page of 16 tokens (vfa_kv4_block_bytes)."""
-    n = lib().vfa_kv4_block_bytes(num_kv_heads, head_dim)
+    n = (_lib or lib()).vfa_kv4_block_bytes(num_kv_heads, head_dim)
     if n == 0:
         raise VfaError(VFA_ERR_UNSUPPORTED, "no 4-bit page size for these arguments")
     return int(n)
@@ -658,10 +685,10 @@ def alloc_kv4_pool(num_blocks: int, num_kv_heads: int, head_dim: int,
 def _kv4_pool(pool, tables, status):
     """Checks; (device, head_dim)."""
     dev = _device(pool, "pool")
-    _dense(pool, torch.uint8, "pool", dev)
-    _dense(tables, torch.int32, "tables", dev)
+    _dense(pool, _U8, "pool", dev)
+    _dense(tables, _I32, "tables", dev)
     if status is not None:
-        _dense(status, torch.int32, "status", dev)
+        _dense(status, _I32, "status", dev)
     if pool.dim() != 3 or tables.dim() != 2:
         raise ValueError("pool must be [num_blocks, num_kv_heads, 18 * head_dim], tables "
                          "[num_seqs, capacity]")
@@ -672,8 +699,8 @@ def _kv4_pool(pool, tables, status):
 
 
 def _token_map(cu_seqlens, start_positions, tables, dev):
-    _dense(cu_seqlens, torch.int32, "cu_seqlens", dev)
-    _dense(start_positions, torch.int32, "start_positions", dev)
+    _dense(cu_seqlens, _I32, "cu_seqlens", dev)
+    _dense(start_positions, _I32, "start_positions", dev)
     S = tables.shape[0]
     if cu_seqlens.numel() != S + 1 or start_positions.numel() != S:
         raise ValueError("cu_seqlens [num_seqs + 1] and start_positions [num_seqs] must match "
@@ -692,7 +719,7 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, tables: torc
     blocks, Hkv, _ = pool.shape
     T = k.shape[0]
     ks, vs = _rows(k, (T, Hkv, D), "k", dev), _rows(v, (T, Hkv, D), "v", dev)
-    st = lib().vfa_kv4_write(k.data_ptr(), v.data_ptr(), ks, vs, T, pool.data_ptr(), blocks,
+    st = (_lib or lib()).vfa_kv4_write(k.data_ptr(), v.data_ptr(), ks, vs, T, pool.data_ptr(), blocks,
                              tables.data_ptr(), tables.shape[1], cu_seqlens.data_ptr(),
                              start_positions.data_ptr(), tables.shape[0], Hkv, D, descale_k,
                              descale_v, _address(status), _raw_stream(stream, dev))
@@ -720,7 +747,7 @@ def kv4_gather(pool: torch.Tensor, tables: torch.Tensor, cu_seqlens: torch.Tenso
         v_out, vs = _empty(shape, torch.bfloat16, pool.device, stream), Hkv * D
     else:
         vs = _rows(v_out, shape, "v_out", dev)
-    st = lib().vfa_kv4_gather(k_out.data_ptr(), v_out.data_ptr(), ks, vs, total_tokens,
+    st = (_lib or lib()).vfa_kv4_gather(k_out.data_ptr(), v_out.data_ptr(), ks, vs, total_tokens,
                               pool.data_ptr(), blocks, tables.data_ptr(), tables.shape[1],
                               cu_seqlens.data_ptr(), start_positions.data_ptr(), tables.shape[0],
                               Hkv, D, descale_k, descale_v, _address(status),
@@ -733,7 +760,7 @@ def kv4_gather(pool: torch.Tensor, tables: torch.Tensor, cu_seqlens: torch.Tenso
 def alloc_kv4_decode_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                device="cuda") -> torch.Tensor:
     """A zero-filled workspace for kv4_decode (its tickets start at zero)."""
-    n = lib().vfa_kv4_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim)
+    n = (_lib or lib()).vfa_kv4_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim)
     if n == 0:
         raise VfaError(VFA_ERR_UNSUPPORTED, "no 4-bit decode workspace for these sizes")
     return torch.zeros(n, dtype=torch.uint8, device=device)
@@ -748,8 +775,8 @@ def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
     (vfa_kv4_decode).  Keep a workspace from alloc_kv4_decode_workspace between calls;
     without one, each call allocates and clears its own."""
     dev, D = _kv4_pool(pool, tables, status)
-    _dense(q, torch.bfloat16, "q", dev)
-    _dense(token_counts, torch.int32, "token_counts", dev)
+    _dense(q, _BF16, "q", dev)
+    _dense(token_counts, _I32, "token_counts", dev)
     if q.dim() != 3 or q.shape[0] != tables.shape[0] or q.shape[2] != D:
         raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
     S, Hq, _ = q.shape
@@ -757,21 +784,21 @@ def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
     if token_counts.numel() != S:
         raise ValueError("token_counts must be [num_seqs]")
     if out is None:
-        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+        out = _empty_rows(q, stream)
     else:
-        _dense(out, torch.bfloat16, "out", dev)
+        _dense(out, _BF16, "out", dev)
     if lse is None:
         lse = _empty((S, Hq), torch.float32, q.device, stream)
     else:
-        _dense(lse, torch.float32, "lse", dev)
+        _dense(lse, _F32, "lse", dev)
     if workspace is None:
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             workspace = alloc_kv4_decode_workspace(S, Hq, Hkv, D, device=q.device)
     else:
-        _dense(workspace, torch.uint8, "workspace", dev)
+        _dense(workspace, _U8, "workspace", dev)
     if out.shape != q.shape or lse.shape != (S, Hq):
         raise ValueError("out must have q's shape and lse [num_seqs, num_q_heads]")
-    st = lib().vfa_kv4_decode(q.data_ptr(), pool.data_ptr(), blocks, tables.data_ptr(),
+    st = (_lib or lib()).vfa_kv4_decode(q.data_ptr(), pool.data_ptr(), blocks, tables.data_ptr(),
                               tables.shape[1], token_counts.data_ptr(), S, Hq, Hkv, D, descale_k,
                               descale_v, softmax_scale, out.data_ptr(), lse.data_ptr(),
                               _address(status), workspace.data_ptr(), workspace.numel(),
@@ -786,7 +813,7 @@ def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
 def alloc_pages_workspace(num_blocks: int, num_seqs: int, num_forks: int = 0,
                           device="cuda") -> torch.Tensor:
     """Scratch of the page operations for at least these sizes."""
-    n = lib().vfa_pages_workspace_bytes(num_blocks, num_seqs, num_forks)
+    n = (_lib or lib()).vfa_pages_workspace_bytes(num_blocks, num_seqs, num_forks)
     if n == 0:
         raise VfaError(VFA_ERR_INVALID_ARG, "no page workspace for these sizes")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -795,11 +822,11 @@ def alloc_pages_workspace(num_blocks: int, num_seqs: int, num_forks: int = 0,
 def _page_state(refcounts, tables, token_counts, status):
     """Checks; (device, num_blocks, capacity, num_seqs)."""
     dev = _device(refcounts, "refcounts")
-    _dense(refcounts, torch.int32, "refcounts", dev)
-    _dense(tables, torch.int32, "tables", dev)
-    _dense(token_counts, torch.int32, "token_counts", dev)
+    _dense(refcounts, _I32, "refcounts", dev)
+    _dense(tables, _I32, "tables", dev)
+    _dense(token_counts, _I32, "token_counts", dev)
     if status is not None:
-        _dense(status, torch.int32, "status", dev)
+        _dense(status, _I32, "status", dev)
     if refcounts.dim() != 1 or tables.dim() != 2 or token_counts.dim() != 1 or \
             token_counts.shape[0] != tables.shape[0]:
         raise ValueError("refcounts [num_blocks], tables [num_seqs, capacity] and token_counts "
@@ -811,15 +838,14 @@ def _page_state(refcounts, tables, token_counts, status):
 def _pool_list(pools, num_blocks, dev):
     """Host arrays of the pools' addresses and page sizes."""
     n = len(pools)
-    ptrs, sizes = [], []
     for i, p in enumerate(pools):
         if p.get_device() != dev or not p.is_contiguous():
             _refuse(p, p.dtype, f"pools[{i}]", dev)
-        if p.dim() < 2 or p.shape[0] != num_blocks:
+        if p.dim() < 2 or p.size(0) != num_blocks:
             raise ValueError(f"pools[{i}] must hold {num_blocks} pages")
-        ptrs.append(p.data_ptr())
-        sizes.append(p.nbytes // max(num_blocks, 1))
-    return (_P * n)(*ptrs), (_I * n)(*sizes), n
+    blocks = max(num_blocks, 1)
+    return ((_P * n)(*[p.data_ptr() for p in pools]),
+            (_I * n)(*[p.nbytes // blocks for p in pools]), n)
 
 
 def pages_extend(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
@@ -827,11 +853,11 @@ def pages_extend(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: to
                  status: Optional[torch.Tensor] = None, stream=None):
     """token_counts += add_tokens, with new pages where rows need them (vfa_pages_extend)."""
     dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
-    _dense(workspace, torch.uint8, "workspace", dev)
-    _dense(add_tokens, torch.int32, "add_tokens", dev)
+    _dense(workspace, _U8, "workspace", dev)
+    _dense(add_tokens, _I32, "add_tokens", dev)
     if add_tokens.shape != token_counts.shape:
         raise ValueError("add_tokens must be [num_seqs]")
-    st = lib().vfa_pages_extend(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+    st = (_lib or lib()).vfa_pages_extend(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
                                 token_counts.data_ptr(), S, add_tokens.data_ptr(), block_size,
                                 workspace.data_ptr(), workspace.numel(), _address(status),
                                 _raw_stream(stream, dev))
@@ -845,15 +871,15 @@ def pages_fork(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torc
     """Rows children[i] become copies of rows parents[i]: full pages shared, a partly filled
     last page copied in every pool (vfa_pages_fork).  A negative parent skips the entry."""
     dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
-    _dense(workspace, torch.uint8, "workspace", dev)
-    _dense(parents, torch.int32, "parents", dev)
-    _dense(children, torch.int32, "children", dev)
+    _dense(workspace, _U8, "workspace", dev)
+    _dense(parents, _I32, "parents", dev)
+    _dense(children, _I32, "children", dev)
     if parents.dim() != 1 or parents.shape != children.shape:
         raise ValueError("parents and children must be [num_forks]")
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
     if parents.shape[0] == 0:
         return
-    st = lib().vfa_pages_fork(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+    st = (_lib or lib()).vfa_pages_fork(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
                               token_counts.data_ptr(), S, parents.data_ptr(), children.data_ptr(),
                               parents.shape[0], ptrs, sizes, n, block_size, workspace.data_ptr(),
                               workspace.numel(), _address(status), _raw_stream(stream, dev))
@@ -866,11 +892,11 @@ def pages_free(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torc
                stream=None):
     """Rows seqs[i] give up their pages (vfa_pages_free).  A negative entry is skipped."""
     dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
-    _dense(seqs, torch.int32, "seqs", dev)
+    _dense(seqs, _I32, "seqs", dev)
     n = seqs.numel()
     if n == 0:
         return
-    st = lib().vfa_pages_free(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+    st = (_lib or lib()).vfa_pages_free(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
                               token_counts.data_ptr(), S, seqs.data_ptr(), n, block_size,
                               _address(status), _raw_stream(stream, dev))
     if st:
@@ -886,18 +912,18 @@ def pages_compact(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: t
     """Moves the used pages to the low end of every pool (vfa_pages_compact); refcounts and
     tables are rewritten in place unless outputs are given.  Returns int32 [1]: used pages."""
     dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
-    _dense(workspace, torch.uint8, "workspace", dev)
+    _dense(workspace, _U8, "workspace", dev)
     refcounts_out = refcounts if refcounts_out is None else refcounts_out
     tables_out = tables if tables_out is None else tables_out
     if num_used is None:
         num_used = _empty(1, torch.int32, refcounts.device, stream)
     for t, x, n in ((refcounts_out, refcounts, "refcounts_out"), (tables_out, tables, "tables_out")):
-        _dense(t, torch.int32, n, dev)
+        _dense(t, _I32, n, dev)
         if t.shape != x.shape:
             raise ValueError(f"{n} must have shape {tuple(x.shape)}")
-    _dense(num_used, torch.int32, "num_used", dev)
+    _dense(num_used, _I32, "num_used", dev)
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
-    st = lib().vfa_pages_compact(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+    st = (_lib or lib()).vfa_pages_compact(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
                                  token_counts.data_ptr(), S, ptrs, sizes, n, block_size,
                                  refcounts_out.data_ptr(), tables_out.data_ptr(),
                                  num_used.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -913,17 +939,17 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
     if not pools:
         return
     dev = _device(src, "src")
-    _dense(src, torch.int32, "src", dev)
-    _dense(dst, torch.int32, "dst", dev)
+    _dense(src, _I32, "src", dev)
+    _dense(dst, _I32, "dst", dev)
     if status is not None:
-        _dense(status, torch.int32, "status", dev)
+        _dense(status, _I32, "status", dev)
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be [n]")
     blocks = pools[0].shape[0]
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
     if src.shape[0] == 0:
         return
-    st = lib().vfa_pages_copy(ptrs, sizes, n, src.data_ptr(), dst.data_ptr(), src.shape[0], blocks,
+    st = (_lib or lib()).vfa_pages_copy(ptrs, sizes, n, src.data_ptr(), dst.data_ptr(), src.shape[0], blocks,
                               _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
@@ -932,7 +958,7 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
 def debug_bounded_wait(status: torch.Tensor, stream=None):
     """vfa_debug_bounded_wait: a wait nothing satisfies must end in VFA_ERR_TIMEOUT."""
     _need(status, torch.int32, "status")
-    _check(lib().vfa_debug_bounded_wait(_ptr(status), _stream(stream)))
+    _check((_lib or lib()).vfa_debug_bounded_wait(_ptr(status), _stream(stream)))
 
 
 def debug_paged_gather(k_pool: torch.Tensor, v_pool: torch.Tensor, tile_blocks: torch.Tensor,
@@ -940,6 +966,6 @@ def debug_paged_gather(k_pool: torch.Tensor, v_pool: torch.Tensor, tile_blocks: 
                        status: Optional[torch.Tensor] = None, stream=None):
     nb, bs, Hkv, D = k_pool.shape
     S, cap = tile_blocks.shape
-    _check(lib().vfa_debug_paged_gather(_ptr(k_pool), _ptr(v_pool), nb, _ptr(tile_blocks),
+    _check((_lib or lib()).vfa_debug_paged_gather(_ptr(k_pool), _ptr(v_pool), nb, _ptr(tile_blocks),
                                         _ptr(tile_block_counts), cap, S, Hkv, D, bs,
                                         _ptr(k_out), _ptr(v_out), _ptr(status), _stream(stream)))
