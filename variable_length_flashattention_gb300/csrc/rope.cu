@@ -24,11 +24,12 @@
 // token's heads) and works out a token's sines and cosines once for all its
 // heads.  Its turns are copied ahead into its own ring in shared memory with
 // 16-byte asynchronous copies, across tokens, so the bytes in flight do not
-// depend on registers.  32768 tokens of 40 heads of 128, forward and backward:
-// 109 and 189 us; without the ring (loads into registers) 131 and 265 us at 16
-// dimensions per lane and 113 and 188 us at 8, which halves what a lane keeps;
-// with the ring at 8 dimensions, whose turns are too short for their
-// instructions, 167 and 250 us.
+// depend on registers.  fp32 work is on pairs of values (f32x2), and what a
+// warp knows of its place comes from a shuffled warp number, so that it lives
+// in uniform registers: the backward was bound by instructions that moved
+// values about (191 us with 428 instructions per turn, 157 with 360).
+// 32768 tokens of 40 heads of 128: forward 108 us (6.2 TB/s), backward 157
+// (6.4 TB/s); loads into registers instead of the ring 113 and 188.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -39,12 +40,13 @@ namespace vfa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kFwdAhead = 6;            // turns copied ahead, CTAs per SM
-constexpr int kFwdCtas = 3;
-constexpr int kBwdAhead = 5;
-constexpr int kBwdCtas = 2;
+// Warps of a CTA, turns copied ahead, CTAs per SM (16 warps: with 24 the
+// forward's reads and writes are spread over more rows, 108 -> 116 us).
+template <bool BWD>
+struct RopeCfg {
+    static constexpr int WARPS = 4, AHEAD = BWD ? 4 : 8, CTAS = 4;
+};
+
 constexpr int kTurn = 1024;             // bytes of a turn of one tensor
 
 // Two floats in a 64-bit register, for the packed fp32 instructions.
@@ -68,6 +70,13 @@ __device__ __forceinline__ f2 f2_mul(f2 a, f2 b)
 {
     f2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f2 f2_sub(f2 a, f2 b)
+{
+    f2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -132,13 +141,12 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16 *pa, __nv_bfloat16 *pb
     *reinterpret_cast<uint4 *>(pb) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// ns: the negated sines.
-__device__ __forceinline__ void rotate(f2 (&v)[8], const f2 (&c)[4], const f2 (&s)[4], const f2 (&ns)[4])
+__device__ __forceinline__ void rotate(f2 (&v)[8], const f2 (&c)[4], const f2 (&s)[4])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const f2 a = v[j], b = v[4 + j];
-        v[j] = f2_fma(a, c[j], f2_mul(b, ns[j]));
+        v[j] = f2_sub(f2_mul(a, c[j]), f2_mul(b, s[j]));
         v[4 + j] = f2_fma(b, c[j], f2_mul(a, s[j]));
     }
 }
@@ -216,18 +224,22 @@ struct Turn {
 // the warp's lane groups, the CTA's warps, and (second kernel) the CTAs.  No
 // atomics.
 template <int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(RopeCfg<BWD>::WARPS * 32, RopeCfg<BWD>::CTAS) rope_kernel(const RopeArgs a)
 {
     constexpr int LPH = D / 16, HPW = 32 / LPH;
-    constexpr int AHEAD = BWD ? kBwdAhead : kFwdAhead, STAGE = BWD ? 2 * kTurn : kTurn;
-    extern __shared__ __align__(16) uint8_t ring[];     // [kWarps][AHEAD][STAGE]
+    constexpr int WARPS = RopeCfg<BWD>::WARPS, AHEAD = RopeCfg<BWD>::AHEAD;
+    constexpr int STAGE = BWD ? 2 * kTurn : kTurn;
+    extern __shared__ __align__(16) uint8_t ring[];     // [WARPS][AHEAD][STAGE]
     __shared__ __align__(16) float s_w[2][D];         // [which][quarter of a lane's 16][lane piece][4]
     grid_wait();
     if (BWD && (a.dweight[0] || a.dweight[1]))
         grid_release();                             // the sums of dw follow
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    // (a shuffle's result is known to be the same in every lane: what follows from
+    // it can live in uniform registers)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int p = lane % LPH, g = lane / LPH;
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < 2 * D; i += (WARPS * 32)) {
         const float *w = a.weight[i / D];
         const int quarter = i % D / (4 * LPH), q = i / 4 % LPH, j = quarter % 2 * 4 + i % 4;
         int da, db;
@@ -241,13 +253,13 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
     const bool turns_dims = 8 * p < a.half;
     const int iq = (a.heads[0] + HPW - 1) / HPW, turns = iq + (a.heads[1] + HPW - 1) / HPW;
     const unsigned segments = a.segments, units = static_cast<unsigned>(a.tokens) * segments;
-    const unsigned warps = gridDim.x * kWarps;
+    const unsigned warps = gridDim.x * WARPS;
     const int per = (turns + a.segments - 1) / a.segments;
     uint8_t *mine = ring + warp * AHEAD * STAGE;
     const uint32_t mine_u32 = smem_u32(mine) + lane * 16;
 
     Turn fill;
-    fill.u = blockIdx.x * kWarps + warp;
+    fill.u = blockIdx.x * WARPS + warp;
     fill.unit(units, warps, segments, per, turns);
     Turn cur = fill;
     // Copies the next turn (or nothing, at the end) as one group.
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
         for (int j = 0; j < 8; ++j)
             dw[0][j] = dw[1][j] = 0;
     }
-    f2 c2[4], s2[4], ns2[4];
+    f2 c2[4], s2[4];
     int stage = 0, t = -1;
     while (cur.u < units) {
         if (cur.t != t) {
@@ -301,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
             for (int j = 0; j < 4; ++j) {
                 c2[j] = f2_pack(c[2 * j], c[2 * j + 1]);
                 s2[j] = f2_pack(BWD ? -s[2 * j] : s[2 * j], BWD ? -s[2 * j + 1] : s[2 * j + 1]);
-                ns2[j] = f2_pack(BWD ? s[2 * j] : -s[2 * j], BWD ? s[2 * j + 1] : -s[2 * j + 1]);
             }
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
@@ -346,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
                 }
             }
             if (turns_dims)
-                rotate(x, c2, s2, ns2);
+                rotate(x, c2, s2);
             if (live)
                 store_pairs<INTER>(dst + da, dst + db, x);
         } else {
             if (turns_dims)
-                rotate(y, c2, s2, ns2);
+                rotate(y, c2, s2);
             if (norm) {
                 if (h - g + HPW > a.heads[which] && !live) {
                     // lanes past the heads hold whatever was there
@@ -359,16 +370,14 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
                     for (int j = 0; j < 8; ++j)
                         x[j] = y[j] = 0;
                 }
-                f2 q = 0, d = 0, g2[8];
+                f2 q = 0, d = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const ulonglong2 w = weights(i);
                     q = f2_fma(x[2 * i], x[2 * i], q);
                     q = f2_fma(x[2 * i + 1], x[2 * i + 1], q);
-                    g2[2 * i] = f2_mul(y[2 * i], w.x);              // u = g w
-                    g2[2 * i + 1] = f2_mul(y[2 * i + 1], w.y);
-                    d = f2_fma(g2[2 * i], x[2 * i], d);
-                    d = f2_fma(g2[2 * i + 1], x[2 * i + 1], d);
+                    d = f2_fma(f2_mul(y[2 * i], w.x), x[2 * i], d);
+                    d = f2_fma(f2_mul(y[2 * i + 1], w.y), x[2 * i + 1], d);
                 }
                 const float r = rsqrtf(head_sum<D>(f2_sum(q)) * (1.f / D) + a.eps);
                 const float m = -head_sum<D>(f2_sum(d)) * (1.f / D) * r * r;
@@ -382,9 +391,14 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
                     for (int j = 0; j < 8; ++j)
                         dw[0][j] = f2_fma(f2_mul(y[j], r2), x[j], dw[0][j]);
                 }
+                // (u = g w once more: keeping it costs 16 registers, and more instructions
+                // to move values about than it saves)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[j] = f2_mul(r2, f2_fma(x[j], m2, g2[j]));
+                for (int i = 0; i < 4; ++i) {
+                    const ulonglong2 w = weights(i);
+                    y[2 * i] = f2_mul(r2, f2_fma(x[2 * i], m2, f2_mul(y[2 * i], w.x)));
+                    y[2 * i + 1] = f2_mul(r2, f2_fma(x[2 * i + 1], m2, f2_mul(y[2 * i + 1], w.y)));
+                }
             }
             if (live)
                 store_pairs<INTER>(dst + da, dst + db, y);
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
         return;
     // partial[cta][which][d], the warps' sums over the ring (no copy is in flight)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    float *s_dw = reinterpret_cast<float *>(ring);      // [kWarps][D]
+    float *s_dw = reinterpret_cast<float *>(ring);      // [WARPS][D]
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         if (!a.dweight[which])
@@ -425,10 +439,10 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) rope_kern
             }
         }
         __syncthreads();
-        for (int d = threadIdx.x; d < D; d += kThreads) {
+        for (int d = threadIdx.x; d < D; d += (WARPS * 32)) {
             float v = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k)
+            for (int k = 0; k < WARPS; ++k)
                 v += s_dw[k * D + d];
             a.partial[(static_cast<long long>(blockIdx.x) * 2 + which) * D + d] = v;
         }
@@ -472,12 +486,13 @@ template <int D, bool BWD>
 cudaError_t launch_d(RopeArgs &a, int sm_count, cudaStream_t stream)
 {
     constexpr int HPW = 32 / (D / 16);
-    constexpr int SMEM = kWarps * (BWD ? kBwdAhead * 2 : kFwdAhead) * kTurn;
-    static_assert(SMEM >= kWarps * D * static_cast<int>(sizeof(float)), "the ring holds the warps' dw");
+    using C = RopeCfg<BWD>;
+    constexpr int SMEM = C::WARPS * C::AHEAD * (BWD ? 2 : 1) * kTurn;
+    static_assert(SMEM >= C::WARPS * D * static_cast<int>(sizeof(float)), "the ring holds the warps' dw");
     a.segments = head_segments(a, (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW,
                                sm_count);
-    const long long need = (static_cast<long long>(a.tokens) * a.segments + kWarps - 1) / kWarps;
-    long long grid = static_cast<long long>(sm_count) * (BWD ? kBwdCtas : kFwdCtas);
+    const long long need = (static_cast<long long>(a.tokens) * a.segments + C::WARPS - 1) / C::WARPS;
+    long long grid = static_cast<long long>(sm_count) * C::CTAS;
     grid = grid < need ? grid : need;
     grid = grid < kRopeMaxCtas ? grid : kRopeMaxCtas;
     a.ctas = static_cast<int>(grid);
@@ -496,7 +511,7 @@ cudaError_t launch_d(RopeArgs &a, int sm_count, cudaStream_t stream)
                 attr_done[a.interleaved][dev] = 1;
         }
     }
-    const cudaError_t e = launch_dependent(kernel, dim3(a.ctas), kThreads, SMEM, stream, a);
+    const cudaError_t e = launch_dependent(kernel, dim3(a.ctas), C::WARPS * 32, SMEM, stream, a);
     if (e != cudaSuccess || !BWD || (!a.dweight[0] && !a.dweight[1]))
         return e;
     return launch_dependent(rope_dw_kernel, dim3(D / 32, 2), 1024, 0, stream, a, D);
