@@ -395,9 +395,11 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 
 // ------------------------------------------------------------ decode
 //
-// Online softmax over the cached tokens of each sequence, G = Hq / Hkv query
-// heads of a kv head together (eight at most per CTA; more heads are more
-// head chunks, whose pages come from L2).
+// Online softmax over the cached tokens of each sequence, the Hq / Hkv query
+// heads of a kv head together: up to 8 as one tile of 8 columns, up to 16 as
+// two that share the unpacked pages (16 heads of 128 on 8 kv heads, 64
+// contexts of 4-8k: 171 us as two chunks of 8, 135 as two tiles); more are
+// more head chunks, whose pages come from L2.
 //
 // Work.  Every sequence counts its pages (1 if empty) and kSeqUnits for its
 // start and end (a query load, a merge of the warps, an output: about as long
@@ -408,9 +410,9 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // in a fixed order by the CTA that takes the last ticket.  No CTA waits for
 // another.
 //
-// Warp w takes every fourth pair of the run's pages (two at a time give a warp
-// two independent chains of products and halve the exchanges of the maximum)
-// and copies them ahead into its own ring of shared-memory stages with 16-byte
+// Warp w takes every fourth group of NP of the run's pages (NP = 2, or 4 at D
+// = 64: several at a time give a warp independent chains of products and
+// share the exchanges of the maximum) and copies them ahead into its own ring of shared-memory stages with 16-byte
 // asynchronous copies; it alone reads what it copied, so the ring needs no
 // barrier, only its copy groups.  (Bulk copies held the issuing warp for about
 // 500 cycles each: four 49k-65k-token contexts took 72 us with every warp
@@ -430,22 +432,31 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // 2^-28), l sums the fp32 values, and m, l, o are fp32.
 constexpr int kConsumers = 4;
 constexpr int kDecThreads = kConsumers * 32;
-constexpr int kHeads = 8;               // query heads of a kv head per CTA
+constexpr int kTile = 8;                // query heads of a tile (columns of a product)
 constexpr int kSeqUnits = 20;           // units of a sequence besides its pages
 constexpr int kMinRun = 24;             // units per CTA at least
-constexpr int kMaxParts = 256;          // runs of one row of units at most (what one CTA merges)
-constexpr int kMaxCtas = 1024;          // in all rows, where there are fewer rows
+constexpr int kMaxCtas = 1024;          // CTAs in all rows, where there are fewer rows
 constexpr float kPShift = 14.f;
 
-template <int D>
+// Tiles of query heads a CTA takes: two where a kv head has more than eight
+// (at D = 256 their accumulators would not fit the registers).
+__host__ __device__ constexpr int head_tiles(int group, int head_dim)
+{
+    return group > kTile && head_dim <= 128 ? 2 : 1;
+}
+
+template <int D, int NT>
 struct DecCfg {
+    static constexpr int HEADS = NT * kTile;                    // of a CTA at most
+    static constexpr int NP = D == 64 ? 4 : 2;                  // pages of a group
     static constexpr int PAGE = 18 * D;                         // bytes of a head page
-    static constexpr int STAGE = 2 * PAGE;                      // a stage holds two pages
-    static constexpr int NS = D == 64 ? 16 : 8;                 // stages of the CTA
-    static constexpr int WS = NS / kConsumers;                  // stages of a warp
-    static constexpr int CTAS = D == 64 ? 5 : D == 128 ? 3 : 2; // resident per SM
+    static constexpr int STAGE = NP * PAGE;                     // a stage holds a group
+    static constexpr int WS = 2;                                // stages of a warp
+    static constexpr int NS = WS * kConsumers;                  // stages of the CTA
+    static constexpr int CTAS = D == 64 ? 5 - NT : D == 128 ? 4 - NT : 2;   // resident per SM
     static constexpr int MT = D / 16;
     static constexpr int KW = D / 32;               // code words of one token per lane
+    static constexpr int PART = HEADS * (D + 4);    // floats of a part: per head o, m, l
 };
 
 // 16 bytes from src + OFF to shared memory at dst + OFF.
@@ -457,17 +468,16 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src)
                  : "memory");
 }
 
-// The 16-byte pieces of two pages in a row, 32 per turn and one per lane:
-// those of the first at p0, then those of the second at p1 (less the first
-// one's size), `mid` the lane's choice in the turn that has both.
-template <int PIECES, int K = 0>
-__device__ __forceinline__ void copy_pair(uint32_t dst, const uint8_t *p0, const uint8_t *mid,
-                                          const uint8_t *p1, int lane)
+// The 16-byte pieces of NP pages in a row, 32 per turn and one per lane; p[i] is
+// page i less the i pages before it.  A turn touches two pages at most.
+template <int NP, int PIECES, int K = 0>
+__device__ __forceinline__ void copy_pages(uint32_t dst, const uint8_t *const (&p)[NP], int lane)
 {
-    if constexpr (K < 2 * PIECES) {
-        if (K + 32 <= 2 * PIECES || K + lane < 2 * PIECES)
-            copy16_async<K * 16>(dst, K + 32 <= PIECES ? p0 : K >= PIECES ? p1 : mid);
-        copy_pair<PIECES, K + 32>(dst, p0, mid, p1, lane);
+    if constexpr (K < NP * PIECES) {
+        constexpr int A = K / PIECES, B = (K + 31) / PIECES < NP ? (K + 31) / PIECES : NP - 1;
+        if (K + 32 <= NP * PIECES || K + lane < NP * PIECES)
+            copy16_async<K * 16>(dst, A == B || K + lane < B * PIECES ? p[A] : p[B]);
+        copy_pages<NP, PIECES, K + 32>(dst, p, lane);
     }
 }
 
@@ -508,8 +518,9 @@ __device__ __forceinline__ int seq_pages(const Kv4DecodeArgs &a, int s, int *tok
 
 // A place in the CTA's run [u0, u1): the segment of sequence s whose units
 // start at `at` in the row (kSeqUnits, then its pages), the run's pages [j0,
-// j1) of it, and (modulo 4) the pairs of the earlier segments, which decide
-// the warp that takes its first pair.
+// j1) of it, and (modulo 4) the groups of NP pages of the earlier segments,
+// which decide the warp that takes its first group.
+template <int NP>
 struct RunCursor {
     int s, at, pages, tokens, j0, j1, base;
     bool bad;
@@ -528,28 +539,29 @@ struct RunCursor {
         }
         return false;
     }
-    // First page of `warp`'s first pair of the segment (at or past j1: none).
+    // First page of `warp`'s first group of the segment (at or past j1: none).
     __device__ __forceinline__ int first(int warp) const
     {
-        return j0 + 2 * ((warp - base) & (kConsumers - 1));
+        return j0 + NP * ((warp - base) & (kConsumers - 1));
     }
     // The next segment; false at the end of the run.
     __device__ __forceinline__ bool next(const Kv4DecodeArgs &a, int u0, int u1)
     {
-        base += (j1 - j0 + 1) / 2;
+        base += (j1 - j0 + NP - 1) / NP;
         at += kSeqUnits + pages;
         ++s;
         return enter(a, u0, u1);
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kernel(const Kv4DecodeArgs a)
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_kernel(const Kv4DecodeArgs a)
 {
-    using C = DecCfg<D>;
-    constexpr int NS = C::NS, MT = C::MT, KW = C::KW;
+    using C = DecCfg<D, NT>;
+    constexpr int NP = C::NP, MT = C::MT, KW = C::KW, PART = C::PART;
+    constexpr int STRIDE = NP * kConsumers;         // pages from a warp's group to its next
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ float s_m[kConsumers][kHeads], s_l[kConsumers][kHeads];
+    __shared__ float s_m[kConsumers][C::HEADS], s_l[kConsumers][C::HEADS];
     __shared__ int s_bad[kConsumers];
     __shared__ int s_scan[kDecThreads / 32];
     __shared__ int s_first, s_first_unit, s_last;
@@ -557,10 +569,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     grid_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.num_q_heads / a.num_kv_heads;
-    const int chunks = (group + kHeads - 1) / kHeads;
+    const int chunks = (group + C::HEADS - 1) / C::HEADS;
     const int kh = blockIdx.y / chunks;
-    const int h0 = kh * group + (blockIdx.y % chunks) * kHeads;     // first query head
-    const int G = min(kHeads, (kh + 1) * group - h0);
+    const int h0 = kh * group + (blockIdx.y % chunks) * C::HEADS;   // first query head
+    const int G = min(C::HEADS, (kh + 1) * group - h0);
 
     // Units before each thread's share of the sequences.
     const int per = (a.num_seqs + kDecThreads - 1) / kDecThreads;
@@ -613,19 +625,19 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     const uint8_t *pool = a.pool + static_cast<size_t>(kh) * C::PAGE;
 
     // ---------------------------------------------------- copies
-    // Fills of this warp's stages, WS pairs ahead.  The ids of its next pairs
-    // in segment `fill`, up to 16, are loaded and checked together: lane l
-    // holds page l % 2 of pair l / 2.  Where there is no page (a lone last
-    // page's neighbour, an empty sequence) or the id is bad, page 0 is copied in
-    // its place and not used.  Every turn commits one group of copies, also
-    // where there is nothing left to copy.
-    RunCursor fill;
+    // Fills of this warp's stages, WS groups ahead.  The ids of its next groups
+    // in segment `fill`, up to 32 pages, are loaded and checked together: lane
+    // l holds page l % NP of group l / NP.  Where there is no page (a last
+    // group's rest, an empty sequence) or the id is bad, page 0 is copied in its
+    // place and not used.  Every turn commits one group of copies, also where
+    // there is nothing left to copy.
+    RunCursor<NP> fill;
     fill.s = s_first;
     fill.at = s_first_unit;
     fill.base = 0;
     if (!fill.enter(a, u0, u1))
         return;                                     // (the whole CTA) no page in this run
-    RunCursor seg = fill;
+    RunCursor<NP> seg = fill;
     int ahead = fill.first(warp), ids = 0, id_lane = 0, left = 0;
     uint32_t bad_ids = 0, bad_stages = 0;
     auto load_ids = [&]() {
@@ -634,8 +646,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                 return;
             ahead = fill.first(warp);
         }
-        left = min(16, (fill.j1 - ahead + 2 * kConsumers - 1) / (2 * kConsumers));
-        const int j = ahead + (lane >> 1) * (2 * kConsumers) + (lane & 1);
+        left = min(32 / NP, (fill.j1 - ahead + STRIDE - 1) / STRIDE);
+        const int j = ahead + (lane / NP) * STRIDE + lane % NP;
         const bool listed = j < fill.j1 && fill.tokens > 0;
         ids = listed ? __ldg(a.tables + static_cast<long long>(fill.s) * a.capacity + j) : 0;
         const bool bad = static_cast<unsigned>(ids) >= static_cast<unsigned>(a.num_blocks);
@@ -649,19 +661,20 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     const bool pages_exist = a.num_blocks > 0;
     auto issue = [&](int ws) {
         if (left > 0) {
-            constexpr int PIECES = C::PAGE / 16;    // 16-byte pieces of a page
-            const uint32_t id0 = __shfl_sync(0xffffffffu, ids, id_lane);
-            const uint32_t id1 = __shfl_sync(0xffffffffu, ids, id_lane + 1);
-            const uint8_t *p0 = my_pool + static_cast<uint64_t>(id0) * page_bytes;
-            const uint8_t *p1 = my_pool + static_cast<uint64_t>(id1) * page_bytes - C::PAGE;
+            const uint8_t *p[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                p[i] = my_pool +
+                       static_cast<uint64_t>(static_cast<uint32_t>(
+                           __shfl_sync(0xffffffffu, ids, id_lane + i))) * page_bytes - i * C::PAGE;
             if (pages_exist)
-                copy_pair<PIECES>(my_ring + ws * C::STAGE, p0, lane >= PIECES % 32 ? p1 : p0, p1, lane);
-            if (bad_ids >> id_lane & 3u) {
+                copy_pages<NP, C::PAGE / 16>(my_ring + ws * C::STAGE, p, lane);
+            if (bad_ids >> id_lane & ((1u << NP) - 1)) {
                 bad_stages |= 1u << ws;
                 if (lane == 0)
                     record(a.status, VFA_ERR_BAD_BLOCK);
             }
-            id_lane += 2;
+            id_lane += NP;
             if (--left == 0)
                 load_ids();
         }
@@ -674,21 +687,24 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
 
     // ---------------------------------------------------- attention
     const int r = lane >> 2, t4 = lane & 3;
-    float *s_o = reinterpret_cast<float *>(dsm + NS * C::STAGE);    // [kConsumers][G][D]
-    int ws = 0;                                     // stage of this warp's next pair
+    float *s_o = reinterpret_cast<float *>(dsm + C::NS * C::STAGE); // [kConsumers][G][D]
+    int ws = 0;                                     // stage of this warp's next group
     bool first_segment = true;
     do {
         const int s = seg.s, n = seg.tokens, j0 = seg.j0, j1 = seg.j1;
         if (seg.bad && tid == 0)
             record(a.status, VFA_ERR_BAD_BLOCK);
 
-        // Q^T operand: head r, dims as K's lanes hold them.
-        uint32_t qb[MT][2];
-        float sc;
-        {
+        // Q^T operands: head r of each tile, dims as K's lanes hold them; the logit
+        // scales of the heads of this lane's accumulators, 2 t4 and 2 t4 + 1.
+        uint32_t qb[NT][MT][2];
+        float sc[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * kTile + r;
             const uint2 *qrow = reinterpret_cast<const uint2 *>(
                 static_cast<const __nv_bfloat16 *>(a.q) +
-                (static_cast<long long>(s) * a.num_q_heads + h0 + (r < G ? r : 0)) * D);
+                (static_cast<long long>(s) * a.num_q_heads + h0 + (h < G ? h : 0)) * D);
             uint2 raw[MT];
             float m = 0.f;
 #pragma unroll
@@ -714,49 +730,54 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                 const uint32_t w[2] = {raw[j].x, raw[j].y};
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    qb[j][c] = r < G ? pack_f16x2(__uint_as_float(w[c] << 16) * up,
-                                                  __uint_as_float(w[c] & 0xffff0000u) * up)
-                                     : 0u;
+                    qb[nt][j][c] = h < G ? pack_f16x2(__uint_as_float(w[c] << 16) * up,
+                                                      __uint_as_float(w[c] & 0xffff0000u) * up)
+                                         : 0u;
             }
-            // of head r (the accumulators hold 2 t4, + 1); positive, or a masked -inf times it
-            // would be no number
-            sc = fmaxf(a.scale_log2 * down, FLT_MIN);
+            // positive, or a masked -inf times it would be no number
+            const float x = fmaxf(a.scale_log2 * down, FLT_MIN);
+            sc[nt][0] = __shfl_sync(0xffffffffu, x, (2 * t4) * 4);
+            sc[nt][1] = __shfl_sync(0xffffffffu, x, (2 * t4 + 1) * 4);
         }
-        const float sc0 = __shfl_sync(0xffffffffu, sc, (2 * t4) * 4);
-        const float sc1 = __shfl_sync(0xffffffffu, sc, (2 * t4 + 1) * 4);
 
-        float m_run[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
-        float o[MT][4];
+        float m_run[NT][2], l_part[NT][2], o[NT][MT][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt) {
+            m_run[nt][0] = m_run[nt][1] = -INFINITY;
+            l_part[nt][0] = l_part[nt][1] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[mt][e] = 0.f;
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[nt][mt][e] = 0.f;
+        }
         bool bad = seg.bad;
 
-        for (int j = seg.first(warp); j < j1; j += 2 * kConsumers) {
+        for (int j = seg.first(warp); j < j1; j += STRIDE) {
             copy_wait<C::WS - 1>();
             __syncwarp();                           // every lane's copies are there for every lane
-            const uint8_t *pair = dsm + (warp * C::WS + ws) * C::STAGE;
-            // tokens of the two pages that count, those of the run's pages
-            const int valid = min(n - j * kPage, j + 1 < j1 ? 2 * kPage : kPage);
+            const uint8_t *stage = dsm + (warp * C::WS + ws) * C::STAGE;
+            // tokens of the group that count, those of the run's pages
+            const int valid = min(n - j * kPage, min(NP, j1 - j) * kPage);
             if (bad_stages) {
                 bad |= (bad_stages >> ws) & 1u;
                 bad_stages &= ~(1u << ws);
             }
             if (valid > 0 && !bad) {
-                // S = K Q^T: two pages, two independent accumulators
-                float sacc[2][4];
-                uint32_t kw[2][2][KW], ks[2][2];
+                // S = K Q^T: an accumulator per page and tile
+                float sacc[NT][NP][4];
+                uint32_t kw[NP][2][KW], ks[NP][2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < NP; ++c) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sacc[c][e] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sacc[nt][c][e] = 0.f;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int tok = r + 8 * half;
-                        const uint8_t *row = pair + c * C::PAGE + tok * (D / 2);
+                        const uint8_t *row = stage + c * C::PAGE + tok * (D / 2);
                         if constexpr (D == 64) {
                             const uint2 v = *reinterpret_cast<const uint2 *>(row + t4 * 8);
                             kw[c][half][0] = v.x;
@@ -772,7 +793,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                             }
                         }
                         // the token's scales for this lane's dims, in order
-                        const uint8_t *sp = pair + c * C::PAGE + 16 * D + tok * (D / 16);
+                        const uint8_t *sp = stage + c * C::PAGE + 16 * D + tok * (D / 16);
                         if constexpr (D == 64) {
                             ks[c][half] = sp[t4] * 0x101u;
                         } else if constexpr (D == 128) {
@@ -790,7 +811,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                     // one word: eight codes of 8 dims = products 2w, 2w + 1; one scale
                     const int si = D == 64 ? 0 : w / 2;         // index of the word's scale
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < NP; ++c) {
                         uint32_t c0[4], c1[4];
                         e2m1x8_to_f16(kw[c][0][w], c0);
                         e2m1x8_to_f16(kw[c][1][w], c1);
@@ -803,74 +824,84 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                             const uint32_t af[4] = {hmul2(c0[2 * q], f0), hmul2(c1[2 * q], f1),
                                                     hmul2(c0[2 * q + 1], f0),
                                                     hmul2(c1[2 * q + 1], f1)};
-                            mma_f16(sacc[c], af, qb[2 * w + q][0], qb[2 * w + q][1]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(sacc[nt][c], af, qb[nt][2 * w + q][0], qb[nt][2 * w + q][1]);
                         }
                     }
                 }
-                // tokens r (0, 1) and r + 8 (2, 3); heads 2 t4 (0, 2) and 2 t4 + 1 (1, 3)
-                if (valid < 2 * kPage) {
+                // tokens r (0, 1) and r + 8 (2, 3); heads 2 t4 (0, 2) and 2 t4 + 1 (1, 3) of the tile
+                if (valid < NP * kPage) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < NP; ++c)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (c * kPage + r + 8 * (e >> 1) >= valid)
-                                sacc[c][e] = -INFINITY;
-                }
-                float bm[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float y = fmax3(fmaxf(sacc[0][h], sacc[0][h + 2]), sacc[1][h], sacc[1][h + 2]);
-#pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1)
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                    bm[h] = y * (h ? sc1 : sc0);    // the scales are positive
+                                for (int nt = 0; nt < NT; ++nt)
+                                    sacc[nt][c][e] = -INFINITY;
                 }
-                if (__any_sync(0xffffffffu, bm[0] > m_run[0] || bm[1] > m_run[1])) {
-                    float f[2];
+                uint32_t pb[NT][NP][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float bm[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float mnew = fmaxf(m_run[h], bm[h]);
-                        f[h] = mnew == m_run[h] ? 1.f : ex2_approx(m_run[h] - mnew);
-                        m_run[h] = mnew;
-                        l_part[h] *= f[h];
-                    }
+                        float y = fmaxf(sacc[nt][0][h], sacc[nt][0][h + 2]);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        o[mt][0] *= f[0];
-                        o[mt][1] *= f[1];
-                        o[mt][2] *= f[0];
-                        o[mt][3] *= f[1];
-                    }
-                }
-                const float e0 = kPShift - m_run[0], e1 = kPShift - m_run[1];
-                uint32_t pb[2][2];
+                        for (int c = 1; c < NP; ++c)
+                            y = fmax3(y, sacc[nt][c][h], sacc[nt][c][h + 2]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float p0 = ex2_approx(fmaf(sacc[c][0], sc0, e0));
-                    const float p1 = ex2_approx(fmaf(sacc[c][1], sc1, e1));
-                    const float p2 = ex2_approx(fmaf(sacc[c][2], sc0, e0));
-                    const float p3 = ex2_approx(fmaf(sacc[c][3], sc1, e1));
-                    l_part[0] += p0 + p2;
-                    l_part[1] += p1 + p3;
-                    pb[c][0] = movm_t(pack_f16x2(p0, p1));
-                    pb[c][1] = movm_t(pack_f16x2(p2, p3));
+                        for (int off = 4; off <= 16; off <<= 1)
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+                        bm[h] = y * sc[nt][h];      // the scales are positive
+                    }
+                    if (__any_sync(0xffffffffu, bm[0] > m_run[nt][0] || bm[1] > m_run[nt][1])) {
+                        float f[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float mnew = fmaxf(m_run[nt][h], bm[h]);
+                            f[h] = mnew == m_run[nt][h] ? 1.f : ex2_approx(m_run[nt][h] - mnew);
+                            m_run[nt][h] = mnew;
+                            l_part[nt][h] *= f[h];
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[nt][mt][0] *= f[0];
+                            o[nt][mt][1] *= f[1];
+                            o[nt][mt][2] *= f[0];
+                            o[nt][mt][3] *= f[1];
+                        }
+                    }
+                    const float e0 = kPShift - m_run[nt][0], e1 = kPShift - m_run[nt][1];
+#pragma unroll
+                    for (int c = 0; c < NP; ++c) {
+                        const float p0 = ex2_approx(fmaf(sacc[nt][c][0], sc[nt][0], e0));
+                        const float p1 = ex2_approx(fmaf(sacc[nt][c][1], sc[nt][1], e1));
+                        const float p2 = ex2_approx(fmaf(sacc[nt][c][2], sc[nt][0], e0));
+                        const float p3 = ex2_approx(fmaf(sacc[nt][c][3], sc[nt][1], e1));
+                        l_part[nt][0] += p0 + p2;
+                        l_part[nt][1] += p1 + p3;
+                        pb[nt][c][0] = movm_t(pack_f16x2(p0, p1));
+                        pb[nt][c][1] = movm_t(pack_f16x2(p2, p3));
+                    }
                 }
 
                 // O^T += V^T P
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint8_t *page = pair + c * C::PAGE;
+                for (int c = 0; c < NP; ++c) {
+                    const uint8_t *page = stage + c * C::PAGE;
 #pragma unroll
                     for (int p = 0; p < (D == 256 ? 2 : 1); ++p) {
                         const int grp = D == 64 ? r >> 1 : r + 8 * p;
                         uint32_t vs = *reinterpret_cast<const uint32_t *>(page + 17 * D + (grp * 4 + t4) * 4);
-                        if (valid < 2 * kPage) {
+                        if (valid < NP * kPage) {
                             // unused rows may hold any bytes: their scales count as zero
-                            const int left = valid - c * kPage;
-                            vs &= (2 * t4 < left ? 0x000000ffu : 0u) |
-                                  (2 * t4 + 1 < left ? 0x0000ff00u : 0u) |
-                                  (2 * t4 + 8 < left ? 0x00ff0000u : 0u) |
-                                  (2 * t4 + 9 < left ? 0xff000000u : 0u);
+                            const int rest = valid - c * kPage;
+                            vs &= (2 * t4 < rest ? 0x000000ffu : 0u) |
+                                  (2 * t4 + 1 < rest ? 0x0000ff00u : 0u) |
+                                  (2 * t4 + 8 < rest ? 0x00ff0000u : 0u) |
+                                  (2 * t4 + 9 < rest ? 0xff000000u : 0u);
                         }
                         const uint32_t f0 = e4m3x2_to_f16(vs & 0xffffu), f1 = e4m3x2_to_f16(vs >> 16);
                         uint32_t even[2][2], odd[2][2];         // [token half][code word]
@@ -903,7 +934,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
                             for (int b = 0; b < 4; ++b) {
                                 const uint32_t af[4] = {hmul2(a0[b], f0), hmul2(a1[b], f0),
                                                         hmul2(a2[b], f1), hmul2(a3[b], f1)};
-                                mma_f16(o[8 * p + 4 * w + b], af, pb[c][0], pb[c][1]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_f16(o[nt][8 * p + 4 * w + b], af, pb[nt][c][0], pb[nt][c][1]);
                             }
                         }
                     }
@@ -916,35 +949,36 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
 
         // ------------------------------------------------ end of the segment
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int off = 4; off <= 16; off <<= 1)
-                l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], off);
-        }
-        if (lane < 4) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                s_m[warp][2 * lane + h] = m_run[h];
-                s_l[warp][2 * lane + h] = l_part[h];
+#pragma unroll
+                for (int off = 4; off <= 16; off <<= 1)
+                    l_part[nt][h] += __shfl_xor_sync(0xffffffffu, l_part[nt][h], off);
+                if (lane < 4) {
+                    s_m[warp][nt * kTile + 2 * lane + h] = m_run[nt][h];
+                    s_l[warp][nt * kTile + 2 * lane + h] = l_part[nt][h];
+                }
+            }
+            // o[mt]: dims of run r: 16 (r + 8 p) + 2 b (D = 64: 8 r + 2 b) in c0, c1, the next in c2, c3
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int d = D == 64 ? r * 8 + 2 * mt : (r + 8 * (mt >> 3)) * 16 + 2 * (mt & 7);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int g = nt * kTile + 2 * t4 + h;
+                    if (g < G)
+                        *reinterpret_cast<float2 *>(&s_o[(warp * G + g) * D + d]) =
+                            make_float2(o[nt][mt][h], o[nt][mt][2 + h]);
+                }
             }
         }
         if (lane == 0)
             s_bad[warp] = bad;
-        // o[mt]: dims of run r: 16 (r + 8 p) + 2 b (D = 64: 8 r + 2 b) in c0, c1, the next in c2, c3
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int d = D == 64 ? r * 8 + 2 * mt : (r + 8 * (mt >> 3)) * 16 + 2 * (mt & 7);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (2 * t4 + h < G)
-                    *reinterpret_cast<float2 *>(&s_o[(warp * G + 2 * t4 + h) * D + d]) =
-                        make_float2(o[mt][h], o[mt][2 + h]);
-        }
         __syncthreads();
         bad = s_bad[0] || s_bad[1] || s_bad[2] || s_bad[3];
         const bool whole = j0 == 0 && j1 == seg.pages;
         // The warps' states merged: four dims per thread and turn.
-        constexpr int PART = kHeads * (D + 4);      // floats of a part: per head o, m, l
         float *part = a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * PART +
                       (first_segment ? 0 : PART);
         auto finish = [&](int g, int d, float4 v, float m, float l) {
@@ -1048,14 +1082,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::CTAS) kv4_decode_kerne
     } while (seg.next(a, u0, u1));
 }
 
-template <int D>
-cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
+template <int D, int NT>
+cudaError_t launch_decode_dn(const Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
 {
-    using C = DecCfg<D>;
+    using C = DecCfg<D, NT>;
     const int group = a.num_q_heads / a.num_kv_heads;
-    const int chunks = (group + kHeads - 1) / kHeads;
-    const int rows = a.num_kv_heads * chunks;
-    const int heads = group < kHeads ? group : kHeads;
+    const int rows = a.num_kv_heads * ((group + C::HEADS - 1) / C::HEADS);
+    const int heads = group < C::HEADS ? group : C::HEADS;
     const size_t smem = static_cast<size_t>(C::NS) * C::STAGE +
                         static_cast<size_t>(kConsumers) * heads * D * sizeof(float);
     // the largest size any call needs, once per device
@@ -1065,9 +1098,9 @@ cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_done[dev]) {
-        e = cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::NS * C::STAGE +
-                                     kConsumers * kHeads * D * static_cast<int>(sizeof(float)));
+                                     kConsumers * C::HEADS * D * static_cast<int>(sizeof(float)));
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
@@ -1083,9 +1116,22 @@ cudaError_t launch_decode_d(Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
                                 (kSeqUnits + (a.capacity > 0 ? a.capacity : 1)) +
                             kMinRun - 1) / kMinRun;
     parts = parts < most ? parts : most;
-    parts = parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts);
-    return launch_dependent(kv4_decode_kernel<D>, dim3(static_cast<int>(parts), rows), kDecThreads, smem,
-                            stream, a);
+    // One CTA merges a sequence's parts, 8 per load latency: up to 256 runs where
+    // a sequence may take them all, 8 per sequence where there are many (one kv
+    // head, 64 contexts of 15-30k tokens of 128: 62 us with 256 runs, 53 with 456).
+    const long long cap = 8LL * a.num_seqs > 256 ? 8LL * a.num_seqs : 256;
+    parts = parts < 1 ? 1 : (parts > cap ? cap : parts);
+    return launch_dependent(kv4_decode_kernel<D, NT>, dim3(static_cast<int>(parts), rows), kDecThreads,
+                            smem, stream, a);
+}
+
+template <int D>
+cudaError_t launch_decode_d(const Kv4DecodeArgs &a, int sm_count, cudaStream_t stream)
+{
+    if constexpr (D <= 128)
+        if (head_tiles(a.num_q_heads / a.num_kv_heads, D) == 2)
+            return launch_decode_dn<D, 2>(a, sm_count, stream);
+    return launch_decode_dn<D, 1>(a, sm_count, stream);
 }
 
 // CTAs over the tokens; with too few tokens for every SM, CTAs share the kv
@@ -1105,13 +1151,10 @@ dim3 move_grid(const Kv4MoveArgs &a, int head_dim, int sm_count)
 // The workspace: partial states, then the tickets.  Where the tickets start
 // does not depend on the number of sequences, so a workspace made for a batch
 // serves smaller ones too.
-size_t part_bytes(int rows, int head_dim)
+size_t part_bytes(int rows, int tiles, int head_dim)
 {
-    // runs: kMaxParts for one row, kMaxCtas in all rows or one per row
-    const long long all = rows > kMaxCtas ? rows : kMaxCtas;
-    const size_t runs = all < static_cast<long long>(rows) * kMaxParts
-                            ? static_cast<size_t>(all) : static_cast<size_t>(rows) * kMaxParts;
-    const size_t n = runs * 2 * kHeads * (head_dim + 4) * sizeof(float);
+    const size_t runs = rows > kMaxCtas ? rows : kMaxCtas;      // in all rows
+    const size_t n = runs * 2 * tiles * kTile * (head_dim + 4) * sizeof(float);
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
@@ -1143,18 +1186,20 @@ cudaError_t launch_kv4_gather(int head_dim, const Kv4MoveArgs &a, int sm_count,
 size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim)
 {
     const int group = num_q_heads / num_kv_heads;
-    const int rows = num_kv_heads * ((group + kHeads - 1) / kHeads);
-    return part_bytes(rows, head_dim) + static_cast<size_t>(num_seqs) * rows * sizeof(int32_t);
+    const int tiles = head_tiles(group, head_dim);
+    const int rows = num_kv_heads * ((group + tiles * kTile - 1) / (tiles * kTile));
+    return part_bytes(rows, tiles, head_dim) + static_cast<size_t>(num_seqs) * rows * sizeof(int32_t);
 }
 
 cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, int sm_count,
                               cudaStream_t stream)
 {
     const int group = a.num_q_heads / a.num_kv_heads;
-    const int rows = a.num_kv_heads * ((group + kHeads - 1) / kHeads);
+    const int tiles = head_tiles(group, head_dim);
+    const int rows = a.num_kv_heads * ((group + tiles * kTile - 1) / (tiles * kTile));
     a.part = static_cast<float *>(workspace);
     a.tickets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
-                                            part_bytes(rows, head_dim));
+                                            part_bytes(rows, tiles, head_dim));
     switch (head_dim) {
     case 64: return launch_decode_d<64>(a, sm_count, stream);
     case 128: return launch_decode_d<128>(a, sm_count, stream);
