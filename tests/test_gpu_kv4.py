@@ -5,9 +5,10 @@ Write and gather are exact.  Decode, per element:
     the multiplication by the scale and the subtraction of the maximum give an error of the
     exponent of at most dx = (D + 16) u32 sum|q k| scale (+ 2 u32 |x| inside it);
   p: e^dx - 1, 2^-21 for ex2, and half an f16 step, 2^-11 of p; l the same without f16;
-  small p: 2^14 p is held in f16, whose values below 2^-14 are 2^-24 apart, so half a step is
-    2^-25 / 2^14 = 2^-39 absolute (relative to the largest weight) for every key: 2^-39 sum |v| / l;
-  out: (2 (e^dx - 1) + 2^-11 + n u32 + 2^-20) sum p |v| / l + 2^-39 sum |v| / l + 2^-8 |out|;
+  small p: 2^10 p is held in f16, whose values below 2^-14 are 2^-24 apart, so half a step is
+    2^-25 / 2^10 = 2^-35 absolute for every key, relative to a reference weight that is at most
+    the largest one (the reference maximum never exceeds the true one): 2^-35 sum |v| / l;
+  out: (2 (e^dx - 1) + 2^-11 + n u32 + 2^-20) sum p |v| / l + 2^-35 sum |v| / l + 2^-8 |out|;
   lse: dx + (n u32 + 2^-20) + 2^-22 |lse| for the logarithm and the final product.
 """
 import math
@@ -162,7 +163,7 @@ def _bounds(ref, n):
     D = out.shape[-1]
     dx = (D + 16) * U * absdot
     p = 2 * np.expm1(dx) + 2.0 ** -11 + n[:, None] * U + 2.0 ** -20
-    return p[..., None] * absv + 2.0 ** -39 * allv + 2.0 ** -8 * np.abs(out) + 1e-30, \
+    return p[..., None] * absv + 2.0 ** -35 * allv + 2.0 ** -8 * np.abs(out) + 1e-30, \
         dx + n[:, None] * U + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(lse == -O.FLT_MAX, 0, lse))
 
 
@@ -214,6 +215,38 @@ def test_decode_scales(vfa, qscale, scale):
     """Flat and peaked softmaxes; query magnitudes far outside f16's range."""
     case = _decode_case([700, 40, 3], 6, 2, 128, seed=5, qscale=qscale)
     _check_decode(_run(vfa, case, softmax_scale=scale), case, scale if scale > 0 else None)
+
+
+@pytest.mark.parametrize("lens", [[40], [9000, 3, 700]])
+@pytest.mark.parametrize("exponent", [12, 24, 40, 90])
+def test_decode_huge_logits(vfa, lens, exponent):
+    """Logits far apart and past 2^24, where their fp32 neighbours are whole units apart: the
+    largest take all the weight, equal ones share it.
+
+    q has one element and the keys multiples of 1/2 there, so the accumulators are exact and a
+    difference is 0 or at least 2^11 / sqrt(64) * log2(e) > 360: the other weights are below
+    2^-360.  Equal weights are equal numbers, so the mean over c of them is off by (c + 2) u32
+    and ex2's 2^-20 of sum |v| / c and the bf16 rounding; lse by four roundings, 2^-22 of itself,
+    and 2^-20 for the logarithm.
+    """
+    D, Hq = 64, 3
+    q, pool, tables, n, dk, dv = _decode_case(lens, Hq, 1, D, seed=exponent)
+    pool[..., 16 * D:] = 0x38                             # every scale 1.0
+    q[:] = 0
+    q[:, 0, 7], q[:, 1, 7], q[:, 2, 7] = 2.0 ** exponent, -2.0 ** exponent, 1.5 * 2.0 ** exponent
+    got = _run(vfa, (q, pool, tables, n, 1.0, 1.0))
+    for s, m in enumerate(lens):
+        k, v = (a[:, 0].reshape(-1, D)[:m]
+                for a in O.page_values(pool[tables[s, :-(-m // 16)]], 1.0, 1.0))
+        for h in range(Hq):
+            x = k[:, 7] * float(q[s, h, 7]) / math.sqrt(D)
+            top = x == x.max()
+            c = int(top.sum())
+            ref = v[top].mean(0)
+            tol = ((c + 2) * U + 2.0 ** -20) * np.abs(v[top]).mean(0) + 2.0 ** -8 * np.abs(ref) + 1e-30
+            assert (np.abs(got[0][s, h].double().cpu().numpy() - ref) <= tol).all()
+            want = x.max() + math.log(c)
+            assert abs(float(got[1][s, h]) - want) <= 2.0 ** -22 * abs(want) + 2.0 ** -20
 
 
 def test_decode_many_small_weights(vfa):

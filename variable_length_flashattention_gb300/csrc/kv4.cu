@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -428,15 +429,22 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // Numbers.  K, V as f16: exact (see the format).  q is multiplied by a power
 // of two per head that puts its largest element at 2^14: f16 then holds every
 // bf16 bit of elements down to 2^-21 of the largest and is within 2^-39 of
-// the largest below.  p is held as 2^14 p in f16 (2^-12 relative for p above
-// 2^-28), l sums the fp32 values, and m, l, o are fp32.
+// the largest below.  Weights are relative to a reference, the maximum when it
+// was last taken: a warp takes it again (an exchange over its lanes and a
+// rescaling) only when a weight would pass it by more than a factor 2^5, so
+// most groups cost one vote.  References stay in units of the accumulators, whose
+// difference is taken before the scale: it is exact near the maximum however
+// large the logits are.  p is held as 2^10 p in f16, at most 2^15 (2^-12
+// relative for p above 2^-24, 2^-35 absolute below), l sums the fp32 values,
+// and the reference, l and o are fp32.
 constexpr int kConsumers = 4;
 constexpr int kDecThreads = kConsumers * 32;
 constexpr int kTile = 8;                // query heads of a tile (columns of a product)
 constexpr int kSeqUnits = 20;           // units of a sequence besides its pages
 constexpr int kMinRun = 24;             // units per CTA at least
 constexpr int kMaxCtas = 1024;          // CTAs in all rows, where there are fewer rows
-constexpr float kPShift = 14.f;
+constexpr float kPShift = 10.f, kSlack = 5.f;    // log2
+constexpr float kNoRef = -0x1p60f;      // below any finite accumulator (2^36 at most)
 
 // Tiles of query heads a CTA takes: two where a kv head has more than eight
 // (at D = 256 their accumulators would not fit the registers).
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
     constexpr int NP = C::NP, MT = C::MT, KW = C::KW, PART = C::PART;
     constexpr int STRIDE = NP * kConsumers;         // pages from a warp's group to its next
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ float s_m[kConsumers][C::HEADS], s_l[kConsumers][C::HEADS];
+    __shared__ float s_m[kConsumers][C::HEADS], s_l[kConsumers][C::HEADS], s_sc[C::HEADS];
     __shared__ int s_bad[kConsumers];
     __shared__ int s_scan[kDecThreads / 32];
     __shared__ int s_first, s_first_unit, s_last;
@@ -740,10 +748,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
             sc[nt][1] = __shfl_sync(0xffffffffu, x, (2 * t4 + 1) * 4);
         }
 
-        float m_run[NT][2], l_part[NT][2], o[NT][MT][4];
+        // per head: the reference, the logit that renews it (both before the scale), the sum
+        float ref[NT][2], limit[NT][2], l_part[NT][2], o[NT][MT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m_run[nt][0] = m_run[nt][1] = -INFINITY;
+            ref[nt][0] = ref[nt][1] = kNoRef;
+            limit[nt][0] = limit[nt][1] = -INFINITY;
             l_part[nt][0] = l_part[nt][1] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -844,25 +854,26 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                 uint32_t pb[NT][NP][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float bm[2];
+                    float top[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float y = fmaxf(sacc[nt][0][h], sacc[nt][0][h + 2]);
+                        top[h] = fmaxf(sacc[nt][0][h], sacc[nt][0][h + 2]);
 #pragma unroll
                         for (int c = 1; c < NP; ++c)
-                            y = fmax3(y, sacc[nt][c][h], sacc[nt][c][h + 2]);
-#pragma unroll
-                        for (int off = 4; off <= 16; off <<= 1)
-                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                        bm[h] = y * sc[nt][h];      // the scales are positive
+                            top[h] = fmax3(top[h], sacc[nt][c][h], sacc[nt][c][h + 2]);
                     }
-                    if (__any_sync(0xffffffffu, bm[0] > m_run[nt][0] || bm[1] > m_run[nt][1])) {
+                    if (__any_sync(0xffffffffu, top[0] > limit[nt][0] || top[1] > limit[nt][1])) {
                         float f[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float mnew = fmaxf(m_run[nt][h], bm[h]);
-                            f[h] = mnew == m_run[nt][h] ? 1.f : ex2_approx(m_run[nt][h] - mnew);
-                            m_run[nt][h] = mnew;
+                            float y = top[h];
+#pragma unroll
+                            for (int off = 4; off <= 16; off <<= 1)
+                                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+                            y = fmaxf(y, ref[nt][h]);
+                            f[h] = ex2_approx((ref[nt][h] - y) * sc[nt][h]);
+                            ref[nt][h] = y;
+                            limit[nt][h] = __fadd_rd(y, __fdiv_rd(kSlack, sc[nt][h]));
                             l_part[nt][h] *= f[h];
                         }
 #pragma unroll
@@ -873,13 +884,16 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                             o[nt][mt][3] *= f[1];
                         }
                     }
-                    const float e0 = kPShift - m_run[nt][0], e1 = kPShift - m_run[nt][1];
+                    const f2 r2 = f2_pack(ref[nt][0], ref[nt][1]), s2 = f2_pack(sc[nt][0], sc[nt][1]);
+                    const f2 shift = f2_pack(kPShift, kPShift);
 #pragma unroll
                     for (int c = 0; c < NP; ++c) {
-                        const float p0 = ex2_approx(fmaf(sacc[nt][c][0], sc[nt][0], e0));
-                        const float p1 = ex2_approx(fmaf(sacc[nt][c][1], sc[nt][1], e1));
-                        const float p2 = ex2_approx(fmaf(sacc[nt][c][2], sc[nt][0], e0));
-                        const float p3 = ex2_approx(fmaf(sacc[nt][c][3], sc[nt][1], e1));
+                        const float2 x = f2_unpack(f2_fma(f2_sub(f2_pack(sacc[nt][c][0], sacc[nt][c][1]), r2),
+                                                          s2, shift));
+                        const float2 z = f2_unpack(f2_fma(f2_sub(f2_pack(sacc[nt][c][2], sacc[nt][c][3]), r2),
+                                                          s2, shift));
+                        const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                        const float p2 = ex2_approx(z.x), p3 = ex2_approx(z.y);
                         l_part[nt][0] += p0 + p2;
                         l_part[nt][1] += p1 + p3;
                         pb[nt][c][0] = movm_t(pack_f16x2(p0, p1));
@@ -956,7 +970,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                 for (int off = 4; off <= 16; off <<= 1)
                     l_part[nt][h] += __shfl_xor_sync(0xffffffffu, l_part[nt][h], off);
                 if (lane < 4) {
-                    s_m[warp][nt * kTile + 2 * lane + h] = m_run[nt][h];
+                    s_m[warp][nt * kTile + 2 * lane + h] = ref[nt][h];
+                    if (warp == 0)
+                        s_sc[nt * kTile + 2 * lane + h] = sc[nt][h];
                     s_l[warp][nt * kTile + 2 * lane + h] = l_part[nt][h];
                 }
             }
@@ -983,28 +999,26 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                       (first_segment ? 0 : PART);
         auto finish = [&](int g, int d, float4 v, float m, float l) {
             const long long out_row = static_cast<long long>(s) * a.num_q_heads + h0 + g;
-            const float f = m == -INFINITY ? 0.f : a.descale_v / l;
+            const float f = l == 0.f ? 0.f : a.descale_v / l;       // no token
             *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D + d) =
                 make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
             if (d == 0 && a.lse)
-                a.lse[out_row] = m == -INFINITY ? -FLT_MAX : (m - kPShift + __log2f(l)) * kLn2;
+                a.lse[out_row] = l == 0.f ? -FLT_MAX : (m * s_sc[g] - kPShift + __log2f(l)) * kLn2;
         };
         for (int e = 4 * tid; e < G * D; e += 4 * kDecThreads) {
             const int g = e / D, d = e % D;
             const float mt = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float l = 0.f;
-            if (mt != -INFINITY) {
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
-                    const float f = ex2_approx(s_m[w][g] - mt);
-                    const float4 v = *reinterpret_cast<const float4 *>(&s_o[(w * G + g) * D + d]);
-                    acc.x = fmaf(v.x, f, acc.x);
-                    acc.y = fmaf(v.y, f, acc.y);
-                    acc.z = fmaf(v.z, f, acc.z);
-                    acc.w = fmaf(v.w, f, acc.w);
-                    l = fmaf(s_l[w][g], f, l);
-                }
+            for (int w = 0; w < kConsumers; ++w) {
+                const float f = ex2_approx((s_m[w][g] - mt) * s_sc[g]);
+                const float4 v = *reinterpret_cast<const float4 *>(&s_o[(w * G + g) * D + d]);
+                acc.x = fmaf(v.x, f, acc.x);
+                acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z);
+                acc.w = fmaf(v.w, f, acc.w);
+                l = fmaf(s_l[w][g], f, l);
             }
             if (!whole) {
                 float *q = part + g * (D + 4);
@@ -1033,7 +1047,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                 const int late = seg.at > xa * run;
                 for (int e = 4 * tid; e < G * D; e += 4 * kDecThreads) {
                     const int g = e / D, d = e % D;
-                    float mt = -INFINITY, l = 0.f;
+                    const float scale = s_sc[g];
+                    float mt = kNoRef, l = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     bool any_bad = false;
                     constexpr int B = 8;            // parts whose loads are in flight together
@@ -1042,8 +1057,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                         float2 ml[B];
 #pragma unroll
                         for (int x = 0; x < B; ++x) {
-                            ml[x] = make_float2(-INFINITY, 0.f);
-                            v[x] = acc;
+                            ml[x] = make_float2(kNoRef, 0.f);
+                            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                             if (x0 + x < parts) {
                                 const float *q = base + (static_cast<long long>(xa + x0 + x) * 2 +
                                                          (x0 + x == 0 ? late : 0)) * PART + g * (D + 4);
@@ -1055,13 +1070,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
 #pragma unroll
                         for (int x = 0; x < B; ++x)
                             mn = fmaxf(mn, ml[x].x);
-                        const float keep = mt == -INFINITY ? 0.f : ex2_approx(mt - mn);
+                        const float keep = ex2_approx((mt - mn) * scale);
                         mt = mn;
                         acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
                         l *= keep;
 #pragma unroll
                         for (int x = 0; x < B; ++x) {
-                            const float f = ml[x].x == -INFINITY ? 0.f : ex2_approx(ml[x].x - mn);
+                            const float f = ex2_approx((ml[x].x - mn) * scale);
                             any_bad |= ml[x].y < 0.f;
                             acc.x = fmaf(v[x].x, f, acc.x);
                             acc.y = fmaf(v[x].y, f, acc.y);

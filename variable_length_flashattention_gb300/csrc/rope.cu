@@ -32,6 +32,7 @@
 // (6.4 TB/s); loads into registers instead of the ring 113 and 188.
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -48,50 +49,6 @@ struct RopeCfg {
 };
 
 constexpr int kTurn = 1024;             // bytes of a turn of one tensor
-
-// Two floats in a 64-bit register, for the packed fp32 instructions.
-typedef unsigned long long f2;
-
-__device__ __forceinline__ f2 f2_pack(float lo, float hi)
-{
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ float2 f2_unpack(f2 v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b)
-{
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ f2 f2_sub(f2 a, f2 b)
-{
-    f2 r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c)
-{
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ float f2_sum(f2 v)
-{
-    const float2 x = f2_unpack(v);
-    return x.x + x.y;
-}
 
 // The 16 dimensions of lane piece p of a head: [a, a + 8) and [b, b + 8).
 template <bool INTER>
