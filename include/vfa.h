@@ -588,7 +588,7 @@ vfa_status vfa_kv4_gather(void *k, void *v, int64_t k_stride, int64_t v_stride, 
  * [0, num_blocks) stores VFA_ERR_BAD_BLOCK and leaves that sequence's out and
  * lse rows (of the kv heads that saw it) as they were.
  * Supported: any num_q_heads that is a multiple of num_kv_heads;
- * num_seqs * (capacity + 16) < 2^31.
+ * num_seqs * (capacity + 64) <= 2^30.
  */
 size_t vfa_kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                       int head_dim);

@@ -280,6 +280,9 @@ def test_kv4_host_checks(vfa):
 
     assert decode(D=96) == vfa.VFA_ERR_UNSUPPORTED
     assert decode(cap=1 << 29, n=1 << 40) == vfa.VFA_ERR_UNSUPPORTED
+    # sequences and pages counted together pass 32 bits, although the pages alone do not
+    assert decode(S=1 << 22, cap=495, n=1 << 40) == vfa.VFA_ERR_UNSUPPORTED
+    assert decode(S=1 << 30, cap=1, n=1 << 40) == vfa.VFA_ERR_UNSUPPORTED
     for kw in (dict(q=None), dict(q=odd), dict(counts=None), dict(out=None), dict(Hq=30),
                dict(Hq=0), dict(dk=0.3), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(w=None), dict(w=odd), dict(n=need - 1), dict(lse=ctypes.c_void_p(0x100002))):

@@ -364,7 +364,8 @@ vfa_status vfa_kv4_decode(const void *q, const void *pool, int num_blocks, const
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(token_counts, 4) || !aligned(lse, 4) ||
         !aligned(device_status, 4))
         return fail(VFA_ERR_INVALID_ARG, "q and out must be 16-byte aligned, the others 4-byte");
-    if (static_cast<long long>(num_seqs) * (static_cast<long long>(capacity) + 16) >= (1LL << 31) ||
+    // the kernel counts pages, and some per sequence besides, in 32 bits
+    if (static_cast<long long>(num_seqs) * (static_cast<long long>(capacity) + 64) > (1LL << 30) ||
         static_cast<long long>(num_kv_heads) * ((num_q_heads / num_kv_heads + 7) / 8) > 65535)
         return fail(VFA_ERR_UNSUPPORTED, "num_seqs * capacity or the head count too large");
     if (!workspace || !aligned(workspace, 256))
