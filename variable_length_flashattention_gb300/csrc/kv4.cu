@@ -399,8 +399,16 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // Online softmax over the cached tokens of each sequence, the Hq / Hkv query
 // heads of a kv head together: up to 8 as one tile of 8 columns, up to 16 as
 // two that share the unpacked pages (16 heads of 128 on 8 kv heads, 64
-// contexts of 4-8k: 171 us as two chunks of 8, 135 as two tiles); more are
+// contexts of 4-8k: 167 us as two chunks of 8, 129 as two tiles); more are
 // more head chunks, whose pages come from L2.
+//
+// Bound: HBM for long batches, 1.125 bytes per dim and token of a kv head.  A
+// call takes 14 us (17 for 64 sequences) plus its pages at 6.39 TB/s, 94% of
+// the copy rate: the chain from counts over tables to the first pages, and the
+// merge behind the last.  8 kv heads of 128, 4 query heads each: 256 sequences
+// of 16-16k tokens 139 us (5.1 TB/s), four of 49-65k 52.5 us (4.9), 64 of 32k
+// 394 us (6.1).  Unpacking comes close behind: 280 instructions per page and head,
+// 2.2 of them a cycle and SM.
 //
 // Work.  Every sequence counts its pages (1 if empty) and kSeqUnits for its
 // start and end (a query load, a merge of the warps, an output: about as long
@@ -412,13 +420,13 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // another.
 //
 // Warp w takes every fourth group of NP of the run's pages (NP = 2, or 4 at D
-// = 64: several at a time give a warp independent chains of products and
-// share the exchanges of the maximum) and copies them ahead into its own ring of shared-memory stages with 16-byte
-// asynchronous copies; it alone reads what it copied, so the ring needs no
-// barrier, only its copy groups.  (Bulk copies held the issuing warp for about
-// 500 cycles each: four 49k-65k-token contexts took 72 us with every warp
-// issuing its own and 87 us from one producer warp.)  Per page, two
-// products on mma.sync m16n8k16 (f16 in, fp32 accumulate):
+// = 64: several at a time give a warp independent chains of products; with one
+// the four long contexts take 64 us) and copies them ahead into its own ring of
+// shared-memory stages with 16-byte asynchronous copies; it alone reads what it
+// copied, so the ring needs no barrier, only its copy groups.  (Bulk copies
+// held the issuing warp for about 500 cycles each: the four long contexts took
+// 72 us with every warp issuing its own and 87 us from one producer warp.)  Per
+// page, two products on mma.sync m16n8k16 (f16 in, fp32 accumulate):
 //   S[16 tokens x 8 heads] = K Q^T    O^T[D x 8 heads] += V^T P
 // The page's order gives every lane its A operands in whole 16-byte words: a
 // lane of K's operand holds 32 consecutive dims of two tokens (two scales
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 constexpr int kConsumers = 4;
 constexpr int kDecThreads = kConsumers * 32;
 constexpr int kTile = 8;                // query heads of a tile (columns of a product)
-constexpr int kSeqUnits = 20;           // units of a sequence besides its pages
+constexpr int kSeqUnits = 24;           // units of a sequence besides its pages
 constexpr int kMinRun = 24;             // units per CTA at least
 constexpr int kMaxCtas = 1024;          // CTAs in all rows, where there are fewer rows
 constexpr float kPShift = 10.f, kSlack = 5.f;    // log2
@@ -462,6 +470,10 @@ struct DecCfg {
     static constexpr int WS = 2;                                // stages of a warp
     static constexpr int NS = WS * kConsumers;                  // stages of the CTA
     static constexpr int CTAS = D == 64 ? 5 - NT : D == 128 ? 4 - NT : 2;   // resident per SM
+    // Merge areas: with two, a warp goes on to the next segment while others still
+    // merge (the four long contexts: 54.0 -> 52.5 us with a sequence's 24 units; with
+    // 20 of them 53.7); at D = 256 the second would cost the other CTA of the SM.
+    static constexpr int AREAS = D == 256 ? 1 : 2;
     static constexpr int MT = D / 16;
     static constexpr int KW = D / 32;               // code words of one token per lane
     static constexpr int PART = HEADS * (D + 4);    // floats of a part: per head o, m, l
@@ -562,6 +574,13 @@ struct RunCursor {
     }
 };
 
+// What the warps of a CTA leave at the end of a segment, besides their outputs.
+template <int HEADS>
+struct MergeArea {
+    float m[kConsumers][HEADS], l[kConsumers][HEADS], scale[HEADS];
+    int bad[kConsumers];
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_kernel(const Kv4DecodeArgs a)
 {
@@ -569,8 +588,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
     constexpr int NP = C::NP, MT = C::MT, KW = C::KW, PART = C::PART;
     constexpr int STRIDE = NP * kConsumers;         // pages from a warp's group to its next
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ float s_m[kConsumers][C::HEADS], s_l[kConsumers][C::HEADS], s_sc[C::HEADS];
-    __shared__ int s_bad[kConsumers];
+    __shared__ MergeArea<C::HEADS> merge[C::AREAS];
     __shared__ int s_scan[kDecThreads / 32];
     __shared__ int s_first, s_first_unit, s_last;
 
@@ -695,8 +713,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
 
     // ---------------------------------------------------- attention
     const int r = lane >> 2, t4 = lane & 3;
-    float *s_o = reinterpret_cast<float *>(dsm + C::NS * C::STAGE); // [kConsumers][G][D]
+    float *const outs = reinterpret_cast<float *>(dsm + C::NS * C::STAGE);  // [AREAS][kConsumers][G][D]
     int ws = 0;                                     // stage of this warp's next group
+    int area = 0;                                   // of this segment's merge
     bool first_segment = true;
     do {
         const int s = seg.s, n = seg.tokens, j0 = seg.j0, j1 = seg.j1;
@@ -962,6 +981,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
         }
 
         // ------------------------------------------------ end of the segment
+        MergeArea<C::HEADS> &mg = merge[area];
+        float *s_o = outs + area * kConsumers * G * D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -970,10 +991,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                 for (int off = 4; off <= 16; off <<= 1)
                     l_part[nt][h] += __shfl_xor_sync(0xffffffffu, l_part[nt][h], off);
                 if (lane < 4) {
-                    s_m[warp][nt * kTile + 2 * lane + h] = ref[nt][h];
+                    mg.m[warp][nt * kTile + 2 * lane + h] = ref[nt][h];
                     if (warp == 0)
-                        s_sc[nt * kTile + 2 * lane + h] = sc[nt][h];
-                    s_l[warp][nt * kTile + 2 * lane + h] = l_part[nt][h];
+                        mg.scale[nt * kTile + 2 * lane + h] = sc[nt][h];
+                    mg.l[warp][nt * kTile + 2 * lane + h] = l_part[nt][h];
                 }
             }
             // o[mt]: dims of run r: 16 (r + 8 p) + 2 b (D = 64: 8 r + 2 b) in c0, c1, the next in c2, c3
@@ -990,9 +1011,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
             }
         }
         if (lane == 0)
-            s_bad[warp] = bad;
+            mg.bad[warp] = bad;
         __syncthreads();
-        bad = s_bad[0] || s_bad[1] || s_bad[2] || s_bad[3];
+        bad = mg.bad[0] || mg.bad[1] || mg.bad[2] || mg.bad[3];
         const bool whole = j0 == 0 && j1 == seg.pages;
         // The warps' states merged: four dims per thread and turn.
         float *part = a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * PART +
@@ -1003,22 +1024,22 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
             *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D + d) =
                 make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
             if (d == 0 && a.lse)
-                a.lse[out_row] = l == 0.f ? -FLT_MAX : (m * s_sc[g] - kPShift + __log2f(l)) * kLn2;
+                a.lse[out_row] = l == 0.f ? -FLT_MAX : (m * mg.scale[g] - kPShift + __log2f(l)) * kLn2;
         };
         for (int e = 4 * tid; e < G * D; e += 4 * kDecThreads) {
             const int g = e / D, d = e % D;
-            const float mt = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
+            const float mt = fmaxf(fmaxf(mg.m[0][g], mg.m[1][g]), fmaxf(mg.m[2][g], mg.m[3][g]));
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float l = 0.f;
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
-                const float f = ex2_approx((s_m[w][g] - mt) * s_sc[g]);
+                const float f = ex2_approx((mg.m[w][g] - mt) * mg.scale[g]);
                 const float4 v = *reinterpret_cast<const float4 *>(&s_o[(w * G + g) * D + d]);
                 acc.x = fmaf(v.x, f, acc.x);
                 acc.y = fmaf(v.y, f, acc.y);
                 acc.z = fmaf(v.z, f, acc.z);
                 acc.w = fmaf(v.w, f, acc.w);
-                l = fmaf(s_l[w][g], f, l);
+                l = fmaf(mg.l[w][g], f, l);
             }
             if (!whole) {
                 float *q = part + g * (D + 4);
@@ -1047,7 +1068,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                 const int late = seg.at > xa * run;
                 for (int e = 4 * tid; e < G * D; e += 4 * kDecThreads) {
                     const int g = e / D, d = e % D;
-                    const float scale = s_sc[g];
+                    const float scale = mg.scale[g];
                     float mt = kNoRef, l = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     bool any_bad = false;
@@ -1092,7 +1113,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                     *ticket = 0;                    // ready for the next call
             }
         }
-        __syncthreads();                            // s_o, s_m, s_l, s_bad are free again
+        if constexpr (C::AREAS == 1)
+            __syncthreads();                        // the area is free again
+        else
+            area ^= 1;      // (read again only behind the next segment's barrier)
         first_segment = false;
     } while (seg.next(a, u0, u1));
 }
@@ -1105,7 +1129,7 @@ cudaError_t launch_decode_dn(const Kv4DecodeArgs &a, int sm_count, cudaStream_t 
     const int rows = a.num_kv_heads * ((group + C::HEADS - 1) / C::HEADS);
     const int heads = group < C::HEADS ? group : C::HEADS;
     const size_t smem = static_cast<size_t>(C::NS) * C::STAGE +
-                        static_cast<size_t>(kConsumers) * heads * D * sizeof(float);
+                        static_cast<size_t>(C::AREAS) * kConsumers * heads * D * sizeof(float);
     // the largest size any call needs, once per device
     static int attr_done[64] = {0};
     int dev = 0;
@@ -1115,7 +1139,8 @@ cudaError_t launch_decode_dn(const Kv4DecodeArgs &a, int sm_count, cudaStream_t 
     if (dev >= 64 || !attr_done[dev]) {
         e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::NS * C::STAGE +
-                                     kConsumers * C::HEADS * D * static_cast<int>(sizeof(float)));
+                                     C::AREAS * kConsumers * C::HEADS * D *
+                                         static_cast<int>(sizeof(float)));
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
@@ -1133,7 +1158,7 @@ cudaError_t launch_decode_dn(const Kv4DecodeArgs &a, int sm_count, cudaStream_t 
     parts = parts < most ? parts : most;
     // One CTA merges a sequence's parts, 8 per load latency: up to 256 runs where
     // a sequence may take them all, 8 per sequence where there are many (one kv
-    // head, 64 contexts of 15-30k tokens of 128: 62 us with 256 runs, 53 with 456).
+    // head, 64 contexts of 15-30k tokens of 128: 59 us with 256 runs, 51 with 456).
     const long long cap = 8LL * a.num_seqs > 256 ? 8LL * a.num_seqs : 256;
     parts = parts < 1 ? 1 : (parts > cap ? cap : parts);
     return launch_dependent(kv4_decode_kernel<D, NT>, dim3(static_cast<int>(parts), rows), kDecThreads,
