@@ -144,6 +144,72 @@ def test_prompt_fork_decode_free_compact(vfa):
         assert (after[0][torch.tensor([0, 4]).cuda()] == 0).all()
 
 
+def test_captured_step_serves_every_token(vfa):
+    """extend -> norm + rotation -> write -> decode captured once and replayed for 40 tokens (over
+    page borders), bit for bit the eager calls; a row joins in between by a fork outside the graph."""
+    rows, Hq, Hkv, D, BS = 5, 8, 2, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn(60, rows, (Hq + 2 * Hkv) * D, generator=g, device="cuda").bfloat16()
+    table = vfa.rope_table([500.0 ** (-i / 64) for i in range(64)])
+    w = 1 + 0.1 * torch.randn(2, D, generator=g, device="cuda")
+
+    def state():
+        refs = torch.zeros(64, dtype=torch.int32, device="cuda")
+        return dict(refs=refs, tables=torch.full((rows, 8), -1, dtype=torch.int32, device="cuda"),
+                    counts=_i32([0] * rows), start=_i32([0] * rows), add=_i32([1, 1, 0, 1, 1]),
+                    cu=_i32([0, 1, 2, 2, 3, 4]), pool=vfa.alloc_kv4_pool(64, Hkv, D),
+                    x=torch.zeros(rows, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device="cuda"),
+                    ws=vfa.alloc_pages_workspace(64, rows, 1), status=_i32([0]),
+                    dws=vfa.alloc_kv4_decode_workspace(rows, Hq, Hkv, D),
+                    out=torch.zeros(rows, Hq, D, dtype=torch.bfloat16, device="cuda"),
+                    lse=torch.zeros(rows, Hq, device="cuda"))
+
+    def step(t):
+        """One token for the rows that take one; packed row i is the i-th of them."""
+        t["start"].copy_(t["counts"])
+        vfa.pages_extend(t["refs"], t["tables"], t["counts"], t["add"], BS, t["ws"],
+                         status=t["status"])
+        pick = torch.where(t["add"] > 0, 0, rows)           # the rows that take a token, first
+        order = torch.argsort(pick + torch.arange(rows, device="cuda"))
+        q, k, v = t["x"].split((Hq * D, Hkv * D, Hkv * D), 1)
+        q, k = vfa.qk_norm_rope(q.view(rows, Hq, D), k.view(rows, Hkv, D),
+                                t["start"][order].contiguous(), table, w[0], w[1])
+        vfa.kv4_write(k, v.view(rows, Hkv, D), t["pool"], t["tables"], t["cu"], t["start"], 0.5, 0.25,
+                      status=t["status"])
+        qs = torch.empty_like(q)
+        qs[order] = q
+        vfa.kv4_decode(qs, t["pool"], t["tables"], t["counts"], 0.5, 0.25, out=t["out"], lse=t["lse"],
+                       workspace=t["dws"], status=t["status"])
+
+    eager, held = state(), state()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(state())                                       # (libraries and allocations are warm)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(held)
+        torch.cuda.synchronize()
+        for i in range(40):
+            if i == 21:                                     # row 2 becomes a sample of row 1
+                for t in (eager, held):
+                    vfa.pages_fork(t["refs"], t["tables"], t["counts"], _i32([1]), _i32([2]),
+                                   [t["pool"]], BS, t["ws"], status=t["status"])
+                    t["add"].fill_(1)
+                    t["cu"].copy_(torch.arange(rows + 1, device="cuda"))
+            for t in (eager, held):
+                t["x"].copy_(qkv[i])
+            step(eager)
+            graph.replay()
+            assert torch.equal(eager["out"], held["out"]) and torch.equal(eager["lse"], held["lse"]), i
+        side.synchronize()
+    for name in ("refs", "tables", "counts", "pool", "status"):
+        assert torch.equal(eager[name], held[name]), name
+    assert held["status"].item() == 0
+    assert held["counts"].tolist() == [40, 40, 40, 40, 40]
+    assert (held["out"].float().abs().amax((1, 2)) > 0).all()
+
+
 def test_bf16_pools_moved_right_before_a_decode_step(vfa):
     """decode_step reads its pools before it waits for the kernel ahead of it; the page
     operations must have finished by then, without a synchronisation between."""

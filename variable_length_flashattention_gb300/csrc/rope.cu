@@ -28,8 +28,8 @@
 // warp knows of its place comes from a shuffled warp number, so that it lives
 // in uniform registers: the backward was bound by instructions that moved
 // values about (191 us with 428 instructions per turn, 157 with 360).
-// 32768 tokens of 40 heads of 128: forward 108 us (6.2 TB/s), backward 157
-// (6.4 TB/s); loads into registers instead of the ring 113 and 188.
+// 32768 tokens of 40 heads of 128: forward 105 us (6.4 TB/s), backward 155
+// (6.5 TB/s); loads into registers instead of the ring 113 and 188.
 #include <cuda_bf16.h>
 
 #include "f32x2.cuh"
