@@ -454,7 +454,7 @@ vfa_status vfa_debug_bounded_wait(int32_t *device_status, vfa_stream_t stream);
  * q_weight, k_weight  device f32 [head_dim], each nullable (no norm).
  * eps          finite, >= 0.
  *
- * Supported: head_dim 64, 128 or 256; rotary_dim a multiple of 16 in
+ * Supported: head_dim 64, 128 or 256; at most 65535 heads; rotary_dim a multiple of 16 in
  * [0, head_dim] (0: positions and table are not read); pointers of bf16
  * tensors 16-byte aligned and strides multiples of 8, at least heads *
  * head_dim.  With tokens == 0 nothing is enqueued and tensors may be NULL.
@@ -522,8 +522,8 @@ vfa_status vfa_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_stride, 
  *              table serves both kinds of pool).
  * device_status  nullable device int32 [1]; the first error is kept, so clear
  *              it before use.
- * Supported: head_dim 64, 128 or 256; num_blocks <= 2^26; pool, k, v 16-byte
- * aligned.
+ * Supported: head_dim 64, 128 or 256; at most 65535 kv heads; num_blocks <=
+ * 2^26; pool, k, v 16-byte aligned.
  */
 size_t vfa_kv4_block_bytes(int num_kv_heads, int head_dim);
 
@@ -614,7 +614,9 @@ vfa_status vfa_kv4_decode(const void *q, const void *pool, int num_blocks, const
  * 4-bit): pools is a host array of num_pools device addresses (16-byte
  * aligned, num_blocks pages each) and page_bytes a host array of their page
  * sizes (multiples of 16); at most 256 pools, and 0 is allowed.  Nothing is
- * read back to the host, so the calls can be captured in a graph.
+ * read back to the host, so the calls can be captured in a graph.  num_blocks
+ * and the entries of one call are at most 2^26; an empty list (no forks, no
+ * rows, no copies) enqueues nothing and may be NULL.
  *
  * New pages are the free pages with the lowest ids, handed out in the order
  * stated, so the results depend on the inputs alone.

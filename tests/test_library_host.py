@@ -228,6 +228,7 @@ def test_norm_rotation_host_checks(vfa):
                                       Hq, Hkv, D, out, f, 512, 256, None)
 
     assert fwd(D=96, stride=1024) == vfa.VFA_ERR_UNSUPPORTED
+    assert fwd(Hq=65536, stride=1 << 30) == vfa.VFA_ERR_UNSUPPORTED
     assert fwd(rot=24) == vfa.VFA_ERR_UNSUPPORTED and b"rotary_dim" in L.vfa_last_error()
     for kw in (dict(q=None), dict(out=None), dict(q=odd), dict(stride=508), dict(stride=504),
                dict(pos=None), dict(table=None), dict(table=odd), dict(axes=0), dict(rot=144),
@@ -260,6 +261,8 @@ def test_kv4_host_checks(vfa):
     for fn in (L.vfa_kv4_write, L.vfa_kv4_gather):
         assert write(fn=fn, D=96) == vfa.VFA_ERR_UNSUPPORTED
         assert write(fn=fn, blocks=(1 << 26) + 1) == vfa.VFA_ERR_UNSUPPORTED
+        assert fn(f, f, 1 << 30, 1 << 30, 4, f, 9, f, 3, f, f, 2, 65536, 128, 1.0, 1.0, None,
+                  None) == vfa.VFA_ERR_UNSUPPORTED
         for kw in (dict(k=None), dict(k=odd), dict(pool=None), dict(pool=odd), dict(tables=None),
                    dict(cu=None), dict(start=None), dict(stride=248), dict(stride=257),
                    dict(total=-1), dict(cap=-1), dict(S=0), dict(dk=0.0), dict(dk=3.0),
@@ -327,6 +330,13 @@ def test_page_operation_host_checks(vfa):
                                                         to, nu, f, need, None, None)
     for args in ((None, f, f), (f, None, f), (f, f, None), (odd, f, f)):
         assert comp(*args) == vfa.VFA_ERR_INVALID_ARG
+    # empty lists may be NULL: the next check in line is the device's
+    none = fork(n=0)
+    assert fork(n=0, par=None, chi=None) == none != vfa.VFA_ERR_INVALID_ARG
+    assert L.vfa_pages_free(f, 100, f, 6, f, 4, None, 0, 16, None, None) == none
+    assert L.vfa_pages_copy(ptrs, sizes, 2, None, None, 0, 9, None, None) == none
+    assert fork(n=(1 << 26) + 1, nb=1 << 40) == vfa.VFA_ERR_UNSUPPORTED
+    assert L.vfa_pages_workspace_bytes(100, 4, (1 << 26) + 1) == 0
     copy = lambda src=f, n=2, nb=9: L.vfa_pages_copy(ptrs, sizes, 2, src, f, n, nb, None, None)
     assert copy(src=None) == vfa.VFA_ERR_INVALID_ARG
     assert copy(n=-1) == vfa.VFA_ERR_INVALID_ARG and copy(nb=0) == vfa.VFA_ERR_INVALID_ARG

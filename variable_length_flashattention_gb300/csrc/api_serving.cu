@@ -33,6 +33,7 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 bool supported_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr int kMaxBlocks = 1 << 26;
+constexpr int kMaxHeads = 65535;            // a token's or a page's bytes stay within 32 bits
 
 // ---------------------------------------------------------------- norm, rotation
 
@@ -44,6 +45,8 @@ vfa_status check_rope(const vfa::RopeArgs &a, int rotary_dim, int head_dim, cons
                     a.heads[0], a.heads[1]);
     if (!supported_head_dim(head_dim))
         return fail(VFA_ERR_UNSUPPORTED, "head_dim %d not supported (64, 128, 256)", head_dim);
+    if (a.heads[0] > kMaxHeads || a.heads[1] > kMaxHeads)
+        return fail(VFA_ERR_UNSUPPORTED, "%d / %d heads, at most %d", a.heads[0], a.heads[1], kMaxHeads);
     if (rotary_dim < 0 || rotary_dim > head_dim)
         return fail(VFA_ERR_INVALID_ARG, "rotary_dim %d outside [0, head_dim]", rotary_dim);
     if (rotary_dim % 16 != 0)
@@ -111,6 +114,8 @@ vfa_status check_kv4(const void *pool, int num_blocks, const int32_t *tables, in
         return fail(VFA_ERR_UNSUPPORTED, "head_dim %d not supported (64, 128, 256)", head_dim);
     if (num_blocks > kMaxBlocks)
         return fail(VFA_ERR_UNSUPPORTED, "num_blocks %d above 2^26 not supported", num_blocks);
+    if (num_kv_heads > kMaxHeads)
+        return fail(VFA_ERR_UNSUPPORTED, "%d kv heads, at most %d", num_kv_heads, kMaxHeads);
     if (!power_of_two(descale_k) || !power_of_two(descale_v))
         return fail(VFA_ERR_INVALID_ARG,
                     "descale_k and descale_v must be powers of two in [2^-64, 2^64]");
@@ -307,7 +312,7 @@ vfa_status vfa_qk_norm_rope_bwd(const void *q, const void *k, int64_t q_stride, 
 
 size_t vfa_kv4_block_bytes(int num_kv_heads, int head_dim)
 {
-    if (num_kv_heads < 1 || !supported_head_dim(head_dim))
+    if (num_kv_heads < 1 || num_kv_heads > kMaxHeads || !supported_head_dim(head_dim))
         return 0;
     return static_cast<size_t>(num_kv_heads) * vfa::kv4_head_page_bytes(head_dim);
 }
@@ -401,7 +406,8 @@ vfa_status vfa_kv4_decode(const void *q, const void *pool, int num_blocks, const
 
 size_t vfa_pages_workspace_bytes(int num_blocks, int num_seqs, int num_forks)
 {
-    if (num_blocks < 1 || num_blocks > kMaxBlocks || num_seqs < 1 || num_forks < 0)
+    if (num_blocks < 1 || num_blocks > kMaxBlocks || num_seqs < 1 || num_forks < 0 ||
+        num_forks > kMaxBlocks)
         return 0;
     return vfa::page_workspace_bytes(num_blocks, num_seqs, num_forks);
 }
@@ -446,8 +452,11 @@ vfa_status vfa_pages_fork(int32_t *refcounts, int num_blocks, int32_t *tables, i
                                 block_size, device_status);
     if (st || (st = page_pools(pools, page_bytes, num_pools, &p)))
         return st;
-    if (num_forks < 0 || !parents || !children || !aligned(parents, 4) || !aligned(children, 4))
+    if (num_forks < 0 || (num_forks > 0 && (!parents || !children)) || !aligned(parents, 4) ||
+        !aligned(children, 4))
         return fail(VFA_ERR_INVALID_ARG, "parents and children must be non-null, aligned pointers");
+    if (num_forks > kMaxBlocks)
+        return fail(VFA_ERR_UNSUPPORTED, "num_forks %d above 2^26 not supported", num_forks);
     if ((st = check_page_workspace(workspace, workspace_bytes, num_blocks, num_seqs, num_forks)))
         return st;
     int sms;
@@ -480,7 +489,7 @@ vfa_status vfa_pages_free(int32_t *refcounts, int num_blocks, const int32_t *tab
                                 block_size, device_status);
     if (st)
         return st;
-    if (n < 0 || !seqs || !aligned(seqs, 4))
+    if (n < 0 || (n > 0 && !seqs) || !aligned(seqs, 4))
         return fail(VFA_ERR_INVALID_ARG, "seqs must be a non-null, aligned pointer");
     int sms;
     if ((st = vfa::device_sm_count(&sms)))
@@ -546,7 +555,8 @@ vfa_status vfa_pages_copy(void *const *pools, const int *page_bytes, int num_poo
     vfa_status st = page_pools(pools, page_bytes, num_pools, &p);
     if (st)
         return st;
-    if (n < 0 || !src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(device_status, 4))
+    if (n < 0 || (n > 0 && (!src || !dst)) || !aligned(src, 4) || !aligned(dst, 4) ||
+        !aligned(device_status, 4))
         return fail(VFA_ERR_INVALID_ARG, "src and dst must be non-null, aligned pointers");
     if (num_blocks < 1)
         return fail(VFA_ERR_INVALID_ARG, "bad size argument");

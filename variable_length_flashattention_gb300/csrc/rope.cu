@@ -446,6 +446,7 @@ cudaError_t launch_d(RopeArgs &a, int sm_count, cudaStream_t stream)
     using C = RopeCfg<BWD>;
     constexpr int SMEM = C::WARPS * C::AHEAD * (BWD ? 2 : 1) * kTurn;
     static_assert(SMEM >= C::WARPS * D * static_cast<int>(sizeof(float)), "the ring holds the warps' dw");
+    static_assert(SMEM + 2 * D * static_cast<int>(sizeof(float)) <= 48 * 1024, "no opt-in needed");
     a.segments = head_segments(a, (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW,
                                sm_count);
     const long long need = (static_cast<long long>(a.tokens) * a.segments + C::WARPS - 1) / C::WARPS;
@@ -454,20 +455,6 @@ cudaError_t launch_d(RopeArgs &a, int sm_count, cudaStream_t stream)
     grid = grid < kRopeMaxCtas ? grid : kRopeMaxCtas;
     a.ctas = static_cast<int>(grid);
     const auto kernel = a.interleaved ? rope_kernel<D, true, BWD> : rope_kernel<D, false, BWD>;
-    if (SMEM + 2 * D * sizeof(float) > 48 * 1024) {
-        static int attr_done[2][64] = {{0}};
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess)
-            return e;
-        if (dev >= 64 || !attr_done[a.interleaved][dev]) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            if (e != cudaSuccess)
-                return e;
-            if (dev < 64)
-                attr_done[a.interleaved][dev] = 1;
-        }
-    }
     const cudaError_t e = launch_dependent(kernel, dim3(a.ctas), C::WARPS * 32, SMEM, stream, a);
     if (e != cudaSuccess || !BWD || (!a.dweight[0] && !a.dweight[1]))
         return e;
