@@ -263,6 +263,27 @@ def test_decode_many_small_weights(vfa):
     _check_decode(_run(vfa, case), case)
 
 
+def test_decode_keeps_bad_numbers_where_they_are(vfa):
+    """NaN and infinity in one query head, a NaN scale in one sequence's pages: the heads of the
+    same tile and the other sequences, some in the same CTA, are right."""
+    case = _decode_case([700, 3, 40, 9, 2500], 8, 2, 64, seed=11)
+    q, pool, tables, n, dk, dv = case
+    bad_q, bad_pool = q.clone(), pool.copy()
+    bad_q[1, 5, 7] = float("nan")
+    bad_q[4, 0] = float("inf")
+    bad_q[4, 1, 3] = float("-inf")
+    bad_pool[tables[2, 1], 1, O.v_scale_byte(3, 16, 64)] = 0x7f
+    bad_pool[tables[2, 1], 1, O.k_scale_byte(4, 0, 64)] = 0xff
+    got = _run(vfa, (bad_q, bad_pool, tables, n, dk, dv))
+    hit = np.zeros((5, 8), bool)
+    hit[1, 5] = hit[4, :2] = hit[2, 4:] = True
+    ref = O.kv4_decode(q.double().numpy(), pool, tables, n, dk, dv)
+    bo, bl = _bounds(ref, n)
+    out, lse = got[0].double().cpu().numpy(), got[1].double().cpu().numpy()
+    assert (np.abs(out - ref[0]) <= bo)[~hit].all() and (np.abs(lse - ref[1]) <= bl)[~hit].all()
+    assert np.isnan(out[hit]).any(-1).all() and not np.isfinite(lse[hit]).any()
+
+
 def test_decode_refuses_bad_pages(vfa):
     """A bad count or page id: status set, that sequence's rows as they were, the others right."""
     case = _decode_case([100, 3000, 50, 20, 64], 4, 2, 128, seed=2)

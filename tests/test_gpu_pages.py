@@ -217,6 +217,24 @@ def test_compact_into_other_tables(vfa):
         assert np.array_equal(d.cpu().numpy(), p)
 
 
+def test_copy_past_32_bits(vfa):
+    """Pages beyond 4 GiB of a pool, copied and compacted."""
+    page = 1 << 20
+    pool = torch.zeros((1 << 32) // page + 9, page, dtype=torch.uint8, device="cuda")
+    last = pool.shape[0] - 1
+    x = torch.randint(0, 256, (2, page), dtype=torch.uint8, device="cuda")
+    pool[last], pool[last - 2] = x[0], x[1]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    vfa.pages_copy([pool], i32([last, last - 2]), i32([last - 1, 5]))
+    assert torch.equal(pool[last - 1], x[0]) and torch.equal(pool[5], x[1])
+    refs = torch.zeros(last + 1, dtype=torch.int32, device="cuda")
+    refs[[last - 2, last]] = 1
+    tables = i32([[last, last - 2]])
+    used = vfa.pages_compact(refs, tables, i32([32]), [pool], 16, vfa.alloc_pages_workspace(last + 1, 1))
+    assert used.item() == 2 and tables.tolist() == [[1, 0]]
+    assert torch.equal(pool[1], x[0]) and torch.equal(pool[0], x[1])
+
+
 @pytest.mark.parametrize("shape", [(16,), (48,), (4096,), (5, 16), (2304,), (16, 8, 64)])
 def test_copy(vfa, shape):
     rng = np.random.default_rng(1)

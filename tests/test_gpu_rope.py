@@ -183,6 +183,25 @@ def test_in_place_and_strided_outputs(vfa):
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
+def test_token_strides_past_32_bits(vfa):
+    """Tokens 2^30 elements apart: the packed case's bits, in place, forward and backward."""
+    T, H, D = 4, 3, 128
+    c = _case(T, H, H, D, 64, 1, True, seed=8, strided=False)
+    q, k, pos, w = _dev(c)
+    table = vfa.rope_table(c["f"])
+    dy = [d.cuda() for d in c["dy"]]
+    want = vfa.qk_norm_rope(q, k, pos, table, *w)
+    wantb = vfa.qk_norm_rope_bwd(q, k, *dy, pos, table, *w)
+    buf = torch.empty((T - 1 << 30) + 4 * H * D, dtype=torch.bfloat16, device="cuda")
+    far = [buf.as_strided((T, H, D), (1 << 30, D, 1), i * H * D) for i in range(4)]
+    for x, f in zip((q, k, *dy), far):
+        f.copy_(x)
+    gotb = vfa.qk_norm_rope_bwd(*far, pos, table, *w, dq=far[2], dk=far[3])
+    got = vfa.qk_norm_rope(far[0], far[1], pos, table, *w, q_out=far[0], k_out=far[1])
+    for a, b in zip((*want, *wantb), (*got, *gotb)):
+        assert torch.equal(a, b)
+
+
 def test_no_tokens(vfa):
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     pos = torch.empty(1, 0, dtype=torch.int32, device="cuda")
