@@ -312,3 +312,39 @@ def test_training_step_gradients(vfa):
                           (got[0], got[1], gv, got[2], got[3]), want):
         err = (a.double().cpu() - b).norm() / b.norm()
         assert err <= 16 * 2.0 ** -8, (name, float(err))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_taken_on_while_some_are_still_written(vfa, D):
+    """varlen_bwd and the rotation's backward with nothing between them.  One tile of keys and 64
+    query heads on one kv head: the kernel of dk and dv is one CTA's long loop, that of dq is done
+    far earlier.  The rotation's backward must see the finished dk: bit for bit the gradients
+    from finished tensors."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    Lq, Lk, H = 4096, 128, 64
+    q, dout = (torch.randn(Lq, H, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn(Lk, 1, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    cuq, cuk = _i32([0, Lq]), _i32([0, Lk])
+    out, lse = vfa.varlen_fwd(q, k, v, cuq, cuk, Lq, D ** -0.5, 0)
+    table = vfa.rope_table([100.0 ** (-i / 16) for i in range(16)])
+    pos = torch.arange(Lk, dtype=torch.int32, device="cuda")
+    w = torch.ones(D, device="cuda")
+    few = torch.randn(Lk, 1, D, generator=g, device="cuda").bfloat16()
+    # every buffer exists before the two calls: an allocation's own kernel would come between
+    dq, dk, dv = torch.empty_like(q), torch.full_like(k, float("nan")), torch.empty_like(v)
+    ws = vfa.alloc_bwd_workspace(1, Lq, H, D)
+    rws = vfa.alloc_qk_norm_rope_bwd_workspace(D)
+    outs = [torch.empty_like(few), torch.empty_like(few), torch.empty_like(w), torch.empty_like(w)]
+
+    def rope():
+        return vfa.qk_norm_rope_bwd(few, k, few, dk, pos, table, w, w, dq=outs[0], dk=outs[1],
+                                    dq_weight=outs[2], dk_weight=outs[3], workspace=rws)
+
+    torch.cuda.synchronize()
+    vfa.varlen_bwd(q, k, v, out, dout, lse, cuq, cuk, D ** -0.5, 0, dq=dq, dk=dk, dv=dv, workspace=ws)
+    rope()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in outs]
+    assert torch.isfinite(dk.float()).all()
+    for a, b in zip(got, rope()):
+        assert torch.equal(a, b)

@@ -556,8 +556,17 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
     // nothing this kernel writes: let it take each SM this kernel's CTAs leave.
     if (!DQ)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (*a.status != VFA_OK)
+    // The dQ kernel waits for the dK/dV kernel before it ends: what is launched
+    // behind it in the same way waits for the dQ kernel alone, and may read dK
+    // and dV.
+    auto wait_for_dkv = [] {
+        if (DQ)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
+    if (*a.status != VFA_OK) {
+        wait_for_dkv();
         return;
+    }
     const int B = a.batch, H = a.num_heads, Hkv = a.num_kv_heads;
     const int tiles = DQ ? a.qtile_start[B] : a.ktile_start[B];
     int32_t *counter = a.status + (DQ ? 2 : 1);
@@ -929,6 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
+    wait_for_dkv();
 }
 
 template <int D>
@@ -970,9 +980,9 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
         // Programmatic dependent launch: the dQ kernel's CTAs start on the SMs
         // the dK/dV kernel's CTAs leave, without waiting for the whole grid.  It
         // reads only the prep and Delta kernels' output, complete before the
-        // dK/dV kernel started (a plain launch after them), so it needs no
-        // griddepcontrol.wait; its atomic unit counter balances CTAs that start
-        // late.
+        // dK/dV kernel started (a plain launch after them), so it waits
+        // (griddepcontrol.wait) only at its end; its atomic unit counter balances
+        // CTAs that start late.
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(q_units, sm_count)));
         cfg.blockDim = dim3(kThreads);
