@@ -247,3 +247,26 @@ def test_captured_backward_beside_an_eager_one(vfa):
             graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(eager, outs))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 3), (5, 7), (3, 1), (8, 2)])
+def test_backward_without_eps(vfa, D, Hq, Hkv):
+    """eps = 0 and head counts that leave lanes of a warp's turn without a head: the rows have a
+    norm, so every gradient is an ordinary number (tolerances as above)."""
+    T, R = 41, 32
+    c = _case(T, Hq, Hkv, D, R, 1, True, seed=D + Hq)
+    q, k, pos, w = _dev(c)
+    dy = [t.cuda() for t in c["dy"]]
+    got = vfa.qk_norm_rope_bwd(q, k, dy[0], dy[1], pos, vfa.rope_table(c["f"]), w[0], w[1], eps=0.0)
+    for i, x in enumerate((c["q"], c["k"])):
+        x, y, wt = _f64(x), _f64(c["dy"][i]), _f64(c["w"][i])
+        dx, dw = O.norm_rope_bwd(x, y, c["pos"].numpy(), c["f"], c["ax"], wt, 0.0, False)
+        g = _amp(y, R, False)
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True))
+        u = g * np.abs(wt)
+        amp = r * (u + np.abs(x) * r * r * (u * np.abs(x)).mean(-1, keepdims=True))
+        tol = (T * x.shape[1] + 96) * U * (g * np.abs(x) * r).sum((0, 1))
+        assert (np.abs(_f64(got[2 + i]) - dw) <= tol).all(), got[2 + i]
+        tol = 2.0 ** -8 * np.abs(dx) + 96 * U * amp * (1 + 2.0 ** -8)
+        assert (np.abs(_f64(got[i]) - dx) <= tol).all()

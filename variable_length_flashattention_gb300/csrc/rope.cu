@@ -322,10 +322,13 @@ __global__ void __launch_bounds__(RopeCfg<BWD>::WARPS * 32, RopeCfg<BWD>::CTAS) 
                 rotate(y, c2, s2);
             if (norm) {
                 if (h - g + HPW > a.heads[which] && !live) {
-                    // lanes past the heads hold whatever was there
+                    // lanes past the heads hold whatever was there: no gradient, on rows that have
+                    // a norm (with eps = 0 a zero row's r is infinite, and 0 r no number)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[j] = y[j] = 0;
+                    for (int j = 0; j < 8; ++j) {
+                        x[j] = f2_pack(1.f, 1.f);
+                        y[j] = 0;
+                    }
                 }
                 f2 q = 0, d = 0;
 #pragma unroll
