@@ -283,3 +283,26 @@ def test_captured_cycle(vfa):
     O.extend(st.refs, st.tables, st.counts, np.array([0] * 4 + [1] * 4 + [0] * 4, np.int32), 4)
     O.free(st.refs, st.tables, st.counts, [4, 5, 6, 7], 4)
     st.check(0)
+
+
+@pytest.mark.parametrize("blocks", [6, 32768, 32769, 70000])
+def test_fork_of_rows_that_list_free_pages(vfa, blocks):
+    """A full page that is not in use when the call is made is listed in the child, not counted
+    and recorded, also where the same call hands that page out as another child's own copy."""
+    st = State(vfa, blocks, 8, 6, 4, page_shapes=((2, 16),), seed=blocks)
+    last = blocks - 1
+    # rows 0 and 1 end in a partly filled page (1, last); page 0 and 3 are free and listed
+    st.refs[[1, 2, last]] = 1
+    st.tables[0, :2], st.tables[1, :3] = (0, 1), (3, 2, last)
+    st.counts[:2] = 6, 10
+    st.d_refs.copy_(torch.from_numpy(st.refs))
+    st.d_tables.copy_(torch.from_numpy(st.tables))
+    st.d_counts.copy_(torch.from_numpy(st.counts))
+    st.vfa.pages_fork(st.d_refs, st.d_tables, st.d_counts, st.i32([0, 1]), st.i32([2, 4]),
+                      st.d_pools, 4, st.ws, status=st.status)
+    # the lowest free pages in the order of the entries: 0 and 3, the ones listed above
+    st.tables[2, :2], st.tables[4, :3] = (0, 0), (3, 2, 3)
+    st.counts[[2, 4]] = 6, 10
+    st.refs[[0, 2, 3]] = 1, 2, 1
+    st.pools[0][0], st.pools[0][3] = st.pools[0][1], st.pools[0][last]
+    st.check(st.vfa.VFA_ERR_BAD_BLOCK)

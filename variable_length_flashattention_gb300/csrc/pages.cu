@@ -45,7 +45,8 @@ struct PageWs {
     int32_t *head;      // [64]: [H_N] pages to assign / move, [H_USED] used pages
     int32_t *chunk;     // [chunks] used pages per chunk
     int32_t *src, *dst; // [num_blocks] page copies
-    int32_t *rank;      // [num_blocks] compact: index of the page's move, -1 none
+    int32_t *rank;      // [num_blocks] compact: index of the page's move, -1 none; fork: the
+                        // pool's use bits when the call began, 32 pages a word
     int32_t *offs;      // [max(num_seqs, forks) + 1] first rank per sequence; fork: entry per rank
     int32_t *plan;      // [forks][4] parent, child, tokens, 0
     int32_t *mark;      // [num_seqs] fork: entry that claimed the child
@@ -117,8 +118,9 @@ __device__ __forceinline__ int used_before(const int32_t *chunk, int n, int *s_w
     return total;
 }
 
+// bits (nullable): the pages' use bits.
 __global__ void __launch_bounds__(kPlanThreads) count_kernel(const int32_t *refs, int num_blocks,
-                                                             int32_t *chunk)
+                                                             int32_t *chunk, int32_t *bits)
 {
     grid_wait();
     grid_release();
@@ -127,7 +129,13 @@ __global__ void __launch_bounds__(kPlanThreads) count_kernel(const int32_t *refs
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const long long id = static_cast<long long>(blockIdx.x) * kChunk + k * kPlanThreads + threadIdx.x;
-        v += id < num_blocks && refs[id] > 0;
+        const bool is_used = id < num_blocks && refs[id] > 0;
+        v += is_used;
+        if (bits) {
+            const uint32_t word = __ballot_sync(0xffffffffu, is_used);
+            if ((threadIdx.x & 31) == 0 && id < num_blocks)
+                bits[id >> 5] = static_cast<int32_t>(word);
+        }
     }
     block_scan(v, &total, s_warp);
     if (threadIdx.x == 0)
@@ -283,7 +291,9 @@ __device__ __forceinline__ void place_fork(const PageArgs &a, const PageWs &w, i
     a.refs[id] = 1;
 }
 
-// The full pages of entry i's parent are shared with its child.
+// The full pages of entry i's parent are shared with its child.  Whether a page
+// is in use is asked of the bits from before the call: this call's new pages
+// have a reference already, or get it meanwhile from another CTA.
 __device__ __forceinline__ void share_pages(const PageArgs &a, const PageWs &w, int i)
 {
     const int p = w.plan[4 * i];
@@ -295,7 +305,7 @@ __device__ __forceinline__ void share_pages(const PageArgs &a, const PageWs &w, 
     for (int j = threadIdx.x; j < full; j += blockDim.x) {
         const int id = from[j];
         to[j] = id;
-        if (id < 0 || id >= a.num_blocks || a.refs[id] <= 0)
+        if (id < 0 || id >= a.num_blocks || !(static_cast<uint32_t>(w.rank[id >> 5]) >> (id & 31) & 1))
             record(a.status, VFA_ERR_BAD_BLOCK);        // not a page in use: not counted
         else
             atomicAdd(&a.refs[id], 1);
@@ -419,6 +429,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(const PageArgs
     __shared__ int s_warp[kPlanThreads / 32];
     int used;
     const uint32_t word = use_word(a, s_bits, &used, s_warp);
+    if (static_cast<int>(threadIdx.x) < (a.num_blocks + 31) / 32)
+        w.rank[threadIdx.x] = static_cast<int32_t>(s_bits[threadIdx.x]);
     const int n = plan_fork(a, w, used, s_warp);
     list_free(word, n, w.dst, s_warp);
     for (int r = threadIdx.x; r < n; r += kPlanThreads)
@@ -686,7 +698,7 @@ cudaError_t launch_pages_extend(const PageArgs &a, cudaStream_t stream)
     const int chunks = chunks_of(a.num_blocks);
     cudaError_t e;
     if ((e = launch_dependent(count_kernel, dim3(chunks), kPlanThreads, 0, stream, a.refs,
-                              a.num_blocks, w.chunk)) ||
+                              a.num_blocks, w.chunk, static_cast<int32_t *>(nullptr))) ||
         (e = launch_dependent(extend_plan_kernel, dim3(1), kPlanThreads, 0, stream, a, w)) ||
         (e = launch_dependent(assign_kernel<false>, dim3(chunks), kPlanThreads, 0, stream, a, w)))
         return e;
@@ -711,7 +723,7 @@ cudaError_t launch_pages_fork(const PageArgs &a, const PagePools &p, int sm_coun
     PageArgs b = a;
     b.copies = p.n > 0;
     if ((e = launch_dependent(count_kernel, dim3(chunks), kPlanThreads, 0, stream, a.refs,
-                              a.num_blocks, w.chunk)) ||
+                              a.num_blocks, w.chunk, w.rank)) ||
         (e = launch_dependent(fork_plan_kernel, dim3(1), kPlanThreads, 0, stream, a, w)) ||
         (e = launch_dependent(assign_kernel<true>, dim3(chunks + a.n), kPlanThreads, 0, stream, b, w)))
         return e;
@@ -737,7 +749,7 @@ cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_c
         if ((e = launch_dependent(compact_small_kernel, dim3(1), kPlanThreads, 0, stream, a, w)))
             return e;
     } else if ((e = launch_dependent(count_kernel, dim3(chunks), kPlanThreads, 0, stream, a.refs,
-                                     a.num_blocks, w.chunk)) ||
+                                     a.num_blocks, w.chunk, static_cast<int32_t *>(nullptr))) ||
                (e = launch_dependent(compact_rank_kernel, dim3(chunks), kPlanThreads, 0, stream, a,
                                      w))) {
         return e;
