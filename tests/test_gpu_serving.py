@@ -348,3 +348,45 @@ def test_gradients_taken_on_while_some_are_still_written(vfa, D):
     assert torch.isfinite(dk.float()).all()
     for a, b in zip(got, rope()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+def test_pages_overwritten_behind_a_decode_step_without_tokens(vfa, splits):
+    """A long decode step, one whose tiles are all empty, and a copy over the first one's pages,
+    with nothing between them: the copy must not start while the first step still reads."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows, per, Hkv, D = 4, 1000, 8, 128
+    blocks = 2 * rows * per
+    kp, vp = (torch.randn(blocks, 16, Hkv, D, generator=g, device="cuda", dtype=torch.bfloat16)
+              for _ in range(2))
+    kp[::2] = float("nan")                                 # no row lists the even pages
+    tables = torch.arange(1, blocks, 2, dtype=torch.int32, device="cuda").view(rows, per)
+    dst = tables.flip(1).reshape(-1).contiguous()          # the pages read last are copied first
+    src = dst - 1
+    q = torch.randn(rows, 32, D, generator=g, device="cuda").bfloat16()
+    full, none = (torch.full((rows,), n, dtype=torch.int32, device="cuda") for n in (per, 0))
+    ws = vfa.alloc_decode_split_workspace(rows, 32, Hkv, D, splits) if splits > 1 else None
+
+    def state():
+        m, l = (torch.empty(rows, 32, device="cuda") for _ in range(2))
+        o = torch.empty(rows, 32, D, device="cuda")
+        vfa.decode_init(m, l, o)
+        return m, l, o
+
+    def step(n, st):
+        if splits > 1:
+            vfa.decode_step_split(q, kp, vp, tables, n, *st, splits, ws)
+        else:
+            vfa.decode_step(q, kp, vp, tables, n, *st)
+
+    want = state()
+    step(full, want)
+    got = state()
+    torch.cuda.synchronize()
+    step(full, got)
+    step(none, got)
+    vfa.pages_copy([kp, vp], src, dst)
+    torch.cuda.synchronize()
+    assert torch.isnan(kp).all()
+    for a, b in zip(want, got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)

@@ -217,8 +217,13 @@ __global__ void __launch_bounds__(kStepWarps * 32) decode_step_kernel(
             atomicCAS(a.status, 0, VFA_ERR_BAD_BLOCK);
         return;
     }
-    if (count == 0 || n_tok == 0)
-        return;                                 // an empty tile leaves the state as it was
+    if (count == 0 || n_tok == 0) {
+        // An empty tile leaves the state as it was.  What is launched behind this grid
+        // waits for it alone, so it must not end before the step ahead of it has, which
+        // may still read pools and tables that the next call changes.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int nb_all = (n_tok + kBlockSize - 1) / kBlockSize;   // blocks holding those tokens
     // This CTA's run of blocks [kb0, kb0 + nb): the whole tile, or run
     // blockIdx.z of num_splits equal runs (possibly empty).

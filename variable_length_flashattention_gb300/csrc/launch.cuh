@@ -1,5 +1,14 @@
 // launch.cuh -- launches that may start while the kernel before them in the
 // stream is still running (programmatic stream serialisation).
+//
+// What orders them.  griddepcontrol.wait waits for the one grid ahead: for it to
+// end and for its writes to be visible.  The grids ahead of that one are done only
+// if it waited for them itself, so every kernel launched this way waits before it
+// ends, also where it has nothing to do or leaves early (the backward's dQ kernel
+// and the paged decode step, which start ahead of their wait, among them).  A
+// kernel that never says launch_dependents lets the next one start at its end,
+// with its writes visible: what may be read before the wait (the paged decode
+// step's queries, tables and pools) is written by such kernels only.
 #pragma once
 
 #include <cuda_runtime.h>
