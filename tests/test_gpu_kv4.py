@@ -392,3 +392,33 @@ def test_offsets_past_32_bits(vfa):
     kk, _ = vfa.kv4_gather(pool, _i32(tables), _i32([0, n]), _i32([0]), n)
     assert np.array_equal(kk.double().cpu().numpy(),
                           O.dequantise(*O.quantise(k.double().numpy(), 1.0), 1.0))
+
+
+@pytest.mark.parametrize("exponent,scale,dk", [(100, 2.0 ** 100, 1.0), (0, 3e38, 2.0 ** 64),
+                                               (120, 0.0, 2.0 ** 40)])
+def test_decode_scale_past_fp32(vfa, exponent, scale, dk):
+    """Logits whose scale passes the largest fp32: they are finite numbers in the definition, the
+    largest takes all the weight (equal ones share it), and lse is past fp32 with its sign.
+
+    Exactly as in test_decode_huge_logits: accumulators are exact, different ones are at least
+    1/2 apart in units of the largest element of q, so all other weights are zero; the mean over
+    the c largest is off by (c + 2) u32 and ex2's 2^-20 of sum |v| / c and the bf16 rounding.
+    """
+    D, lens = 64, [40, 3, 900]
+    q, pool, tables, n, _, _ = _decode_case(lens, 2, 1, D, seed=exponent)
+    pool[..., 16 * D:] = 0x38                             # every scale 1.0
+    q[:] = 0
+    q[:, 0, 7], q[:, 1, 7] = 2.0 ** exponent, -1.5 * 2.0 ** exponent
+    got = vfa.kv4_decode(q.cuda(), torch.from_numpy(pool).cuda(), _i32(tables), _i32(n), dk, 1.0, scale)
+    for s, m in enumerate(lens):
+        k, v = (a[:, 0].reshape(-1, D)[:m]
+                for a in O.page_values(pool[tables[s, :-(-m // 16)]], 1.0, 1.0))
+        for h in range(2):
+            x = k[:, 7] * float(q[s, h, 7])
+            top = x == x.max()
+            ref = v[top].mean(0)
+            c = int(top.sum())
+            tol = ((c + 2) * U + 2.0 ** -20) * np.abs(v[top]).mean(0) + 2.0 ** -8 * np.abs(ref) + 1e-30
+            assert (np.abs(got[0][s, h].double().cpu().numpy() - ref) <= tol).all(), (s, h)
+            if x.max() != 0:
+                assert float(got[1][s, h]) == math.copysign(math.inf, x.max())

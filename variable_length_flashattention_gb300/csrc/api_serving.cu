@@ -395,9 +395,10 @@ vfa_status vfa_kv4_decode(const void *q, const void *pool, int num_blocks, const
     a.num_blocks = num_blocks;
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
-    a.scale_log2 = static_cast<float>(
+    const double scale_log2 =
         (softmax_scale > 0.f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(double(head_dim))) *
-        descale_k * 1.4426950408889634);
+        descale_k * 1.4426950408889634;
+    a.scale_log2 = scale_log2 > FLT_MAX ? INFINITY : static_cast<float>(scale_log2);
     a.descale_v = descale_v;
     return launched(vfa::launch_kv4_decode(head_dim, a, workspace, sms,
                                            reinterpret_cast<cudaStream_t>(stream)),

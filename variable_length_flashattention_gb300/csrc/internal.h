@@ -256,7 +256,7 @@ struct Kv4DecodeArgs {
     float *part;                            // workspace: partial states
     int32_t *tickets;                       // workspace: [num_seqs, head chunks], zero between calls
     int num_seqs, capacity, num_blocks, num_q_heads, num_kv_heads;
-    float scale_log2;                       // logit scale * descale_k * log2(e)
+    float scale_log2;                       // logit scale * descale_k * log2(e), inf past fp32
     float descale_v;
 };
 

@@ -761,8 +761,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NT>::CTAS) kv4_decode_k
                                                       __uint_as_float(w[c] & 0xffff0000u) * up)
                                          : 0u;
             }
-            // positive, or a masked -inf times it would be no number
-            const float x = fmaxf(a.scale_log2 * down, FLT_MIN);
+            // positive, or a masked -inf times it would be no number; finite, or the zero between
+            // equal logits times it would (at FLT_MAX any other difference has weight zero)
+            const float x = fminf(fmaxf(a.scale_log2 * down, FLT_MIN), FLT_MAX);
             sc[nt][0] = __shfl_sync(0xffffffffu, x, (2 * t4) * 4);
             sc[nt][1] = __shfl_sync(0xffffffffu, x, (2 * t4 + 1) * 4);
         }
