@@ -613,10 +613,10 @@ vfa_status vfa_kv4_decode(const void *q, const void *pool, int num_blocks, const
  * One such state serves any number of pools (K and V of every layer, bf16 or
  * 4-bit): pools is a host array of num_pools device addresses (16-byte
  * aligned, num_blocks pages each) and page_bytes a host array of their page
- * sizes (multiples of 16); at most 256 pools, and 0 is allowed.  Nothing is
- * read back to the host, so the calls can be captured in a graph.  num_blocks
- * and the entries of one call are at most 2^26; an empty list (no forks, no
- * rows, no copies) enqueues nothing and may be NULL.
+ * sizes (multiples of 16, at most 2^31 - 4096); at most 256 pools, and 0 is
+ * allowed.  Nothing is read back to the host, so the calls can be captured in
+ * a graph.  num_blocks and the entries of one call are at most 2^26; an empty
+ * list (no forks, no rows, no copies) enqueues nothing and may be NULL.
  *
  * New pages are the free pages with the lowest ids, handed out in the order
  * stated, so the results depend on the inputs alone.

@@ -369,3 +369,33 @@ def test_binding_checks_of_the_serving_operators(vfa):
     for step, f in zip(t[:, 0].tolist(), (1.0, 1e-5, -2.5)):
         turns = (step % 2 ** 64) / 2 ** 64
         assert abs(turns - f / (2 * math.pi) % 1.0) < 1e-15
+
+
+def test_page_sizes_past_32_bits_are_refused(vfa):
+    L = vfa.lib()
+    f = ctypes.c_void_p(0x100000)
+    ptrs = (ctypes.c_void_p * 1)(0x100000)
+
+    def copy(size):
+        return L.vfa_pages_copy(ptrs, (ctypes.c_int * 1)(size), 1, f, f, 2, 9, None, None)
+
+    # past 2^31 - 4096 the 4096-byte pieces of a page are no longer counted in 32 bits
+    for size in (2 ** 31 - 16, 2 ** 31 - 4096 + 16):
+        assert copy(size) == vfa.VFA_ERR_UNSUPPORTED and b"at most" in L.vfa_last_error()
+    need = L.vfa_pages_workspace_bytes(9, 2, 0)
+    assert L.vfa_pages_compact(f, 9, f, 3, f, 2, ptrs, (ctypes.c_int * 1)(2 ** 31 - 16), 1, 16, f, f, f,
+                               f, need, None, None) == vfa.VFA_ERR_UNSUPPORTED
+
+    class Pool:                                # (a page of more than 4 GiB)
+        nbytes = 2 * (2 ** 32 + 16)
+        get_device = lambda self: 0
+        is_contiguous = lambda self: True
+        dim = lambda self: 2
+        size = lambda self, i: 2
+        data_ptr = lambda self: 0x100000
+
+    with pytest.raises(ValueError, match="32 bits"):
+        vfa._pool_list([Pool()], 2, 0)
+    with pytest.raises(ValueError, match="32 bits"):
+        vfa._fits(5, 2 ** 32 + 16)
+    vfa._fits(0, 2 ** 31 - 1)

@@ -3,6 +3,7 @@
 // argument checks and launches.  Nothing here allocates or frees device
 // memory.
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -34,6 +35,7 @@ bool supported_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr int kMaxBlocks = 1 << 26;
 constexpr int kMaxHeads = 65535;            // a token's or a page's bytes stay within 32 bits
+constexpr int kMaxPageBytes = INT_MAX - 4095;       // the copy counts a page's pieces in 32 bits
 
 // ---------------------------------------------------------------- norm, rotation
 
@@ -214,6 +216,9 @@ vfa_status page_pools(void *const *pools, const int *page_bytes, int num_pools, 
         if (!pools[i] || !aligned(pools[i], 16) || page_bytes[i] < 16 || page_bytes[i] % 16 != 0)
             return fail(VFA_ERR_INVALID_ARG,
                         "pool %d must be 16-byte aligned with pages of a multiple of 16 bytes", i);
+        if (page_bytes[i] > kMaxPageBytes)
+            return fail(VFA_ERR_UNSUPPORTED, "pool %d has pages of %d bytes, at most %d", i,
+                        page_bytes[i], kMaxPageBytes);
         p->ptr[i] = static_cast<uint8_t *>(pools[i]);
         p->page_bytes[i] = page_bytes[i];
     }

@@ -465,6 +465,13 @@ def _refuse(t, dtype, name, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _fits(*sizes):
+    """The C ABI takes sizes as int32, and ctypes would cut a larger one without a word."""
+    for n in sizes:
+        if n > 0x7fffffff:
+            raise ValueError(f"size {n} does not fit 32 bits")
+
+
 def _device(t: torch.Tensor, name: str) -> int:
     """The current device, which must be t's: kernels are launched there."""
     dev = t.get_device()
@@ -566,7 +573,7 @@ def _rope_inputs(q, k, positions, table, q_weight, k_weight):
             _refuse(positions, _I32, "positions", dev)
         pshape = positions.shape
         axes = 1 if len(pshape) == 1 else pshape[0]
-        if not 1 <= len(pshape) <= 2 or pshape[-1] != T:
+        if not 1 <= len(pshape) <= 2 or pshape[-1] != T or axes > 0x7fffffff:
             raise ValueError("positions must be [tokens] or [axes, tokens]")
     if q_weight is not None:
         _rope_weight(q_weight, "q_weight", D, dev)
@@ -692,6 +699,7 @@ def _kv4_pool(pool, tables, status):
     if pool.dim() != 3 or tables.dim() != 2:
         raise ValueError("pool must be [num_blocks, num_kv_heads, 18 * head_dim], tables "
                          "[num_seqs, capacity]")
+    _fits(*tables.shape)
     D, rest = divmod(pool.shape[2], 18)
     if rest:
         raise ValueError("pool pages must hold 18 * head_dim bytes per kv head")
@@ -819,7 +827,7 @@ def alloc_pages_workspace(num_blocks: int, num_seqs: int, num_forks: int = 0,
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _page_state(refcounts, tables, token_counts, status):
+def _page_state(refcounts, tables, token_counts, status, block_size):
     """Checks; (device, num_blocks, capacity, num_seqs)."""
     dev = _device(refcounts, "refcounts")
     _dense(refcounts, _I32, "refcounts", dev)
@@ -832,7 +840,9 @@ def _page_state(refcounts, tables, token_counts, status):
         raise ValueError("refcounts [num_blocks], tables [num_seqs, capacity] and token_counts "
                          "[num_seqs]")
     S, cap = tables.shape
-    return dev, refcounts.shape[0], cap, S
+    blocks = refcounts.shape[0]
+    _fits(blocks, cap, S, block_size)
+    return dev, blocks, cap, S
 
 
 def _pool_list(pools, num_blocks, dev):
@@ -844,15 +854,16 @@ def _pool_list(pools, num_blocks, dev):
         if p.dim() < 2 or p.size(0) != num_blocks:
             raise ValueError(f"pools[{i}] must hold {num_blocks} pages")
     blocks = max(num_blocks, 1)
-    return ((_P * n)(*[p.data_ptr() for p in pools]),
-            (_I * n)(*[p.nbytes // blocks for p in pools]), n)
+    sizes = [p.nbytes // blocks for p in pools]
+    _fits(num_blocks, *sizes)
+    return (_P * n)(*[p.data_ptr() for p in pools]), (_I * n)(*sizes), n
 
 
 def pages_extend(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
                  add_tokens: torch.Tensor, block_size: int, workspace: torch.Tensor,
                  status: Optional[torch.Tensor] = None, stream=None):
     """token_counts += add_tokens, with new pages where rows need them (vfa_pages_extend)."""
-    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status, block_size)
     _dense(workspace, _U8, "workspace", dev)
     _dense(add_tokens, _I32, "add_tokens", dev)
     if add_tokens.shape != token_counts.shape:
@@ -870,12 +881,13 @@ def pages_fork(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torc
                workspace: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None):
     """Rows children[i] become copies of rows parents[i]: full pages shared, a partly filled
     last page copied in every pool (vfa_pages_fork).  A negative parent skips the entry."""
-    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status, block_size)
     _dense(workspace, _U8, "workspace", dev)
     _dense(parents, _I32, "parents", dev)
     _dense(children, _I32, "children", dev)
     if parents.dim() != 1 or parents.shape != children.shape:
         raise ValueError("parents and children must be [num_forks]")
+    _fits(parents.shape[0])
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
     if parents.shape[0] == 0:
         return
@@ -891,9 +903,10 @@ def pages_free(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torc
                seqs: torch.Tensor, block_size: int, status: Optional[torch.Tensor] = None,
                stream=None):
     """Rows seqs[i] give up their pages (vfa_pages_free).  A negative entry is skipped."""
-    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status, block_size)
     _dense(seqs, _I32, "seqs", dev)
     n = seqs.numel()
+    _fits(n)
     if n == 0:
         return
     st = (_lib or lib()).vfa_pages_free(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
@@ -911,7 +924,7 @@ def pages_compact(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: t
                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the used pages to the low end of every pool (vfa_pages_compact); refcounts and
     tables are rewritten in place unless outputs are given.  Returns int32 [1]: used pages."""
-    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status)
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status, block_size)
     _dense(workspace, _U8, "workspace", dev)
     refcounts_out = refcounts if refcounts_out is None else refcounts_out
     tables_out = tables if tables_out is None else tables_out
@@ -945,6 +958,7 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
         _dense(status, _I32, "status", dev)
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be [n]")
+    _fits(src.shape[0])
     blocks = pools[0].shape[0]
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
     if src.shape[0] == 0:
