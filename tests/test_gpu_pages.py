@@ -306,3 +306,105 @@ def test_fork_of_rows_that_list_free_pages(vfa, blocks):
     st.refs[[0, 2, 3]] = 1, 2, 1
     st.pools[0][0], st.pools[0][3] = st.pools[0][1], st.pools[0][last]
     st.check(st.vfa.VFA_ERR_BAD_BLOCK)
+
+
+@pytest.mark.parametrize("blocks,S,seed", [(32768, 24, 6), (32769, 24, 7), (36864, 5, 8),
+                                           (36865, 40, 9), (70000, 24, 10)])
+def test_histories_of_large_pools(vfa, blocks, S, seed):
+    """Pools around and above the largest that one CTA plans (32768 pages): thousands of pages
+    given, shared, taken back and moved over many chunks, some requests without enough pages."""
+    bs = 3
+    cap = 3 * blocks // S
+    st = State(vfa, blocks, S, cap, bs, page_shapes=((1, 16), (2, 16)), forks=S, seed=seed)
+    rng = np.random.default_rng(seed)
+    refused = moved = 0
+    for step in range(9):
+        free = int((st.refs <= 0).sum())
+        want = rng.random(S) ** 3 * (rng.random(S) < 0.7)
+        # half of the free pages, or (every third step) more than there are
+        want = want / max(want.sum(), 1e-9) * free * bs * (1.4 if step % 3 == 1 else 0.5)
+        add = np.minimum(want.astype(np.int64) + (rng.random(S) < 0.3), cap * bs - st.counts)
+        before = st.counts.copy()
+        st.extend(add)
+        refused += bool(add.any() and np.array_equal(before, st.counts))
+        empty, live = np.flatnonzero(st.counts == 0), np.flatnonzero(st.counts > 0)
+        if len(empty) and len(live):
+            n = rng.integers(1, len(empty) + 1)
+            parents = rng.choice(live, n)
+            parents[rng.random(n) < 0.1] = -1
+            pools = st.pools, st.d_pools
+            if step % 4 == 2:                              # the pages alone, no pool
+                st.pools, st.d_pools = [], []
+            st.fork(parents, rng.permutation(empty)[:n])
+            st.pools, st.d_pools = pools
+        gone = np.flatnonzero(rng.random(S) < 0.4)
+        st.free(np.concatenate((gone, gone[:1], [-1])))
+        if step % 3 == 2:
+            used = int((st.refs > 0).sum())
+            moved += int((st.refs[used:] > 0).sum())
+            st.compact()
+    assert refused >= 1 and moved > 1000
+
+
+def test_refusals_of_a_large_pool_change_nothing(vfa):
+    st = State(vfa, 40000, 6, 39000, 4, page_shapes=((1, 16),))
+    st.extend([4 * 38997 + 1, 4, 0, 0, 0, 0])
+    v = st.vfa
+
+    def refused(call, code):
+        call()
+        st.check(code)
+
+    ext = lambda add: v.pages_extend(st.d_refs, st.d_tables, st.d_counts, st.i32(add), 4, st.ws,
+                                     status=st.status)
+    fork = lambda p, c: v.pages_fork(st.d_refs, st.d_tables, st.d_counts, st.i32(p), st.i32(c),
+                                     st.d_pools, 4, st.ws, status=st.status)
+    refused(lambda: ext([0, -1, 0, 0, 0, 0]), v.VFA_ERR_BAD_BLOCK)
+    refused(lambda: ext([16, 0, 0, 0, 0, 0]), v.VFA_ERR_BAD_BLOCK)       # past the row's capacity
+    refused(lambda: ext([0, 4 * 1002, 0, 0, 0, 0]), v.VFA_ERR_NO_PAGES)
+    refused(lambda: fork([0, 0], [2, 2]), v.VFA_ERR_BAD_BLOCK)
+    refused(lambda: fork([0], [1]), v.VFA_ERR_BAD_BLOCK)
+    refused(lambda: fork([0, 6], [2, 3]), v.VFA_ERR_BAD_BLOCK)
+    st.extend([0, 4 * 1001, 0, 0, 0, 0])                   # exactly the rest
+    refused(lambda: fork([0], [2]), v.VFA_ERR_NO_PAGES)    # no page for the copy
+    st.free([0])
+    st.fork([1, 1], [2, 5])
+    st.compact()
+
+
+@pytest.mark.parametrize("blocks", [20000, 40000])
+def test_more_rows_than_one_cta_keeps(vfa, blocks):
+    """5000 rows: the rows' places are kept in the workspace (a CTA's shared memory holds 4096)."""
+    test_random_histories(vfa, blocks, 5000, 3, 16, blocks)
+
+
+def test_captured_cycle_of_a_large_pool(vfa):
+    """Fork, extend and free in one graph, replayed over several chunks."""
+    st = State(vfa, 50000, 12, 9000, 4, page_shapes=((1, 16),), seed=2)
+    st.extend([4 * 8000 + 1, 4 * 3000, 30] + [0] * 9)
+    st.free([1])
+    st.extend([0, 4 * 4000 + 3] + [0] * 10)
+    parents, children = st.i32([0, 1, 2, 0]), st.i32([4, 5, 6, 7])
+    add = st.i32([0] * 4 + [5, 1, 4000, 1] + [0] * 4)
+    v = st.vfa
+
+    def cycle():
+        v.pages_fork(st.d_refs, st.d_tables, st.d_counts, parents, children, st.d_pools, 4, st.ws)
+        v.pages_extend(st.d_refs, st.d_tables, st.d_counts, add, 4, st.ws)
+        v.pages_free(st.d_refs, st.d_tables, st.d_counts, children, 4)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            cycle()
+        for _ in range(3):
+            g.replay()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        O.fork(st.refs, st.tables, st.counts, [0, 1, 2, 0], [4, 5, 6, 7], st.pools, 4)
+        O.extend(st.refs, st.tables, st.counts,
+                 np.array([0] * 4 + [5, 1, 4000, 1] + [0] * 4, np.int32), 4)
+        O.free(st.refs, st.tables, st.counts, [4, 5, 6, 7], 4)
+    st.check(0)
