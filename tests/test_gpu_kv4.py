@@ -422,3 +422,45 @@ def test_decode_scale_past_fp32(vfa, exponent, scale, dk):
             assert (np.abs(got[0][s, h].double().cpu().numpy() - ref) <= tol).all(), (s, h)
             if x.max() != 0:
                 assert float(got[1][s, h]) == math.copysign(math.inf, x.max())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(17, 1), (32, 1), (66, 2)])
+def test_decode_several_head_chunks(vfa, D, Hq, Hkv):
+    """More query heads per kv head than one CTA takes, the last chunk of them almost empty."""
+    case = _decode_case([1, 16, 0, 17, 130, 333], Hq, Hkv, D, seed=Hq * D)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _run(vfa, case, status=status)
+    assert vfa.read_status(status) == 0
+    _check_decode(got, case)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(34, 1, 64), (20, 1, 128), (40, 2, 128), (11, 1, 256)])
+def test_decode_head_chunks_over_several_runs(vfa, Hq, Hkv, D):
+    """Long sequences cut into runs, with several head chunks per kv head: every chunk has
+    partial states and tickets of its own, and the workspace serves again."""
+    case = _decode_case([6000, 3, 700, 0, 2500], Hq, Hkv, D, seed=Hq)
+    ws = vfa.alloc_kv4_decode_workspace(5, Hq, Hkv, D)
+    per = 8 if D == 256 else 16
+    rows = Hkv * -(-(Hq // Hkv) // per)
+    first = _run(vfa, case, workspace=ws)
+    _check_decode(first, case)
+    assert (ws[-5 * rows * 4:] == 0).all()                # the tickets
+    second = _run(vfa, case, workspace=ws)
+    assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
+
+
+def test_bad_cu_seqlens_are_recorded_as_such(vfa):
+    """Every token these prefix sums place has a page, so nothing else can be recorded."""
+    D, Hkv, total = 64, 2, 33
+    x = torch.randn(total, Hkv, D).bfloat16().cuda()
+    pool = vfa.alloc_kv4_pool(12, Hkv, D)
+    tables = _i32(np.arange(12).reshape(3, 4))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for cu in ([0, 25, 20, total], [1, 20, 24, total], [0, 20, 24, total + 1], [-1, 20, 24, total]):
+        for call in (lambda: vfa.kv4_write(x, x, pool, tables, _i32(cu), _i32([0, 0, 0]), status=status),
+                     lambda: vfa.kv4_gather(pool, tables, _i32(cu), _i32([0, 0, 0]), total,
+                                            status=status)):
+            status.zero_()
+            call()
+            assert vfa.read_status(status) == vfa.VFA_ERR_BAD_SEQLENS, cu
