@@ -270,3 +270,26 @@ def test_backward_without_eps(vfa, D, Hq, Hkv):
         assert (np.abs(_f64(got[2 + i]) - dw) <= tol).all(), got[2 + i]
         tol = 2.0 ** -8 * np.abs(dx) + 96 * U * amp * (1 + 2.0 ** -8)
         assert (np.abs(_f64(got[i]) - dx) <= tol).all()
+
+
+@pytest.mark.parametrize("T,H,D", [(20000, 8, 64), (30001, 1, 128), (6000, 12, 256)])
+def test_weight_gradients_are_summed_as_a_tree(vfa, T, H, D):
+    """The sums of dweight run over lanes, warps and CTAs side by side.  A lane adds one term per
+    turn of its warp: with four warps in four CTAs of every SM, each taking whole tokens, at most
+    ceil(T / (16 SMs)) tokens of ceil(H / (512 / D)) turns; then log2(512 / D) <= 3 exchanges, 4
+    warps, ceil(4 SMs / 32) CTAs per slice and 5 exchanges of the slices.  A term is within 32 u32
+    (above), so the error is at most (depth + 32) u32 sum |g x r|, far below the chain of all
+    T * H terms."""
+    c = _case(T, H, H, D, 32, 1, True, seed=T)
+    q, k, pos, w = _dev(c)
+    dy = [t.cuda() for t in c["dy"]]
+    got = vfa.qk_norm_rope_bwd(q, k, dy[0], dy[1], pos, vfa.rope_table(c["f"]), w[0], w[1])
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert T >= 32 * sms                                   # (fewer tokens: their heads are shared)
+    depth = -(-T // (16 * sms)) * -(-H * D // 512) + 3 + 4 + -(-4 * sms // 32) + 5
+    for i, x in enumerate((c["q"], c["k"])):
+        x, y, wt = _f64(x), _f64(c["dy"][i]), _f64(c["w"][i])
+        _, dw = O.norm_rope_bwd(x, y, c["pos"].numpy(), c["f"], c["ax"], wt, 1e-6, False)
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6)
+        tol = (depth + 32) * U * (_amp(y, 32, False) * np.abs(x) * r).sum((0, 1))
+        assert (np.abs(_f64(got[2 + i]) - dw) <= tol).all()
