@@ -727,10 +727,10 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, tables: torc
     blocks, Hkv, _ = pool.shape
     T = k.shape[0]
     ks, vs = _rows(k, (T, Hkv, D), "k", dev), _rows(v, (T, Hkv, D), "v", dev)
-    st = (_lib or lib()).vfa_kv4_write(k.data_ptr(), v.data_ptr(), ks, vs, T, pool.data_ptr(), blocks,
-                             tables.data_ptr(), tables.shape[1], cu_seqlens.data_ptr(),
-                             start_positions.data_ptr(), tables.shape[0], Hkv, D, descale_k,
-                             descale_v, _address(status), _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_kv4_write(
+        k.data_ptr(), v.data_ptr(), ks, vs, T, pool.data_ptr(), blocks, tables.data_ptr(),
+        tables.shape[1], cu_seqlens.data_ptr(), start_positions.data_ptr(), tables.shape[0], Hkv, D,
+        descale_k, descale_v, _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -755,11 +755,10 @@ def kv4_gather(pool: torch.Tensor, tables: torch.Tensor, cu_seqlens: torch.Tenso
         v_out, vs = _empty(shape, torch.bfloat16, pool.device, stream), Hkv * D
     else:
         vs = _rows(v_out, shape, "v_out", dev)
-    st = (_lib or lib()).vfa_kv4_gather(k_out.data_ptr(), v_out.data_ptr(), ks, vs, total_tokens,
-                              pool.data_ptr(), blocks, tables.data_ptr(), tables.shape[1],
-                              cu_seqlens.data_ptr(), start_positions.data_ptr(), tables.shape[0],
-                              Hkv, D, descale_k, descale_v, _address(status),
-                              _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_kv4_gather(
+        k_out.data_ptr(), v_out.data_ptr(), ks, vs, total_tokens, pool.data_ptr(), blocks,
+        tables.data_ptr(), tables.shape[1], cu_seqlens.data_ptr(), start_positions.data_ptr(),
+        tables.shape[0], Hkv, D, descale_k, descale_v, _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
     return k_out, v_out
@@ -806,11 +805,11 @@ def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
         _dense(workspace, _U8, "workspace", dev)
     if out.shape != q.shape or lse.shape != (S, Hq):
         raise ValueError("out must have q's shape and lse [num_seqs, num_q_heads]")
-    st = (_lib or lib()).vfa_kv4_decode(q.data_ptr(), pool.data_ptr(), blocks, tables.data_ptr(),
-                              tables.shape[1], token_counts.data_ptr(), S, Hq, Hkv, D, descale_k,
-                              descale_v, softmax_scale, out.data_ptr(), lse.data_ptr(),
-                              _address(status), workspace.data_ptr(), workspace.numel(),
-                              _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_kv4_decode(
+        q.data_ptr(), pool.data_ptr(), blocks, tables.data_ptr(), tables.shape[1],
+        token_counts.data_ptr(), S, Hq, Hkv, D, descale_k, descale_v, softmax_scale, out.data_ptr(),
+        lse.data_ptr(), _address(status), workspace.data_ptr(), workspace.numel(),
+        _raw_stream(stream, dev))
     if st:
         _check(st)
     return out, lse
@@ -868,10 +867,10 @@ def pages_extend(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: to
     _dense(add_tokens, _I32, "add_tokens", dev)
     if add_tokens.shape != token_counts.shape:
         raise ValueError("add_tokens must be [num_seqs]")
-    st = (_lib or lib()).vfa_pages_extend(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
-                                token_counts.data_ptr(), S, add_tokens.data_ptr(), block_size,
-                                workspace.data_ptr(), workspace.numel(), _address(status),
-                                _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_pages_extend(
+        refcounts.data_ptr(), blocks, tables.data_ptr(), cap, token_counts.data_ptr(), S,
+        add_tokens.data_ptr(), block_size, workspace.data_ptr(), workspace.numel(),
+        _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -891,10 +890,10 @@ def pages_fork(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torc
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
     if parents.shape[0] == 0:
         return
-    st = (_lib or lib()).vfa_pages_fork(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
-                              token_counts.data_ptr(), S, parents.data_ptr(), children.data_ptr(),
-                              parents.shape[0], ptrs, sizes, n, block_size, workspace.data_ptr(),
-                              workspace.numel(), _address(status), _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_pages_fork(
+        refcounts.data_ptr(), blocks, tables.data_ptr(), cap, token_counts.data_ptr(), S,
+        parents.data_ptr(), children.data_ptr(), parents.shape[0], ptrs, sizes, n, block_size,
+        workspace.data_ptr(), workspace.numel(), _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -909,9 +908,9 @@ def pages_free(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torc
     _fits(n)
     if n == 0:
         return
-    st = (_lib or lib()).vfa_pages_free(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
-                              token_counts.data_ptr(), S, seqs.data_ptr(), n, block_size,
-                              _address(status), _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_pages_free(
+        refcounts.data_ptr(), blocks, tables.data_ptr(), cap, token_counts.data_ptr(), S,
+        seqs.data_ptr(), n, block_size, _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -936,11 +935,10 @@ def pages_compact(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: t
             raise ValueError(f"{n} must have shape {tuple(x.shape)}")
     _dense(num_used, _I32, "num_used", dev)
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
-    st = (_lib or lib()).vfa_pages_compact(refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
-                                 token_counts.data_ptr(), S, ptrs, sizes, n, block_size,
-                                 refcounts_out.data_ptr(), tables_out.data_ptr(),
-                                 num_used.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                 _address(status), _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_pages_compact(
+        refcounts.data_ptr(), blocks, tables.data_ptr(), cap, token_counts.data_ptr(), S, ptrs,
+        sizes, n, block_size, refcounts_out.data_ptr(), tables_out.data_ptr(), num_used.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _address(status), _raw_stream(stream, dev))
     if st:
         _check(st)
     return num_used
@@ -963,8 +961,9 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
     ptrs, sizes, n = _pool_list(pools, blocks, dev)
     if src.shape[0] == 0:
         return
-    st = (_lib or lib()).vfa_pages_copy(ptrs, sizes, n, src.data_ptr(), dst.data_ptr(), src.shape[0], blocks,
-                              _address(status), _raw_stream(stream, dev))
+    st = (_lib or lib()).vfa_pages_copy(
+        ptrs, sizes, n, src.data_ptr(), dst.data_ptr(), src.shape[0], blocks, _address(status),
+        _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -972,7 +971,7 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
 def debug_bounded_wait(status: torch.Tensor, stream=None):
     """vfa_debug_bounded_wait: a wait nothing satisfies must end in VFA_ERR_TIMEOUT."""
     _need(status, torch.int32, "status")
-    _check((_lib or lib()).vfa_debug_bounded_wait(_ptr(status), _stream(stream)))
+    _check(lib().vfa_debug_bounded_wait(_ptr(status), _stream(stream)))
 
 
 def debug_paged_gather(k_pool: torch.Tensor, v_pool: torch.Tensor, tile_blocks: torch.Tensor,
@@ -980,6 +979,6 @@ def debug_paged_gather(k_pool: torch.Tensor, v_pool: torch.Tensor, tile_blocks: 
                        status: Optional[torch.Tensor] = None, stream=None):
     nb, bs, Hkv, D = k_pool.shape
     S, cap = tile_blocks.shape
-    _check((_lib or lib()).vfa_debug_paged_gather(_ptr(k_pool), _ptr(v_pool), nb, _ptr(tile_blocks),
+    _check(lib().vfa_debug_paged_gather(_ptr(k_pool), _ptr(v_pool), nb, _ptr(tile_blocks),
                                         _ptr(tile_block_counts), cap, S, Hkv, D, bs,
                                         _ptr(k_out), _ptr(v_out), _ptr(status), _stream(stream)))
