@@ -400,14 +400,17 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // heads of a kv head together: up to 8 as one tile of 8 columns, up to 16 as
 // two that share the unpacked pages (16 heads of 128 on 8 kv heads, 64
 // contexts of 4-8k: 167 us as two chunks of 8, 129 as two tiles); more are
-// more head chunks, whose pages come from L2.
+// more head chunks, whose pages come from L2.  Two tiles are bound by latency,
+// not by the second product: 239 registers leave eight warps per SM, which issue
+// 1.7 instructions a cycle with no pipe above 35%, and wait most for the results
+// of the instruction ahead.
 //
 // Bound: HBM for long batches, 1.125 bytes per dim and token of a kv head.  A
 // call takes 14 us (17 for 64 sequences) plus its pages at 6.39 TB/s, 94% of
 // the copy rate: the chain from counts over tables to the first pages, and the
 // merge behind the last.  8 kv heads of 128, 4 query heads each: 256 sequences
-// of 16-16k tokens 139 us (5.1 TB/s), four of 49-65k 52.5 us (4.9), 64 of 32k
-// 394 us (6.1).  Unpacking comes close behind: 280 instructions per page and head,
+// of 16-16k tokens 139 us (5.1 TB/s), four of 49-65k 52.8 us (4.9), 64 of 32k
+// 390 us (6.1).  Unpacking comes close behind: 280 instructions per page and head,
 // 2.2 of them a cycle and SM.
 //
 // Work.  Every sequence counts its pages (1 if empty) and kSeqUnits for its
@@ -442,9 +445,11 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_gather_kernel(const Kv4Mo
 // rescaling) only when a weight would pass it by more than a factor 2^5, so
 // most groups cost one vote.  References stay in units of the accumulators, whose
 // difference is taken before the scale: it is exact near the maximum however
-// large the logits are.  p is held as 2^10 p in f16, at most 2^15 (2^-12
+// large the logits are.  p is held as 2^10 p in f16, at most 2^15 (2^-11
 // relative for p above 2^-24, 2^-35 absolute below), l sums the fp32 values,
-// and the reference, l and o are fp32.
+// and the reference, l and o are fp32.  The roundings of p average out over the
+// keys: 0.8 to 2.0 10^-4 of the output before its own rounding to bf16, 1.65 10^-3
+// (2-norms; contexts of 150 to 65k tokens, normally distributed q, K and V).
 constexpr int kConsumers = 4;
 constexpr int kDecThreads = kConsumers * 32;
 constexpr int kTile = 8;                // query heads of a tile (columns of a product)

@@ -29,7 +29,10 @@
 // in uniform registers: the backward was bound by instructions that moved
 // values about (191 us with 428 instructions per turn, 157 with 360).
 // 32768 tokens of 40 heads of 128: forward 105 us (6.4 TB/s), backward 155
-// (6.5 TB/s); loads into registers instead of the ring 113 and 188.
+// (6.5 TB/s); loads into registers instead of the ring 113 and 188.  With few
+// tokens per warp latency shows: 8649 tokens of 8 + 8 heads of 64 take the backward
+// 18.5 us in a graph against 7.8 of bytes, for the chain table, position, sine at
+// the head of every token and the second launch for the sums of dw.
 #include <cuda_bf16.h>
 
 #include "f32x2.cuh"
