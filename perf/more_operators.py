@@ -182,7 +182,7 @@ def _prepare_varlen(case, seed):
             s["ws"] = vfa.alloc_workspace(len(lq), sum(lq), sum(lk), hq, d, device=_dev())
             if s["train"]:
                 s["bws"] = vfa.alloc_bwd_workspace(len(lq), sum(lq), hq, d, device=_dev(),
-                                                   num_kv_heads=hkv, sink_tokens=case["sinks"])
+                                                   sink_tokens=case["sinks"])
         return s
     # what the forward pass of the prompt left, and the weights of earlier chunks
     s["lse"] = torch.cat([_sequence_lse(s, b) for b in range(len(lq))])
