@@ -122,6 +122,10 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(const SchedArgs a)
     const int causal = a.causal;                         // 0 none, 1 top-left, 2 bottom-right
     const bool window = causal && a.window_left >= 0;
 
+    // Whatever the outcome, the prefill's CTAs count from zero: with no items they
+    // must not take what an unset workspace holds (a negative number, say) for one.
+    if (tid == 0 && a.next_item)
+        *a.next_item = 0;
     const int tiles_cap = max_tiles(B, a.total_q, a.block_q);
     const bool in_smem = B + 1 <= kSmemSeqs;
     if (static_cast<long long>(tiles_cap) * H > a.item_capacity ||
@@ -350,8 +354,6 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(const SchedArgs a)
     }
     if (tid == 0) {
         *a.n_items = static_cast<int>(nitems);
-        if (a.next_item)
-            *a.next_item = 0;
         *a.status = VFA_OK;
     }
 }
