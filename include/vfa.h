@@ -136,6 +136,27 @@ vfa_status vfa_varlen_fwd(const void *q, const void *k, const void *v,
                           size_t workspace_bytes, vfa_stream_t stream);
 
 /*
+ * vfa_varlen_fwd with sinks: where a window hides keys, the first sink_tokens
+ * keys of each sequence stay visible.  Local key j is visible to local query
+ * i iff j <= i + off and (j >= i + off - window_left or j < sink_tokens), off
+ * as in vfa_varlen_fwd.  Only the key tiles of the sinks and of the window are
+ * read.
+ *
+ * sink_tokens  >= 0 (else VFA_ERR_INVALID_ARG), any number: 0, or no window
+ *              (window_left < 0), is vfa_varlen_fwd.
+ * Other arguments, results, workspace and errors as in vfa_varlen_fwd.  k and
+ * v are finite: a hidden key's weight is zero, but the product with it is
+ * formed for the other rows' sake.
+ */
+vfa_status vfa_varlen_fwd_sinks(const void *q, const void *k, const void *v,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                int total_q, int total_k, int max_seqlen_q, int batch,
+                                int num_heads, int num_kv_heads, int head_dim,
+                                float softmax_scale, int causal, int window_left,
+                                int sink_tokens, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, vfa_stream_t stream);
+
+/*
  * vfa_varlen_fwd with q and k given as FP8 E4M3 codes (1 byte each: 1 sign,
  * 4 exponent bits with bias 7, 3 mantissa bits, no infinities), each tensor
  * with one descale factor: element value = descale * code.  v stays bf16.
@@ -280,6 +301,27 @@ vfa_status vfa_varlen_bwd(const void *q, const void *k, const void *v, const voi
                           int num_heads, int num_kv_heads, int head_dim, float softmax_scale,
                           int causal, int window_left, void *dq, void *dk, void *dv,
                           void *workspace, size_t workspace_bytes, vfa_stream_t stream);
+
+/*
+ * Gradients of vfa_varlen_fwd_sinks: vfa_varlen_bwd under its mask.  A sink
+ * gets a gradient from every query that sees it; the steps of the sinks' key
+ * tiles are cut into chunks that run side by side and are added in a fixed
+ * order, so results are bit-identical from run to run.
+ *
+ * workspace    vfa_varlen_bwd_sinks_workspace_bytes() bytes for at least
+ *              these sizes and sink_tokens (at most 40 MB more than
+ *              vfa_varlen_bwd's); without a window vfa_varlen_bwd's suffice.
+ */
+size_t vfa_varlen_bwd_sinks_workspace_bytes(int batch, int total_q, int num_heads, int head_dim,
+                                            int sink_tokens);
+
+vfa_status vfa_varlen_bwd_sinks(const void *q, const void *k, const void *v, const void *out,
+                                const void *dout, const float *lse, const int32_t *cu_seqlens_q,
+                                const int32_t *cu_seqlens_k, int total_q, int total_k, int batch,
+                                int num_heads, int num_kv_heads, int head_dim,
+                                float softmax_scale, int causal, int window_left,
+                                int sink_tokens, void *dq, void *dk, void *dv, void *workspace,
+                                size_t workspace_bytes, vfa_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Paged GQA decode                                                          */

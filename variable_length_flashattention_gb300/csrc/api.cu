@@ -250,6 +250,7 @@ vfa_status vfa_varlen_schedule(const int32_t *cu_seqlens_q, const int32_t *cu_se
     a.block_k = block_k;
     a.causal = causal;
     a.window_left = window_left < 0 ? -1 : window_left;
+    a.sink_tokens = 0;
     a.pair = pair_tiles != 0;
     a.items = reinterpret_cast<int4 *>(items);
     a.item_capacity = items_capacity;
@@ -273,7 +274,7 @@ static vfa_status varlen_fwd_impl(const void *q, const void *k, const void *v,
                                   float softmax_scale, int causal, int window_left, void *out,
                                   float *lse, void *workspace, size_t workspace_bytes,
                                   vfa_stream_t stream, int qk_fp8, float descale_q,
-                                  float descale_k)
+                                  float descale_k, int sink_tokens)
 {
     if (!q || !k || !v || !cu_seqlens_q || !cu_seqlens_k || !out || !lse || !workspace)
         return fail(VFA_ERR_INVALID_ARG, "null pointer argument");
@@ -330,6 +331,7 @@ static vfa_status varlen_fwd_impl(const void *q, const void *k, const void *v,
     sa.block_k = bk;
     sa.causal = causal;
     sa.window_left = window_left < 0 ? -1 : window_left;
+    sa.sink_tokens = window_left < 0 ? 0 : sink_tokens;
     sa.pair = vfa::pairs_for(head_dim) ? 1 : 0;
     sa.items = items;
     sa.item_capacity = wl.item_capacity;
@@ -376,6 +378,7 @@ static vfa_status varlen_fwd_impl(const void *q, const void *k, const void *v,
     pa.qk_fp8 = qk_fp8;
     pa.causal = causal;
     pa.window_left = sa.window_left;
+    pa.sink_tokens = sa.sink_tokens;
     const int grid = wl.item_capacity < dev.sm_count ? wl.item_capacity : dev.sm_count;
     e = vfa::launch_prefill(head_dim, pa, grid, s);
     if (e != cudaSuccess)
@@ -392,7 +395,24 @@ vfa_status vfa_varlen_fwd(const void *q, const void *k, const void *v,
 {
     return varlen_fwd_impl(q, k, v, cu_seqlens_q, cu_seqlens_k, total_q, total_k, max_seqlen_q,
                            batch, num_heads, num_kv_heads, head_dim, softmax_scale, causal,
-                           window_left, out, lse, workspace, workspace_bytes, stream, 0, 1.f, 1.f);
+                           window_left, out, lse, workspace, workspace_bytes, stream, 0, 1.f, 1.f,
+                           0);
+}
+
+vfa_status vfa_varlen_fwd_sinks(const void *q, const void *k, const void *v,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                int total_q, int total_k, int max_seqlen_q, int batch,
+                                int num_heads, int num_kv_heads, int head_dim,
+                                float softmax_scale, int causal, int window_left, int sink_tokens,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                vfa_stream_t stream)
+{
+    if (sink_tokens < 0)
+        return fail(VFA_ERR_INVALID_ARG, "sink_tokens %d is negative", sink_tokens);
+    return varlen_fwd_impl(q, k, v, cu_seqlens_q, cu_seqlens_k, total_q, total_k, max_seqlen_q,
+                           batch, num_heads, num_kv_heads, head_dim, softmax_scale, causal,
+                           window_left, out, lse, workspace, workspace_bytes, stream, 0, 1.f, 1.f,
+                           sink_tokens);
 }
 
 vfa_status vfa_varlen_fwd_fp8(const void *q_fp8, const void *k_fp8, const void *v,
@@ -411,7 +431,7 @@ vfa_status vfa_varlen_fwd_fp8(const void *q_fp8, const void *k_fp8, const void *
     return varlen_fwd_impl(q_fp8, k_fp8, v, cu_seqlens_q, cu_seqlens_k, total_q, total_k,
                            max_seqlen_q, batch, num_heads, num_kv_heads, head_dim, softmax_scale,
                            causal, window_left, out, lse, workspace, workspace_bytes, stream, 1,
-                           descale_q, descale_k);
+                           descale_q, descale_k, 0);
 }
 
 size_t vfa_varlen_bwd_workspace_bytes(int batch, int total_q, int num_heads, int head_dim)
@@ -421,12 +441,13 @@ size_t vfa_varlen_bwd_workspace_bytes(int batch, int total_q, int num_heads, int
     return vfa::bwd_workspace_bytes(batch, total_q, num_heads, head_dim);
 }
 
-vfa_status vfa_varlen_bwd(const void *q, const void *k, const void *v, const void *out,
-                          const void *dout, const float *lse, const int32_t *cu_seqlens_q,
-                          const int32_t *cu_seqlens_k, int total_q, int total_k, int batch,
-                          int num_heads, int num_kv_heads, int head_dim, float softmax_scale,
-                          int causal, int window_left, void *dq, void *dk, void *dv,
-                          void *workspace, size_t workspace_bytes, vfa_stream_t stream)
+static vfa_status varlen_bwd_impl(const void *q, const void *k, const void *v, const void *out,
+                                  const void *dout, const float *lse, const int32_t *cu_seqlens_q,
+                                  const int32_t *cu_seqlens_k, int total_q, int total_k, int batch,
+                                  int num_heads, int num_kv_heads, int head_dim,
+                                  float softmax_scale, int causal, int window_left,
+                                  int sink_tokens, void *dq, void *dk, void *dv, void *workspace,
+                                  size_t workspace_bytes, vfa_stream_t stream)
 {
     if (!q || !k || !v || !out || !dout || !lse || !cu_seqlens_q || !cu_seqlens_k || !dq ||
         !dk || !dv || !workspace)
@@ -455,7 +476,10 @@ vfa_status vfa_varlen_bwd(const void *q, const void *k, const void *v, const voi
     if (static_cast<long long>(total_q) * num_heads * head_dim > (1LL << 31) ||
         static_cast<long long>(total_k) * num_heads > (1LL << 31))
         return fail(VFA_ERR_UNSUPPORTED, "tensor too large");
-    const size_t need = vfa::bwd_workspace_bytes(batch, total_q, num_heads, head_dim);
+    const bool sinks = window_left >= 0 && sink_tokens > 0;
+    const size_t need =
+        sinks ? vfa::bwd_sinks_workspace_bytes(batch, total_q, num_heads, head_dim, sink_tokens)
+              : vfa::bwd_workspace_bytes(batch, total_q, num_heads, head_dim);
     if (workspace_bytes < need)
         return fail(VFA_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes,
                     need);
@@ -476,7 +500,11 @@ vfa_status vfa_varlen_bwd(const void *q, const void *k, const void *v, const voi
         (st = encode_packed_map(&a.tm_qs, q, total_q, num_heads, head_dim, box_q)) ||
         (st = encode_packed_map(&a.tm_dos, dout, total_q, num_heads, head_dim, box_q)))
         return st;
-    vfa::bwd_workspace_split(workspace, batch, total_q, num_heads, &a);
+    if (sinks)
+        vfa::bwd_sinks_workspace_split(workspace, batch, total_q, num_heads, &a);
+    else
+        vfa::bwd_workspace_split(workspace, batch, total_q, num_heads, &a);
+    a.sink_tokens = sinks ? sink_tokens : 0;
     a.cu_q = cu_seqlens_q;
     a.cu_k = cu_seqlens_k;
     a.out = out;
@@ -501,6 +529,43 @@ vfa_status vfa_varlen_bwd(const void *q, const void *k, const void *v, const voi
     if (e != cudaSuccess)
         return cuda_fail(e, "backward launch");
     return VFA_OK;
+}
+
+vfa_status vfa_varlen_bwd(const void *q, const void *k, const void *v, const void *out,
+                          const void *dout, const float *lse, const int32_t *cu_seqlens_q,
+                          const int32_t *cu_seqlens_k, int total_q, int total_k, int batch,
+                          int num_heads, int num_kv_heads, int head_dim, float softmax_scale,
+                          int causal, int window_left, void *dq, void *dk, void *dv,
+                          void *workspace, size_t workspace_bytes, vfa_stream_t stream)
+{
+    return varlen_bwd_impl(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_k, total_q, total_k,
+                           batch, num_heads, num_kv_heads, head_dim, softmax_scale, causal,
+                           window_left, 0, dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+size_t vfa_varlen_bwd_sinks_workspace_bytes(int batch, int total_q, int num_heads, int head_dim,
+                                            int sink_tokens)
+{
+    if (batch < 1 || total_q < 0 || num_heads < 1 || !supported_head_dim(head_dim) ||
+        sink_tokens < 0)
+        return 0;
+    return vfa::bwd_sinks_workspace_bytes(batch, total_q, num_heads, head_dim, sink_tokens);
+}
+
+vfa_status vfa_varlen_bwd_sinks(const void *q, const void *k, const void *v, const void *out,
+                                const void *dout, const float *lse, const int32_t *cu_seqlens_q,
+                                const int32_t *cu_seqlens_k, int total_q, int total_k, int batch,
+                                int num_heads, int num_kv_heads, int head_dim,
+                                float softmax_scale, int causal, int window_left, int sink_tokens,
+                                void *dq, void *dk, void *dv, void *workspace,
+                                size_t workspace_bytes, vfa_stream_t stream)
+{
+    if (sink_tokens < 0)
+        return fail(VFA_ERR_INVALID_ARG, "sink_tokens %d is negative", sink_tokens);
+    return varlen_bwd_impl(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_k, total_q, total_k,
+                           batch, num_heads, num_kv_heads, head_dim, softmax_scale, causal,
+                           window_left, sink_tokens, dq, dk, dv, workspace, workspace_bytes,
+                           stream);
 }
 
 vfa_status vfa_paged_decode_init(float *m, float *l, float *o, int num_seqs, int num_q_heads,

@@ -37,6 +37,12 @@
 // counter, and consecutive units overlap (the next unit's own tiles load and
 // its first score products run while the current one finishes).  dK, dV and
 // dQ leave through a per-warp shared-memory stage.
+// Sinks (keys j < sink_tokens that a window leaves visible; the instantiations
+// with SINK).  A query tile's sink blocks are streamed ahead of its window's.
+// A key tile that holds sinks sees every later query of its sequence, where
+// the others see a window: its steps are cut into chunks that are units of
+// their own, about kSinkUnits in all, whose dV and dK go to the workspace in
+// fp32; bwd_sinks_kernel adds them in the order of the chunks.
 // The math warps evaluate masks only on steps that need them, as one
 // interval of visible columns per thread.  Every wait is bounded; on expiry
 // the CTA records VFA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and
@@ -151,11 +157,22 @@ __device__ void block_prefix(int B, int32_t *out, int *warp_sums, CountFn count)
         out[B] = carry;
 }
 
+// Key tiles of a sequence of lk keys that hold sinks.
+__device__ __forceinline__ int sink_tiles(const BwdArgs &a, int lk)
+{
+    return (min(a.sink_tokens, lk) + kOwn - 1) / kOwn;
+}
+
+// STEP: queries of a step of the dK/dV kernel; SPLIT: its units per key tile.
+template <int STEP, int SPLIT, bool SINK>
 __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdArgs a)
 {
     __shared__ int warp_sums[32];
     __shared__ int s_bad;
+    __shared__ unsigned long long s_steps;
     const int B = a.batch;
+    if (threadIdx.x == 0)
+        s_steps = 0;
     if (threadIdx.x == 0)
         s_bad = (a.cu_q[0] != 0 || a.cu_k[0] != 0 || a.cu_q[B] != a.total_q ||
                  a.cu_k[B] != a.total_k);
@@ -173,6 +190,34 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdArgs a)
         return lq > 0 ? (lq + kOwn - 1) / kOwn : 0;
     });
     __syncthreads();
+    if (SINK && !s_bad) {
+        // steps of a sequence's first sink tile (the others have as many or fewer)
+        auto steps_of = [&](int b) {
+            const int lq = a.cu_q[b + 1] - a.cu_q[b];
+            return static_cast<long long>((lq + STEP - 1) / STEP) * (a.num_heads / a.num_kv_heads);
+        };
+        auto tiles_of = [&](int b) { return sink_tiles(a, a.cu_k[b + 1] - a.cu_k[b]); };
+        unsigned long long mine = 0;
+        for (int b = threadIdx.x; b < B; b += kPrepThreads)
+            mine += steps_of(b) * tiles_of(b);
+        if (mine)
+            atomicAdd(&s_steps, mine);
+        __syncthreads();
+        const unsigned long long all = s_steps * a.num_kv_heads * SPLIT;
+        const long long per =
+            max(static_cast<long long>(kSinkMinSteps),
+                static_cast<long long>((all + kSinkUnits - 1) / kSinkUnits));
+        auto chunks_of = [&](int b) { return max(1, static_cast<int>((steps_of(b) + per - 1) / per)); };
+        for (int b = threadIdx.x; b < B; b += kPrepThreads)
+            a.sink_chunks[b] = chunks_of(b);
+        if (threadIdx.x == 0)
+            a.sink_chunks[B] = static_cast<int>(min(per, 0x7fffffffll));
+        block_prefix(B, a.sink_start, warp_sums, [&](int b) { return tiles_of(b) * chunks_of(b); });
+        block_prefix(B, a.part_start, warp_sums, [&](int b) {
+            return chunks_of(b) > 1 ? tiles_of(b) * chunks_of(b) : 0;
+        });
+        __syncthreads();
+    }
     if (threadIdx.x == 0) {
         a.status[1] = 0;                 // unit counters of the two main kernels
         a.status[2] = 0;
@@ -264,6 +309,14 @@ __device__ __forceinline__ void query_row_span(long long i, long long j_base, in
     *hi = clamp_col(h);
 }
 
+// Columns of a query row that are visible: [lo, hi), and with sinks those below
+// min(hi, sink).
+template <bool SINK>
+__device__ __forceinline__ bool in_span(int c, int lo, int hi, int sink)
+{
+    return c < hi && (c >= lo || (SINK && c < sink));
+}
+
 // P^T and dS^T of this thread's key row over its NC query columns: p =
 // 2^(s scale_log2 + nl) (0 outside the visible columns [lo, hi) when MASK)
 // and ds = p (dp + nd), with nl = -lse log2(e) and nd = -Delta of each column
@@ -302,12 +355,12 @@ __device__ __forceinline__ void key_row_grads(const uint32_t (&sr)[NC], const ui
 }
 
 // dS of this thread's query row over its NC key columns: p = 2^(s
-// scale_log2 + nl) (0 outside [lo, hi) when MASK), ds = p (dp + nd) with the
+// scale_log2 + nl) (0 outside the row's span when MASK), ds = p (dp + nd) with the
 // row's nl = -lse log2(e) and nd = -Delta.
-template <bool MASK, int NC>
+template <bool MASK, bool SINK, int NC>
 __device__ __forceinline__ void query_row_grads(const uint32_t (&sr)[NC], const uint32_t (&dr)[NC],
                                                 float scale_log2, float nl, float nd, int lo,
-                                                int hi, uint32_t (&dk2)[NC / 2])
+                                                int hi, int sink, uint32_t (&dk2)[NC / 2])
 {
     const float2 c2 = make_float2(scale_log2, scale_log2);
     const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
@@ -317,8 +370,8 @@ __device__ __forceinline__ void query_row_grads(const uint32_t (&sr)[NC], const 
                                     c2, nl2);
         float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
         if (MASK) {
-            p0 = (e >= lo && e < hi) ? p0 : 0.f;
-            p1 = (e + 1 >= lo && e + 1 < hi) ? p1 : 0.f;
+            p0 = in_span<SINK>(e, lo, hi, sink) ? p0 : 0.f;
+            p1 = in_span<SINK>(e + 1, lo, hi, sink) ? p1 : 0.f;
         }
         const float2 g = __fadd2_rn(make_float2(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])),
                                     nd2);
@@ -450,6 +503,18 @@ __device__ __forceinline__ void store_tile32(uint32_t taddr, float f, uint32_t s
     __syncwarp();
 }
 
+// 32 accumulator columns of the thread's row, as they are.
+__device__ __forceinline__ void store_part32(uint32_t taddr, float *dst)
+{
+    uint32_t rr[32];
+    tmem_ld32(taddr, rr);
+    tmem_wait_ld_r(rr);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        reinterpret_cast<uint4 *>(dst)[c] =
+            make_uint4(rr[4 * c], rr[4 * c + 1], rr[4 * c + 2], rr[4 * c + 3]);
+}
+
 // ------------------------------------------------------------ the two main kernels
 
 // One unit of work, decoded by the loading warp and handed to the others
@@ -460,11 +525,15 @@ struct BwdUnit {
     int q0, lq, k0, lk;          // the sequence's rows and lengths
     int first, n_blk, n_steps;   // streamed blocks [first, first + n_blk); steps (x group)
     int valid;                   // 0: no more units
+    // with sinks: dQ: blocks [0, n_sink) come first; dK/dV: this unit's first step of
+    // its tile's, the partial it writes (-1: the gradients themselves), and whether
+    // there is nothing to do (a tile whose chunks are units)
+    int n_sink, step0, part, skip;
 };
 
 // Unit u of the dK/dV kernel (DQ false) or the dQ kernel (DQ true); `tiles`
 // is the number of 128-row tiles of all sequences.
-template <int D, bool DQ>
+template <int D, bool DQ, bool SINK>
 __device__ BwdUnit decode_unit(const BwdArgs &a, int u, int tiles)
 {
     using C = BwdCfg<D, DQ>;
@@ -473,11 +542,18 @@ __device__ BwdUnit decode_unit(const BwdArgs &a, int u, int tiles)
     BwdUnit w;
     const int per_head = tiles * SPLIT;
     const int n_heads = DQ ? a.num_heads : a.num_kv_heads;
-    w.valid = u < per_head * n_heads;
+    w.n_sink = w.step0 = w.skip = 0;
+    w.part = -1;
+    // the chunks of the sinks' tiles come first
+    const int sink_units = SINK && !DQ ? a.sink_start[a.batch] * SPLIT : 0;
+    const bool chunked = SINK && !DQ && u < sink_units * n_heads;
+    u -= SINK && !chunked ? sink_units * n_heads : 0;
+    w.valid = chunked || u < per_head * n_heads;
     if (!w.valid)
         return w;
-    w.head = u / per_head;
-    const int r = u % per_head;
+    const int per_row = chunked ? sink_units : per_head;
+    w.head = u / per_row;
+    const int r = u % per_row;
     // dQ: each head's tiles run last-first (a causal sequence's longest key
     // ranges first); dK/dV: in order (a sequence's first key tiles see the
     // most queries); a key tile's column halves are neighbours
@@ -485,9 +561,17 @@ __device__ BwdUnit decode_unit(const BwdArgs &a, int u, int tiles)
     w.dh = r % SPLIT;
     if (DQ)
         gt = tiles - 1 - gt;
-    const int32_t *start = DQ ? a.qtile_start : a.ktile_start;
+    const int32_t *start = DQ ? a.qtile_start : chunked ? a.sink_start : a.ktile_start;
     w.b = owner_of(start, a.batch, gt);
     w.t = gt - start[w.b];
+    int chunk = 0, chunks = 1;
+    if (chunked) {
+        chunks = a.sink_chunks[w.b];
+        if (chunks > 1)
+            w.part = ((a.part_start[w.b] + w.t) * a.num_kv_heads + w.head) * SPLIT + w.dh;
+        chunk = w.t % chunks;
+        w.t /= chunks;
+    }
     w.q0 = a.cu_q[w.b];
     w.lq = a.cu_q[w.b + 1] - w.q0;
     w.k0 = a.cu_k[w.b];
@@ -501,8 +585,10 @@ __device__ BwdUnit decode_unit(const BwdArgs &a, int u, int tiles)
         const int j_lo = w.t * kOwn, j_hi = min(w.lk, j_lo + kOwn);
         lo = a.causal ? max(0ll, j_lo - off) : 0;
         hi = w.lq - 1;
-        if (wl >= 0)
+        const bool holds_sinks = SINK && j_lo < a.sink_tokens;
+        if (wl >= 0 && !holds_sinks)
             hi = min(hi, static_cast<long long>(j_hi) - 1 - off + wl);
+        w.skip = holds_sinks && !chunked;
     } else {
         // keys some row of this tile sees: j <= i + off (causal), j >= i + off
         // - window_left (window)
@@ -515,7 +601,31 @@ __device__ BwdUnit decode_unit(const BwdArgs &a, int u, int tiles)
     w.first = lo <= hi ? static_cast<int>(lo / STEP) : 0;
     w.n_blk = lo <= hi ? static_cast<int>(hi / STEP) + 1 - w.first : 0;
     w.n_steps = DQ ? w.n_blk : w.n_blk * (a.num_heads / a.num_kv_heads);
+    if (SINK && DQ) {
+        // sink blocks below the window's; all of them where the window is past the keys
+        const long long seen = lo <= hi ? min(lo / STEP * STEP, static_cast<long long>(w.lk))
+                                        : max(0ll, hi + 1);
+        w.n_sink = static_cast<int>((min(static_cast<long long>(a.sink_tokens), seen) + STEP - 1) / STEP);
+        w.n_steps += w.n_sink;
+    }
+    if (chunked) {
+        const int per = a.sink_chunks[a.batch];
+        w.step0 = static_cast<int>(min(static_cast<long long>(chunk) * per,
+                                       static_cast<long long>(w.n_steps)));
+        w.n_steps = chunks > 1 ? min(per, w.n_steps - w.step0) : w.n_steps;
+    }
+    if (w.skip)
+        w.n_steps = 0;
     return w;
+}
+
+// The streamed block of the unit's step s.
+template <bool DQ, bool SINK>
+__device__ __forceinline__ int block_of(const BwdUnit &w, int s)
+{
+    if (DQ)
+        return SINK ? (s < w.n_sink ? s : w.first + s - w.n_sink) : w.first + s;
+    return w.first + (SINK ? s + w.step0 : s) % w.n_blk;
 }
 
 // Persistent CTAs, one per SM, take units from an atomic counter.  Warp 0
@@ -539,7 +649,7 @@ __device__ BwdUnit decode_unit(const BwdArgs &a, int u, int tiles)
 // the next unit's first scores run during the current unit's epilogue; only
 // its first accumulating product waits for the epilogue (epi_done) to have
 // read the accumulators.
-template <int D, bool DQ>
+template <int D, bool DQ, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_constant__ BwdArgs a)
 {
     using C = BwdCfg<D, DQ>;
@@ -650,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
             for (uint32_t n = 0; ok; ++n) {
                 if (!mbar_wait(unit_empty(n & 1), ((n >> 1) & 1u) ^ 1u, abort))
                     break;
-                const BwdUnit w = decode_unit<D, DQ>(a, atomicAdd(counter, 1), tiles);
+                const BwdUnit w = decode_unit<D, DQ, SINK>(a, atomicAdd(counter, 1), tiles);
                 s_unit[n & 1] = w;
                 mbar_arrive(unit_full(n & 1));
                 if (!w.valid)
@@ -675,9 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                     mbar_arrive_expect_tx(ring_full(st), C::STAGE_BYTES);
                     // dK/dV: step s = (query head of the group, query block);
                     // dQ: key block of the head's kv head
-                    const int blk = w.first + (DQ ? s : s % w.n_blk);
+                    const int blk = block_of<DQ, SINK>(w, s);
                     const int row = (DQ ? w.k0 : w.q0) + blk * STEP;
-                    const int head = DQ ? w.head / group : w.head * group + s / w.n_blk;
+                    const int head = DQ ? w.head / group
+                                        : w.head * group + (SINK ? s + w.step0 : s) / w.n_blk;
                     load_rows<DB, STEP>(stage0(st), str0, ring_full(st), head, row, STEP);
                     load_rows<DB, STEP>(stage1(st), str1, ring_full(st), head, row, STEP);
                 }
@@ -797,6 +908,21 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                 row_out = (static_cast<size_t>(w.k0 + own) * Hkv + w.head) * D + w.dh * C::DKV +
                           half * DH;
             const bool own_valid = DQ ? own < w.lq : own < w.lk;
+            if (SINK && !DQ && w.skip)
+                continue;
+            // a chunk's partial: dV, then dK, 128 rows of DKV columns each
+            float *part = nullptr;
+            if (SINK && !DQ && w.part >= 0)
+                part = a.part + (static_cast<size_t>(w.part) * 2 * kOwn + r) * C::DKV + half * DH;
+            if (w.n_steps == 0 && part) {
+#pragma unroll
+                for (int d = 0; d < DH; d += 4) {
+                    *reinterpret_cast<float4 *>(part + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    *reinterpret_cast<float4 *>(part + kOwn * C::DKV + d) =
+                        make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                continue;
+            }
             if (w.n_steps == 0) {
                 // no key / query pairs: zero gradients
                 if (own_valid) {
@@ -826,11 +952,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
             for (int s = (half - static_cast<int>(g & 1u)) & 1; s < w.n_steps && ok; s += 2) {
                 const uint32_t gs = g + s;
                 const int x = gs & 1;
-                const int blk = w.first + (DQ ? s : s % w.n_blk);
+                const int blk = block_of<DQ, SINK>(w, s);
                 const int c0 = blk * STEP;                 // the step's first streamed column
                 if (!DQ) {
                     // -lse log2(e) and -Delta of the step's query columns
-                    const int hq = w.head * group + s / w.n_blk;
+                    const int hq = w.head * group + (SINK ? s + w.step0 : s) / w.n_blk;
                     __syncwarp();
 #pragma unroll
                     for (int c = 0; c < NCH; ++c) {
@@ -848,11 +974,13 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                 if (DQ)
                     full = slo + STEP <= w.lk && olo + kOwn <= w.lq &&
                            (!a.causal || slo + STEP - 1 <= olo + off) &&
-                           (wl < 0 || slo >= olo + kOwn - 1 + off - wl);
+                           (wl < 0 || slo >= olo + kOwn - 1 + off - wl ||
+                            (SINK && slo + STEP <= a.sink_tokens));
                 else
                     full = olo + kOwn <= w.lk && slo + STEP <= w.lq &&
                            (!a.causal || olo + kOwn - 1 <= slo + off) &&
-                           (wl < 0 || olo >= slo + STEP - 1 + off - wl);
+                           (wl < 0 || olo >= slo + STEP - 1 + off - wl ||
+                            (SINK && olo + kOwn <= a.sink_tokens));
                 ok = mbar_wait_warp(s_full(x), (gs >> 1) & 1u, abort);
                 if (!ok)
                     break;
@@ -868,13 +996,16 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                     const int cb = c0 + 32 * c;            // the chunk's first streamed column
                     if (DQ) {
                         if (full) {
-                            query_row_grads<false, 32>(sr, dr, scale_log2, nl_row, nd_row, 0, 32,
-                                                       dk2);
+                            query_row_grads<false, SINK, 32>(sr, dr, scale_log2, nl_row, nd_row,
+                                                             0, 32, 0, dk2);
                         } else {
                             int lo, hi;
                             query_row_span(own, cb, w.lk, w.lq, a.causal, wl, off, &lo, &hi);
-                            query_row_grads<true, 32>(sr, dr, scale_log2, nl_row, nd_row, lo, hi,
-                                                      dk2);
+                            if (SINK && own >= w.lq)
+                                hi = -1;                   // no row: no sinks either
+                            query_row_grads<true, SINK, 32>(sr, dr, scale_log2, nl_row, nd_row,
+                                                            lo, hi, SINK ? a.sink_tokens - cb : 0,
+                                                            dk2);
                         }
                     } else {
                         uint32_t pk[16];
@@ -883,7 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                             key_row_grads<false, 32>(sr, dr, scale_log2, cstat, 0, 32, pk, dk2);
                         } else {
                             int lo, hi;
-                            key_row_span(own, cb, w.lk, w.lq, a.causal, wl, off, &lo, &hi);
+                            key_row_span(own, cb, w.lk, w.lq, a.causal,
+                                         SINK && own < a.sink_tokens ? -1 : wl, off, &lo, &hi);
                             key_row_grads<true, 32>(sr, dr, scale_log2, cstat, lo, hi, pk, dk2);
                         }
                         // P^T (bf16 pairs) over the first half of the chunk's S^T columns
@@ -911,7 +1043,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                 const size_t base_out = row_out - static_cast<size_t>(lane) * stride;
 #pragma unroll 1
                 for (int cb = 0; cb < DH; cb += 32) {
-                    if (DQ) {
+                    if (SINK && !DQ && part) {
+                        store_part32(tmem + lane_addr + C::COL_DV + half * DH + cb, part + cb);
+                        store_part32(tmem + lane_addr + C::COL_DK + half * DH + cb,
+                                     part + kOwn * C::DKV + cb);
+                    } else if (DQ) {
                         store_tile32(tmem + lane_addr + C::COL_DQ + half * DH + cb, a.scale, stage,
                                      lane, dq + base_out + cb, stride, n_valid);
                     } else {
@@ -941,7 +1077,52 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
     wait_for_dkv();
 }
 
+// dV and dK of the sinks' tiles that were cut: the chunks' partials in order.
+// A CTA takes kSinkRows rows of a tile, a thread four columns of them.
+constexpr int kSinkRows = 4;
+
 template <int D>
+__global__ void __launch_bounds__(2 * kSinkRows * D / 4) bwd_sinks_kernel(const BwdArgs a)
+{
+    using C = BwdCfg<D, false>;
+    if (*a.status != VFA_OK)
+        return;
+    const int head = blockIdx.y, row = blockIdx.z * kSinkRows + threadIdx.x / (D / 4) % kSinkRows;
+    const bool is_dk = threadIdx.x >= kSinkRows * D / 4;
+    const int col = threadIdx.x % (D / 4) * 4, dh = col / C::DKV;
+    const int units = a.sink_start[a.batch];
+    for (int u = blockIdx.x; u < units;) {
+        const int b = owner_of(a.sink_start, a.batch, u);
+        const int chunks = a.sink_chunks[b], x = u - a.sink_start[b];
+        if (x % chunks == 0 && chunks > 1) {
+            const int k0 = a.cu_k[b], key = x / chunks * kOwn + row;
+            const size_t stride = static_cast<size_t>(a.num_kv_heads) * C::DSPLIT * 2 * kOwn * C::DKV;
+            const float *src =
+                a.part +
+                ((((static_cast<size_t>(a.part_start[b]) + x) * a.num_kv_heads + head) * C::DSPLIT + dh) *
+                     2 * kOwn + (is_dk ? kOwn : 0) + row) * C::DKV + col % C::DKV;
+            if (key < a.cu_k[b + 1] - k0) {
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int c = 0; c < chunks; ++c) {
+                    const float4 p = __ldcs(reinterpret_cast<const float4 *>(src + c * stride));
+                    s.x += p.x;
+                    s.y += p.y;
+                    s.z += p.z;
+                    s.w += p.w;
+                }
+                const float f = is_dk ? a.scale : 1.f;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_dk ? a.dk : a.dv) +
+                                     (static_cast<size_t>(k0 + key) * a.num_kv_heads + head) * D + col;
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
+            }
+        }
+        u += gridDim.x;
+    }
+}
+
+template <int D, bool SINK>
 cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound, int sm_count,
                          cudaStream_t s)
 {
@@ -951,16 +1132,17 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
     if (e != cudaSuccess)
         return e;
     if (dev < 64 && !attr_done[dev]) {
-        if ((e = cudaFuncSetAttribute(bwd_main_kernel<D, false>,
+        if ((e = cudaFuncSetAttribute(bwd_main_kernel<D, false, SINK>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(BwdCfg<D, false>::SMEM))) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(bwd_main_kernel<D, true>,
+            (e = cudaFuncSetAttribute(bwd_main_kernel<D, true, SINK>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(BwdCfg<D, true>::SMEM))) != cudaSuccess)
             return e;
         attr_done[dev] = 1;
     }
-    bwd_prep_kernel<<<1, kPrepThreads, 0, s>>>(a);
+    bwd_prep_kernel<BwdCfg<D, false>::STEP, BwdCfg<D, false>::DSPLIT, SINK>
+        <<<1, kPrepThreads, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     bwd_delta_kernel<D><<<sm_count * 8, 256, 0, s>>>(a);
@@ -971,8 +1153,8 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
         static_cast<long long>(key_tile_bound) * BwdCfg<D, false>::DSPLIT * a.num_kv_heads;
     const long long q_units = static_cast<long long>(q_tile_bound) * a.num_heads;
     if (kv_units > 0) {
-        bwd_main_kernel<D, false><<<static_cast<int>(std::min<long long>(kv_units, sm_count)),
-                                    kThreads, BwdCfg<D, false>::SMEM, s>>>(a);
+        const int grid = SINK ? sm_count : static_cast<int>(std::min<long long>(kv_units, sm_count));
+        bwd_main_kernel<D, false, SINK><<<grid, kThreads, BwdCfg<D, false>::SMEM, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
     }
@@ -993,12 +1175,32 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
         attr[0].val.programmaticStreamSerializationAllowed = kv_units > 0 ? 1 : 0;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&cfg, bwd_main_kernel<D, true>, a)) != cudaSuccess)
+        if ((e = cudaLaunchKernelEx(&cfg, bwd_main_kernel<D, true, SINK>, a)) != cudaSuccess)
             return e;
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
     }
+    if (SINK && kv_units > 0 && q_units > 0) {
+        // behind the dQ kernel, which waits for the dK/dV kernel
+        const dim3 grid(kSinkUnits, a.num_kv_heads, kOwn / kSinkRows);
+        bwd_sinks_kernel<D><<<grid, 2 * kSinkRows * D / 4, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess)
+            return e;
+    }
     return cudaSuccess;
+}
+
+// Most partials of chunks: a tile is cut where it has over `per` steps, which
+// gives less than twice its steps over `per`; all tiles' steps over `per` are at
+// most kSinkUnits, and `per` is at least kSinkMinSteps.
+size_t sink_parts(int batch, int total_q, int num_heads, int head_dim, int sink_tokens)
+{
+    const long long split = head_dim == 256 ? 2 : 1;
+    const long long tiles = (static_cast<long long>(sink_tokens) + kOwn - 1) / kOwn;
+    const long long blocks = total_q / bwd_kv_step_rows(head_dim) + static_cast<long long>(batch);
+    // a double, since the product may pass 64 bits
+    const double steps = static_cast<double>(split * num_heads) * tiles * blocks;
+    return 2 * static_cast<size_t>(std::min<double>(kSinkUnits, steps / kSinkMinSteps + 1));
 }
 
 }  // namespace
@@ -1031,13 +1233,39 @@ void bwd_workspace_split(void *ws, int batch, int total_q, int num_heads, BwdArg
     a->delta = reinterpret_cast<float *>(p + n);
 }
 
+size_t bwd_sinks_workspace_bytes(int batch, int total_q, int num_heads, int head_dim,
+                                 int sink_tokens)
+{
+    const size_t lists = (3 * (static_cast<size_t>(batch) + 1) * sizeof(int32_t) + 255) &
+                         ~static_cast<size_t>(255);
+    const size_t part = 2 * static_cast<size_t>(kOwn) * (head_dim == 256 ? 128 : head_dim) * sizeof(float);
+    return bwd_workspace_bytes(batch, total_q, num_heads, head_dim) + lists +
+           sink_parts(batch, total_q, num_heads, head_dim, sink_tokens) * part;
+}
+
+void bwd_sinks_workspace_split(void *ws, int batch, int total_q, int num_heads, BwdArgs *a)
+{
+    bwd_workspace_split(ws, batch, total_q, num_heads, a);
+    const size_t n = static_cast<size_t>(batch) + 1;
+    int32_t *p = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) +
+                                             bwd_workspace_bytes(batch, total_q, num_heads, 0));
+    a->sink_start = p;
+    a->sink_chunks = p + n;
+    a->part_start = p + 2 * n;
+    a->part = reinterpret_cast<float *>(p) + ((3 * n + 63) & ~static_cast<size_t>(63));
+}
+
 cudaError_t launch_bwd(int head_dim, const BwdArgs &a, int key_tile_bound, int q_tile_bound,
                        int sm_count, cudaStream_t stream)
 {
+    const bool sinks = a.window_left >= 0 && a.sink_tokens > 0;
+    auto run = [&](auto with, auto without) {
+        return (sinks ? with : without)(a, key_tile_bound, q_tile_bound, sm_count, stream);
+    };
     switch (head_dim) {
-    case 64: return launch_bwd_d<64>(a, key_tile_bound, q_tile_bound, sm_count, stream);
-    case 128: return launch_bwd_d<128>(a, key_tile_bound, q_tile_bound, sm_count, stream);
-    case 256: return launch_bwd_d<256>(a, key_tile_bound, q_tile_bound, sm_count, stream);
+    case 64: return run(launch_bwd_d<64, true>, launch_bwd_d<64, false>);
+    case 128: return run(launch_bwd_d<128, true>, launch_bwd_d<128, false>);
+    case 256: return run(launch_bwd_d<256, true>, launch_bwd_d<256, false>);
     default: return cudaErrorInvalidValue;
     }
 }

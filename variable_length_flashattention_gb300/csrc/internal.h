@@ -52,6 +52,7 @@ struct SchedArgs {
     int batch, total_q, total_k, max_seqlen_q, num_heads, block_q, block_k;
     int causal;           // 0 none, 1 top-left, 2 bottom-right
     int window_left;      // < 0 none; else keys j >= row + off - window_left only (causal != 0)
+    int sink_tokens;      // with a window: keys j < sink_tokens stay visible (0: none)
     int pair;             // non-zero: two consecutive tiles of a group per item
     int4 *items;          // two int4 per item
     int item_capacity;
@@ -86,6 +87,7 @@ struct PrefillArgs {
     int causal;           // 0 none, 1 top-left, 2 bottom-right
     int window_left;      // < 0 none; else keys j >= row + off - window_left only
     int qk_fp8;           // non-zero: tm_q / tm_k map FP8 E4M3 codes (any supported head_dim)
+    int sink_tokens;      // with a window: keys j < sink_tokens stay visible (0: none)
 };
 
 // Whether the forward for `head_dim` runs two q tiles per work item.
@@ -162,7 +164,19 @@ struct BwdArgs {
     int batch, total_q, total_k, num_heads, num_kv_heads;
     float scale, scale_log2;
     int causal, window_left;
+    // With a window: keys j < sink_tokens stay visible (0: none).  Their key tiles see every
+    // later query, so each is cut into chunks of its steps (see the dK/dV kernel).
+    int sink_tokens;
+    int32_t *sink_start;                    // workspace: [batch + 1] first sink unit per sequence
+    int32_t *sink_chunks;                   // workspace: [batch + 1] chunks per sink tile; [batch]:
+                                            // steps of a chunk
+    int32_t *part_start;                    // workspace: [batch + 1] first partial per sequence
+    float *part;                            // workspace: partial dV, dK of the chunks
 };
+
+// What the sinks' tiles are cut into, over all kv heads, and the fewest steps a chunk has.
+constexpr int kSinkUnits = 152;
+constexpr int kSinkMinSteps = 32;
 
 // Rows the backward streams per step (queries past a key tile, keys past a
 // query tile); its TMA maps use boxes of this many rows.
@@ -189,6 +203,10 @@ __host__ __device__ constexpr int bwd_dq_step_rows(int head_dim)
 // Workspace bytes of the backward and its split into the BwdArgs pointers.
 size_t bwd_workspace_bytes(int batch, int total_q, int num_heads, int head_dim);
 void bwd_workspace_split(void *ws, int batch, int total_q, int num_heads, BwdArgs *a);
+// The same with sink_tokens > 0: what the chunks of the sinks' tiles need follows.
+size_t bwd_sinks_workspace_bytes(int batch, int total_q, int num_heads, int head_dim,
+                                 int sink_tokens);
+void bwd_sinks_workspace_split(void *ws, int batch, int total_q, int num_heads, BwdArgs *a);
 // prep, Delta, then the persistent dK/dV and dQ kernels (one CTA per SM each,
 // taking (key tile, kv head) and (q tile, head) units from atomic counters).
 cudaError_t launch_bwd(int head_dim, const BwdArgs &a, int key_tile_bound, int q_tile_bound,

@@ -78,7 +78,9 @@ __device__ __forceinline__ void record_error(int32_t *status, int code)
     atomicCAS(status, 0, code);
 }
 
-template <int D, bool F8>
+// SINK: with a window, the first p.sink_tokens keys of a sequence stay visible.
+// Their key tiles below the window's come first: [0, sink) and [first, end).
+template <int D, bool F8, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs p)
 {
     using C = Cfg<D, F8>;
@@ -156,6 +158,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // The work list is written by the scheduler grid launched just before.
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // The item's walk over its key tiles: from start_of to it.w with next_tile.
+    auto sink_of = [&](int first, int lk) {
+        return SINK ? min(first, (min(p.sink_tokens, lk) + BK - 1) / BK) : 0;
+    };
+    auto start_of = [&](int first, int sink) { return SINK && sink > 0 ? 0 : first; };
+    auto next_tile = [&](int j, int first, int sink) {
+        return SINK && j + 1 == sink ? first : j + 1;
+    };
     // Take the next item from the ring (consumer side); false at the end.
     // The item visits key tiles [first, it.w).
     auto next_item = [&](uint32_t n, int4 &it, int4 &seq, int &first) -> bool {
@@ -196,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (it.x < 0)
                     break;
                 const int i = it.y, h = it.z, j_end = it.w;
-                if (j_end <= first)
+                const int sink = sink_of(first, seq.z), j_start = start_of(first, sink);
+                if (j_end <= j_start)
                     continue;
                 const int q_row0 = seq.x + i * BQ;
                 const int k_row0 = seq.w;
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     tma_load_3d(sQ + qb * C::Q_BYTES + db * (BQ * 128), &p.tm_q, q_full(qb),
                                 db * C::QK_BLOCK, h, q_row0);
                 ++qit;
-                for (int j = first; j < j_end; ++j) {
+                for (int j = j_start; j < j_end; j = next_tile(j, first, sink)) {
                     const int st = kfills % NS;
                     if (!mbar_wait(k_empty(st), ((kfills / NS) & 1u) ^ 1u, abort)) {
                         ok = false;
@@ -296,15 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (!more)
                     break;
                 const int j_end = it.w;
-                if (j_end <= first)
+                const int sink = sink_of(first, seq.z), j_start = start_of(first, sink);
+                if (j_end <= j_start)
                     continue;
+                int done = 0;                         // tiles of this item so far
                 const int qb = qit % NQ;
                 if (!mbar_wait(q_full(qb), (qit / NQ) & 1u, abort)) {
                     ok = false;
                     break;
                 }
                 const uint64_t qd = q_desc0 + qb * (C::Q_BYTES >> 4);
-                for (int j = first; j < j_end; ++j) {
+                for (int j = j_start; j < j_end; j = next_tile(j, first, sink)) {
                     const int st = kv % NS;
                     const int x = g % NSB;
                     if (!mbar_wait(k_full(st), (kv / NS) & 1u, abort) ||
@@ -336,16 +349,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     mma_commit_w(k_empty(st));
                     if (j == j_end - 1)
                         mma_commit_w(q_empty(qb));
-                    if (j > first && !issue_pv(g - 1, kv - 1, j - 1 > first)) {
+                    if (done > 0 && !issue_pv(g - 1, kv - 1, done > 1)) {
                         ok = false;
                         break;
                     }
+                    ++done;
                     ++g;
                     ++kv;
                 }
                 if (!ok)
                     break;
-                if (!issue_pv(g - 1, kv - 1, j_end - 1 > first)) {
+                if (!issue_pv(g - 1, kv - 1, done > 1)) {
                     ok = false;
                     break;
                 }
@@ -383,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const bool row_valid = q_local < lq;
             const long long tok = static_cast<long long>(q0) + q_local;
 
-            if (j_end <= first) {
+            const int n_sink = sink_of(first, lk), j_start = start_of(first, n_sink);
+            if (j_end <= j_start) {
                 if (row_valid) {
                     uint4 z = make_uint4(0, 0, 0, 0);
                     uint4 *dst = reinterpret_cast<uint4 *>(out + (tok * H + h) * D);
@@ -398,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             float m_used = -INFINITY;     // reference max, log2 units of the scaled score
             float l = 0.f;
             bool ok = true;
-            for (int j = first; j < j_end; ++j) {
+            for (int j = j_start; j < j_end; j = next_tile(j, first, n_sink)) {
                 const int x = g % NSB;
                 if (!mbar_wait(s_full(x), (g / NSB) & 1u, abort)) {
                     ok = false;
@@ -425,20 +440,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int off = p.causal == 2 ? lk - lq : 0;
                 const int wl = p.window_left;
                 const bool need_lo =
-                    wl >= 0 && k_base < static_cast<long long>(i) * BQ + BQ - 1 + off - wl;
+                    wl >= 0 && k_base < static_cast<long long>(i) * BQ + BQ - 1 + off - wl &&
+                    (!SINK || k_base + BK > p.sink_tokens);
                 const bool need_mask = need_lo || (k_base + BK > lk) ||
                                        (p.causal && k_base + BK - 1 > i * BQ + off);
                 if (need_mask) {
-                    // keys in [lo, lim) visible
+                    // keys in [lo, lim) visible, and those below sink
                     const int lim = (p.causal ? min(lk, max(0, q_local + off + 1)) : lk) - k_base;
                     const int lo = need_lo ? static_cast<int>(min(
                                                  static_cast<long long>(BK),
                                                  max(0ll, static_cast<long long>(q_local) + off -
                                                               wl - k_base)))
                                            : 0;
+                    const int sink = SINK ? p.sink_tokens - k_base : 0;
 #pragma unroll
                     for (int c = 0; c < BK; ++c)
-                        s[c] = (c < lim && c >= lo) ? s[c] : -INFINITY;
+                        s[c] = (c < lim && (c >= lo || (SINK && c < sink))) ? s[c] : -INFINITY;
                 }
                 float mx[8];
 #pragma unroll
@@ -454,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const float m_tile = mt_raw == -INFINITY ? -INFINITY : mt_raw * scale_log2;
                 const float m_new = fmaxf(m_used, m_tile);
                 const bool grow = m_new > m_used + 8.0f;    // also true for m_used = -inf
-                if (j == first) {
+                if (j == j_start) {
                     m_used = m_new;
                 } else if (__any_sync(0xffffffffu, grow)) {
                     // O must hold the previous tile's product before it is rescaled.
@@ -565,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool SINK>
 cudaError_t launch_d(const PrefillArgs &a, int grid, cudaStream_t stream)
 {
     static int attr_done[64] = {0};
@@ -574,7 +591,8 @@ cudaError_t launch_d(const PrefillArgs &a, int grid, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     if (dev < 64 && !attr_done[dev]) {
-        e = cudaFuncSetAttribute(prefill_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(prefill_kernel<D, F8, SINK>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(Cfg<D, F8>::SMEM));
         if (e != cudaSuccess)
             return e;
@@ -591,7 +609,7 @@ cudaError_t launch_d(const PrefillArgs &a, int grid, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, F8>, a);
+    e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, F8, SINK>, a);
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();
@@ -603,9 +621,12 @@ cudaError_t launch_prefill(int head_dim, const PrefillArgs &a, int grid, cudaStr
 {
     if (pairs_for(head_dim))
         return launch_prefill_pair(head_dim, a, grid, stream);
-    if (head_dim == 256)
-        return a.qk_fp8 ? launch_d<256, true>(a, grid, stream)
-                        : launch_d<256, false>(a, grid, stream);
+    if (head_dim == 256) {
+        if (a.qk_fp8)
+            return launch_d<256, true, false>(a, grid, stream);
+        return a.window_left >= 0 && a.sink_tokens > 0 ? launch_d<256, false, true>(a, grid, stream)
+                                                       : launch_d<256, false, false>(a, grid, stream);
+    }
     return cudaErrorInvalidValue;
 }
 

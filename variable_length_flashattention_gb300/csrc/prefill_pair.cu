@@ -36,6 +36,10 @@
 //     32-column chunk to a TMA tile store; in a sequence's last tile, plain
 //     stores write eight whole 64-byte row segments per instruction;
 //   * TMEM: O_a, O_b (D columns each), S/P_a, S/P_b (128 columns each);
+//   * with a window, sinks (first keys that stay visible) are key tiles of
+//     their own ahead of the window's: an item's tiles are [0, sinks) and
+//     [first, end), in ascending order, and a tile that both kinds of key
+//     share is masked by both rules;
 //   * an FP8 instantiation takes Q and K as E4M3 codes: their tiles are half
 //     the bytes (at head_dim 64 rows of 64 bytes, stored with the 64-byte
 //     swizzle) and S = Q K^T runs as kind::f8f6f4 in 32-byte k-steps; the
@@ -101,17 +105,20 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale when the max 
 // a row's visible columns are [lo, lim), and scores outside become -inf, so
 // they drop out of the max and 2^(-inf) = 0 (the scale is > 0, so no
 // -inf * 0).  lim_lo / lo_hi are the warp's smallest lim and largest lo: a
-// chunk inside [lo_hi, lim_lo) needs no mask.  LO: a sliding window's edge
-// can cut into the tile (otherwise lo = 0).
-template <bool LO>
+// chunk inside [lo_hi, lim_lo) needs no mask.  WIN 1: a sliding window's edge
+// can cut into the tile (otherwise lo = 0).  WIN 2: columns below `sink` are
+// visible whatever lo is.
+template <int WIN>
 __device__ __forceinline__ void mask_chunk(uint32_t (&sr)[32], int cb, int lim, int lim_lo, int lo,
-                                           int lo_hi)
+                                           int lo_hi, int sink)
 {
-    if (cb + 32 <= lim_lo && (!LO || cb >= lo_hi))
+    if (cb + 32 <= lim_lo && (!WIN || cb >= lo_hi || (WIN == 2 && cb + 32 <= sink)))
         return;
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-        sr[e] = (cb + e < lim && (!LO || cb + e >= lo)) ? sr[e] : __float_as_uint(-INFINITY);
+        sr[e] = (cb + e < lim && (!WIN || cb + e >= lo || (WIN == 2 && cb + e < sink)))
+                    ? sr[e]
+                    : __float_as_uint(-INFINITY);
 }
 
 // O rows *= f for this warp's 32 lanes, 16 columns at a time (rare path).
@@ -131,15 +138,77 @@ __device__ __forceinline__ void rescale_rows(uint32_t o_addr, float f)
     tmem_wait_st();
 }
 
+// Key tiles that hold sinks of a sequence of lk keys.
+__device__ __forceinline__ int sink_tiles(int sink_tokens, int lk, int block_k)
+{
+    return (min(sink_tokens, lk) + block_k - 1) / block_k;
+}
+
 // The key tiles of one work item: slot x (0 = tile a, 1 = tile b) visits
 // [first[x], end[x]) (empty when end <= first), and the item loads the union
 // [j0, j1) of the non-empty ranges, which the scheduler keeps contiguous.
+// Both are walked with j = next(j) from j0 to j1; before(j) is the tile ahead
+// of j.
 struct ItemSpan {
     int first[2], end[2];
     int j0, j1;
     __device__ __forceinline__ bool live(int x) const { return end[x] > first[x]; }
     __device__ __forceinline__ bool has(int x, int j) const { return j >= first[x] && j < end[x]; }
+    __device__ __forceinline__ int first_of(int x) const { return first[x]; }
+    __device__ __forceinline__ int last_of(int x) const { return end[x] - 1; }
+    __device__ __forceinline__ int next(int j) const { return j + 1; }
+    __device__ __forceinline__ int before(int j) const { return j - 1; }
 };
+
+// The same with sinks: slot x visits [0, sink[x]) as well, sink[x] <= first[x],
+// and the item loads [0, sinks) and the union [w0, j1) of the windows.
+struct SinkSpan {
+    int first[2], end[2], sink[2];
+    int j0, j1, sinks, w0;
+    __device__ __forceinline__ bool live(int x) const { return sink[x] > 0 || end[x] > first[x]; }
+    __device__ __forceinline__ bool has(int x, int j) const
+    {
+        return j >= 0 && (j < sink[x] || (j >= first[x] && j < end[x]));
+    }
+    __device__ __forceinline__ int first_of(int x) const { return sink[x] > 0 ? 0 : first[x]; }
+    __device__ __forceinline__ int last_of(int x) const
+    {
+        return (end[x] > first[x] ? end[x] : sink[x]) - 1;
+    }
+    __device__ __forceinline__ int next(int j) const { return j + 1 == sinks ? w0 : j + 1; }
+    __device__ __forceinline__ int before(int j) const
+    {
+        return j == w0 && sinks > 0 ? sinks - 1 : j - 1;
+    }
+};
+
+__device__ __forceinline__ SinkSpan sink_span(const int4 &it, const int4 &itb, int tiles)
+{
+    SinkSpan sp;
+    const bool has_b = itb.x >= 0;
+    sp.first[0] = itb.z;
+    sp.end[0] = it.w;
+    sp.first[1] = has_b ? itb.w : 0;
+    sp.end[1] = has_b ? itb.y : 0;
+    sp.sinks = 0;
+    bool any = false;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        sp.sink[x] = min(sp.first[x], tiles);
+        sp.sinks = max(sp.sinks, sp.sink[x]);
+        if (sp.end[x] > sp.first[x]) {
+            sp.w0 = any ? min(sp.w0, sp.first[x]) : sp.first[x];
+            sp.j1 = any ? max(sp.j1, sp.end[x]) : sp.end[x];
+            any = true;
+        }
+    }
+    if (any)
+        sp.sinks = min(sp.sinks, sp.w0);      // sinks the window's tiles reach are among those
+    else
+        sp.w0 = sp.j1 = sp.sinks;             // sinks alone, or nothing
+    sp.j0 = sp.sinks > 0 ? 0 : sp.w0;
+    return sp;
+}
 
 __device__ __forceinline__ ItemSpan item_span(const int4 &it, const int4 &itb)
 {
@@ -162,7 +231,8 @@ __device__ __forceinline__ ItemSpan item_span(const int4 &it, const int4 &itb)
     return sp;
 }
 
-template <int D, bool WIN, bool F8>
+// WIN 0: no window; 1: a sliding window; 2: a window and sinks.
+template <int D, int WIN, bool F8>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_pair_kernel(const __grid_constant__ PrefillArgs p)
 {
@@ -250,6 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         seq = s_item[slot][2];
         return it.x >= 0;
     };
+    auto span_of = [&](const int4 &it, const int4 &itb, const int4 &seq) {
+        if constexpr (WIN == 2)
+            return sink_span(it, itb, sink_tiles(p.sink_tokens, seq.z, BK));
+        else
+            return item_span(it, itb);
+    };
     // Drain after an abort: the last fill of each ring slot may still be in flight.
     auto last_fill_wait = [&](uint32_t fills, int nslots, int slot, uint32_t bar) {
         const uint32_t k = fills / nslots + (static_cast<uint32_t>(slot) < fills % nslots ? 1u : 0u);
@@ -289,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it.x < 0)
                     break;
                 const int h = it.z;
-                const ItemSpan sp = item_span(it, itb);
+                const auto sp = span_of(it, itb, seq);
                 if (sp.j1 <= sp.j0)
                     continue;
                 for (int x = 0; x < 2 && ok; ++x) {
@@ -306,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     db * C::QK_BLOCK, h, seq.x + i * BQ);
                     ++qloads[x];
                 }
-                for (int j = sp.j0; j < sp.j1 && ok; ++j) {
+                for (int j = sp.j0; j < sp.j1 && ok; j = sp.next(j)) {
                     const int st = kfills % NS;
                     if (!mbar_wait(k_empty(st), ((kfills / NS) & 1u) ^ 1u, abort)) {
                         ok = false;
@@ -341,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!more)
                     break;
                 const int h = it.z;
-                const ItemSpan sp = item_span(it, itb);
-                for (int j = sp.j0; j < sp.j1; ++j) {
+                const auto sp = span_of(it, itb, seq);
+                for (int j = sp.j0; j < sp.j1; j = sp.next(j)) {
                     const int st = vfills % NS;
                     if (!mbar_wait(v_empty(st), ((vfills / NS) & 1u) ^ 1u, abort)) {
                         ok = false;
@@ -439,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(item_empty(n & 1));
                 if (!more)
                     break;
-                const ItemSpan sp = item_span(it, itb);
+                const auto sp = span_of(it, itb, seq);
                 if (sp.j1 <= sp.j0)
                     continue;
                 if ((sp.live(0) && !mbar_wait(q_full(0), qloads[0] & 1u, abort)) ||
@@ -450,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // Slot x runs key tiles [first[x], end[x]) of the item's [j0, j1);
                 // without a window both start at 0 and b's range ends first.
-                for (int j = sp.j0; j < sp.j1 && ok; ++j) {
+                for (int j = sp.j0; j < sp.j1 && ok; j = sp.next(j)) {
                     const int st = kv % NS;
                     const int st_prev = (kv + NS - 1) % NS;
                     const bool a_in = sp.has(0, j), b_in = sp.has(1, j);
@@ -460,12 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (a_in) {
                         issue_qk(0, st);                          // S_a(j)
-                        if (j == sp.end[0] - 1)
+                        if (j == sp.last_of(0))
                             mma_commit_w(q_empty(0));
                     }
-                    if (sp.has(1, j - 1)) {
+                    const int jp = sp.before(j);
+                    if (sp.has(1, jp)) {
                         // O_b += P_b(j-1) V(j-1); V(j-1) is then free
-                        if (!issue_pv(1, st_prev, kv - 1, j - 1 > sp.first[1])) {
+                        if (!issue_pv(1, st_prev, kv - 1, jp > sp.first_of(1))) {
                             ok = false;
                             break;
                         }
@@ -473,11 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (b_in) {
                         issue_qk(1, st);                          // S_b(j)
-                        if (j == sp.end[1] - 1)
+                        if (j == sp.last_of(1))
                             mma_commit_w(q_empty(1));
                     }
                     mma_commit_w(k_empty(st));
-                    if (a_in && !issue_pv(0, st, kv, j > sp.first[0])) {   // O_a += P_a(j) V(j)
+                    if (a_in && !issue_pv(0, st, kv, j > sp.first_of(0))) {   // O_a += P_a(j) V(j)
                         ok = false;
                         break;
                     }
@@ -496,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 if (sp.has(1, sp.j1 - 1)) {
                     const int st_last = (kv + NS - 1) % NS;
-                    if (!issue_pv(1, st_last, kv - 1, sp.j1 - 1 > sp.first[1])) {
+                    if (!issue_pv(1, st_last, kv - 1, sp.j1 - 1 > sp.first_of(1))) {
                         ok = false;
                         break;
                     }
@@ -529,11 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t g = 0;                               // this slot's tiles so far
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
         // Masked tiles mask the keys past a row's last visible one and, in the
-        // sliding-window instantiation, those below the window's edge too (one
+        // sliding-window instantiations, those below the window's edge too (one
         // masked variant per instantiation keeps the register allocation of
         // the plain kernel).
         using Plain = std::integral_constant<int, 0>;
-        using Masked = std::integral_constant<int, WIN ? 2 : 1>;
+        using Masked = std::integral_constant<int, WIN + 1>;
 
         for (uint32_t n = 0;; ++n) {
             int4 it, itb, seq;
@@ -548,9 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;                             // no second tile in this item
             const int h = it.z;
             // this slot's key tiles [j_first, j_end)
-            const int j_first = x == 0 ? itb.z : itb.w;
-            const int j_end = x == 0 ? it.w : itb.y;
+            const int w_first = x == 0 ? itb.z : itb.w;
+            const int w_end = x == 0 ? it.w : itb.y;
             const int q0 = seq.x, lq = seq.y, lk = seq.z;
+            // with sinks: [0, n_sink) ahead of [w_first, w_end)
+            const int n_sink = WIN == 2 ? min(w_first, sink_tiles(p.sink_tokens, lk, BK)) : 0;
+            const int j_first = n_sink > 0 ? 0 : w_first;
+            const int j_end = w_end;                  // n_sink where the window is empty
             const int q_local = i * BQ + r;
             const bool row_valid = q_local < lq;
             const long long tok = static_cast<long long>(q0) + q_local;
@@ -570,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_used = -INFINITY;                 // reference max, log2 units
             float l = 0.f;
             bool ok = true;
-            for (int j = j_first; j < j_end && ok; ++j) {
+            for (int j = j_first; j < j_end && ok;
+                 j = WIN == 2 && j + 1 == n_sink ? w_first : j + 1) {
                 if (!mbar_wait(s_full(x), g & 1u, abort)) {
                     ok = false;
                     break;
@@ -583,8 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need_hi =
                     (k_base + BK > lk) || (p.causal && k_base + BK - 1 > i * BQ + off);
                 // the tile's last row has the highest window edge
-                const bool need_lo = WIN && k_base < static_cast<long long>(i) * BQ + BQ - 1 +
-                                                         off - p.window_left;
+                const bool need_lo = WIN &&
+                                     k_base < static_cast<long long>(i) * BQ + BQ - 1 + off -
+                                                  p.window_left &&
+                                     (WIN != 2 || k_base + BK > p.sink_tokens);
                 // this row's visible columns end at lim; warp-wide bounds of lim
                 const bool need_mask = need_hi || need_lo;
                 const int lim =
@@ -603,8 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto tile = [&](auto masked) -> bool {
                     constexpr int MK = decltype(masked)::value;
                     // banded tiles: this row's visible columns start at lo
-                    int lo = 0, lo_lo = 0, lo_hi = 0;
-                    if (MK == 2) {
+                    int lo = 0, lo_lo = 0, lo_hi = 0, sink = 0;
+                    if (MK == 3)
+                        sink = min(BK, max(0, p.sink_tokens - k_base));
+                    if (MK >= 2) {
                         const int off = p.causal == 2 ? lk - lq : 0;
                         lo = static_cast<int>(
                             min(static_cast<long long>(BK),
@@ -626,14 +712,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool empty[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        empty[c] = MK > 0 && (32 * c >= lim_hi || (MK == 2 && 32 * c + 32 <= lo_lo));
+                        empty[c] = MK > 0 && (32 * c >= lim_hi ||
+                                              (MK >= 2 && 32 * c + 32 <= lo_lo && 32 * c >= sink));
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         if (empty[c])
                             continue;
                         if (MK > 0)
-                            mask_chunk<MK == 2>(sc[c], 32 * c, lim, lim_lo, lo, lo_hi);
+                            mask_chunk<(MK > 0 ? MK - 1 : 0)>(sc[c], 32 * c, lim, lim_lo, lo, lo_hi, sink);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sc[c][2 * e]),
@@ -776,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool WIN, bool F8>
+template <int D, int WIN, bool F8>
 cudaError_t launch_pair_dw(const PrefillArgs &a, int grid, cudaStream_t stream)
 {
     static int attr_done[64] = {0};
@@ -808,15 +895,17 @@ cudaError_t launch_pair_dw(const PrefillArgs &a, int grid, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-// The sliding-window mask and FP8 Q / K have their own instantiations.
+// The sliding-window mask, sinks and FP8 Q / K have their own instantiations.
 template <int D>
 cudaError_t launch_pair_d(const PrefillArgs &a, int grid, cudaStream_t stream)
 {
     if (a.qk_fp8)
-        return a.window_left >= 0 ? launch_pair_dw<D, true, true>(a, grid, stream)
-                                  : launch_pair_dw<D, false, true>(a, grid, stream);
-    return a.window_left >= 0 ? launch_pair_dw<D, true, false>(a, grid, stream)
-                              : launch_pair_dw<D, false, false>(a, grid, stream);
+        return a.window_left >= 0 ? launch_pair_dw<D, 1, true>(a, grid, stream)
+                                  : launch_pair_dw<D, 0, true>(a, grid, stream);
+    if (a.window_left >= 0 && a.sink_tokens > 0)
+        return launch_pair_dw<D, 2, false>(a, grid, stream);
+    return a.window_left >= 0 ? launch_pair_dw<D, 1, false>(a, grid, stream)
+                              : launch_pair_dw<D, 0, false>(a, grid, stream);
 }
 
 }  // namespace

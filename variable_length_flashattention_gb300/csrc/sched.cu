@@ -35,6 +35,11 @@
 // clamped arithmetic series, the largest cost sits next to the first index
 // where the flat part begins, and a group keeps its tiles in i-descending
 // order (longest first wherever the keys reach past the last query).
+//
+// Sinks (first keys that stay visible past the window) change no order and no
+// window range: the prefill adds the sinks' key tiles below a tile's first one
+// itself.  Only the tiles from i_z on, which would see nothing, are written as
+// the empty window [st, st) behind the sequence's st sink tiles.
 #include "internal.h"
 
 namespace vfa {
@@ -322,6 +327,10 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(const SchedArgs a)
             // key tiles [max(0, i r + g), c(i)) below n1; none from n1 on
             if (i < seq_n1[b] && c > 0)
                 f = max(0, i * static_cast<int>(r) + seq_g[b]);
+            else if (i >= seq_n1[b] && a.sink_tokens > 0)
+                f = c = static_cast<int>(
+                    (static_cast<unsigned>(min(a.sink_tokens, a.cu_k[b + 1] - a.cu_k[b])) + bk - 1) >>
+                    lbk);
             else
                 c = 0;
             rank = nt - 1 - i;

@@ -49,6 +49,8 @@ SIGNATURES = [
     ("vfa_varlen_fwd_tile_shape", _I, [_I, _P, _P, _P]),
     ("vfa_varlen_fwd", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _P, _P,
                             _S, _P]),
+    ("vfa_varlen_fwd_sinks", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I,
+                                  _P, _P, _P, _S, _P]),
     ("vfa_varlen_fwd_fp8", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I,
                                 _I, _P, _P, _P, _S, _P]),
     ("vfa_varlen_fwd_noalloc", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P,
@@ -58,6 +60,9 @@ SIGNATURES = [
     ("vfa_varlen_bwd_workspace_bytes", _S, [_I, _I, _I, _I]),
     ("vfa_varlen_bwd", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I,
                             _P, _P, _P, _P, _S, _P]),
+    ("vfa_varlen_bwd_sinks_workspace_bytes", _S, [_I, _I, _I, _I, _I]),
+    ("vfa_varlen_bwd_sinks", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I,
+                                  _I, _I, _P, _P, _P, _P, _S, _P]),
     ("vfa_paged_decode_init", _I, [_P, _P, _P, _I, _I, _I, _P, _P]),
     ("vfa_paged_decode_step", _I, [_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P,
                                    _P, _P, _P, _P]),
@@ -177,12 +182,13 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
                cu_seqlens_k: torch.Tensor, max_seqlen_q: int, softmax_scale: float,
                causal, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-               stream=None, window_left: int = -1):
+               stream=None, window_left: int = -1, sink_tokens: int = 0):
     """out bf16 [Tq, H, D], lse f32 [Tq, H] = varlen attention forward (vfa_varlen_fwd).
 
     k, v may hold fewer heads than q (a divisor of H): query head h reads kv
     head h // (H // Hkv).  causal: 0 / False, 1 / True (top-left), 2
-    (bottom-right); window_left >= 0 adds a sliding window (needs causal)."""
+    (bottom-right); window_left >= 0 adds a sliding window (needs causal), past
+    which the first sink_tokens keys stay visible (vfa_varlen_fwd_sinks)."""
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, n)
     _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
@@ -204,14 +210,30 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     _need(lse, torch.float32, "lse")
     if workspace is None:
         workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q.device)
-    st = lib().vfa_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
-                              total_q, total_k, int(max_seqlen_q), batch, H, Hkv, D,
-                              float(softmax_scale), int(causal), int(window_left), _ptr(out),
-                              _ptr(lse), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(),
-                              _stream(stream))
+    if sink_tokens != 0:
+        st = lib().vfa_varlen_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
+                                        _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q),
+                                        batch, H, Hkv, D, float(softmax_scale), int(causal),
+                                        int(window_left), _sinks(sink_tokens), _ptr(out), _ptr(lse),
+                                        _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(),
+                                        _stream(stream))
+    else:
+        st = lib().vfa_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
+                                  _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q), batch, H,
+                                  Hkv, D, float(softmax_scale), int(causal), int(window_left),
+                                  _ptr(out), _ptr(lse), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st)
     return out, lse
+
+
+def _sinks(n: int) -> int:
+    """A sink count as the C ABI takes it; ctypes would cut a larger one without a word."""
+    n = int(n)
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"sink_tokens {n} does not fit 32 bits")
+    return n
 
 
 def varlen_fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor,
@@ -250,8 +272,12 @@ def varlen_fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor,
 
 
 def alloc_bwd_workspace(batch: int, total_q: int, num_heads: int, head_dim: int,
-                        device="cuda") -> torch.Tensor:
-    n = lib().vfa_varlen_bwd_workspace_bytes(batch, total_q, num_heads, head_dim)
+                        device="cuda", sink_tokens: int = 0) -> torch.Tensor:
+    if sink_tokens != 0:
+        n = lib().vfa_varlen_bwd_sinks_workspace_bytes(batch, total_q, num_heads, head_dim,
+                                                       _sinks(sink_tokens))
+    else:
+        n = lib().vfa_varlen_bwd_workspace_bytes(batch, total_q, num_heads, head_dim)
     if n == 0:
         raise VfaError(VFA_ERR_UNSUPPORTED, "backward workspace size query rejected its arguments")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -262,8 +288,9 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
                cu_seqlens_k: torch.Tensor, softmax_scale: float, causal,
                window_left: int = -1, dq: Optional[torch.Tensor] = None,
                dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
-               workspace: Optional[torch.Tensor] = None, stream=None):
-    """(dq, dk, dv) bf16 = gradients of varlen_fwd for upstream gradient dout (vfa_varlen_bwd)."""
+               workspace: Optional[torch.Tensor] = None, stream=None, sink_tokens: int = 0):
+    """(dq, dk, dv) bf16 = gradients of varlen_fwd for upstream gradient dout (vfa_varlen_bwd;
+    with sink_tokens vfa_varlen_bwd_sinks, and a workspace made for as many)."""
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
         _need(t, torch.bfloat16, n)
     _need(lse, torch.float32, "lse")
@@ -281,12 +308,22 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
         _need(t, torch.bfloat16, n)
     if workspace is None:
-        workspace = alloc_bwd_workspace(batch, total_q, H, D, device=q.device)
-    st = lib().vfa_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
-                              _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q, total_k, batch, H,
-                              Hkv, D, float(softmax_scale), int(causal), int(window_left),
-                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace = alloc_bwd_workspace(batch, total_q, H, D, device=q.device,
+                                        sink_tokens=max(sink_tokens, 0))
+    if sink_tokens != 0:
+        st = lib().vfa_varlen_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout),
+                                        _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q,
+                                        total_k, batch, H, Hkv, D, float(softmax_scale),
+                                        int(causal), int(window_left), _sinks(sink_tokens),
+                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(),
+                                        _stream(stream))
+    else:
+        st = lib().vfa_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
+                                  _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q, total_k, batch,
+                                  H, Hkv, D, float(softmax_scale), int(causal), int(window_left),
+                                  _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st)
     return dq, dk, dv, workspace
 
