@@ -1,7 +1,8 @@
 /*
  * vfa.h -- C ABI of libvfa: variable-length FlashAttention forward and paged
  * GQA decode for NVIDIA GB300 (sm_103a), with the operators around them
- * (query / key norm and rotation, a 4-bit paged cache, page operations).
+ * (query / key norm and rotation, a 4-bit paged cache, page operations, a
+ * cache bounded by window and sinks or by eviction).
  *
  * Conventions shared by every entry point:
  *   - Every pointer argument named as a device buffer is a CUDA device
@@ -442,6 +443,60 @@ vfa_status vfa_paged_decode_finalize(const float *l, const float *o, int num_seq
                                      vfa_stream_t stream);
 
 /*
+ * Attention of one new token per sequence over a paged bf16 cache, in one
+ * launch: no state, whole contexts, with a window and sinks.  With n =
+ * token_counts[s] the query is the token at position n - 1, which the cache
+ * holds already:
+ *   out[s, h] = sum_j p_j v_j / sum_j p_j, p_j = exp(softmax_scale q.k_j),
+ * over the tokens j < n with j >= n - 1 - window_left or j < sink_tokens,
+ * query head h on kv head h / (num_q_heads / num_kv_heads), and lse = the
+ * natural log of sum_j p_j.  token_counts[s] == 0 gives out = 0 and lse =
+ * -FLT_MAX.  Only pages that hold such tokens are read, and what their other
+ * slots hold does not matter.  The batch's pages are spread over the SMs,
+ * whatever the lengths.
+ *
+ * q, out       device bf16 [num_seqs, num_q_heads, head_dim].
+ * k_pool, v_pool  device bf16 [num_blocks, 16, num_kv_heads, head_dim].
+ * tables       device int32 [num_seqs, capacity]: physical page of each
+ *              logical one.
+ * token_counts device int32 [num_seqs], in [0, capacity * 16].
+ * window_left  < 0: no window (sink_tokens then changes nothing).
+ * sink_tokens  >= 0.
+ * softmax_scale  <= 0 means 1/sqrt(head_dim); NaN or inf is
+ *              VFA_ERR_INVALID_ARG.
+ * lse          nullable device f32 [num_seqs, num_q_heads].
+ * key_weights  nullable device f32 [num_seqs, num_kv_heads, capacity * 16]:
+ *              the accumulated weight of each slot of a row's pages.  With
+ *              it, key_weights_out (may be key_weights) gets, at every visible
+ *              token, key_weights + the sum of p_j / sum_j p_j over the kv
+ *              head's query heads; other slots are left as they were.
+ * workspace    device scratch of vfa_paged_decode_workspace_bytes() bytes,
+ *              256-byte aligned, with the capacity (0: without key_weights).
+ *              It must hold zeros before its first use; every call leaves what
+ *              has to be zero that way.  A workspace made for num_seqs
+ *              sequences and a capacity serves smaller ones with the same
+ *              heads and head_dim too, and calls without key_weights; one made
+ *              with capacity 0 is not for calls with them.  Calls sharing it
+ *              must be stream-ordered.
+ * Device-detected: a token count out of range or a page id outside [0,
+ * num_blocks) among those it reads stores VFA_ERR_BAD_BLOCK in device_status
+ * (nullable device int32 [1], the first error is kept) and leaves that
+ * sequence's out, lse and key_weights_out as they were.
+ * Supported: head_dim 64, 128 or 256; pages of 16 tokens; any num_q_heads that
+ * is a multiple of num_kv_heads; num_seqs * (capacity + 64) <= 2^30.
+ */
+size_t vfa_paged_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                        int capacity);
+
+vfa_status vfa_paged_decode(const void *q, const void *k_pool, const void *v_pool, int num_blocks,
+                            const int32_t *tables, int capacity, const int32_t *token_counts,
+                            int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                            int window_left, int sink_tokens, float softmax_scale, void *out,
+                            float *lse, const float *key_weights, float *key_weights_out,
+                            int32_t *device_status, void *workspace, size_t workspace_bytes,
+                            vfa_stream_t stream);
+
+/*
  * Test hook for the block-table gather of vfa_paged_decode_step: runs the
  * same device address computation and writes, for every sequence s, listed
  * block b < count_s, token t and kv head kh, the K and V rows it reads into
@@ -735,6 +790,111 @@ vfa_status vfa_pages_compact(const int32_t *refcounts, int num_blocks, const int
 vfa_status vfa_pages_copy(void *const *pools, const int *page_bytes, int num_pools,
                           const int32_t *src, const int32_t *dst, int n, int num_blocks,
                           int32_t *device_status, vfa_stream_t stream);
+
+/*
+ * Rows give up their last tokens: token_counts_out[s] = new_counts[s] where 0
+ * <= new_counts[s] < token_counts[s], and the pages behind the last token left
+ * lose a reference.  A negative or equal new count leaves a row as it is.  A
+ * new count above the old one, a bad old count, or a last page that would be
+ * cut in two and that another row lists as well (its refcount before the call
+ * is above 1) leaves the row as it is and is recorded as VFA_ERR_BAD_BLOCK; bad
+ * page ids and refcounts that are 0 already are recorded and skipped.  Table
+ * entries keep their old values.
+ *
+ * refcounts_out, token_counts_out  may be refcounts and token_counts.
+ * workspace     device scratch of 8 * num_seqs bytes, 16-byte aligned.
+ */
+vfa_status vfa_pages_truncate(const int32_t *refcounts, int num_blocks, const int32_t *tables,
+                              int capacity, const int32_t *token_counts, int num_seqs,
+                              const int32_t *new_counts, int block_size, int32_t *refcounts_out,
+                              int32_t *token_counts_out, void *workspace, size_t workspace_bytes,
+                              int32_t *device_status, vfa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Eviction by attention weight                                              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The accumulated attention weight of packed keys, for a prompt:
+ *   key_weights_out[b, hk, j] = key_weights[b, hk, j] + the sum over the query
+ *   heads of kv head hk and the queries i of sequence b that see key j of
+ *   exp(softmax_scale q_i.k_j - lse_i)
+ * with lse from vfa_varlen_fwd (or _sinks) under the same mask.  Key j of
+ * sequence b is slot j of its row, as in vfa_paged_decode, which adds later
+ * queries to the same sums.
+ *
+ * q, k, lse, cu_seqlens_q/k, totals, max_seqlen_q, heads, head_dim,
+ * softmax_scale, causal, window_left, sink_tokens: as in vfa_varlen_fwd_sinks.
+ * key_weights, key_weights_out  device f32 [batch, num_kv_heads, row_stride],
+ *              may be the same; entries past a sequence's keys are left as they
+ *              were.  row_stride is at least the longest key length.
+ * workspace    device scratch of vfa_varlen_key_weights_workspace_bytes()
+ *              bytes, 256-byte aligned; its first int32 is the device status
+ *              word: VFA_ERR_BAD_SEQLENS (bad cu_seqlens, a q length above
+ *              max_seqlen_q, more keys than row_stride; nothing is written) or
+ *              VFA_ERR_TIMEOUT.  Calls sharing it must be stream-ordered.
+ * The sums run in a fixed order: results are bit-identical from run to run.
+ */
+size_t vfa_varlen_key_weights_workspace_bytes(int batch, int total_q, int total_k, int max_seqlen_q,
+                                              int num_heads);
+
+vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse,
+                                  const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                  int total_q, int total_k, int max_seqlen_q, int batch,
+                                  int num_heads, int num_kv_heads, int head_dim,
+                                  float softmax_scale, int causal, int window_left,
+                                  int sink_tokens, const float *key_weights,
+                                  float *key_weights_out, int64_t row_stride, void *workspace,
+                                  size_t workspace_bytes, vfa_stream_t stream);
+
+/*
+ * Tokens of little weight leave a paged bf16 cache (one layer's pools).  Of
+ * the n = token_counts[s] tokens of a row b = min(n, budgets[s]) stay (a
+ * negative budget: all), for every kv head its own:
+ *   - those with positions below s0 = min(sink_tokens, b),
+ *   - those with the last min(recent_tokens, b - s0) positions,
+ *   - of the others those with the largest key_weights, ties by the lowest slot
+ *     (weights in the order of floats, any NaN the largest).
+ * Kept tokens at slots >= b move, in ascending order, to the free slots below
+ * b, in ascending order; the other slots of the pools stay as they are.
+ * key_weights_out and positions_out get the values of the slots below b, and
+ * key_weights_out zeros for the slots in [b, n), which tokens to come will take.
+ * kept[s] = b; token_counts and the pages stay as they are, so that every layer
+ * is called with the same ones, each with its own weights, positions and
+ * history; vfa_pages_truncate with kept comes last.  Attention over the kept
+ * tokens needs no order; a window over slots has no meaning after an eviction.
+ *
+ * key_weights  device f32 [num_seqs, num_kv_heads, capacity * 16].
+ * positions    device int32, the same shape: which token of its sequence a slot
+ *              holds, for slots below history[s][0]; slots past it were
+ *              appended since and hold the tokens slot + history[s][1].
+ * history      device int32 [num_seqs, 2], zeros for a new sequence (as its
+ *              key_weights): becomes (b, history[s][1] + n - b).
+ * key_weights_out, positions_out, history_out  may be the inputs.
+ * refcounts    device int32 [num_blocks], as in the page operations: a row that
+ *              loses tokens must be alone on the pages that hold its first b
+ *              slots (refcount 1), since they are written.
+ * kept         device int32 [num_seqs].
+ * workspace    device scratch of vfa_cache_evict_workspace_bytes() bytes,
+ *              256-byte aligned, no initial value.  Calls sharing it must be
+ *              stream-ordered.
+ * Device-detected: a bad count, history or page id, or a page shared as above,
+ * stores VFA_ERR_BAD_BLOCK in device_status (nullable; the first error is kept):
+ * the row's slots, key_weights_out and positions_out stay as they were, kept[s]
+ * is n and history_out[s] is history[s].  Stored positions that are not one per
+ * token may name more than b tokens that stay: the lowest slots of them do.
+ * Supported: head_dim 64, 128 or 256; pages of 16 tokens.
+ */
+size_t vfa_cache_evict_workspace_bytes(int num_seqs, int num_kv_heads, int capacity);
+
+vfa_status vfa_cache_evict(void *k_pool, void *v_pool, const int32_t *refcounts, int num_blocks,
+                           const int32_t *tables, int capacity, const int32_t *token_counts,
+                           const int32_t *budgets, int num_seqs, int num_kv_heads, int head_dim,
+                           const float *key_weights, const int32_t *positions,
+                           const int32_t *history, int sink_tokens, int recent_tokens,
+                           float *key_weights_out, int32_t *positions_out, int32_t *history_out,
+                           int32_t *kept, void *workspace, size_t workspace_bytes,
+                           int32_t *device_status, vfa_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                    */

@@ -140,7 +140,7 @@ def evict(refcounts, tables, counts, budgets, weights, positions, history, sinks
         for h in range(hkv):
             pos = [int(positions[s, h, j]) if j < known else j + gone for j in range(n)]
             safe = [p < first or p >= n + gone - last for p in pos]
-            order = sorted(range(n), key=lambda j: (not safe[j], -weights[s, h, j], j))
+            order = sorted(range(n), key=lambda j: (not safe[j], 0.0 if safe[j] else -weights[s, h, j], j))
             keep = set(order[:b])
             src = list(range(b))
             movers = [j for j in range(b, n) if j in keep]

@@ -170,6 +170,12 @@ vfa_status vfa::set_error(vfa_status st, const char *message)
     return fail(st, "%s", message);
 }
 
+vfa_status vfa::encode_tile_map(CUtensorMap *map, const void *base, int rows, int heads,
+                                int head_dim, int box_rows)
+{
+    return encode_packed_map(map, base, rows, heads, head_dim, box_rows);
+}
+
 vfa_status vfa::device_sm_count(int *sm_count)
 {
     DeviceInfo dev;

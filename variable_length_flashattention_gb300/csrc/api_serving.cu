@@ -517,6 +517,45 @@ vfa_status vfa_pages_free(int32_t *refcounts, int num_blocks, const int32_t *tab
                     "page free launch");
 }
 
+vfa_status vfa_pages_truncate(const int32_t *refcounts, int num_blocks, const int32_t *tables,
+                              int capacity, const int32_t *token_counts, int num_seqs,
+                              const int32_t *new_counts, int block_size, int32_t *refcounts_out,
+                              int32_t *token_counts_out, void *workspace, size_t workspace_bytes,
+                              int32_t *device_status, vfa_stream_t stream)
+{
+    vfa_status st = check_pages(refcounts, num_blocks, tables, capacity, token_counts, num_seqs,
+                                block_size, device_status);
+    if (st)
+        return st;
+    if (!new_counts || !refcounts_out || !token_counts_out || !aligned(new_counts, 4) ||
+        !aligned(refcounts_out, 4) || !aligned(token_counts_out, 4))
+        return fail(VFA_ERR_INVALID_ARG,
+                    "new_counts and the outputs must be non-null, aligned pointers");
+    const size_t need = 2 * static_cast<size_t>(num_seqs) * sizeof(int32_t);
+    if (!workspace || !aligned(workspace, 16))
+        return fail(VFA_ERR_INVALID_ARG, "workspace must be a non-null, 16-byte aligned pointer");
+    if (workspace_bytes < need)
+        return fail(VFA_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    int sms;
+    if ((st = vfa::device_sm_count(&sms)))
+        return st;
+    vfa::PageArgs a = {};
+    a.refs = const_cast<int32_t *>(refcounts);
+    a.refs_out = refcounts_out;
+    a.tables = const_cast<int32_t *>(tables);
+    a.counts = const_cast<int32_t *>(token_counts);
+    a.counts_out = token_counts_out;
+    a.new_counts = new_counts;
+    a.status = device_status;
+    a.ws = static_cast<int32_t *>(workspace);
+    a.num_blocks = num_blocks;
+    a.num_seqs = num_seqs;
+    a.capacity = capacity;
+    a.block_size = block_size;
+    return launched(vfa::launch_pages_truncate(a, sms, reinterpret_cast<cudaStream_t>(stream)),
+                    "page truncate launch");
+}
+
 vfa_status vfa_pages_compact(const int32_t *refcounts, int num_blocks, const int32_t *tables,
                              int capacity, const int32_t *token_counts, int num_seqs,
                              void *const *pools, const int *page_bytes, int num_pools,

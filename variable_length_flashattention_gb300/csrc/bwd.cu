@@ -53,17 +53,16 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tiles.cuh"
 
 namespace vfa {
 
 namespace {
 
-constexpr int kOwn = 128;          // rows of a CTA's own tile (keys, resp. queries)
 constexpr int kMathWarps = 8;      // four TMEM lane quarters x two column halves
 constexpr int kFirstMathWarp = 4;
 constexpr int kMathThreads = kMathWarps * 32;
 constexpr int kThreads = (kFirstMathWarp + kMathWarps) * 32;   // + TMA, MMA, two idle warps
-constexpr int kPrepThreads = 1024;
 constexpr uint32_t kEpiStage = 32 * 64;    // per math warp: 32 rows x 32 bf16 columns of output
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -115,47 +114,6 @@ struct BwdCfg {
 };
 
 // ------------------------------------------------------------ prep
-
-// Exclusive prefix sum over blockDim.x-wide chunks of per-sequence counts;
-// out[b] = sum of count(b') for b' < b, out[B] = the total.
-template <typename CountFn>
-__device__ void block_prefix(int B, int32_t *out, int *warp_sums, CountFn count)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int carry = 0;
-    for (int base = 0; base < B; base += kPrepThreads) {
-        const int b = base + tid;
-        const int nt = b < B ? count(b) : 0;
-        int x = nt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o)
-                x += y;
-        }
-        if (lane == 31)
-            warp_sums[warp] = x;
-        __syncthreads();
-        if (warp == 0) {
-            int w = warp_sums[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, w, o);
-                if (lane >= o)
-                    w += y;
-            }
-            warp_sums[lane] = w;
-        }
-        __syncthreads();
-        const int excl = x - nt + (warp > 0 ? warp_sums[warp - 1] : 0);
-        if (b < B)
-            out[b] = carry + excl;
-        carry += warp_sums[31];
-        __syncthreads();
-    }
-    if (tid == 0)
-        out[B] = carry;
-}
 
 // Key tiles of a sequence of lk keys that hold sinks.
 __device__ __forceinline__ int sink_tiles(const BwdArgs &a, int lk)
@@ -257,42 +215,6 @@ __global__ void bwd_delta_kernel(const BwdArgs a)
 
 // ------------------------------------------------------------ shared pieces
 
-// Largest b with start[b] <= gt (start is a non-decreasing prefix sum).
-__device__ __forceinline__ int owner_of(const int32_t *start, int B, int gt)
-{
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= gt)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
-}
-
-// The visible part of (at most 32) consecutive columns, [lo, hi) (empty when hi <= lo),
-// clamped to [-1, 33] so it fits an int.
-__device__ __forceinline__ int clamp_col(long long x)
-{
-    return static_cast<int>(x < -1 ? -1 : (x > 33 ? 33 : x));
-}
-
-// Key j's visible queries among i_base, i_base + 1, ... (the dK/dV kernel's
-// columns): i < Lq, and i >= j - off (causal), i <= j - off + window_left.
-__device__ __forceinline__ void key_row_span(long long j, long long i_base, int lk, int lq,
-                                             int causal, int wl, long long off, int *lo, int *hi)
-{
-    long long l = causal ? j - off - i_base : 0;
-    long long h = lq - i_base;
-    if (wl >= 0)
-        h = min(h, j - off + wl - i_base + 1);
-    if (j >= lk)
-        h = l;
-    *lo = clamp_col(l);
-    *hi = clamp_col(h);
-}
-
 // Query i's visible keys among j_base, j_base + 1, ... (the dQ kernel's
 // columns): j < Lk, and j <= i + off (causal), j >= i + off - window_left.
 __device__ __forceinline__ void query_row_span(long long i, long long j_base, int lk, int lq,
@@ -377,36 +299,6 @@ __device__ __forceinline__ void query_row_grads(const uint32_t (&sr)[NC], const 
                                     nd2);
         const float2 ds = __fmul2_rn(make_float2(p0, p1), g);
         dk2[e >> 1] = pack_bf16x2(ds.x, ds.y);
-    }
-}
-
-// Loads a tile of `rows` rows (a multiple of the map's box height BOX) of
-// every 64-column block of row `row0`, head `head` into a 128-byte-swizzled
-// buffer holding `rows` rows per column block.
-template <int DB, int BOX>
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                          int head, int row0, int rows)
-{
-    for (int db = 0; db < DB; ++db)
-        for (int r = 0; r < rows; r += BOX)
-            tma_load_3d(dst + db * (rows * 128) + r * 128, map, bar, db * 64, head, row0 + r);
-}
-
-// S (or S^T) = A B^T over K = D for A a 128-row operand and B a STEP-row
-// operand, both K-major in 128-byte-swizzled column blocks.
-template <int D, int STEP>
-__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t a_buf, uint32_t b_buf,
-                                             uint32_t idesc)
-{
-    const uint64_t a0 = sdesc_sw128(a_buf, 16, 1024), b0 = sdesc_sw128(b_buf, 16, 1024);
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t ao = ((kk >> 2) * (kOwn * 128) + (kk & 3) * 32) >> 4;
-        const uint64_t bo = ((kk >> 2) * (STEP * 128) + (kk & 3) * 32) >> 4;
-        if (kk == 0)
-            mma_ss_w<0>(d_tmem, a0 + ao, b0 + bo, idesc);
-        else
-            mma_ss_w<1>(d_tmem, a0 + ao, b0 + bo, idesc);
     }
 }
 

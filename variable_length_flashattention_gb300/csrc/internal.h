@@ -282,6 +282,80 @@ size_t kv4_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_head
 cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, int sm_count,
                               cudaStream_t stream);
 
+// ------------------------------------------------------------ key weights
+
+struct KeyWeightArgs {
+    CUtensorMap tm_q, tm_k;                 // boxes of 64 columns x 1 head x 128 rows, 128-byte swizzle
+    const int32_t *cu_q, *cu_k;
+    const float *lse;                       // f32 [total_q, num_heads], natural log
+    const float *weights;                   // [batch, num_kv_heads, weight_stride]
+    float *weights_out;                     // may be weights
+    long long weight_stride;
+    int32_t *status;                        // workspace: status word, unit counter
+    int32_t *tile_start, *unit_start;       // workspace: [batch + 1] first 128-key tile, first unit
+    float *part;                            // workspace: [2 * chunks, num_heads, total_k]
+    int batch, total_q, total_k, max_seqlen_q, num_heads, num_kv_heads;
+    int chunk_steps;                        // set by the launcher: query blocks of a unit
+    float scale_log2;
+    int causal, window_left, sink_tokens;
+};
+
+size_t key_weights_workspace_bytes(int batch, int total_k, int max_seqlen_q, int num_heads);
+cudaError_t launch_key_weights(int head_dim, KeyWeightArgs &a, void *workspace, int sm_count,
+                               cudaStream_t stream);
+
+// ------------------------------------------------------------ one-launch decode
+
+struct PagedDecodeArgs {
+    const void *q;                          // bf16 [num_seqs, num_q_heads, D]
+    const void *k_pool, *v_pool;            // bf16 [num_blocks, 16, num_kv_heads, D]
+    const int32_t *tables, *counts;         // [num_seqs, capacity], [num_seqs] tokens
+    void *out;                              // bf16, as q
+    float *lse;                             // [num_seqs, num_q_heads], nullable
+    const float *weights;                   // [num_seqs, num_kv_heads, weight_stride], nullable
+    float *weights_out;                     // may be weights
+    long long weight_stride;
+    int32_t *status;                        // nullable
+    float *part;                            // workspace: partial states
+    int32_t *tickets;                       // workspace: [num_seqs, head chunks], zero between calls
+    float2 *ml;                             // workspace: reference and sum, [num_seqs, num_q_heads]
+    float *logits;                          // workspace: [num_seqs, num_kv_heads, max_pages, 16, group]
+    int num_seqs, capacity, num_blocks, num_q_heads, num_kv_heads;
+    int window_left, sink_tokens;           // < 0: no window
+    int max_pages;                          // set by the launcher: pages a sequence reads at most
+    float scale_log2;                       // logit scale * log2(e), > 0
+};
+
+// capacity > 0: with room for the logits of key weights.
+size_t paged_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int capacity);
+cudaError_t launch_paged_decode(int head_dim, PagedDecodeArgs &a, void *workspace,
+                                size_t workspace_bytes, int sm_count, cudaStream_t stream);
+
+// ------------------------------------------------------------ eviction
+
+struct EvictArgs {
+    void *k_pool, *v_pool;                  // bf16 [num_blocks, 16, num_kv_heads, D]
+    const int32_t *refs;                    // [num_blocks]
+    const int32_t *tables, *counts;         // [num_seqs, capacity], [num_seqs] tokens
+    const int32_t *budgets;                 // [num_seqs], < 0: no limit
+    const float *weights;                   // [num_seqs, num_kv_heads, capacity * 16]
+    const int32_t *positions;               // the same
+    const int32_t *history;                 // [num_seqs, 2]: stored positions, tokens evicted before
+    float *weights_out;                     // may be the inputs
+    int32_t *positions_out, *history_out;
+    int32_t *kept;                          // [num_seqs]
+    int32_t *status;                        // nullable
+    int32_t *moves;                         // workspace: [num_seqs * num_kv_heads] moves, -1: refused
+    uint32_t *bits;                         // workspace: [rows][(capacity + 1) / 2] kept slots
+    int32_t *lists;                         // workspace: [rows][capacity * 16] targets, then sources
+    int num_seqs, capacity, num_blocks, num_kv_heads, sink_tokens, recent_tokens;
+};
+
+size_t evict_workspace_bytes(int num_seqs, int num_kv_heads, int capacity);
+cudaError_t launch_evict(int head_dim, EvictArgs &a, void *workspace, int sm_count,
+                         cudaStream_t stream);
+
 // ------------------------------------------------------------ page operations
 
 constexpr int kMaxPagePools = 256;
@@ -302,6 +376,8 @@ struct PageArgs {
     const int32_t *parents, *children;      // fork: [n]
     const int32_t *seqs;                    // free: [n]
     int32_t *num_used;                      // compact: [1]
+    const int32_t *new_counts;              // truncate: [num_seqs]
+    int32_t *counts_out;                    // truncate: may equal counts
     int32_t *status;                        // nullable
     int32_t *ws;                            // workspace
     int num_blocks, num_seqs, capacity, block_size, n;
@@ -313,11 +389,18 @@ cudaError_t launch_pages_extend(const PageArgs &a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PageArgs &a, const PagePools &p, int sm_count,
                               cudaStream_t stream);
 cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t stream);
+// ws: 2 * num_seqs ints
+cudaError_t launch_pages_truncate(const PageArgs &a, int sm_count, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_count,
                                  cudaStream_t stream);
 // pairs of the lists src and dst, n of them.
 cudaError_t launch_pages_copy(const PagePools &p, const int32_t *src, const int32_t *dst, int n,
                               int num_blocks, int32_t *status, int sm_count, cudaStream_t stream);
+
+// A bf16 tensor [rows, heads, head_dim] as a TMA map with boxes of 64 columns x 1 head x
+// box_rows rows, 128-byte swizzle.
+vfa_status encode_tile_map(CUtensorMap *map, const void *base, int rows, int heads, int head_dim,
+                           int box_rows);
 
 // SMs of the current device, which must be the one this library is built for.
 vfa_status device_sm_count(int *sm_count);

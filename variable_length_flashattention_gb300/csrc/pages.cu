@@ -1,4 +1,4 @@
-// pages.cu -- the pages of paged K/V pools: extend, fork, free, compact, copy.
+// pages.cu -- the pages of paged K/V pools: extend, fork, free, truncate, compact, copy.
 //
 // State: refs[num_blocks] (users of a page, 0 = free), tables[num_seqs,
 // capacity] (physical page of each logical page), counts[num_seqs] (tokens).
@@ -477,6 +477,59 @@ __global__ void __launch_bounds__(256) free_kernel(const PageArgs a)
     }
 }
 
+// ------------------------------------------------------------ truncate
+//
+// Two launches: the rows are judged by the references from before the call (a
+// page that is cut in two must not be another row's as well), one thread each,
+// then every row that shrinks gives up its pages, one CTA each.
+
+__global__ void __launch_bounds__(256) truncate_plan_kernel(const PageArgs a)
+{
+    grid_wait();
+    grid_release();
+    const int first = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
+    if (a.refs_out != a.refs)
+        for (int i = first; i < a.num_blocks; i += step)
+            a.refs_out[i] = a.refs[i];
+    for (int s = first; s < a.num_seqs; s += step) {
+        const int n = a.counts[s], m = a.new_counts[s];
+        const bool valid = n >= 0 && n <= static_cast<long long>(a.capacity) * a.block_size;
+        bool ok = m >= 0 && m < n && valid;
+        bool bad = m >= 0 && m != n && !ok;
+        if (ok && m % a.block_size != 0) {
+            const int id = a.tables[static_cast<long long>(s) * a.capacity + m / a.block_size];
+            if (id >= 0 && id < a.num_blocks && a.refs[id] > 1) {
+                ok = false;
+                bad = true;
+            }
+        }
+        if (bad)
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        // its pages [first, second) go
+        auto pages = [&](int x) {
+            return static_cast<int>((static_cast<long long>(x) + a.block_size - 1) / a.block_size);
+        };
+        a.ws[2 * s] = ok ? pages(m) : 0;
+        a.ws[2 * s + 1] = ok ? pages(n) : 0;
+        a.counts_out[s] = ok ? m : n;
+    }
+}
+
+__global__ void __launch_bounds__(256) truncate_kernel(const PageArgs a)
+{
+    grid_wait();
+    const int s = blockIdx.x, end = a.ws[2 * s + 1];
+    for (int j = a.ws[2 * s] + threadIdx.x; j < end; j += blockDim.x) {
+        const int id = a.tables[static_cast<long long>(s) * a.capacity + j];
+        if (id < 0 || id >= a.num_blocks) {
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        } else if (atomicSub(&a.refs_out[id], 1) <= 0) {
+            atomicAdd(&a.refs_out[id], 1);
+            record(a.status, VFA_ERR_BAD_BLOCK);
+        }
+    }
+}
+
 // ------------------------------------------------------------ compact
 //
 // With U used pages, the used pages at or above U move, in ascending order,
@@ -739,6 +792,15 @@ cudaError_t launch_pages_fork(const PageArgs &a, const PagePools &p, int sm_coun
 cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t stream)
 {
     return launch_dependent(free_kernel, dim3(a.n), 256, 0, stream, a);
+}
+
+cudaError_t launch_pages_truncate(const PageArgs &a, int sm_count, cudaStream_t stream)
+{
+    const int n = a.refs_out != a.refs && a.num_blocks > a.num_seqs ? a.num_blocks : a.num_seqs;
+    const int ctas = (n + 255) / 256;
+    const cudaError_t e = launch_dependent(truncate_plan_kernel, dim3(ctas < 4 * sm_count ? ctas : 4 * sm_count),
+                                           256, 0, stream, a);
+    return e != cudaSuccess ? e : launch_dependent(truncate_kernel, dim3(a.num_seqs), 256, 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_count,

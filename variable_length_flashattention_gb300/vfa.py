@@ -93,6 +93,16 @@ SIGNATURES = [
     ("vfa_pages_compact", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _S, _P,
                                _P]),
     ("vfa_pages_copy", _I, [_P, _P, _I, _P, _P, _I, _I, _P, _P]),
+    ("vfa_pages_truncate", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _S, _P, _P]),
+    ("vfa_paged_decode_workspace_bytes", _S, [_I, _I, _I, _I, _I]),
+    ("vfa_paged_decode", _I, [_P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P,
+                              _P, _P, _P, _S, _P]),
+    ("vfa_varlen_key_weights_workspace_bytes", _S, [_I, _I, _I, _I, _I]),
+    ("vfa_varlen_key_weights", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I,
+                                    _P, _P, _L, _P, _S, _P]),
+    ("vfa_cache_evict_workspace_bytes", _S, [_I, _I, _I]),
+    ("vfa_cache_evict", _I, [_P, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P,
+                             _P, _P, _P, _S, _P, _P]),
     ("vfa_read_status", _I, [_P, _P, _P]),
 ]
 
@@ -149,6 +159,14 @@ def _need(t: torch.Tensor, dtype, name: str):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _int32(n, name) -> int:
+    """n as the C ABI takes it; ctypes would cut a larger one without a word."""
+    n = int(n)
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name} {n} does not fit 32 bits")
+    return n
 
 
 def version() -> str:
@@ -214,7 +232,7 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
         st = lib().vfa_varlen_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
                                         _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q),
                                         batch, H, Hkv, D, float(softmax_scale), int(causal),
-                                        int(window_left), _sinks(sink_tokens), _ptr(out), _ptr(lse),
+                                        int(window_left), _int32(sink_tokens, "sink_tokens"), _ptr(out), _ptr(lse),
                                         _ptr(workspace),
                                         workspace.numel() * workspace.element_size(),
                                         _stream(stream))
@@ -226,14 +244,6 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
                                   workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st)
     return out, lse
-
-
-def _sinks(n: int) -> int:
-    """A sink count as the C ABI takes it; ctypes would cut a larger one without a word."""
-    n = int(n)
-    if not -0x80000000 <= n <= 0x7fffffff:
-        raise ValueError(f"sink_tokens {n} does not fit 32 bits")
-    return n
 
 
 def varlen_fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor,
@@ -275,7 +285,7 @@ def alloc_bwd_workspace(batch: int, total_q: int, num_heads: int, head_dim: int,
                         device="cuda", sink_tokens: int = 0) -> torch.Tensor:
     if sink_tokens != 0:
         n = lib().vfa_varlen_bwd_sinks_workspace_bytes(batch, total_q, num_heads, head_dim,
-                                                       _sinks(sink_tokens))
+                                                       _int32(sink_tokens, "sink_tokens"))
     else:
         n = lib().vfa_varlen_bwd_workspace_bytes(batch, total_q, num_heads, head_dim)
     if n == 0:
@@ -314,7 +324,7 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
         st = lib().vfa_varlen_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout),
                                         _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q,
                                         total_k, batch, H, Hkv, D, float(softmax_scale),
-                                        int(causal), int(window_left), _sinks(sink_tokens),
+                                        int(causal), int(window_left), _int32(sink_tokens, "sink_tokens"),
                                         _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(),
                                         _stream(stream))
@@ -1003,6 +1013,245 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor,
         _raw_stream(stream, dev))
     if st:
         _check(st)
+
+
+def pages_truncate(refcounts: torch.Tensor, tables: torch.Tensor, token_counts: torch.Tensor,
+                   new_counts: torch.Tensor, block_size: int,
+                   refcounts_out: Optional[torch.Tensor] = None,
+                   token_counts_out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None):
+    """Rows shrink to new_counts tokens and give up the pages behind them (vfa_pages_truncate);
+    refcounts and token_counts are rewritten in place unless outputs are given.  A negative
+    new count leaves a row as it is."""
+    dev, blocks, cap, S = _page_state(refcounts, tables, token_counts, status, block_size)
+    refcounts_out = refcounts if refcounts_out is None else refcounts_out
+    token_counts_out = token_counts if token_counts_out is None else token_counts_out
+    for t, x, n in ((new_counts, token_counts, "new_counts"),
+                    (refcounts_out, refcounts, "refcounts_out"),
+                    (token_counts_out, token_counts, "token_counts_out")):
+        _dense(t, _I32, n, dev)
+        if t.shape != x.shape:
+            raise ValueError(f"{n} must have shape {tuple(x.shape)}")
+    if workspace is None:
+        workspace = _empty(8 * S, torch.uint8, refcounts.device, stream)
+    else:
+        _dense(workspace, _U8, "workspace", dev)
+    st = (_lib or lib()).vfa_pages_truncate(
+        refcounts.data_ptr(), blocks, tables.data_ptr(), cap, token_counts.data_ptr(), S,
+        new_counts.data_ptr(), block_size, refcounts_out.data_ptr(), token_counts_out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+# ----------------------------------------------------------------- a bounded bf16 cache
+
+def _bf16_cache(k_pool, v_pool, tables, token_counts, status):
+    """Checks; (device, num_blocks, num_kv_heads, head_dim, num_seqs, capacity)."""
+    dev = _device(k_pool, "k_pool")
+    _dense(k_pool, _BF16, "k_pool", dev)
+    _dense(v_pool, _BF16, "v_pool", dev)
+    _dense(tables, _I32, "tables", dev)
+    _dense(token_counts, _I32, "token_counts", dev)
+    if status is not None:
+        _dense(status, _I32, "status", dev)
+    if k_pool.dim() != 4 or k_pool.shape[1] != 16 or v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must be [num_blocks, 16, num_kv_heads, head_dim]")
+    if tables.dim() != 2 or token_counts.shape != tables.shape[:1]:
+        raise ValueError("tables must be [num_seqs, capacity] and token_counts [num_seqs]")
+    blocks, _, Hkv, D = k_pool.shape
+    S, cap = tables.shape
+    _fits(blocks, Hkv, D, S, cap)
+    return dev, blocks, Hkv, D, S, cap
+
+
+def alloc_paged_decode_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                 capacity: int = 0, device="cuda") -> torch.Tensor:
+    """A workspace for paged_decode (what starts at zero does); capacity: pages of a row, for
+    calls with key_weights."""
+    _fits(num_seqs, num_q_heads, num_kv_heads, capacity)
+    n = (_lib or lib()).vfa_paged_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                         capacity)
+    if n == 0:
+        raise VfaError(VFA_ERR_UNSUPPORTED, "no paged decode workspace for these sizes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    # the logits at the end need no value
+    ws[:(_lib or lib()).vfa_paged_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                         head_dim, 0)].zero_()
+    return ws
+
+
+def paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, tables: torch.Tensor,
+                 token_counts: torch.Tensor, window_left: int = -1, sink_tokens: int = 0,
+                 softmax_scale: float = 0.0, key_weights: Optional[torch.Tensor] = None,
+                 key_weights_out: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 stream=None):
+    """(out bf16 [S, Hq, D], lse f32 [S, Hq]): one new token per sequence, the last of its
+    token_counts, over a paged bf16 cache with a window and sinks (vfa_paged_decode).
+
+    key_weights f32 [S, Hkv, 16 * capacity]: the weight every visible token gets is added, in
+    place unless key_weights_out is given.  Keep a workspace from
+    alloc_paged_decode_workspace between calls; without one, each call allocates and clears
+    its own."""
+    dev, blocks, Hkv, D, S, cap = _bf16_cache(k_pool, v_pool, tables, token_counts, status)
+    _dense(q, _BF16, "q", dev)
+    if q.dim() != 3 or q.shape[0] != S or q.shape[2] != D:
+        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
+    Hq = q.shape[1]
+    _fits(Hq)
+    if out is None:
+        out = _empty_rows(q, stream)
+    else:
+        _dense(out, _BF16, "out", dev)
+    if lse is None:
+        lse = _empty((S, Hq), torch.float32, q.device, stream)
+    else:
+        _dense(lse, _F32, "lse", dev)
+    if out.shape != q.shape or lse.shape != (S, Hq):
+        raise ValueError("out must have q's shape and lse [num_seqs, num_q_heads]")
+    if key_weights is not None:
+        key_weights_out = key_weights if key_weights_out is None else key_weights_out
+        for t, n in ((key_weights, "key_weights"), (key_weights_out, "key_weights_out")):
+            _dense(t, _F32, n, dev)
+            if t.shape != (S, Hkv, 16 * cap):
+                raise ValueError(f"{n} must be [num_seqs, num_kv_heads, 16 * capacity]")
+    elif key_weights_out is not None:
+        raise ValueError("key_weights_out needs key_weights")
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = alloc_paged_decode_workspace(S, Hq, Hkv, D, 0 if key_weights is None else cap,
+                                                     device=q.device)
+    else:
+        _dense(workspace, _U8, "workspace", dev)
+    st = (_lib or lib()).vfa_paged_decode(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), blocks, tables.data_ptr(), cap,
+        token_counts.data_ptr(), S, Hq, Hkv, D, _int32(window_left, "window_left"),
+        _int32(sink_tokens, "sink_tokens"), softmax_scale, out.data_ptr(), lse.data_ptr(),
+        _address(key_weights), _address(key_weights_out), _address(status), workspace.data_ptr(),
+        workspace.numel(), _raw_stream(stream, dev))
+    if st:
+        _check(st)
+    return out, lse
+
+
+def alloc_key_weights_workspace(batch: int, total_q: int, total_k: int, max_seqlen_q: int,
+                                num_heads: int, device="cuda") -> torch.Tensor:
+    """Scratch of varlen_key_weights; its first int32 is the call's status word."""
+    _fits(batch, total_q, total_k, max_seqlen_q, num_heads)
+    n = (_lib or lib()).vfa_varlen_key_weights_workspace_bytes(batch, total_q, total_k, max_seqlen_q,
+                                                               num_heads)
+    if n == 0:
+        raise VfaError(VFA_ERR_INVALID_ARG, "no key weights workspace for these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def varlen_key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
+                       cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_seqlen_q: int,
+                       softmax_scale: float, causal, key_weights: torch.Tensor,
+                       window_left: int = -1, sink_tokens: int = 0,
+                       key_weights_out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """key_weights f32 [batch, Hkv, L] plus the attention weight that every packed key got
+    (vfa_varlen_key_weights), in place unless key_weights_out is given; returns the sums.
+
+    q [Tq, H, D], k [Tk, Hkv, D], lse [Tq, H] and the mask as in varlen_fwd, whose lse it is;
+    key j of sequence b is entry j of row b.  read_status(workspace) tells of bad lengths."""
+    dev = _device(q, "q")
+    _dense(q, _BF16, "q", dev)
+    _dense(k, _BF16, "k", dev)
+    _dense(lse, _F32, "lse", dev)
+    _dense(cu_seqlens_q, _I32, "cu_seqlens_q", dev)
+    _dense(cu_seqlens_k, _I32, "cu_seqlens_k", dev)
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2] or lse.shape != q.shape[:2] or \
+            k.shape[1] == 0 or q.shape[1] % k.shape[1] != 0:
+        raise ValueError("q [Tq, H, D], k [Tk, Hkv, D] and lse [Tq, H] must agree, Hkv dividing H")
+    batch = cu_seqlens_q.numel() - 1
+    if cu_seqlens_k.numel() != batch + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+    (Tq, H, D), (Tk, Hkv, _) = q.shape, k.shape
+    key_weights_out = key_weights if key_weights_out is None else key_weights_out
+    for t, n in ((key_weights, "key_weights"), (key_weights_out, "key_weights_out")):
+        _dense(t, _F32, n, dev)
+        if t.dim() != 3 or t.shape[:2] != (batch, Hkv) or t.shape != key_weights.shape:
+            raise ValueError(f"{n} must be [batch, num_kv_heads, L]")
+    _fits(Tq, Tk, H, D, batch)
+    max_seqlen_q = _int32(max_seqlen_q, "max_seqlen_q")
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = alloc_key_weights_workspace(batch, Tq, Tk, max_seqlen_q, H, device=q.device)
+    else:
+        _dense(workspace, _U8, "workspace", dev)
+    st = (_lib or lib()).vfa_varlen_key_weights(
+        q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(),
+        cu_seqlens_k.data_ptr(), Tq, Tk, max_seqlen_q, batch, H, Hkv, D, softmax_scale, int(causal),
+        _int32(window_left, "window_left"), _int32(sink_tokens, "sink_tokens"),
+        key_weights.data_ptr(), key_weights_out.data_ptr(), key_weights.shape[2],
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if st:
+        _check(st)
+    return key_weights_out
+
+
+def alloc_evict_workspace(num_seqs: int, num_kv_heads: int, capacity: int,
+                          device="cuda") -> torch.Tensor:
+    """Scratch of cache_evict for at least these sizes."""
+    _fits(num_seqs, num_kv_heads, capacity)
+    n = (_lib or lib()).vfa_cache_evict_workspace_bytes(num_seqs, num_kv_heads, capacity)
+    if n == 0:
+        raise VfaError(VFA_ERR_INVALID_ARG, "no eviction workspace for these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def cache_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, refcounts: torch.Tensor,
+                tables: torch.Tensor, token_counts: torch.Tensor, budgets: torch.Tensor,
+                key_weights: torch.Tensor, positions: torch.Tensor, history: torch.Tensor,
+                sink_tokens: int = 0, recent_tokens: int = 0,
+                key_weights_out: Optional[torch.Tensor] = None,
+                positions_out: Optional[torch.Tensor] = None,
+                history_out: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """The tokens of little weight leave one layer's paged bf16 cache (vfa_cache_evict): of every
+    row min(token_counts, budgets) tokens stay, each kv head its own.
+
+    key_weights f32 and positions int32 [S, Hkv, 16 * capacity], history int32 [S, 2] (zeros at
+    first); rewritten in place unless outputs are given.  Returns kept int32 [S], for
+    pages_truncate once every layer has been called."""
+    dev, blocks, Hkv, D, S, cap = _bf16_cache(k_pool, v_pool, tables, token_counts, status)
+    key_weights_out = key_weights if key_weights_out is None else key_weights_out
+    positions_out = positions if positions_out is None else positions_out
+    history_out = history if history_out is None else history_out
+    if kept is None:
+        kept = _empty(S, torch.int32, tables.device, stream)
+    rows = (S, Hkv, 16 * cap)
+    for t, dtype, shape, n in ((refcounts, _I32, (blocks,), "refcounts"), (budgets, _I32, (S,), "budgets"),
+                               (key_weights, _F32, rows, "key_weights"),
+                               (key_weights_out, _F32, rows, "key_weights_out"),
+                               (positions, _I32, rows, "positions"),
+                               (positions_out, _I32, rows, "positions_out"),
+                               (history, _I32, (S, 2), "history"),
+                               (history_out, _I32, (S, 2), "history_out"), (kept, _I32, (S,), "kept")):
+        _dense(t, dtype, n, dev)
+        if t.shape != shape:
+            raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
+    if workspace is None:
+        n = (_lib or lib()).vfa_cache_evict_workspace_bytes(S, Hkv, cap)
+        workspace = _empty(n, torch.uint8, tables.device, stream)
+    else:
+        _dense(workspace, _U8, "workspace", dev)
+    st = (_lib or lib()).vfa_cache_evict(
+        k_pool.data_ptr(), v_pool.data_ptr(), refcounts.data_ptr(), blocks, tables.data_ptr(), cap,
+        token_counts.data_ptr(), budgets.data_ptr(), S, Hkv, D, key_weights.data_ptr(),
+        positions.data_ptr(), history.data_ptr(), _int32(sink_tokens, "sink_tokens"),
+        _int32(recent_tokens, "recent_tokens"), key_weights_out.data_ptr(),
+        positions_out.data_ptr(), history_out.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _address(status), _raw_stream(stream, dev))
+    if st:
+        _check(st)
+    return kept
 
 
 def debug_bounded_wait(status: torch.Tensor, stream=None):
