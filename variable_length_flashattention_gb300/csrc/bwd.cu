@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdArgs a)
         block_prefix(B, a.part_start, warp_sums, [&](int b) {
             return chunks_of(b) > 1 ? tiles_of(b) * chunks_of(b) : 0;
         });
+        block_prefix(B, a.cut_start, warp_sums, [&](int b) { return chunks_of(b) > 1 ? tiles_of(b) : 0; });
         __syncthreads();
     }
     if (threadIdx.x == 0) {
@@ -970,8 +971,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
 }
 
 // dV and dK of the sinks' tiles that were cut: the chunks' partials in order.
-// A CTA takes kSinkRows rows of a tile, a thread four columns of them.
-constexpr int kSinkRows = 4;
+// A CTA takes kSinkRows rows of a tile and kv head at a time, a thread four
+// columns of them.
+constexpr int kSinkRows = 4, kSinkShares = kOwn / kSinkRows;
 
 template <int D>
 __global__ void __launch_bounds__(2 * kSinkRows * D / 4) bwd_sinks_kernel(const BwdArgs a)
@@ -979,38 +981,37 @@ __global__ void __launch_bounds__(2 * kSinkRows * D / 4) bwd_sinks_kernel(const 
     using C = BwdCfg<D, false>;
     if (*a.status != VFA_OK)
         return;
-    const int head = blockIdx.y, row = blockIdx.z * kSinkRows + threadIdx.x / (D / 4) % kSinkRows;
+    const int sub_row = threadIdx.x / (D / 4) % kSinkRows;
     const bool is_dk = threadIdx.x >= kSinkRows * D / 4;
     const int col = threadIdx.x % (D / 4) * 4, dh = col / C::DKV;
-    const int units = a.sink_start[a.batch];
-    for (int u = blockIdx.x; u < units;) {
-        const int b = owner_of(a.sink_start, a.batch, u);
-        const int chunks = a.sink_chunks[b], x = u - a.sink_start[b];
-        if (x % chunks == 0 && chunks > 1) {
-            const int k0 = a.cu_k[b], key = x / chunks * kOwn + row;
-            const size_t stride = static_cast<size_t>(a.num_kv_heads) * C::DSPLIT * 2 * kOwn * C::DKV;
-            const float *src =
-                a.part +
-                ((((static_cast<size_t>(a.part_start[b]) + x) * a.num_kv_heads + head) * C::DSPLIT + dh) *
-                     2 * kOwn + (is_dk ? kOwn : 0) + row) * C::DKV + col % C::DKV;
-            if (key < a.cu_k[b + 1] - k0) {
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const long long items = static_cast<long long>(a.cut_start[a.batch]) * a.num_kv_heads * kSinkShares;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int row = static_cast<int>(it % kSinkShares) * kSinkRows + sub_row;
+        const int head = static_cast<int>(it / kSinkShares % a.num_kv_heads);
+        const int cut = static_cast<int>(it / kSinkShares / a.num_kv_heads);
+        const int b = owner_of(a.cut_start, a.batch, cut), t = cut - a.cut_start[b];
+        const int chunks = a.sink_chunks[b], k0 = a.cu_k[b], key = t * kOwn + row;
+        if (key >= a.cu_k[b + 1] - k0)
+            continue;
+        const size_t stride = static_cast<size_t>(a.num_kv_heads) * C::DSPLIT * 2 * kOwn * C::DKV;
+        const float *src =
+            a.part +
+            ((((static_cast<size_t>(a.part_start[b]) + t * chunks) * a.num_kv_heads + head) * C::DSPLIT + dh) *
+                 2 * kOwn + (is_dk ? kOwn : 0) + row) * C::DKV + col % C::DKV;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-                for (int c = 0; c < chunks; ++c) {
-                    const float4 p = __ldcs(reinterpret_cast<const float4 *>(src + c * stride));
-                    s.x += p.x;
-                    s.y += p.y;
-                    s.z += p.z;
-                    s.w += p.w;
-                }
-                const float f = is_dk ? a.scale : 1.f;
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_dk ? a.dk : a.dv) +
-                                     (static_cast<size_t>(k0 + key) * a.num_kv_heads + head) * D + col;
-                *reinterpret_cast<uint2 *>(dst) =
-                    make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
-            }
+        for (int c = 0; c < chunks; ++c) {
+            const float4 p = __ldcs(reinterpret_cast<const float4 *>(src + c * stride));
+            s.x += p.x;
+            s.y += p.y;
+            s.z += p.z;
+            s.w += p.w;
         }
-        u += gridDim.x;
+        const float f = is_dk ? a.scale : 1.f;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_dk ? a.dk : a.dv) +
+                             (static_cast<size_t>(k0 + key) * a.num_kv_heads + head) * D + col;
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
     }
 }
 
@@ -1074,8 +1075,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
     }
     if (SINK && kv_units > 0 && q_units > 0) {
         // behind the dQ kernel, which waits for the dK/dV kernel
-        const dim3 grid(kSinkUnits, a.num_kv_heads, kOwn / kSinkRows);
-        bwd_sinks_kernel<D><<<grid, 2 * kSinkRows * D / 4, 0, s>>>(a);
+        bwd_sinks_kernel<D><<<4 * sm_count, 2 * kSinkRows * D / 4, 0, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
     }
@@ -1128,7 +1128,7 @@ void bwd_workspace_split(void *ws, int batch, int total_q, int num_heads, BwdArg
 size_t bwd_sinks_workspace_bytes(int batch, int total_q, int num_heads, int head_dim,
                                  int sink_tokens)
 {
-    const size_t lists = (3 * (static_cast<size_t>(batch) + 1) * sizeof(int32_t) + 255) &
+    const size_t lists = (4 * (static_cast<size_t>(batch) + 1) * sizeof(int32_t) + 255) &
                          ~static_cast<size_t>(255);
     const size_t part = 2 * static_cast<size_t>(kOwn) * (head_dim == 256 ? 128 : head_dim) * sizeof(float);
     return bwd_workspace_bytes(batch, total_q, num_heads, head_dim) + lists +
@@ -1144,7 +1144,8 @@ void bwd_sinks_workspace_split(void *ws, int batch, int total_q, int num_heads, 
     a->sink_start = p;
     a->sink_chunks = p + n;
     a->part_start = p + 2 * n;
-    a->part = reinterpret_cast<float *>(p) + ((3 * n + 63) & ~static_cast<size_t>(63));
+    a->cut_start = p + 3 * n;
+    a->part = reinterpret_cast<float *>(p) + ((4 * n + 63) & ~static_cast<size_t>(63));
 }
 
 cudaError_t launch_bwd(int head_dim, const BwdArgs &a, int key_tile_bound, int q_tile_bound,

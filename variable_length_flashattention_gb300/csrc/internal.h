@@ -171,6 +171,7 @@ struct BwdArgs {
     int32_t *sink_chunks;                   // workspace: [batch + 1] chunks per sink tile; [batch]:
                                             // steps of a chunk
     int32_t *part_start;                    // workspace: [batch + 1] first partial per sequence
+    int32_t *cut_start;                     // workspace: [batch + 1] first cut tile per sequence
     float *part;                            // workspace: partial dV, dK of the chunks
 };
 

@@ -641,32 +641,91 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) paged_decode_kernel(co
 // weights_out = weights + the sum over a kv head's query heads of exp(logit) / l,
 // one thread per visible token, CTAs (row, split) with row = (sequence, kv head).
 // Bound: HBM, 8 bytes per token and kv head and 4 per query head.
-constexpr int kWeightThreads = 256;
+// The heads' references and sums are the same for a CTA's tokens and wait in shared
+// memory; a thread has kWeightTurns tokens' logits in flight.
+constexpr int kWeightThreads = 256, kWeightTurns = 4, kWeightHeads = 64;
 
+// The logits of a token's query heads, N at a time.
+template <int N>
+__device__ __forceinline__ void load_logits(const float *x, float (&v)[N])
+{
+    if constexpr (N == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(x));
+        v[0] = y.x;
+        v[1] = y.y;
+        v[2] = y.z;
+        v[3] = y.w;
+    } else {
+        v[0] = __ldcg(x);
+    }
+}
+
+// N: query heads loaded together (4 where the group is a multiple of it).
+template <int N>
 __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(const PagedDecodeArgs a)
 {
     grid_wait();
+    __shared__ float2 s_ml[kWeightHeads];               // reference, 1 / sum
+    __shared__ int s_bad;
     const int s = blockIdx.x / a.num_kv_heads, kh = blockIdx.x % a.num_kv_heads;
     const int group = a.num_q_heads / a.num_kv_heads;
     const View v = view_of(a, s);
     const long long row = blockIdx.x;
     const float2 *ml = a.ml + static_cast<long long>(s) * a.num_q_heads + kh * group;
     const int end = v.tokens > 0 ? v.pages * kPage : 0;
-    for (int i = blockIdx.y * kWeightThreads + threadIdx.x; i < end; i += gridDim.y * kWeightThreads) {
-        const int page = v.page(i / kPage);
-        if (!(visible(a, v, page) >> (i % kPage) & 1u))
-            continue;
-        const float *x = a.logits + (row * a.max_pages * kPage + i) * group;
-        float sum = 0.f;
-        bool bad = false;
-        for (int h = 0; h < group; ++h) {
-            const float2 q = __ldcg(ml + h);
-            bad |= q.y < 0.f;
-            sum += ex2_approx((__ldcg(x + h) - q.x) * a.scale_log2) / q.y;
+    const int step = gridDim.y * kWeightThreads;
+    if (blockIdx.y * kWeightThreads >= end)
+        return;
+    if (threadIdx.x == 0)
+        s_bad = 0;
+    __syncthreads();
+    for (int h = threadIdx.x; h < group; h += kWeightThreads) {
+        const float2 q = __ldcg(ml + h);
+        if (q.y < 0.f)
+            s_bad = 1;
+        if (h < kWeightHeads)
+            s_ml[h] = make_float2(q.x, 1.f / q.y);
+    }
+    __syncthreads();
+    if (s_bad)
+        return;
+    for (int i0 = blockIdx.y * kWeightThreads + threadIdx.x; i0 < end; i0 += step * kWeightTurns) {
+        float sum[kWeightTurns], old[kWeightTurns];
+        long long at[kWeightTurns];
+#pragma unroll
+        for (int t = 0; t < kWeightTurns; ++t) {
+            const int i = i0 + t * step, page = i < end ? v.page(i / kPage) : 0;
+            at[t] = i < end && (visible(a, v, page) >> (i % kPage) & 1u)
+                        ? row * a.weight_stride + page * kPage + i % kPage
+                        : -1;
+            old[t] = at[t] >= 0 ? a.weights[at[t]] : 0.f;
+            sum[t] = 0.f;
         }
-        const long long at = row * a.weight_stride + page * kPage + i % kPage;
-        if (!bad)
-            a.weights_out[at] = a.weights[at] + sum;
+        for (int h = 0; h < group; h += N) {
+            float x[kWeightTurns][N];
+#pragma unroll
+            for (int t = 0; t < kWeightTurns; ++t)
+                if (at[t] >= 0)
+                    load_logits<N>(a.logits + (row * a.max_pages * kPage + i0 + t * step) * group + h, x[t]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float2 q;
+                if (h + e < kWeightHeads) {
+                    q = s_ml[h + e];
+                } else {
+                    q = __ldcg(ml + h + e);
+                    q.y = 1.f / q.y;
+                }
+#pragma unroll
+                for (int t = 0; t < kWeightTurns; ++t)
+                    if (at[t] >= 0)
+                        sum[t] = fmaf(ex2_approx((x[t][e] - q.x) * a.scale_log2), q.y, sum[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kWeightTurns; ++t)
+            if (at[t] >= 0)
+                a.weights_out[at[t]] = old[t] + sum[t];
     }
 }
 
@@ -711,16 +770,16 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int rows, int sm_count, cudaStrea
         return launch_dependent(paged_decode_kernel<D, false>, grid, kThreads, smem, stream, a);
     if ((e = launch_dependent(paged_decode_kernel<D, true>, grid, kThreads, smem, stream, a)) != cudaSuccess)
         return e;
-    // eight tokens a thread at most, and CTAs for every SM
+    // kWeightTurns tokens a thread, but CTAs for every SM where there are few
     const long long units = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
-    long long splits = (static_cast<long long>(a.max_pages) * kPage + 8 * kWeightThreads - 1) /
-                       (8 * kWeightThreads);
+    const long long slots = static_cast<long long>(a.max_pages) * kPage;
+    long long splits = (slots + kWeightTurns * kWeightThreads - 1) / (kWeightTurns * kWeightThreads);
     const long long fill = (8LL * sm_count + units - 1) / units;
-    const long long all = (static_cast<long long>(a.max_pages) * kPage + kWeightThreads - 1) / kWeightThreads;
+    const long long all = (slots + kWeightThreads - 1) / kWeightThreads;
     splits = splits > fill ? splits : fill;
     splits = splits < all ? splits : all;
     splits = splits < 1 ? 1 : (splits > 65535 ? 65535 : splits);
-    return launch_dependent(paged_weights_kernel,
+    return launch_dependent(group % 4 == 0 ? paged_weights_kernel<4> : paged_weights_kernel<1>,
                             dim3(static_cast<unsigned>(units), static_cast<unsigned>(splits)),
                             kWeightThreads, 0, stream, a);
 }

@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(256) free_kernel(const PageArgs a)
 //
 // Two launches: the rows are judged by the references from before the call (a
 // page that is cut in two must not be another row's as well), one thread each,
-// then every row that shrinks gives up its pages, one CTA each.
+// then every row that shrinks gives up its pages, some CTAs each.
 
 __global__ void __launch_bounds__(256) truncate_plan_kernel(const PageArgs a)
 {
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(256) truncate_kernel(const PageArgs a)
 {
     grid_wait();
     const int s = blockIdx.x, end = a.ws[2 * s + 1];
-    for (int j = a.ws[2 * s] + threadIdx.x; j < end; j += blockDim.x) {
+    for (int j = a.ws[2 * s] + blockIdx.y * blockDim.x + threadIdx.x; j < end; j += gridDim.y * blockDim.x) {
         const int id = a.tables[static_cast<long long>(s) * a.capacity + j];
         if (id < 0 || id >= a.num_blocks) {
             record(a.status, VFA_ERR_BAD_BLOCK);
@@ -798,9 +798,13 @@ cudaError_t launch_pages_truncate(const PageArgs &a, int sm_count, cudaStream_t 
 {
     const int n = a.refs_out != a.refs && a.num_blocks > a.num_seqs ? a.num_blocks : a.num_seqs;
     const int ctas = (n + 255) / 256;
+    // a page per thread, as long as that takes no more CTAs than run side by side
+    const int most = (a.capacity + 255) / 256, room = 8 * sm_count / a.num_seqs;
+    const int shares = most < room ? most : (room < 1 ? 1 : room);
     const cudaError_t e = launch_dependent(truncate_plan_kernel, dim3(ctas < 4 * sm_count ? ctas : 4 * sm_count),
                                            256, 0, stream, a);
-    return e != cudaSuccess ? e : launch_dependent(truncate_kernel, dim3(a.num_seqs), 256, 0, stream, a);
+    return e != cudaSuccess ? e : launch_dependent(truncate_kernel, dim3(a.num_seqs, shares), 256, 0, stream,
+                                                   a);
 }
 
 cudaError_t launch_pages_compact(const PageArgs &a, const PagePools &p, int sm_count,

@@ -302,64 +302,59 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(const SchedArgs a)
     const long long nitems = carry * H;
     __syncthreads();
 
-    // Items, one thread per tile writing all its heads.  Sequence b's groups
-    // start at H * seq_first[b], head h's group at + h * units(nt); the
-    // tile's rank in its group (cost descending, then i) is i - i_hi for
-    // capped tiles (equal cost, i ascending), then the rising tiles with i
-    // falling, then the zero-cost tiles with i ascending; it lands in item
-    // rank (single) or rank / 2, slot rank % 2 (pairs).
-    for (int t = tid; t < ntiles; t += kThreads) {
-        int lo = 0, hi = B - 1;                     // largest b with tile_start[b] <= t
+    // Items, one thread each, so that a warp writes whole neighbouring ones (one thread
+    // per tile writing all its heads took 17 us for 352 tiles of 32 heads: its stores
+    // were scattered pieces of items).  Sequence b's groups start at H *
+    // seq_first[b], head h's group at + h * units(nt); item u of a group holds the
+    // tile of rank u (single) or the tiles of ranks 2u and 2u + 1 (pairs).  The rank
+    // of a tile in its group (cost descending, then i) is i - i_hi for capped tiles
+    // (equal cost, i ascending), then the rising tiles with i falling, then the
+    // zero-cost tiles with i ascending; with a window i descending.
+    struct Tile {
+        int i, first, end;                          // key tiles [first, end)
+    };
+    auto tile_of = [&](int b, int rank) {
+        const int nt = seq_nt[b], cap = seq_cap[b], i_lo = seq_ilo[b], i_hi = seq_ihi[b];
+        Tile t;
+        t.i = window                  ? nt - 1 - rank
+              : rank < nt - i_hi      ? i_hi + rank
+              : rank < nt - i_lo      ? i_hi - 1 - (rank - (nt - i_hi))
+                                      : rank - (nt - i_lo);
+        t.end = causal ? min(cap, max(0, (t.i + 1) * static_cast<int>(r) + seq_e[b])) : cap;
+        t.first = 0;
+        if (window) {
+            // key tiles [max(0, i r + g), c(i)) below n1; none from n1 on
+            if (t.i < seq_n1[b] && t.end > 0)
+                t.first = max(0, t.i * static_cast<int>(r) + seq_g[b]);
+            else if (t.i >= seq_n1[b] && a.sink_tokens > 0)
+                t.first = t.end = static_cast<int>(
+                    (static_cast<unsigned>(min(a.sink_tokens, a.cu_k[b + 1] - a.cu_k[b])) + bk - 1) >>
+                    lbk);
+            else
+                t.end = 0;
+        }
+        return t;
+    };
+    for (long long pos = tid; pos < nitems; pos += kThreads) {
+        int lo = 0, hi = nseq - 1;                  // largest rank whose groups start at or below pos
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tile_start[mid] <= t)
+            if (static_cast<long long>(seq_first[ord[mid]]) * H <= pos)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        const int b = lo;
-        const int i = t - tile_start[b];
-        const int nt = seq_nt[b], cap = seq_cap[b], i_lo = seq_ilo[b], i_hi = seq_ihi[b];
-        int c = causal ? min(cap, max(0, (i + 1) * static_cast<int>(r) + seq_e[b])) : cap;
-        int f = 0;                                  // first key tile
-        int rank;
-        if (window) {
-            // key tiles [max(0, i r + g), c(i)) below n1; none from n1 on
-            if (i < seq_n1[b] && c > 0)
-                f = max(0, i * static_cast<int>(r) + seq_g[b]);
-            else if (i >= seq_n1[b] && a.sink_tokens > 0)
-                f = c = static_cast<int>(
-                    (static_cast<unsigned>(min(a.sink_tokens, a.cu_k[b + 1] - a.cu_k[b])) + bk - 1) >>
-                    lbk);
-            else
-                c = 0;
-            rank = nt - 1 - i;
-        } else {
-            rank = i >= i_hi ? i - i_hi
-                   : i >= i_lo ? (nt - i_hi) + (i_hi - 1 - i)
-                               : (nt - i_lo) + i;
+        const int b = ord[lo], nt = seq_nt[b], per_head = units(nt);
+        const int at = static_cast<int>(pos - static_cast<long long>(seq_first[b]) * H);
+        const int h = at / per_head, u = at % per_head, rank = a.pair ? 2 * u : u;
+        const Tile ta = tile_of(b, rank);
+        int4 second = make_int4(-1, 0, ta.first, 0);
+        if (a.pair && rank + 1 < nt) {
+            const Tile tb = tile_of(b, rank + 1);
+            second = make_int4(tb.i, tb.end, ta.first, tb.first);
         }
-        const int slot = a.pair ? (rank & 1) : 0;
-        const int unit = a.pair ? rank >> 1 : rank;
-        const int per_head = units(nt);
-        const bool alone = !a.pair || rank == nt - 1;
-        long long pos = static_cast<long long>(seq_first[b]) * H + unit;
-        for (int h = 0; h < H; ++h, pos += per_head) {
-            // slot a writes its first key tile into the second int4's z, slot b
-            // into w; each slot writes only its own words
-            int *w = reinterpret_cast<int *>(a.items + 2 * pos);
-            if (slot == 0) {
-                a.items[2 * pos] = make_int4(b, i, h, c);
-                if (alone)
-                    a.items[2 * pos + 1] = make_int4(-1, 0, f, 0);
-                else
-                    w[6] = f;
-            } else {
-                w[4] = i;
-                w[5] = c;
-                w[7] = f;
-            }
-        }
+        a.items[2 * pos] = make_int4(b, ta.i, h, ta.end);
+        a.items[2 * pos + 1] = second;
     }
     if (tid == 0) {
         *a.n_items = static_cast<int>(nitems);
