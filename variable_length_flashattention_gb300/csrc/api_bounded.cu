@@ -188,11 +188,11 @@ vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse
         !aligned(cu_seqlens_k, 4) || !aligned(key_weights, 4) || !aligned(key_weights_out, 4))
         return fail(VFA_ERR_INVALID_ARG, "q and k must be 16-byte aligned, the others 4-byte");
     // tensors as the forward takes them, and a unit count of 32 bits
-    const long long tiles = static_cast<long long>(total_k) / 128 + batch;
-    const long long blocks = (static_cast<long long>(max_seqlen_q) + 1023) / 1024;
+    const long long pairs = static_cast<long long>(total_k) / 256 + batch;
+    const long long chunks = static_cast<long long>(max_seqlen_q) / 1024 + 1;
     if (static_cast<long long>(total_q) * num_heads > (1LL << 31) ||
         static_cast<long long>(total_k) * num_heads > (1LL << 31) || num_kv_heads > kMaxHeads ||
-        static_cast<double>(tiles) * static_cast<double>(blocks) * num_heads > double(1LL << 30))
+        static_cast<double>(pairs) * static_cast<double>(chunks) * num_heads > double(1LL << 30))
         return fail(VFA_ERR_UNSUPPORTED, "tensor too large");
     vfa_status st = check_workspace(
         workspace, workspace_bytes,
@@ -203,7 +203,8 @@ vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse
     if ((st = vfa::device_sm_count(&sms)))
         return st;
     vfa::KeyWeightArgs a = {};
-    if ((st = vfa::encode_tile_map(&a.tm_q, q, total_q, num_heads, head_dim, 128)) ||
+    if ((st = vfa::encode_tile_map(&a.tm_q, q, total_q, num_heads, head_dim,
+                                   vfa::key_weights_rows(head_dim))) ||
         (st = vfa::encode_tile_map(&a.tm_k, k, total_k, num_kv_heads, head_dim, 128)))
         return st;
     a.cu_q = cu_seqlens_q;

@@ -232,21 +232,19 @@ __device__ __forceinline__ void query_row_span(long long i, long long j_base, in
     *hi = clamp_col(h);
 }
 
-// Columns of a query row that are visible: [lo, hi), and with sinks those below
-// min(hi, sink).
-template <bool SINK>
-__device__ __forceinline__ bool in_span(int c, int lo, int hi, int sink)
+// -lse log2(e); of a row without visible keys (lse = -FLT_MAX), whose scores are all hidden, 0
+__device__ __forceinline__ float neg_lse(float lse)
 {
-    return c < hi && (c >= lo || (SINK && c < sink));
+    return lse == -FLT_MAX ? 0.f : -lse * kLog2e;
 }
 
 // P^T and dS^T of this thread's key row over its NC query columns: p =
-// 2^(s scale_log2 + nl) (0 outside the visible columns [lo, hi) when MASK)
+// 2^(s scale_log2 + nl)
 // and ds = p (dp + nd), with nl = -lse log2(e) and nd = -Delta of each column
 // read from shared memory (NC floats each at wstat, wstat + 128).
-template <bool MASK, int NC>
+template <int NC>
 __device__ __forceinline__ void key_row_grads(const uint32_t (&sr)[NC], const uint32_t (&dr)[NC],
-                                              float scale_log2, uint32_t wstat, int lo, int hi,
+                                              float scale_log2, uint32_t wstat,
                                               uint32_t (&pk)[NC / 2], uint32_t (&dk2)[NC / 2])
 {
     const float2 c2 = make_float2(scale_log2, scale_log2);
@@ -262,11 +260,7 @@ __device__ __forceinline__ void key_row_grads(const uint32_t (&sr)[NC], const ui
                                                     __uint_as_float(sr[e + u + 1])),
                                         c2, make_float2(__uint_as_float(nla),
                                                         __uint_as_float(nlb)));
-            float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
-            if (MASK) {
-                p0 = (e + u >= lo && e + u < hi) ? p0 : 0.f;
-                p1 = (e + u + 1 >= lo && e + u + 1 < hi) ? p1 : 0.f;
-            }
+            const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
             const float2 g = __fadd2_rn(make_float2(__uint_as_float(dr[e + u]),
                                                     __uint_as_float(dr[e + u + 1])),
                                         make_float2(__uint_as_float(nda), __uint_as_float(ndb)));
@@ -278,12 +272,12 @@ __device__ __forceinline__ void key_row_grads(const uint32_t (&sr)[NC], const ui
 }
 
 // dS of this thread's query row over its NC key columns: p = 2^(s
-// scale_log2 + nl) (0 outside the row's span when MASK), ds = p (dp + nd) with the
+// scale_log2 + nl), ds = p (dp + nd) with the
 // row's nl = -lse log2(e) and nd = -Delta.
-template <bool MASK, bool SINK, int NC>
+template <int NC>
 __device__ __forceinline__ void query_row_grads(const uint32_t (&sr)[NC], const uint32_t (&dr)[NC],
-                                                float scale_log2, float nl, float nd, int lo,
-                                                int hi, int sink, uint32_t (&dk2)[NC / 2])
+                                                float scale_log2, float nl, float nd,
+                                                uint32_t (&dk2)[NC / 2])
 {
     const float2 c2 = make_float2(scale_log2, scale_log2);
     const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
@@ -291,11 +285,7 @@ __device__ __forceinline__ void query_row_grads(const uint32_t (&sr)[NC], const 
     for (int e = 0; e < NC; e += 2) {
         const float2 t = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])),
                                     c2, nl2);
-        float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
-        if (MASK) {
-            p0 = in_span<SINK>(e, lo, hi, sink) ? p0 : 0.f;
-            p1 = in_span<SINK>(e + 1, lo, hi, sink) ? p1 : 0.f;
-        }
+        const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
         const float2 g = __fadd2_rn(make_float2(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])),
                                     nd2);
         const float2 ds = __fmul2_rn(make_float2(p0, p1), g);
@@ -835,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
             float nl_row = 0.f, nd_row = 0.f;
             if (DQ && own_valid) {
                 const size_t srow = static_cast<size_t>(w.q0 + own) * H + w.head;
-                nl_row = -a.lse[srow] * kLog2e;
+                nl_row = neg_lse(a.lse[srow]);
                 nd_row = -a.delta[srow];
             }
             const int group = H / Hkv;
@@ -855,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                     for (int c = 0; c < NCH; ++c) {
                         const int i = c0 + 32 * c + lane;
                         const size_t srow = static_cast<size_t>(w.q0 + i) * H + hq;
-                        stat[64 * c + lane] = i < w.lq ? -a.lse[srow] * kLog2e : 0.f;
+                        stat[64 * c + lane] = i < w.lq ? neg_lse(a.lse[srow]) : 0.f;
                         stat[64 * c + 32 + lane] = i < w.lq ? -a.delta[srow] : 0.f;
                     }
                     __syncwarp();
@@ -888,29 +878,27 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
                     uint32_t dk2[16];
                     const int cb = c0 + 32 * c;            // the chunk's first streamed column
                     if (DQ) {
-                        if (full) {
-                            query_row_grads<false, SINK, 32>(sr, dr, scale_log2, nl_row, nd_row,
-                                                             0, 32, 0, dk2);
-                        } else {
+                        if (!full) {
                             int lo, hi;
                             query_row_span(own, cb, w.lk, w.lq, a.causal, wl, off, &lo, &hi);
-                            if (SINK && own >= w.lq)
+                            if (own >= w.lq)
                                 hi = -1;                   // no row: no sinks either
-                            query_row_grads<true, SINK, 32>(sr, dr, scale_log2, nl_row, nd_row,
-                                                            lo, hi, SINK ? a.sink_tokens - cb : 0,
-                                                            dk2);
+                            uint32_t from = ~below(lo);
+                            if (SINK)
+                                from |= below(a.sink_tokens - cb);
+                            hide(sr, below(hi) & from);
                         }
+                        query_row_grads(sr, dr, scale_log2, nl_row, nd_row, dk2);
                     } else {
                         uint32_t pk[16];
                         const uint32_t cstat = wstat + 256 * c;
-                        if (full) {
-                            key_row_grads<false, 32>(sr, dr, scale_log2, cstat, 0, 32, pk, dk2);
-                        } else {
+                        if (!full) {
                             int lo, hi;
                             key_row_span(own, cb, w.lk, w.lq, a.causal,
                                          SINK && own < a.sink_tokens ? -1 : wl, off, &lo, &hi);
-                            key_row_grads<true, 32>(sr, dr, scale_log2, cstat, lo, hi, pk, dk2);
+                            hide(sr, below(hi) & ~below(lo));
                         }
+                        key_row_grads(sr, dr, scale_log2, cstat, pk, dk2);
                         // P^T (bf16 pairs) over the first half of the chunk's S^T columns
                         st_cols<16>(st_addr, pk);
                     }

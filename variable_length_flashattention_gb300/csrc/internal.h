@@ -286,20 +286,24 @@ cudaError_t launch_kv4_decode(int head_dim, Kv4DecodeArgs &a, void *workspace, i
 // ------------------------------------------------------------ key weights
 
 struct KeyWeightArgs {
-    CUtensorMap tm_q, tm_k;                 // boxes of 64 columns x 1 head x 128 rows, 128-byte swizzle
+    CUtensorMap tm_q, tm_k;                 // boxes of 64 columns x 1 head x key_weights_rows() or 128
+                                            // rows, 128-byte swizzle
     const int32_t *cu_q, *cu_k;
     const float *lse;                       // f32 [total_q, num_heads], natural log
     const float *weights;                   // [batch, num_kv_heads, weight_stride]
     float *weights_out;                     // may be weights
     long long weight_stride;
     int32_t *status;                        // workspace: status word, unit counter
-    int32_t *tile_start, *unit_start;       // workspace: [batch + 1] first 128-key tile, first unit
-    float *part;                            // workspace: [2 * chunks, num_heads, total_k]
+    int32_t *pair_start, *unit_start;       // workspace: [batch + 1] first pair of key tiles, first unit
+    float *part;                            // workspace: [chunks, num_kv_heads, total_k]
     int batch, total_q, total_k, max_seqlen_q, num_heads, num_kv_heads;
-    int chunk_steps;                        // set by the launcher: query blocks of a unit
+    int chunk_steps, step;                  // set by the launcher: steps of a unit, queries of a step
     float scale_log2;
     int causal, window_left, sink_tokens;
 };
+
+// Queries of a step: the rows of a box of tm_q.
+__host__ __device__ constexpr int key_weights_rows(int head_dim) { return head_dim == 256 ? 64 : 128; }
 
 size_t key_weights_workspace_bytes(int batch, int total_k, int max_seqlen_q, int num_heads);
 cudaError_t launch_key_weights(int head_dim, KeyWeightArgs &a, void *workspace, int sm_count,

@@ -28,10 +28,17 @@
 //     is published on its own and O_x += P_x V runs per half, so the tensor
 //     core starts on the first 64 keys while the second half is still being
 //     exponentiated;
-//   * in a masked tile (causal diagonal, ragged key tail) a 32-column chunk
-//     that is valid for all 32 rows of a warp skips the mask, and one that
-//     is masked for all of them skips its exponentials;
-//   * O / l leaves through a 2 KB shared-memory stage per warp (no cross-warp
+//   * in a masked tile (causal diagonal, ragged key tail, a window's edge, the
+//     last sinks) the chunks of 32 columns in which a row of the warp has a
+//     hidden one are masked in registers, and the tile goes on like any other.
+//     A masked tile is one or two of a short item's tiles, and code of its own
+//     for all of it is fetched anew each time (a warp waited for instructions
+//     15% of its time): with the mask alone apart, 16 sequences of up to 2048
+//     tokens take 834 TFLOP/s instead of 714, 4 of 8192 with a window of 1024
+//     and sinks 632 us instead of 864.  Long unmasked items at head_dim 64 (4
+//     of 8192, causal: 1468 us against 1548) keep a masked tile of its own,
+//     where a chunk that is masked for all rows skips its exponentials;
+//   * O / l leaves through two 2 KB shared-memory stages per warp (no cross-warp
 //     handshake): a warp whose 32 rows all lie in the sequence hands each
 //     32-column chunk to a TMA tile store; in a sequence's last tile, plain
 //     stores write eight whole 64-byte row segments per instruction;
@@ -76,7 +83,8 @@ struct PairCfg {
     static constexpr uint32_t Q_BYTES = BQ * D * QK_ELEM;
     static constexpr uint32_t K_BYTES = BK * D * QK_ELEM;
     static constexpr uint32_t KV_BYTES = BK * D * 2;      // one V stage
-    static constexpr uint32_t WARP_STAGE = 32 * 64;       // one warp's 32 rows x 32 output columns
+    static constexpr uint32_t STAGE = 32 * 64;            // 32 rows x 32 output columns
+    static constexpr uint32_t WARP_STAGE = 2 * STAGE;     // a warp's two, taken in turn
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 2 * D;              // S_x at S_COL + x * BK; O_x at x * D
     static constexpr int NUM_BARS = 4 + 4 * NS + 15;
@@ -102,23 +110,16 @@ constexpr int kItemConsumers = 10;  // MMA + V loader + one arrival per softmax 
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale when the max grows by > 2^8
 
 // Masks one 32-column chunk of scores (columns cb..cb+31 of the key tile):
-// a row's visible columns are [lo, lim), and scores outside become -inf, so
-// they drop out of the max and 2^(-inf) = 0 (the scale is > 0, so no
-// -inf * 0).  lim_lo / lo_hi are the warp's smallest lim and largest lo: a
-// chunk inside [lo_hi, lim_lo) needs no mask.  WIN 1: a sliding window's edge
-// can cut into the tile (otherwise lo = 0).  WIN 2: columns below `sink` are
-// visible whatever lo is.
-template <int WIN>
-__device__ __forceinline__ void mask_chunk(uint32_t (&sr)[32], int cb, int lim, int lim_lo, int lo,
-                                           int lo_hi, int sink)
+// scores at a row's first hidden column lim and past it become -inf, so they
+// drop out of the max and 2^(-inf) = 0 (the scale is > 0, so no -inf * 0).  lim_lo
+// is the warp's smallest lim: a chunk below it needs no mask.
+__device__ __forceinline__ void mask_chunk(uint32_t (&sr)[32], int cb, int lim, int lim_lo)
 {
-    if (cb + 32 <= lim_lo && (!WIN || cb >= lo_hi || (WIN == 2 && cb + 32 <= sink)))
+    if (cb + 32 <= lim_lo)
         return;
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-        sr[e] = (cb + e < lim && (!WIN || cb + e >= lo || (WIN == 2 && cb + e < sink)))
-                    ? sr[e]
-                    : __float_as_uint(-INFINITY);
+        sr[e] = cb + e < lim ? sr[e] : __float_as_uint(-INFINITY);
 }
 
 // O rows *= f for this warp's 32 lanes, 16 columns at a time (rare path).
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sQ = base;                           // Q_a, Q_b
     const uint32_t sK = sQ + 2 * C::Q_BYTES;
     const uint32_t sV = sK + NS * C::K_BYTES;
-    const uint32_t sO = sV + NS * C::KV_BYTES;          // output staging, 2 KB per softmax warp
+    const uint32_t sO = sV + NS * C::KV_BYTES;          // output staging, 4 KB per softmax warp
     const uint32_t bars = sO + 8 * C::WARP_STAGE;
     auto q_full = [&](int x) { return bars + 8u * x; };
     auto q_empty = [&](int x) { return bars + 8u * (2 + x); };
@@ -605,12 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int H = p.num_heads;
         uint32_t g = 0;                               // this slot's tiles so far
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-        // Masked tiles mask the keys past a row's last visible one and, in the
-        // sliding-window instantiations, those below the window's edge too (one
-        // masked variant per instantiation keeps the register allocation of
-        // the plain kernel).
+        // A tile masked in place where it needs it, or (head_dim 64 without a window)
+        // a plain and a masked form of it.
+        constexpr bool IN_PLACE = D == 128 || WIN > 0;
         using Plain = std::integral_constant<int, 0>;
-        using Masked = std::integral_constant<int, WIN + 1>;
+        using Masked = std::integral_constant<int, 1>;
+        using InPlace = std::integral_constant<int, -1>;
 
         for (uint32_t n = 0;; ++n) {
             int4 it, itb, seq;
@@ -673,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need_mask = need_hi || need_lo;
                 const int lim =
                     need_mask ? (p.causal ? min(lk, max(0, q_local + off + 1)) : lk) - k_base : BK;
-                const int lim_lo = need_mask ? __reduce_min_sync(0xffffffffu, lim) : BK;
-                const int lim_hi = need_mask ? __reduce_max_sync(0xffffffffu, lim) : BK;
+                const int lim_lo = !IN_PLACE && need_mask ? __reduce_min_sync(0xffffffffu, lim) : BK;
+                const int lim_hi = !IN_PLACE && need_mask ? __reduce_max_sync(0xffffffffu, lim) : BK;
 
                 // The whole key tile's 128 scores of this row are loaded with one
                 // wait.  The row max comes from the registers first; the reference
@@ -686,19 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // being exponentiated.
                 auto tile = [&](auto masked) -> bool {
                     constexpr int MK = decltype(masked)::value;
-                    // banded tiles: this row's visible columns start at lo
-                    int lo = 0, lo_lo = 0, lo_hi = 0, sink = 0;
-                    if (MK == 3)
-                        sink = min(BK, max(0, p.sink_tokens - k_base));
-                    if (MK >= 2) {
-                        const int off = p.causal == 2 ? lk - lq : 0;
-                        lo = static_cast<int>(
-                            min(static_cast<long long>(BK),
-                                max(0ll, static_cast<long long>(q_local) + off - p.window_left -
-                                             k_base)));
-                        lo_lo = __reduce_min_sync(0xffffffffu, lo);
-                        lo_hi = __reduce_max_sync(0xffffffffu, lo);
-                    }
                     uint32_t sc[4][32];
                     tmem_ld32(s_addr, sc[0]);
                     tmem_ld32(s_addr + 32, sc[1]);
@@ -712,15 +700,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool empty[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        empty[c] = MK > 0 && (32 * c >= lim_hi ||
-                                              (MK >= 2 && 32 * c + 32 <= lo_lo && 32 * c >= sink));
+                        empty[c] = MK > 0 && 32 * c >= lim_hi;
+                    if (MK < 0 && need_mask) {
+                        // the row's visible columns: [from, lim), and those below sinks
+                        const int from = WIN ? static_cast<int>(min(
+                                                   static_cast<long long>(BK),
+                                                   max(0ll, static_cast<long long>(q_local) + off -
+                                                                p.window_left - k_base)))
+                                             : 0;
+                        const int sinks = WIN == 2 ? min(BK, max(0, p.sink_tokens - k_base)) : 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            auto below = [&](int x) {
+                                const int n = min(32, max(0, x - 32 * c));
+                                return n == 32 ? 0xffffffffu : (1u << n) - 1u;
+                            };
+                            uint32_t see = below(lim);       // one bit a column
+                            if (WIN)
+                                see &= ~below(from) | (WIN == 2 ? below(sinks) : 0u);
+                            if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    sc[c][e] = see >> e & 1u ? sc[c][e] : __float_as_uint(-INFINITY);
+                            }
+                        }
+                    }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         if (empty[c])
                             continue;
                         if (MK > 0)
-                            mask_chunk<(MK > 0 ? MK - 1 : 0)>(sc[c], 32 * c, lim, lim_lo, lo, lo_hi, sink);
+                            mask_chunk(sc[c], 32 * c, lim, lim_lo);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(sc[c][2 * e]),
@@ -780,7 +791,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += l2.x + l2.y;
                     return true;
                 };
-                ok = need_mask ? tile(Masked{}) : tile(Plain{});
+                if constexpr (IN_PLACE)
+                    ok = tile(InPlace{});
+                else
+                    ok = need_mask ? tile(Masked{}) : tile(Plain{});
                 ++g;
             }
             if (!ok)
@@ -808,11 +822,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t rr[32];
                 tmem_ld32(o_addr + cb * 32, rr);
                 tmem_wait_ld_r(rr);
-                // the stage's previous tile store has read it
+                // the stage's previous tile store, the one before the last, has read it
                 if (lane == 0)
-                    bulk_wait_group_read0();
+                    bulk_wait_group_read1();
                 __syncwarp();
-                const uint32_t row = wstage + lane * 64;
+                const uint32_t stage = wstage + (cb & 1) * C::STAGE;
+                const uint32_t row = stage + lane * 64;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     st_shared_v4(row + ((c ^ ((lane >> 1) & 3)) << 4),
@@ -828,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&p.tm_o, wstage, cb * 32, h, q0 + i * BQ + quarter * 32);
+                        tma_store_3d(&p.tm_o, stage, cb * 32, h, q0 + i * BQ + quarter * 32);
                         bulk_commit_group();
                     }
                 } else {
@@ -838,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int rw = 8 * k + (lane >> 2), ch = lane & 3;
                         const int rt = quarter * 32 + rw;          // row within the tile
                         const uint4 v =
-                            ld_shared_v4(wstage + rw * 64 + ((ch ^ ((rw >> 1) & 3)) << 4));
+                            ld_shared_v4(stage + rw * 64 + ((ch ^ ((rw >> 1) & 3)) << 4));
                         if (rt < tile_rows)
                             *reinterpret_cast<uint4 *>(out_tile + static_cast<long long>(rt) * H * D +
                                                        cb * 32 + ch * 8) = v;

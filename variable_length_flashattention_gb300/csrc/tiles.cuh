@@ -88,6 +88,25 @@ __device__ __forceinline__ void key_row_span(long long j, long long i_base, int 
     *hi = clamp_col(h);
 }
 
+// The columns below x, one bit each.
+__device__ __forceinline__ uint32_t below(int x)
+{
+    const int n = min(32, max(0, x));
+    return n == 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Scores of hidden columns (bits of `see` that are 0) become -inf: their p is 0.  Where a
+// warp sees all of a chunk nothing is done; the rest of a step is the same code
+// for masked and unmasked ones, which a short range of steps would fetch anew.
+__device__ __forceinline__ void hide(uint32_t (&sr)[32], uint32_t see)
+{
+    if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            sr[e] = see >> e & 1u ? sr[e] : __float_as_uint(-INFINITY);
+    }
+}
+
 // Loads a tile of `rows` rows (a multiple of the map's box height BOX) of
 // every 64-column block of row `row0`, head `head` into a 128-byte-swizzled
 // buffer holding `rows` rows per column block.
