@@ -258,7 +258,7 @@ vfa_status vfa_cache_evict(void *k_pool, void *v_pool, const int32_t *refcounts,
         !aligned(positions, 4) || !aligned(history, 4) || !aligned(key_weights_out, 4) ||
         !aligned(positions_out, 4) || !aligned(history_out, 4) || !aligned(kept, 4))
         return fail(VFA_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
-    if (static_cast<long long>(num_seqs) * num_kv_heads > INT_MAX)
+    if (static_cast<long long>(num_seqs) * num_kv_heads > (1 << 27))      // clusters of up to 8 CTAs
         return fail(VFA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads too large");
     if ((st = check_workspace(workspace, workspace_bytes,
                               vfa::evict_workspace_bytes(num_seqs, num_kv_heads, capacity))))

@@ -214,6 +214,50 @@ __global__ void bwd_delta_kernel(const BwdArgs a)
     }
 }
 
+// The same for the instantiations with sinks: D / 8 lanes per row with 16-byte loads, two
+// rows of a lane in flight (49879 tokens of 16 heads of 64: %DELTA% us, 59 with a warp per
+// row; the order of a sum, and with it the last bits, differs from the other's).
+template <int D>
+__global__ void __launch_bounds__(256) bwd_delta_wide_kernel(const BwdArgs a)
+{
+    if (*a.status != VFA_OK)
+        return;
+    constexpr int LANES = D / 8, TURNS = 2;
+    const long long rows = static_cast<long long>(a.total_q) * a.num_heads;
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.x / LANES;
+    const int l = threadIdx.x % LANES;
+    const uint4 *o = static_cast<const uint4 *>(a.out), *g = static_cast<const uint4 *>(a.dout);
+    // whole warps go round together: the last turns' lanes past the end take part in the sums
+    const long long first = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / LANES;
+    const long long warp_first = (static_cast<long long>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31)) / LANES;
+    for (long long r = first, w = warp_first; w < rows; r += step * TURNS, w += step * TURNS) {
+        uint4 x[TURNS], y[TURNS];
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) {
+            const long long row = r + t * step;
+            x[t] = y[t] = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+                x[t] = __ldcs(o + row * LANES + l);
+                y[t] = __ldg(g + row * LANES + l);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) {
+            const uint32_t xs[4] = {x[t].x, x[t].y, x[t].z, x[t].w}, ys[4] = {y[t].x, y[t].y, y[t].z, y[t].w};
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s += __uint_as_float(xs[e] << 16) * __uint_as_float(ys[e] << 16) +
+                     __uint_as_float(xs[e] & 0xffff0000u) * __uint_as_float(ys[e] & 0xffff0000u);
+#pragma unroll
+            for (int k = LANES / 2; k > 0; k >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, k);
+            if (l == 0 && r + t * step < rows)
+                a.delta[r + t * step] = s;
+        }
+    }
+}
+
 // ------------------------------------------------------------ shared pieces
 
 // Query i's visible keys among j_base, j_base + 1, ... (the dQ kernel's
@@ -1026,7 +1070,10 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
         <<<1, kPrepThreads, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    bwd_delta_kernel<D><<<sm_count * 8, 256, 0, s>>>(a);
+    if (SINK)
+        bwd_delta_wide_kernel<D><<<sm_count * 8, 256, 0, s>>>(a);
+    else
+        bwd_delta_kernel<D><<<sm_count * 8, 256, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     // persistent grids: one CTA per SM (fewer when there are fewer units)

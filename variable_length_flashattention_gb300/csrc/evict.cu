@@ -10,29 +10,40 @@
 // history[s][1].
 //
 // Two kernels:
-//   select   one CTA per (sequence, kv head).  The border weight is found by its
-//            bits, 11, 11 and 10 at a time from the top, by counting the weights
-//            that share the bits so far (weights map to unsigned integers of the
-//            same order).  Then every warp takes a run of slots: ballots give the
-//            ranks of ties, free slots and movers, sums over the warps their
-//            starts.  Weights and positions are rewritten here;
+//   select   a cluster of up to 8 CTAs per (sequence, kv head), each with a run of the
+//            slots.  Every slot has a key, an unsigned integer in the order of the
+//            weights, the largest for tokens that stay whatever their weight: the
+//            b largest keys stay, ties by the lowest slot.  The border key is
+//            found by its bits, 11, 11 and 10 at a time from the top, by counting
+//            the keys that share the bits so far; the counts of a cluster's CTAs are
+//            added up in the first one's shared memory.  Then every warp takes a run
+//            of slots: ballots give the ranks of ties, free slots and movers, sums over
+//            warps and CTAs their starts.  Weights and positions are rewritten here.
+//            One CTA per row took 41 us for 64 sequences of 1056 tokens on 8 kv
+//            heads and 57 for 8 of 4000-32768, a cluster %SEL1% and %SEL2%;
 //   move     the rows of K and V by the lists, 16 bytes per thread, and the
 //            sequences' new state.
 // Bound: HBM, 8 D bytes per moved token and kv head, and 12 to 16 bytes per token for weights
-// and positions.
+// and positions; for small rows the chain of the select kernel's counts.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "internal.h"
 #include "launch.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace vfa {
 
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMostCtas = 8;            // of a cluster
+constexpr int kSmemKeys = 4096;         // keys a CTA keeps in shared memory
+constexpr uint32_t kStays = 0xffffffffu;    // the key of a token that stays whatever its weight
 constexpr int kMoveThreads = 256;
 
 __device__ __forceinline__ void record(int32_t *status, int code)
@@ -68,46 +79,77 @@ __device__ __forceinline__ Plan plan_of(const EvictArgs &a, int s)
     return p;
 }
 
-// Weights in the order of unsigned integers; any NaN is the largest.
+// Weights in the order of unsigned integers below kStays; any NaN is the largest.
 __device__ __forceinline__ uint32_t order_of(float w)
 {
     const uint32_t u = __float_as_uint(w + 0.f);          // -0 is 0
     if (w != w)
-        return 0xffffffffu;
+        return kStays - 1;
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sum over the CTA's warps of one value per warp (its lane 0's).
-__device__ __forceinline__ int warp_start(int v, int *s_warp, int *total)
+// What the CTAs of a cluster tell each other: their sums of three values.
+struct Shared {
+    int bins[kBins];
+    int warp[3][kSelWarps];
+    int sums[3][kMostCtas];             // of every CTA, by rank
+    int digit, left;
+};
+
+// Sums ahead of this warp, in the order of ranks and warps, of N values per warp (its lane
+// 0's); total[i] gets the cluster's.  Everybody calls it.
+template <int N>
+__device__ __forceinline__ void warp_starts(cg::cluster_group &cluster, Shared &sh, const int (&v)[N],
+                                            int (&start)[N], int (&total)[N])
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     __syncthreads();
     if (lane == 0)
-        s_warp[warp] = v;
-    __syncthreads();
-    int x = s_warp[lane], y = x;                           // 32 warps
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o)
-            y += z;
+        for (int i = 0; i < N; ++i)
+            sh.warp[i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        start[i] = total[i] = 0;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) {
+            start[i] += w < warp ? sh.warp[i][w] : 0;
+            total[i] += sh.warp[i][w];
+        }
     }
-    *total = __shfl_sync(0xffffffffu, y, 31);
-    return __shfl_sync(0xffffffffu, y - x, warp);
+    if (ctas == 1)
+        return;
+    if (threadIdx.x < ctas)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            cluster.map_shared_rank(&sh, threadIdx.x)->sums[i][rank] = total[i];
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        total[i] = 0;
+        for (int c = 0; c < ctas; ++c) {
+            start[i] += c < rank ? sh.sums[i][c] : 0;
+            total[i] += sh.sums[i][c];
+        }
+    }
+    cluster.sync();                     // the sums are read: they may be written again
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a)
 {
-    static_assert(kSelWarps == 32, "one lane per warp in warp_start");
     grid_wait();
     grid_release();
-    __shared__ int s_bins[kBins];
-    __shared__ int s_warp[kSelWarps];
-    __shared__ int s_digit, s_left;
-    const int row = blockIdx.x, s = row / a.num_kv_heads;
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ Shared sh;
+    extern __shared__ uint32_t s_keys[];
+    const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+    const int row = blockIdx.x / ctas, s = row / a.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Plan p = plan_of(a, s);
-    // pages that are none, or that a move would write although another row has them
+    // pages that are none, or that a move would write although another row has them: every
+    // CTA of the row looks at all of them and comes to the same verdict
     bool bad = p.bad;
     if (!bad) {
         const int pages = (p.n + kPage - 1) / kPage, written = p.b < p.n ? (p.b + kPage - 1) / kPage : 0;
@@ -117,7 +159,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         }
     }
     if (__syncthreads_or(bad)) {
-        if (tid == 0) {
+        if (tid == 0 && rank == 0) {
             a.moves[row] = -1;
             record(a.status, VFA_ERR_BAD_BLOCK);
         }
@@ -131,94 +173,126 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     uint32_t *bits = a.bits + static_cast<long long>(row) * ((a.capacity + 1) / 2);
     int32_t *to = a.lists + at, *from = to + static_cast<long long>(a.capacity) * (kPage / 2);
     auto position = [&](int j) { return p.position(j, j < p.known ? pos[j] : 0); };
+    // This CTA's slots, whole words of 32.
+    const int words = (p.n + 31) / 32, share = (words + ctas - 1) / ctas;
+    const int c0 = min(words, rank * share), c1 = min(words, c0 + share);
+    const int j0 = c0 * 32, j1 = min(p.n, c1 * 32);
 
     int moves = 0;
     if (p.b < p.n) {
-        // Tokens that stay whatever their weight, and how many others do.
-        int safe = 0;
-        for (int j = tid; j < p.n; j += kSelThreads)
-            safe += p.safe(position(j));
-        int total;
-        warp_start(__reduce_add_sync(0xffffffffu, safe), s_warp, &total);
-        // More than may stay (stored positions that are not one per token): the lowest
-        // slots of them do.
-        const bool crowd = total > p.b;
-        int left = crowd ? p.b : p.b - total;
-        // The border: the left-th largest weight of the others, and how many of that
-        // weight stay.
+        // Keys: in shared memory, or (long runs) where the lists will be.
+        uint32_t *keys = c1 - c0 <= kSmemKeys / 32 ? s_keys - j0 : reinterpret_cast<uint32_t *>(to);
+        for (int j = j0 + tid; j < j1; j += kSelThreads)
+            keys[j] = p.safe(position(j)) ? kStays : order_of(w[j]);
+        // The border: the b-th largest key, and how many of those that equal it stay.
         uint32_t border = 0, known_bits = 0;
-        if (left > 0 && !crowd) {
+        int left = p.b;
+        if (left > 0) {
             for (int turn = 0; turn < 3; ++turn) {
                 const int shift = turn == 0 ? 21 : (turn == 1 ? 10 : 0);
                 const uint32_t mask = turn == 2 ? 1023u : 2047u;
-                __syncthreads();
                 for (int i = tid; i < kBins; i += kSelThreads)
-                    s_bins[i] = 0;
-                __syncthreads();
-                for (int j = tid; j < p.n; j += kSelThreads) {
-                    const uint32_t k = order_of(w[j]);
-                    if ((k & known_bits) == border && !p.safe(position(j)))
-                        atomicAdd(&s_bins[k >> shift & mask], 1);
+                    sh.bins[i] = 0;
+                if (ctas > 1)
+                    cluster.sync();                 // the first CTA's bins are clear
+                else
+                    __syncthreads();
+                for (int j = j0 + tid; j < j1; j += kSelThreads) {
+                    const uint32_t k = keys[j];
+                    if ((k & known_bits) == border)
+                        atomicAdd(&sh.bins[k >> shift & mask], 1);
                 }
-                __syncthreads();
-                // thread t holds the two bins 2047 - 2t, 2046 - 2t: a scan from the top
-                const int hi = s_bins[kBins - 1 - 2 * tid], lo = s_bins[kBins - 2 - 2 * tid];
-                int x = hi + lo;
+                if (ctas > 1) {
+                    __syncthreads();
+                    if (rank > 0) {
+                        Shared *first = cluster.map_shared_rank(&sh, 0);
+                        for (int i = tid; i < kBins; i += kSelThreads)
+                            if (sh.bins[i])
+                                atomicAdd(&first->bins[i], sh.bins[i]);
+                    }
+                    cluster.sync();
+                } else {
+                    __syncthreads();
+                }
+                if (rank == 0) {
+                    // thread t holds the eight bins from 2047 - 8t down: a scan from the top
+                    constexpr int PER = kBins / kSelThreads;
+                    int mine[PER], x = 0;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o)
-                        x += y;
+                    for (int i = 0; i < PER; ++i) {
+                        mine[i] = sh.bins[kBins - 1 - PER * tid - i];
+                        x += mine[i];
+                    }
+                    const int sum = x;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, x, o);
+                        if (lane >= o)
+                            x += y;
+                    }
+                    if (lane == 31)
+                        sh.warp[0][warp] = x;
+                    __syncthreads();
+                    int before = x - sum;
+#pragma unroll
+                    for (int i = 0; i < kSelWarps; ++i)
+                        before += i < warp ? sh.warp[0][i] : 0;
+                    if (before < left && left <= before + sum) {
+                        int digit = kBins - 1 - PER * tid;
+#pragma unroll
+                        for (int i = 0; i < PER - 1; ++i)
+                            if (left > before + mine[i]) {
+                                before += mine[i];
+                                --digit;
+                            } else {
+                                break;
+                            }
+                        for (int c = 0; c < ctas; ++c) {
+                            Shared *other = cluster.map_shared_rank(&sh, c);
+                            other->digit = digit;
+                            other->left = left - before;
+                        }
+                    }
                 }
-                int all;
-                const int before = warp_start(__shfl_sync(0xffffffffu, x, 31), s_warp, &all) + x - hi - lo;
-                if (before < left && left <= before + hi) {
-                    s_digit = kBins - 1 - 2 * tid;
-                    s_left = left - before;
-                } else if (before + hi < left && left <= before + hi + lo) {
-                    s_digit = kBins - 2 - 2 * tid;
-                    s_left = left - before - hi;
-                }
-                __syncthreads();
-                border |= static_cast<uint32_t>(s_digit) << shift;
+                if (ctas > 1)
+                    cluster.sync();
+                else
+                    __syncthreads();
+                border |= static_cast<uint32_t>(sh.digit) << shift;
                 known_bits |= mask << shift;
-                left = s_left;
+                left = sh.left;
             }
         }
-        const bool any = left > 0 && !crowd;    // a border exists
-        // Warps take runs of slots, whole words of 32.
-        const int words = (p.n + 31) / 32, per = (words + kSelWarps - 1) / kSelWarps;
-        const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
-        int ties = 0;
+        // Warps take runs of the CTA's words.
+        const int per = (c1 - c0 + kSelWarps - 1) / kSelWarps;
+        const int w0 = min(c1, c0 + warp * per), w1 = min(c1, w0 + per);
+        const bool any = p.b > 0;
+        int ties[1] = {0}, rank_of[1], all[1];
         for (int i = w0; i < w1; ++i) {
             const int j = i * 32 + lane;
-            const bool tie = j < p.n && (crowd ? p.safe(position(j))
-                                               : any && order_of(w[j]) == border && !p.safe(position(j)));
-            ties += __popc(__ballot_sync(0xffffffffu, tie));
+            ties[0] += __popc(__ballot_sync(0xffffffffu, any && j < j1 && keys[j] == border));
         }
-        int rank = warp_start(ties, s_warp, &total);
-        int holes = 0, movers = 0;
+        warp_starts<1>(cluster, sh, ties, rank_of, all);
+        int counts[2] = {0, 0}, start[2], total[2];         // free slots, movers
         for (int i = w0; i < w1; ++i) {
             const int j = i * 32 + lane;
-            bool keep = false, tie = false;
-            if (j < p.n) {
-                const uint32_t k = order_of(w[j]);
-                const bool safe_one = p.safe(position(j));
-                keep = !crowd && (safe_one || (any && k > border));
-                tie = crowd ? safe_one : any && !keep && k == border;
-            }
+            const uint32_t k = j < j1 ? keys[j] : 0u;
+            const bool tie = any && j < j1 && k == border;
             const uint32_t t = __ballot_sync(0xffffffffu, tie);
-            keep |= tie && rank + __popc(t & ((1u << lane) - 1)) < left;
-            rank += __popc(t);
+            const bool keep = (any && j < j1 && k > border) ||
+                              (tie && rank_of[0] + __popc(t & ((1u << lane) - 1)) < left);
+            rank_of[0] += __popc(t);
             const uint32_t word = __ballot_sync(0xffffffffu, keep);
             if (lane == 0)
                 bits[i] = word;
             const uint32_t low = __ballot_sync(0xffffffffu, j < p.b);
-            holes += __popc(~word & low);
-            movers += __popc(word & ~low);
+            counts[0] += __popc(~word & low);
+            counts[1] += __popc(word & ~low);
         }
-        const int hole0 = warp_start(holes, s_warp, &moves), mover0 = warp_start(movers, s_warp, &total);
-        int h = hole0, m = mover0;
+        // (behind this nobody of the cluster reads keys: the lists may be written)
+        warp_starts<2>(cluster, sh, counts, start, total);
+        moves = total[0];
+        int h = start[0], m = start[1];
         for (int i = w0; i < w1; ++i) {
             const int j = i * 32 + lane;
             const uint32_t word = bits[i], low = __ballot_sync(0xffffffffu, j < p.b);
@@ -230,27 +304,35 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
             h += __popc(hb);
             m += __popc(mb);
         }
-        __syncthreads();
+        // the lists are there for every CTA of the cluster
+        __threadfence();
+        if (ctas > 1)
+            cluster.sync();
+        else
+            __syncthreads();
     }
     // Weights and positions: slots that stay, then those that are filled, then
     // (weights) zeros for the tokens to come.
     const bool copy_w = w_out != w, copy_p = pos_out != pos;
-    for (int j = tid; j < p.b; j += kSelThreads) {
+    for (int j = j0 + tid; j < min(p.b, j1); j += kSelThreads) {
         const bool stay = p.b == p.n || (bits[j / 32] >> (j % 32) & 1u);
         if (stay && copy_w)
             w_out[j] = w[j];
         if (stay && (copy_p || j >= p.known))
             pos_out[j] = position(j);
     }
-    for (int i = tid; i < moves; i += kSelThreads) {
-        const int j = to[i], f = from[i];
+    for (int i = rank * kSelThreads + tid; i < moves; i += ctas * kSelThreads) {
+        const int j = __ldcg(to + i), f = __ldcg(from + i);
         w_out[j] = w[f];
         pos_out[j] = position(f);
     }
-    __syncthreads();
-    for (int j = p.b + tid; j < p.n; j += kSelThreads)
+    if (ctas > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    for (int j = max(p.b, j0) + tid; j < j1; j += kSelThreads)
         w_out[j] = 0.f;
-    if (tid == 0)
+    if (tid == 0 && rank == 0)
         a.moves[row] = moves;
 }
 
@@ -308,9 +390,27 @@ template <int D>
 cudaError_t launch_d(const EvictArgs &a, int sm_count, cudaStream_t stream)
 {
     const long long rows = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
-    cudaError_t e = launch_dependent(evict_select_kernel, dim3(static_cast<unsigned>(rows)), kSelThreads, 0,
-                                     stream, a);
-    if (e != cudaSuccess)
+    // CTAs of a row: one for each 2048 slots, up to a cluster's eight
+    const long long slots = static_cast<long long>(a.capacity) * kPage;
+    int ctas = 1;
+    while (ctas < kMostCtas && ctas * 2048LL < slots)
+        ctas *= 2;
+    const long long share = (slots / 32 + ctas) / ctas * 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (share < kSmemKeys ? share : kSmemKeys) * sizeof(uint32_t);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess)
         return e;
     // CTAs for every SM; a row has capacity * 8 moves at most
     constexpr int per = (kMoveThreads / (D / 4) > 0 ? kMoveThreads / (D / 4) : 1) * 4;

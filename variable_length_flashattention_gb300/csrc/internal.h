@@ -295,7 +295,7 @@ struct KeyWeightArgs {
     long long weight_stride;
     int32_t *status;                        // workspace: status word, unit counter
     int32_t *pair_start, *unit_start;       // workspace: [batch + 1] first pair of key tiles, first unit
-    float *part;                            // workspace: [chunks, num_kv_heads, total_k]
+    float *part;                            // workspace: [chunks, 2, num_kv_heads, total_k]
     int batch, total_q, total_k, max_seqlen_q, num_heads, num_kv_heads;
     int chunk_steps, step;                  // set by the launcher: steps of a unit, queries of a step
     float scale_log2;

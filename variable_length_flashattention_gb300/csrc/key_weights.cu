@@ -33,12 +33,12 @@ namespace vfa {
 namespace {
 
 constexpr int kTiles = 2;          // key tiles of a unit
-constexpr int kMathWarps = 8;      // a warpgroup per tile
-constexpr int kFirstMathWarp = 4;
+constexpr int kMathWarps = 16;     // a warpgroup per tile and half of the columns
+constexpr int kStatWarp = 2, kFirstMathWarp = 4;
 constexpr int kThreads = (kFirstMathWarp + kMathWarps) * 32;
-// 384 threads launch with 168 registers each: 128 * 120 + 256 * 192 = 384 * 168
-constexpr int kLoadRegs = 120;
-constexpr int kMathRegs = 192;
+// 640 threads launch with 96 registers each: 128 * 64 + 512 * 104 = 640 * 96
+constexpr int kLoadRegs = 64;
+constexpr int kMathRegs = 104;
 constexpr int kFewUnits = 608;     // four for every SM
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -46,13 +46,14 @@ template <int D>
 struct KwCfg {
     static constexpr int DB = D / 64;
     static constexpr int STEP = key_weights_rows(D);
-    static constexpr int NCH = STEP / 32;
+    static constexpr int NCH = STEP / 32, NH = NCH / 2;     // 32-column chunks; of a warpgroup's half
+    static constexpr int NSTAT = 4;                         // stages of the queries' -lse log2(e)
     static constexpr uint32_t TILE = kOwn * D * 2;          // a tile of K
     static constexpr uint32_t BLOCK = STEP * D * 2;         // a block of Q
     static constexpr int NSTAGE = D == 64 ? 8 : (D == 128 ? 4 : 2);
-    static constexpr int NUM_BARS = 2 * NSTAGE + 4 * kTiles + 4 + 2 + 1;
-    static constexpr uint32_t STAT = STEP * sizeof(float);  // per math warp: -lse log2(e)
-    static constexpr size_t SMEM = 1024 + kTiles * TILE + NSTAGE * BLOCK + kMathWarps * STAT + NUM_BARS * 8;
+    static constexpr int NUM_BARS = 2 * NSTAGE + 4 * kTiles + 4 + 2 + 1 + 2 * NSTAT;
+    static constexpr uint32_t STAT = STEP * sizeof(float);
+    static constexpr size_t SMEM = 1024 + kTiles * TILE + NSTAGE * BLOCK + NSTAT * STAT + NUM_BARS * 8;
     static constexpr uint32_t IDESC = idesc_bf16_f32(kOwn, STEP, false, false);
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(kTiles * 2 * STEP <= 512, "TMEM budget");
@@ -133,23 +134,25 @@ struct KwUnit {
     int valid;                   // 0: no more units
 };
 
-// Sums of this thread's key row over one block's columns: p = 2^(s scale_log2 + nl),
-// nl of every column from shared memory.
+// Sums of this thread's key row over 32 columns: p = 2^(s scale_log2 + nl), nl of every
+// column from shared memory, all of them asked for before the first is used.
 __device__ __forceinline__ void add_weights(const uint32_t (&sr)[32], float scale_log2, uint32_t stat,
                                             float2 (&acc)[4])
 {
+    uint4 nl[4];
     const float2 c2 = make_float2(scale_log2, scale_log2);
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        const uint4 nl = ld_shared_v4(stat + e * 4);
+    for (int e = 0; e < 32; e += 2) {
+        if (e % 16 == 0) {
 #pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-            const float2 t = __ffma2_rn(
-                make_float2(__uint_as_float(sr[e + u]), __uint_as_float(sr[e + u + 1])), c2,
-                make_float2(__uint_as_float(u ? nl.z : nl.x), __uint_as_float(u ? nl.w : nl.y)));
-            const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            acc[(e + u) / 2 % 4] = __fadd2_rn(acc[(e + u) / 2 % 4], p);
+            for (int u = 0; u < 4; ++u)
+                nl[u] = ld_shared_v4(stat + e * 4 + u * 16);
         }
+        const uint4 q = nl[e / 4 % 4];
+        const float2 t = __ffma2_rn(
+            make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2,
+            make_float2(__uint_as_float(e & 2 ? q.z : q.x), __uint_as_float(e & 2 ? q.w : q.y)));
+        acc[e / 2 % 4] = __fadd2_rn(acc[e / 2 % 4], make_float2(ex2_approx(t.x), ex2_approx(t.y)));
     }
 }
 
@@ -157,7 +160,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_constant__ KeyWeightArgs a)
 {
     using C = KwCfg<D>;
-    constexpr int DB = C::DB, NSTAGE = C::NSTAGE, STEP = C::STEP, NCH = C::NCH;
+    constexpr int DB = C::DB, NSTAGE = C::NSTAGE, STEP = C::STEP, NCH = C::NCH, NH = C::NH, NSTAT = C::NSTAT;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem_base;
     __shared__ int s_abort;
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     const uint32_t sK = (raw + 1023u) & ~1023u;
     const uint32_t sRing = sK + kTiles * C::TILE;
     const uint32_t sStat = sRing + NSTAGE * C::BLOCK;
-    const uint32_t bars = sStat + kMathWarps * C::STAT;
+    const uint32_t bars = sStat + NSTAT * C::STAT;
     auto ring_full = [&](int i) { return bars + 8u * i; };
     auto ring_empty = [&](int i) { return bars + 8u * (NSTAGE + i); };
     constexpr uint32_t E = 2 * NSTAGE;
@@ -184,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     const uint32_t own_full = bars + 8u * (E + 4 * kTiles + 4);
     const uint32_t own_empty = bars + 8u * (E + 4 * kTiles + 5);
     const uint32_t drain_bar = bars + 8u * (E + 4 * kTiles + 6);
+    auto stat_full = [&](int i) { return bars + 8u * (E + 4 * kTiles + 7 + i); };
+    auto stat_empty = [&](int i) { return bars + 8u * (E + 4 * kTiles + 7 + NSTAT + i); };
     volatile int *abort = &s_abort;
 
     if (tid == 0) {
@@ -195,14 +200,18 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
         for (int x = 0; x < kTiles; ++x)
             for (int i = 0; i < 2; ++i) {
                 mbar_init(s_full(x, i), 1);
-                mbar_init(s_free(x, i), 128);       // tile x's warpgroup
+                mbar_init(s_free(x, i), 256);       // tile x's warpgroups
             }
         for (int x = 0; x < 2; ++x) {
             mbar_init(unit_full(x), 1);
-            mbar_init(unit_empty(x), 1 + kMathWarps);
+            mbar_init(unit_empty(x), 2 + kMathWarps);
         }
         mbar_init(own_full, 1);
         mbar_init(own_empty, 1);
+        for (int i = 0; i < NSTAT; ++i) {
+            mbar_init(stat_full(i), 1);
+            mbar_init(stat_empty(i), kMathWarps);
+        }
         mbar_init(drain_bar, 1);
         fence_barrier_init();
     }
@@ -272,15 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
                                         w.k0 + (w.t + i) * kOwn, kOwn);
                 ++owns;
                 const int per = w.both.end - w.both.first;
-                for (int s = w.s0; s < w.s0 + w.n; ++s, ++g) {
+                int head = w.s0 / per, blk = w.both.first + w.s0 % per;
+                for (int s = 0; s < w.n; ++s, ++g) {
                     const int st = g % NSTAGE;
                     if (!mbar_wait(ring_empty(st), ((g / NSTAGE) & 1u) ^ 1u, abort)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(ring_full(st), C::BLOCK);
-                    load_rows<DB, STEP>(sRing + st * C::BLOCK, &a.tm_q, ring_full(st), w.kh * group + s / per,
-                                        w.q0 + (w.both.first + s % per) * STEP, STEP);
+                    load_rows<DB, STEP>(sRing + st * C::BLOCK, &a.tm_q, ring_full(st), w.kh * group + head,
+                                        w.q0 + blk * STEP, STEP);
+                    if (++blk == w.both.end) {
+                        blk = w.both.first;
+                        ++head;
+                    }
                 }
             }
             if (*abort) {
@@ -311,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
                 break;
             }
             ++owns;
-            const int per = w.both.end - w.both.first;
-            for (int s = w.s0; s < w.s0 + w.n && ok; ++s, ++g) {
-                const int st = g % NSTAGE, blk = w.both.first + s % per;
+            int blk = w.both.first + w.s0 % (w.both.end - w.both.first);
+            for (int s = 0; s < w.n && ok; ++s, ++g) {
+                const int st = g % NSTAGE;
                 if (!mbar_wait_warp(ring_full(st), (g / NSTAGE) & 1u, abort)) {
                     ok = false;
                     break;
@@ -334,24 +348,71 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
                     ++used[x];
                 }
                 mma_commit_w(ring_empty(st));
-                if (s == w.s0 + w.n - 1)
+                if (s == w.n - 1)
                     mma_commit_w(own_empty);
+                blk = blk + 1 == w.both.end ? w.both.first : blk + 1;
             }
         }
         if (!ok || *abort) {
             mma_commit_w(drain_bar);
             mbar_wait_drain(drain_bar, 0);
         }
+    } else if (warp == kStatWarp) {
+        // ------------------------------------------------------------ -lse log2(e) of the queries
+        uint32_t g = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            KwUnit w;
+            const bool more = take_unit(n, w);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(unit_empty(n & 1));
+            if (!more)
+                break;
+            const int per = w.both.end - w.both.first;
+            int head = w.s0 / per, blk = w.both.first + w.s0 % per;
+            // NCH per lane, loaded a step ahead
+            float nl[NCH];
+            auto load = [&]() {
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    const int i = blk * STEP + 32 * c + lane;
+                    nl[c] = i < w.lq ? -__ldg(a.lse + static_cast<size_t>(w.q0 + i) * H + w.kh * group + head) *
+                                           kLog2e
+                                     : 0.f;
+                }
+            };
+            load();
+            for (int s = 0; s < w.n; ++s, ++g) {
+                const int st = g % NSTAT;
+                if (!mbar_wait_warp(stat_empty(st), ((g / NSTAT) & 1u) ^ 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                float *dst = reinterpret_cast<float *>(smem_raw + (sStat + st * C::STAT - raw));
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)       // a query that sees nothing (lse = -FLT_MAX) is hidden
+                    dst[32 * c + lane] = nl[c] > FLT_MAX ? 0.f : nl[c];
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(stat_full(st));
+                if (++blk == w.both.end) {
+                    blk = w.both.first;
+                    ++head;
+                }
+                if (s + 1 < w.n)
+                    load();
+            }
+        }
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
         // ------------------------------------------------------------ weights
-        const int quarter = warp & 3, x = (warp - kFirstMathWarp) >> 2;     // x: its tile
+        const int quarter = warp & 3, wg = (warp - kFirstMathWarp) >> 2;
+        const int x = wg & 1, half = wg >> 1;         // its tile, half of the columns
         const int r = quarter * 32 + lane;            // key row of the tile
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t wstat = sStat + (warp - kFirstMathWarp) * C::STAT;
-        float *stat = reinterpret_cast<float *>(smem_raw + (wstat - raw));
-        uint32_t used = 0;
+        uint32_t g = 0, used = 0;                     // steps, buffers of the tile so far
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
             KwUnit w;
@@ -365,43 +426,32 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
             const long long olo = static_cast<long long>(w.t + x) * kOwn;
             const int own = (w.t + x) * kOwn + r;
             const int wl = own < a.sink_tokens ? -1 : a.window_left;
-            const Blocks mine = w.tile[x];
-            const int per = w.both.end - w.both.first, s_end = w.s0 + w.n;
-            // the tile's next step from s on (steps whose block does not see it pass by)
-            auto seen_from = [&](int s) {
-                while (s < s_end && !mine.has(w.both.first + s % per))
-                    ++s;
-                return s;
-            };
-            // -lse log2(e) of a block's queries, NCH per lane, loaded a step ahead
-            float nl[NCH];
-            auto load_stats = [&](int s) {
-#pragma unroll
-                for (int c = 0; c < NCH; ++c) {
-                    const int i = (w.both.first + s % per) * STEP + 32 * c + lane;
-                    nl[c] = s < s_end && i < w.lq
-                                ? -__ldg(a.lse + static_cast<size_t>(w.q0 + i) * H + w.kh * group + s / per) *
-                                      kLog2e
-                                : 0.f;
-                    // a query that sees nothing (lse = -FLT_MAX): its scores are hidden
-                    nl[c] = nl[c] > FLT_MAX ? 0.f : nl[c];
-                }
-            };
+            const Blocks mine = x ? w.tile[1] : w.tile[0];
             float2 acc[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 acc[e] = make_float2(0.f, 0.f);
-            int s = seen_from(w.s0);
-            load_stats(s);
-            while (s < s_end) {
-                const int i = used & 1, blk = w.both.first + s % per;
-                __syncwarp();                       // the last block's stats are read
-#pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                    stat[32 * c + lane] = nl[c];
+            int s = 0, blk = w.both.first + w.s0 % (w.both.end - w.both.first);
+            // a step's queries are read, or its block does not see the tile
+            auto pass = [&]() {
                 __syncwarp();
-                const int next = seen_from(s + 1);
-                load_stats(next);
+                if (lane == 0)
+                    mbar_arrive(stat_empty(g % NSTAT));
+                ++g;
+                ++s;
+                blk = blk + 1 == w.both.end ? w.both.first : blk + 1;
+            };
+            while (s < w.n && ok) {
+                // (a step that passes by is waited for too: its stage is not given up twice)
+                ok = mbar_wait_warp(stat_full(g % NSTAT), (g / NSTAT) & 1u, abort);
+                if (!ok)
+                    break;
+                if (!mine.has(blk)) {
+                    pass();
+                    continue;
+                }
+                const int i = used & 1;
+                const uint32_t stat = sStat + g % NSTAT * C::STAT;
                 const long long slo = static_cast<long long>(blk) * STEP;
                 // a block every pair of which is visible needs no mask
                 const bool full = olo + kOwn <= w.lk && slo + STEP <= w.lq &&
@@ -414,34 +464,41 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
                 ++used;
                 tc_fence_after();
                 const uint32_t addr = tmem + lane_addr + (2 * x + i) * STEP;
-                uint32_t sr[NCH][32];
-#pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                    tmem_ld32(addr + 32 * c, sr[c]);
-                tmem_wait_ld_r(sr[0]);
-#pragma unroll
-                for (int c = 1; c < NCH; ++c)
-                    tmem_bind_r(sr[c]);
-                tc_fence_before();
-                mbar_arrive(s_free(x, i));
-                if (!full) {
-#pragma unroll
-                    for (int c = 0; c < NCH; ++c) {
+                if (full) {
+                    uint32_t ra[32], rb[32];
+                    tmem_ld32(addr + 32 * half * NH, ra);
+                    tmem_wait_ld_r(ra);
+                    if constexpr (NH == 2) {
+                        // the second chunk is on its way while the first is added up
+                        tmem_ld32(addr + 32 * half * NH + 32, rb);
+                        add_weights(ra, a.scale_log2, stat + 128 * half * NH, acc);
+                        tmem_wait_ld_r(rb);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(s_free(x, i));
+                    add_weights(NH == 2 ? rb : ra, a.scale_log2, stat + 128 * (half * NH + NH - 1), acc);
+                } else {
+                    // little code for the few masked steps
+#pragma unroll 1
+                    for (int c = half * NH; c < half * NH + NH; ++c) {
+                        uint32_t sr[32];
+                        tmem_ld32(addr + 32 * c, sr);
+                        tmem_wait_ld_r(sr);
                         int lo, hi;
                         key_row_span(own, slo + 32 * c, w.lk, w.lq, a.causal, wl, off, &lo, &hi);
-                        hide(sr[c], below(hi) & ~below(lo));
+                        hide(sr, below(hi) & ~below(lo));
+                        add_weights(sr, a.scale_log2, stat + 128 * c, acc);
                     }
+                    tc_fence_before();
+                    mbar_arrive(s_free(x, i));
                 }
-#pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                    add_weights(sr[c], a.scale_log2, wstat + 128 * c, acc);
-                s = next;
+                pass();
             }
             if (!ok)
                 break;
             const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
             if (own < w.lk)
-                a.part[(static_cast<size_t>(w.chunk) * a.num_kv_heads + w.kh) * a.total_k + w.k0 + own] =
+                a.part[(static_cast<size_t>(w.chunk * 2 + half) * a.num_kv_heads + w.kh) * a.total_k + w.k0 + own] =
                     sum.x + sum.y;
         }
     }
@@ -468,7 +525,7 @@ __global__ void __launch_bounds__(kTiles * kOwn) kw_sum_kernel(const KeyWeightAr
         const int k0 = a.cu_k[b], lk = a.cu_k[b + 1] - k0, lq = a.cu_q[b + 1] - a.cu_q[b];
         const int j = t * kOwn + threadIdx.x;
         const Blocks both = pair_blocks(blocks_of(a, lq, lk, t, a.step), blocks_of(a, lq, lk, t + 1, a.step));
-        const int chunks = ((both.end - both.first) * group + a.chunk_steps - 1) / a.chunk_steps;
+        const int parts = 2 * (((both.end - both.first) * group + a.chunk_steps - 1) / a.chunk_steps);
         if (j >= lk)
             continue;
         const size_t at = (static_cast<size_t>(b) * a.num_kv_heads + kh) * a.weight_stride + j;
@@ -476,7 +533,7 @@ __global__ void __launch_bounds__(kTiles * kOwn) kw_sum_kernel(const KeyWeightAr
         const float old = a.weights[at];
         float sum = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < chunks; ++c)
+        for (int c = 0; c < parts; ++c)
             sum += __ldcg(src + static_cast<size_t>(c) * a.num_kv_heads * a.total_k);
         a.weights_out[at] = old + sum;
     }
@@ -526,7 +583,7 @@ size_t key_weights_workspace_bytes(int batch, int total_k, int max_seqlen_q, int
     // query heads (of 64 queries at least): ceil(steps / per) in each kv head
     const int per = chunk_steps_for(total_k, num_heads);
     const long long steps = (static_cast<long long>(max_seqlen_q) + 63) / 64 * num_heads;
-    return list_bytes(batch) + static_cast<size_t>(steps / per + num_heads) * total_k * sizeof(float);
+    return list_bytes(batch) + 2 * static_cast<size_t>(steps / per + num_heads) * total_k * sizeof(float);
 }
 
 cudaError_t launch_key_weights(int head_dim, KeyWeightArgs &a, void *workspace, int sm_count,
