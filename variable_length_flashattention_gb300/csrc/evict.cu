@@ -42,6 +42,7 @@ constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMostCtas = 8;            // of a cluster
+constexpr int kTurns = 4;               // slots a thread has loads in flight for
 constexpr int kSmemKeys = 4096;         // keys a CTA keeps in shared memory
 constexpr uint32_t kStays = 0xffffffffu;    // the key of a token that stays whatever its weight
 constexpr int kMoveThreads = 256;
@@ -93,7 +94,7 @@ struct Shared {
     int bins[kBins];
     int warp[3][kSelWarps];
     int sums[3][kMostCtas];             // of every CTA, by rank
-    int digit, left;
+    int digit, left, exact, bad;
 };
 
 // Sums ahead of this warp, in the order of ranks and warps, of N values per warp (its lane
@@ -148,17 +149,32 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int row = blockIdx.x / ctas, s = row / a.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Plan p = plan_of(a, s);
-    // pages that are none, or that a move would write although another row has them: every
-    // CTA of the row looks at all of them and comes to the same verdict
+    // This CTA's slots, whole words of 32.
+    const int words = p.bad ? 0 : (p.n + 31) / 32, share = (words + ctas - 1) / ctas;
+    const int c0 = min(words, rank * share), c1 = min(words, c0 + share);
+    const int j0 = c0 * 32, j1 = min(p.n, c1 * 32);
+    // pages that are none, or that a move would write although another row has them, among
+    // those of its slots
     bool bad = p.bad;
     if (!bad) {
-        const int pages = (p.n + kPage - 1) / kPage, written = p.b < p.n ? (p.b + kPage - 1) / kPage : 0;
-        for (int j = tid; j < pages; j += kSelThreads) {
+        const int written = p.b < p.n ? (p.b + kPage - 1) / kPage : 0;
+        for (int j = j0 / kPage + tid; j * kPage < j1; j += kSelThreads) {
             const int id = a.tables[static_cast<long long>(s) * a.capacity + j];
             bad |= id < 0 || id >= a.num_blocks || (j < written && a.refs[id] != 1);
         }
     }
-    if (__syncthreads_or(bad)) {
+    bad = __syncthreads_or(bad);
+    if (ctas > 1) {
+        // the row is refused as a whole
+        if (tid == 0)
+            sh.bad = 0;
+        cluster.sync();
+        if (bad && tid < ctas)
+            cluster.map_shared_rank(&sh, tid)->bad = 1;
+        cluster.sync();
+        bad = sh.bad;
+    }
+    if (bad) {
         if (tid == 0 && rank == 0) {
             a.moves[row] = -1;
             record(a.status, VFA_ERR_BAD_BLOCK);
@@ -173,18 +189,25 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     uint32_t *bits = a.bits + static_cast<long long>(row) * ((a.capacity + 1) / 2);
     int32_t *to = a.lists + at, *from = to + static_cast<long long>(a.capacity) * (kPage / 2);
     auto position = [&](int j) { return p.position(j, j < p.known ? pos[j] : 0); };
-    // This CTA's slots, whole words of 32.
-    const int words = (p.n + 31) / 32, share = (words + ctas - 1) / ctas;
-    const int c0 = min(words, rank * share), c1 = min(words, c0 + share);
-    const int j0 = c0 * 32, j1 = min(p.n, c1 * 32);
-
     int moves = 0;
     if (p.b < p.n) {
         // Keys: in shared memory, or (long runs) where the lists will be.
         uint32_t *keys = c1 - c0 <= kSmemKeys / 32 ? s_keys - j0 : reinterpret_cast<uint32_t *>(to);
-        for (int j = j0 + tid; j < j1; j += kSelThreads)
-            keys[j] = p.safe(position(j)) ? kStays : order_of(w[j]);
+        for (int j = j0 + tid; j < j1; j += kSelThreads * kTurns) {
+            uint32_t k[kTurns];
+#pragma unroll
+            for (int t = 0; t < kTurns; ++t) {
+                const int i = j + t * kSelThreads;
+                k[t] = i < j1 ? (p.safe(position(i)) ? kStays : order_of(w[i])) : 0u;
+            }
+#pragma unroll
+            for (int t = 0; t < kTurns; ++t)
+                if (j + t * kSelThreads < j1)
+                    keys[j + t * kSelThreads] = k[t];
+        }
         // The border: the b-th largest key, and how many of those that equal it stay.
+        // (Where all keys that share the border's bits so far stay, none has to be
+        // told apart any more: the border is just below them.)
         uint32_t border = 0, known_bits = 0;
         int left = p.b;
         if (left > 0) {
@@ -193,65 +216,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
                 const uint32_t mask = turn == 2 ? 1023u : 2047u;
                 for (int i = tid; i < kBins; i += kSelThreads)
                     sh.bins[i] = 0;
-                if (ctas > 1)
-                    cluster.sync();                 // the first CTA's bins are clear
-                else
-                    __syncthreads();
+                __syncthreads();
                 for (int j = j0 + tid; j < j1; j += kSelThreads) {
                     const uint32_t k = keys[j];
                     if ((k & known_bits) == border)
                         atomicAdd(&sh.bins[k >> shift & mask], 1);
                 }
-                if (ctas > 1) {
-                    __syncthreads();
-                    if (rank > 0) {
-                        Shared *first = cluster.map_shared_rank(&sh, 0);
-                        for (int i = tid; i < kBins; i += kSelThreads)
-                            if (sh.bins[i])
-                                atomicAdd(&first->bins[i], sh.bins[i]);
-                    }
+                if (ctas > 1)
                     cluster.sync();
-                } else {
+                else
                     __syncthreads();
+                // Every CTA adds up its share of the bins, from the top: rank r's and thread
+                // t's are the `per` bins from 2047 - (r * threads + t) * per down.
+                const int per = kBins / kSelThreads / ctas, top = kBins - 1 - (rank * kSelThreads + tid) * per;
+                int mine[kBins / kSelThreads], sum = 0;
+#pragma unroll
+                for (int i = 0; i < kBins / kSelThreads; ++i)
+                    mine[i] = 0;
+                for (int c = 0; c < ctas; ++c) {
+                    const int *bins = cluster.map_shared_rank(&sh, c)->bins;
+#pragma unroll
+                    for (int i = 0; i < kBins / kSelThreads; ++i)
+                        if (i < per)
+                            mine[i] += bins[top - i];
                 }
-                if (rank == 0) {
-                    // thread t holds the eight bins from 2047 - 8t down: a scan from the top
-                    constexpr int PER = kBins / kSelThreads;
-                    int mine[PER], x = 0;
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        mine[i] = sh.bins[kBins - 1 - PER * tid - i];
-                        x += mine[i];
-                    }
-                    const int sum = x;
+                for (int i = 0; i < kBins / kSelThreads; ++i)
+                    sum += mine[i];
+                int x = sum;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int y = __shfl_up_sync(0xffffffffu, x, o);
-                        if (lane >= o)
-                            x += y;
-                    }
-                    if (lane == 31)
-                        sh.warp[0][warp] = x;
-                    __syncthreads();
-                    int before = x - sum;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o)
+                        x += y;
+                }
+                const int in_warp[1] = {__shfl_sync(0xffffffffu, x, 31)};
+                int start[1], total[1];
+                warp_starts<1>(cluster, sh, in_warp, start, total);
+                int before = start[0] + x - sum;
+                if (before < left && left <= before + sum) {
+                    int digit = top, count = 0;
 #pragma unroll
-                    for (int i = 0; i < kSelWarps; ++i)
-                        before += i < warp ? sh.warp[0][i] : 0;
-                    if (before < left && left <= before + sum) {
-                        int digit = kBins - 1 - PER * tid;
-#pragma unroll
-                        for (int i = 0; i < PER - 1; ++i)
-                            if (left > before + mine[i]) {
+                    for (int i = 0; i < kBins / kSelThreads; ++i)
+                        if (i < per && count == 0) {
+                            if (left <= before + mine[i]) {
+                                count = mine[i];
+                            } else {
                                 before += mine[i];
                                 --digit;
-                            } else {
-                                break;
                             }
-                        for (int c = 0; c < ctas; ++c) {
-                            Shared *other = cluster.map_shared_rank(&sh, c);
-                            other->digit = digit;
-                            other->left = left - before;
                         }
+                    for (int c = 0; c < ctas; ++c) {
+                        Shared *other = cluster.map_shared_rank(&sh, c);
+                        other->digit = digit;
+                        other->left = left - before;
+                        other->exact = count == left - before;
                     }
                 }
                 if (ctas > 1)
@@ -261,6 +280,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
                 border |= static_cast<uint32_t>(sh.digit) << shift;
                 known_bits |= mask << shift;
                 left = sh.left;
+                if (sh.exact && border > 0) {
+                    border -= 1;
+                    left = 0;
+                    break;
+                }
             }
         }
         // Warps take runs of the CTA's words.
@@ -314,17 +338,46 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     // Weights and positions: slots that stay, then those that are filled, then
     // (weights) zeros for the tokens to come.
     const bool copy_w = w_out != w, copy_p = pos_out != pos;
-    for (int j = j0 + tid; j < min(p.b, j1); j += kSelThreads) {
-        const bool stay = p.b == p.n || (bits[j / 32] >> (j % 32) & 1u);
-        if (stay && copy_w)
-            w_out[j] = w[j];
-        if (stay && (copy_p || j >= p.known))
-            pos_out[j] = position(j);
+    const int first = rank * kSelThreads + tid, step = ctas * kSelThreads;
+    for (int j = first; j < p.b; j += step * kTurns) {
+        bool stay[kTurns];
+        float wv[kTurns];
+        int pv[kTurns];
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int i = j + t * step;
+            stay[t] = i < p.b && (p.b == p.n || (__ldcg(bits + i / 32) >> (i % 32) & 1u));
+            wv[t] = i < p.b && copy_w ? w[i] : 0.f;
+            pv[t] = i < p.b ? position(i) : 0;
+        }
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int i = j + t * step;
+            if (stay[t] && copy_w)
+                w_out[i] = wv[t];
+            if (stay[t] && (copy_p || i >= p.known))
+                pos_out[i] = pv[t];
+        }
     }
-    for (int i = rank * kSelThreads + tid; i < moves; i += ctas * kSelThreads) {
-        const int j = __ldcg(to + i), f = __ldcg(from + i);
-        w_out[j] = w[f];
-        pos_out[j] = position(f);
+    for (int i = first; i < moves; i += step * kTurns) {
+        int j[kTurns], pv[kTurns];
+        float wv[kTurns];
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            j[t] = -1;
+            if (i + t * step < moves) {
+                const int f = __ldcg(from + i + t * step);
+                j[t] = __ldcg(to + i + t * step);
+                wv[t] = w[f];
+                pv[t] = position(f);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t)
+            if (j[t] >= 0) {
+                w_out[j[t]] = wv[t];
+                pos_out[j[t]] = pv[t];
+            }
     }
     if (ctas > 1)
         cluster.sync();
