@@ -399,6 +399,25 @@ def test_truncate(vfa, in_place):
         assert vfa.read_status(status) == (vfa.VFA_ERR_BAD_BLOCK if bad else 0)
 
 
+def test_truncate_many_rows(vfa):
+    """More rows and pages than one CTA takes."""
+    rng = np.random.default_rng(3)
+    S, cap, blocks = 1200, 40, 30000
+    counts = rng.integers(0, 16 * cap + 1, S)
+    tables = rng.integers(0, blocks, (S, cap)).astype(np.int32)
+    refs = np.zeros(blocks, dtype=np.int32)
+    for s in range(S):
+        np.add.at(refs, tables[s, :-(-counts[s] // 16)], 1)
+    new = np.minimum(counts, rng.integers(-1, 16 * cap, S))
+    want_r, want_c, bad = O.truncate(refs, tables, counts, new, 16)
+    for in_place in (True, False):
+        r, c = _i32(refs), _i32(counts)
+        outs = {} if in_place else {"refcounts_out": torch.full_like(r, 7), "token_counts_out": c.clone()}
+        vfa.pages_truncate(r, _i32(tables), c, _i32(new), 16, **outs)
+        assert np.array_equal((r if in_place else outs["refcounts_out"]).cpu().numpy(), want_r)
+        assert np.array_equal((c if in_place else outs["token_counts_out"]).cpu().numpy(), want_c)
+
+
 # ------------------------------------------------------------------ together
 
 def test_a_bounded_cache_in_use(vfa):

@@ -161,6 +161,11 @@ def _need(t: torch.Tensor, dtype, name: str):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _plain(t: torch.Tensor, dtype) -> bool:
+    """What _need asks for, in one expression (it says what is wrong)."""
+    return t.is_cuda and t.dtype is dtype and t.is_contiguous()
+
+
 def _int32(n, name) -> int:
     """n as the C ABI takes it; ctypes would cut a larger one without a word."""
     n = int(n)
@@ -207,42 +212,43 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     head h // (H // Hkv).  causal: 0 / False, 1 / True (top-left), 2
     (bottom-right); window_left >= 0 adds a sliding window (needs causal), past
     which the first sink_tokens keys stay visible (vfa_varlen_fwd_sinks)."""
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t, torch.bfloat16, n)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
-    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k")
-    if (q.dim() != 3 or k.shape != v.shape or k.dim() != 3 or q.shape[2] != k.shape[2] or
-            q.shape[1] % k.shape[1] != 0):
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not (_plain(q, bf16) and _plain(k, bf16) and _plain(v, bf16) and _plain(cu_seqlens_q, i32) and
+            _plain(cu_seqlens_k, i32)):
+        for t, d, n in ((q, bf16, "q"), (k, bf16, "k"), (v, bf16, "v"),
+                        (cu_seqlens_q, i32, "cu_seqlens_q"), (cu_seqlens_k, i32, "cu_seqlens_k")):
+            _need(t, d, n)
+    qshape, kshape = q.shape, k.shape
+    if (len(qshape) != 3 or kshape != v.shape or len(kshape) != 3 or qshape[2] != kshape[2] or
+            qshape[1] % kshape[1] != 0):
         raise ValueError("q, k, v must be [tokens, heads, head_dim]; k/v heads must divide q heads")
-    total_q, H, D = q.shape
-    Hkv = k.shape[1]
-    total_k = k.shape[0]
+    total_q, H, D = qshape
+    total_k, Hkv, _ = kshape
     batch = cu_seqlens_q.numel() - 1
     if cu_seqlens_k.numel() != batch + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
     if out is None:
         out = torch.empty_like(q)
+    elif not _plain(out, bf16):
+        _need(out, bf16, "out")
     if lse is None:
         lse = torch.empty((total_q, H), dtype=torch.float32, device=q.device)
-    _need(out, torch.bfloat16, "out")
-    _need(lse, torch.float32, "lse")
+    elif not _plain(lse, torch.float32):
+        _need(lse, torch.float32, "lse")
     if workspace is None:
         workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q.device)
+    ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+           total_q, total_k, int(max_seqlen_q), batch, H, Hkv, D, float(softmax_scale), int(causal),
+           int(window_left))
+    outs = (out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+            torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None
+            else stream.cuda_stream)
     if sink_tokens != 0:
-        st = lib().vfa_varlen_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
-                                        _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q),
-                                        batch, H, Hkv, D, float(softmax_scale), int(causal),
-                                        int(window_left), _int32(sink_tokens, "sink_tokens"), _ptr(out), _ptr(lse),
-                                        _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(),
-                                        _stream(stream))
+        st = (_lib or lib()).vfa_varlen_fwd_sinks(*ins, _int32(sink_tokens, "sink_tokens"), *outs)
     else:
-        st = lib().vfa_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
-                                  _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q), batch, H,
-                                  Hkv, D, float(softmax_scale), int(causal), int(window_left),
-                                  _ptr(out), _ptr(lse), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st)
+        st = (_lib or lib()).vfa_varlen_fwd(*ins, *outs)
+    if st:
+        _check(st)
     return out, lse
 
 
@@ -301,11 +307,14 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
                workspace: Optional[torch.Tensor] = None, stream=None, sink_tokens: int = 0):
     """(dq, dk, dv) bf16 = gradients of varlen_fwd for upstream gradient dout (vfa_varlen_bwd;
     with sink_tokens vfa_varlen_bwd_sinks, and a workspace made for as many)."""
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
-        _need(t, torch.bfloat16, n)
-    _need(lse, torch.float32, "lse")
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
-    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k")
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    if not (_plain(q, bf16) and _plain(k, bf16) and _plain(v, bf16) and _plain(out, bf16) and
+            _plain(dout, bf16) and _plain(lse, f32) and _plain(cu_seqlens_q, i32) and
+            _plain(cu_seqlens_k, i32)):
+        for t, d, n in ((q, bf16, "q"), (k, bf16, "k"), (v, bf16, "v"), (out, bf16, "out"),
+                        (dout, bf16, "dout"), (lse, f32, "lse"), (cu_seqlens_q, i32, "cu_seqlens_q"),
+                        (cu_seqlens_k, i32, "cu_seqlens_k")):
+            _need(t, d, n)
     if (q.dim() != 3 or k.shape != v.shape or out.shape != q.shape or dout.shape != q.shape or
             q.shape[2] != k.shape[2] or q.shape[1] % k.shape[1] != 0):
         raise ValueError("q, out, dout [Tq, H, D] and k, v [Tk, Hkv, D] with Hkv dividing H")
@@ -316,25 +325,23 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, torch.bfloat16, n)
+        if not _plain(t, bf16):
+            _need(t, bf16, n)
     if workspace is None:
         workspace = alloc_bwd_workspace(batch, total_q, H, D, device=q.device,
                                         sink_tokens=max(sink_tokens, 0))
+    ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+           cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), total_q, total_k, batch, H, Hkv, D,
+           float(softmax_scale), int(causal), int(window_left))
+    outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+            torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None
+            else stream.cuda_stream)
     if sink_tokens != 0:
-        st = lib().vfa_varlen_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout),
-                                        _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q,
-                                        total_k, batch, H, Hkv, D, float(softmax_scale),
-                                        int(causal), int(window_left), _int32(sink_tokens, "sink_tokens"),
-                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(),
-                                        _stream(stream))
+        st = (_lib or lib()).vfa_varlen_bwd_sinks(*ins, _int32(sink_tokens, "sink_tokens"), *outs)
     else:
-        st = lib().vfa_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
-                                  _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q, total_k, batch,
-                                  H, Hkv, D, float(softmax_scale), int(causal), int(window_left),
-                                  _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st)
+        st = (_lib or lib()).vfa_varlen_bwd(*ins, *outs)
+    if st:
+        _check(st)
     return dq, dk, dv, workspace
 
 
@@ -1227,15 +1234,14 @@ def cache_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, refcounts: torch.Ten
     if kept is None:
         kept = _empty(S, torch.int32, tables.device, stream)
     rows = (S, Hkv, 16 * cap)
-    for t, dtype, shape, n in ((refcounts, _I32, (blocks,), "refcounts"), (budgets, _I32, (S,), "budgets"),
-                               (key_weights, _F32, rows, "key_weights"),
-                               (key_weights_out, _F32, rows, "key_weights_out"),
-                               (positions, _I32, rows, "positions"),
-                               (positions_out, _I32, rows, "positions_out"),
-                               (history, _I32, (S, 2), "history"),
-                               (history_out, _I32, (S, 2), "history_out"), (kept, _I32, (S,), "kept")):
-        _dense(t, dtype, n, dev)
-        if t.shape != shape:
+    want = ((refcounts, _I32, (blocks,), "refcounts"), (budgets, _I32, (S,), "budgets"),
+            (key_weights, _F32, rows, "key_weights"), (key_weights_out, _F32, rows, "key_weights_out"),
+            (positions, _I32, rows, "positions"), (positions_out, _I32, rows, "positions_out"),
+            (history, _I32, (S, 2), "history"), (history_out, _I32, (S, 2), "history_out"),
+            (kept, _I32, (S,), "kept"))
+    for t, dtype, shape, n in want:
+        if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _dense(t, dtype, n, dev)
             raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
     if workspace is None:
         n = (_lib or lib()).vfa_cache_evict_workspace_bytes(S, Hkv, cap)
