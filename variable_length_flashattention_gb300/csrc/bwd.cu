@@ -215,7 +215,7 @@ __global__ void bwd_delta_kernel(const BwdArgs a)
 }
 
 // The same for the instantiations with sinks: D / 8 lanes per row with 16-byte loads, two
-// rows of a lane in flight (49879 tokens of 16 heads of 64: %DELTA% us, 59 with a warp per
+// rows of a lane in flight (49879 tokens of 16 heads of 64: 37 us, 59 with a warp per
 // row; the order of a sum, and with it the last bits, differs from the other's).
 template <int D>
 __global__ void __launch_bounds__(256) bwd_delta_wide_kernel(const BwdArgs a)

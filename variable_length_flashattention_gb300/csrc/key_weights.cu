@@ -6,20 +6,23 @@
 // tile a column sum is a row sum, which one thread adds up in registers:
 //   * a unit is (kv head, pair of 128-key tiles, chunk of steps); a step is a block
 //     of queries of one query head.  The pair of K tiles stays in shared memory,
-//     the blocks stream past through a TMA ring: a block is read once for 256
-//     keys (with one tile per unit the blocks took 5 TB/s from L2 and the kernel
-//     twice as long: 1257 us against %MEAS% for 38577 tokens of 32 + 8 heads of
-//     128);
+//     the blocks stream past through a TMA ring, each read once for 256 keys;
 //   * the tensor core forms S^T = K Q^T of each tile into one of two TMEM buffers of
-//     its own; warpgroup x takes tile x, one key row per thread, and adds
-//     2^(s scale log2e - lse log2e) over the row's visible columns, four chains of
-//     two side by side, block after block: the order of a sum is fixed;
+//     its own; a warpgroup takes half of the columns of one tile, one key row per
+//     thread, and adds 2^(s scale log2e - lse log2e) over the row's visible columns,
+//     four chains of two side by side, block after block: the order of a sum is
+//     fixed.  -lse log2e of a step's queries comes from a warp of its own through
+//     a ring;
 //   * a unit's sums go to the workspace, and a second kernel adds them over the
-//     chunks, in order, to the weights.
+//     chunks and halves, in order, to the weights.
 // One CTA per SM takes units from an atomic counter.
 //
-// Bound: the tensor core (2 D flops per visible pair and query head against one
-// exponential and 2.3 instructions of a thread).
+// Bound.  38577 tokens of 32 + 8 heads of 128 take 0.8 ms, 1.0 PFLOP/s (52% of the
+// measured peak).  The products alone, with every handshake, take 0.55, the
+// exponentials (32 a cycle and SM) 0.38; the rest is their overlap, which four warps per
+// scheduler do not complete.  Steps on the way: one tile per unit 1.26 ms; eight
+// warps and a tile's masked steps in the common code 0.94, in code of their own
+// 0.82.  K as an operand in TMEM was the same (0.83).
 #include <algorithm>
 #include <cfloat>
 
