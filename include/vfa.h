@@ -483,7 +483,8 @@ vfa_status vfa_paged_decode_finalize(const float *l, const float *o, int num_seq
  * (nullable device int32 [1], the first error is kept) and leaves that
  * sequence's out, lse and key_weights_out as they were.
  * Supported: head_dim 64, 128 or 256; pages of 16 tokens; any num_q_heads that
- * is a multiple of num_kv_heads; num_seqs * (capacity + 64) <= 2^30.
+ * is a multiple of num_kv_heads; num_seqs * (capacity + 64) <= 2^30 and
+ * capacity, num_blocks <= 2^26.
  */
 size_t vfa_paged_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                         int capacity);
@@ -883,7 +884,8 @@ vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse
  * the row's slots, key_weights_out and positions_out stay as they were, kept[s]
  * is n and history_out[s] is history[s].  Stored positions that are not one per
  * token may name more than b tokens that stay: the lowest slots of them do.
- * Supported: head_dim 64, 128 or 256; pages of 16 tokens.
+ * Supported: head_dim 64, 128 or 256; pages of 16 tokens; capacity and num_blocks <=
+ * 2^26.
  */
 size_t vfa_cache_evict_workspace_bytes(int num_seqs, int num_kv_heads, int capacity);
 

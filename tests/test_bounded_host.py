@@ -130,3 +130,18 @@ def test_binding_refuses(vfa):
         vfa.alloc_evict_workspace(1, 1, 1 << 31, device="cpu")
     with pytest.raises(vfa.VfaError):
         vfa.alloc_paged_decode_workspace(1, 3, 2, 64, device="cpu")
+
+
+def test_rows_of_more_pages_than_a_pool(vfa):
+    """A row's slots, and what a thread adds to a slot's number, stay within 32 bits."""
+    most, uns = 1 << 26, vfa.VFA_ERR_UNSUPPORTED
+    good = [FAKE, FAKE, FAKE, 10, FAKE, 4, FAKE, 2, 8, 2, 128, 16, 4, 0.1, FAKE, FAKE, FAKE, FAKE, NUL,
+            FAKE, 1 << 30, NUL]
+    _calls(vfa, "vfa_paged_decode", good, [(5, most + 1, uns, b"capacity")])
+    good = [FAKE, FAKE, FAKE, 10, FAKE, 4, FAKE, FAKE, 2, 2, 128, FAKE, FAKE, FAKE, 1, 1, FAKE, FAKE, FAKE,
+            FAKE, FAKE, 1 << 30, NUL, NUL]
+    _calls(vfa, "vfa_cache_evict", good, [(5, most + 1, uns, b"capacity")])
+    L = vfa.lib()
+    assert L.vfa_paged_decode_workspace_bytes(1, 2, 2, 64, most) > L.vfa_paged_decode_workspace_bytes(1, 2, 2, 64, 0)
+    assert L.vfa_paged_decode_workspace_bytes(1, 2, 2, 64, most + 1) == 0
+    assert L.vfa_cache_evict_workspace_bytes(1, 2, most) > 0 == L.vfa_cache_evict_workspace_bytes(1, 2, most + 1)

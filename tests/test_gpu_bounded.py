@@ -554,3 +554,42 @@ def test_steps_in_a_graph_and_on_another_stream(vfa):
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(want, state))
         assert all(torch.equal(a, c) for a, c in zip(want_out, got))
+
+
+def test_offsets_past_32_bits(vfa):
+    """Pages past 2^32 bytes of a pool, and slots past 2^31 of all rows: as in a small cache."""
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    hkv, d, lens, shift, cap = 2, 64, [40, 0, 3, 0, 100], 1_200_000, 1 << 24
+    k, v, tables, rng = _cache(lens, hkv, d, seed=11)
+    q = torch.from_numpy(rng.standard_normal((5, 4, d))).bfloat16().cuda()
+    blocks = k.shape[0]
+    results = []
+    for far in (False, True):
+        t = _i32(tables)
+        pools = [x.cuda() for x in (k, v)]
+        refs = torch.zeros(blocks, dtype=torch.int32, device="cuda")
+        if far:
+            pools = [torch.zeros(shift + blocks, 16, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            for x, y in zip(pools, (k, v)):
+                x[shift:] = y.cuda()
+            refs = torch.zeros(shift + blocks, dtype=torch.int32, device="cuda")
+            t = torch.full((5, cap), -1, dtype=torch.int32, device="cuda")
+            t[:, :tables.shape[1]] = torch.where(_i32(tables) < 0, -1, _i32(tables) + shift)
+        refs[-blocks:] = 1
+        rows = (5, hkv, 16 * t.shape[1])
+        w = torch.zeros(rows, device="cuda")
+        p = torch.zeros(rows, dtype=torch.int32, device="cuda")
+        h = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+        n = _i32(lens)
+        out, lse = vfa.paged_decode(q, *pools, t, n, key_weights=w)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kept = vfa.cache_evict(*pools, refs, t, n, _i32([16, 0, 2, 5, 70]), w, p, h, 2, 8, status=status)
+        vfa.pages_truncate(refs, t, n, kept, 16, status=status)
+        assert vfa.read_status(status) == 0
+        results.append((out, lse, kept, h, n, w[:, :, :112].clone(), p[:, :, :112].clone(), refs[-blocks:].clone(),
+                        *(x[-blocks:].nan_to_num() for x in pools)))
+        assert not w[:, :, 112:].any() and not p[:, :, 112:].any()
+        del pools, w, p, t, refs
+        torch.cuda.empty_cache()
+    assert all(torch.equal(a, b) for a, b in zip(*results))

@@ -34,7 +34,7 @@ bool supported_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr int kMaxBlocks = 1 << 26;
 constexpr int kMaxHeads = 65535;
-constexpr int kMaxCapacity = INT_MAX / 16;      // a row's slots are counted in 32 bits
+constexpr int kMaxCapacity = 1 << 26;           // no more pages than a pool; slots and steps fit 32 bits
 
 vfa_status check_workspace(const void *workspace, size_t bytes, size_t need)
 {
@@ -61,7 +61,7 @@ vfa_status check_cache(const void *k_pool, const void *v_pool, int num_blocks, c
     if (num_kv_heads > kMaxHeads)
         return fail(VFA_ERR_UNSUPPORTED, "%d kv heads, at most %d", num_kv_heads, kMaxHeads);
     if (capacity > kMaxCapacity)
-        return fail(VFA_ERR_UNSUPPORTED, "capacity %d above %d pages", capacity, kMaxCapacity);
+        return fail(VFA_ERR_UNSUPPORTED, "capacity %d above 2^26 pages not supported", capacity);
     if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(tables, 4) ||
         !aligned(token_counts, 4) || !aligned(device_status, 4))
         return fail(VFA_ERR_INVALID_ARG, "pools must be 16-byte aligned, int32 arrays 4-byte");
@@ -219,7 +219,7 @@ vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse
     a.max_seqlen_q = max_seqlen_q;
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
-    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.scale_log2 = std::fmin(softmax_scale * 1.4426950408889634f, FLT_MAX);
     a.causal = causal;
     a.window_left = window_left < 0 ? -1 : window_left;
     a.sink_tokens = window_left < 0 ? 0 : sink_tokens;

@@ -108,7 +108,9 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const KeyWeightAr
     __syncthreads();
     auto pairs_of = [&](int b) {
         const int lq = a.cu_q[b + 1] - a.cu_q[b], lk = a.cu_k[b + 1] - a.cu_k[b];
-        if (lq < 0 || lk < 0 || lq > a.max_seqlen_q || lk > a.weight_stride) {
+        // (compared, too: a difference of 32 bits may wrap)
+        if (a.cu_q[b + 1] < a.cu_q[b] || a.cu_k[b + 1] < a.cu_k[b] || lq > a.max_seqlen_q ||
+            lk > a.weight_stride) {
             s_bad = 1;
             return 0;
         }
