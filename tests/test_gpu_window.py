@@ -214,3 +214,18 @@ def test_training_step_in_a_graph(vfa):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_results_at_any_allowed_address(vfa, d):
+    """An output at a multiple of 16 bytes that is none of 32: the same bits, and nothing around it."""
+    c = _case([200, 0, 129], [200, 5, 129], 4, 2, d, 21)
+    q, k, v, cq, ck = _dev(c)
+    want, lse = vfa.varlen_fwd(q, k, v, cq, ck, c.max_seqlen_q, c.softmax_scale, 1, window_left=40, sink_tokens=3)
+    flat = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:-8].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    _, lse2 = vfa.varlen_fwd(q, k, v, cq, ck, c.max_seqlen_q, c.softmax_scale, 1, window_left=40, sink_tokens=3,
+                             out=out)
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
+    assert (flat[:8] == 7.0).all() and (flat[-8:] == 7.0).all()
