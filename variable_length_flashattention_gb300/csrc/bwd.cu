@@ -52,6 +52,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "tiles.cuh"
 
@@ -125,6 +126,7 @@ __device__ __forceinline__ int sink_tiles(const BwdArgs &a, int lk)
 template <int STEP, int SPLIT, bool SINK>
 __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdArgs a)
 {
+    grid_release();             // the Delta kernel reads nothing of this one's
     __shared__ int warp_sums[32];
     __shared__ int s_bad;
     __shared__ unsigned long long s_steps;
@@ -185,12 +187,14 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdArgs a)
 }
 
 // ------------------------------------------------------------ Delta
+//
+// Runs beside the prep kernel, one CTA's chain of prefix sums, and waits for it
+// before it ends: the dK/dV kernel behind it waits for this one alone.
 
 template <int D>
 __global__ void bwd_delta_kernel(const BwdArgs a)
 {
-    if (*a.status != VFA_OK)
-        return;
+    grid_release();
     const int lane = threadIdx.x & 31;
     const long long rows = static_cast<long long>(a.total_q) * a.num_heads;
     const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
@@ -212,6 +216,7 @@ __global__ void bwd_delta_kernel(const BwdArgs a)
         if (lane == 0)
             a.delta[r] = s;
     }
+    grid_wait();
 }
 
 // The same for the instantiations with sinks: D / 8 lanes per row with 16-byte loads, two
@@ -220,8 +225,7 @@ __global__ void bwd_delta_kernel(const BwdArgs a)
 template <int D>
 __global__ void __launch_bounds__(256) bwd_delta_wide_kernel(const BwdArgs a)
 {
-    if (*a.status != VFA_OK)
-        return;
+    grid_release();
     constexpr int LANES = D / 8, TURNS = 2;
     const long long rows = static_cast<long long>(a.total_q) * a.num_heads;
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x / LANES;
@@ -256,6 +260,7 @@ __global__ void __launch_bounds__(256) bwd_delta_wide_kernel(const BwdArgs a)
                 a.delta[r + t * step] = s;
         }
     }
+    grid_wait();
 }
 
 // ------------------------------------------------------------ shared pieces
@@ -589,10 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_main_kernel(const __grid_cons
     __shared__ int s_abort;
     __shared__ BwdUnit s_unit[2];
 
-    // The dQ kernel, launched next with programmatic dependent launch, reads
-    // nothing this kernel writes: let it take each SM this kernel's CTAs leave.
-    if (!DQ)
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The dK/dV kernel waits for the Delta kernel, and with it for the prep kernel.  The
+    // dQ kernel, launched next with programmatic dependent launch, reads what
+    // those two wrote and nothing this kernel writes: from here on let it take each SM
+    // this kernel's CTAs leave.
+    if (!DQ) {
+        grid_wait();
+        grid_release();
+    } else if (SINK) {
+        grid_release();             // the sums of the sinks' chunks, always next, wait for it
+    }
     // The dQ kernel waits for the dK/dV kernel before it ends: what is launched
     // behind it in the same way waits for the dQ kernel alone, and may read dK
     // and dV.
@@ -1011,6 +1022,7 @@ template <int D>
 __global__ void __launch_bounds__(2 * kSinkRows * D / 4) bwd_sinks_kernel(const BwdArgs a)
 {
     using C = BwdCfg<D, false>;
+    grid_wait();
     if (*a.status != VFA_OK)
         return;
     const int sub_row = threadIdx.x / (D / 4) % kSinkRows;
@@ -1070,11 +1082,8 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
         <<<1, kPrepThreads, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    if (SINK)
-        bwd_delta_wide_kernel<D><<<sm_count * 8, 256, 0, s>>>(a);
-    else
-        bwd_delta_kernel<D><<<sm_count * 8, 256, 0, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    if ((e = launch_dependent(SINK ? bwd_delta_wide_kernel<D> : bwd_delta_kernel<D>, dim3(sm_count * 8), 256, 0,
+                              s, a)) != cudaSuccess)
         return e;
     // persistent grids: one CTA per SM (fewer when there are fewer units)
     const long long kv_units =
@@ -1082,17 +1091,16 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
     const long long q_units = static_cast<long long>(q_tile_bound) * a.num_heads;
     if (kv_units > 0) {
         const int grid = SINK ? sm_count : static_cast<int>(std::min<long long>(kv_units, sm_count));
-        bwd_main_kernel<D, false, SINK><<<grid, kThreads, BwdCfg<D, false>::SMEM, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess)
+        if ((e = launch_dependent(bwd_main_kernel<D, false, SINK>, dim3(grid), kThreads,
+                                  BwdCfg<D, false>::SMEM, s, a)) != cudaSuccess)
             return e;
     }
     if (q_units > 0) {
         // Programmatic dependent launch: the dQ kernel's CTAs start on the SMs
         // the dK/dV kernel's CTAs leave, without waiting for the whole grid.  It
-        // reads only the prep and Delta kernels' output, complete before the
-        // dK/dV kernel started (a plain launch after them), so it waits
-        // (griddepcontrol.wait) only at its end; its atomic unit counter balances
-        // CTAs that start late.
+        // reads only the prep and Delta kernels' output, complete before any
+        // dK/dV CTA let it start, so it waits (griddepcontrol.wait) only at its
+        // end; its atomic unit counter balances CTAs that start late.
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(q_units, sm_count)));
         cfg.blockDim = dim3(kThreads);
@@ -1110,8 +1118,8 @@ cudaError_t launch_bwd_d(const BwdArgs &a, int key_tile_bound, int q_tile_bound,
     }
     if (SINK && kv_units > 0 && q_units > 0) {
         // behind the dQ kernel, which waits for the dK/dV kernel
-        bwd_sinks_kernel<D><<<4 * sm_count, 2 * kSinkRows * D / 4, 0, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess)
+        if ((e = launch_dependent(bwd_sinks_kernel<D>, dim3(4 * sm_count), 2 * kSinkRows * D / 4, 0, s, a)) !=
+            cudaSuccess)
             return e;
     }
     return cudaSuccess;

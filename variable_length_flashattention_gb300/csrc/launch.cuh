@@ -23,7 +23,8 @@ __device__ __forceinline__ void grid_wait()
 }
 
 // The next kernel of the stream may be scheduled from here on.  Only for a
-// kernel whose successor is known to begin with grid_wait(): the last kernel
+// kernel whose successor is known to begin with grid_wait(), or to read nothing
+// that this one writes (the backward's Delta and dQ kernels): the last kernel
 // of a call must not say this, since a decode step behind it reads its pools,
 // tables and queries before it waits.
 __device__ __forceinline__ void grid_release()
