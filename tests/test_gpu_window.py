@@ -229,3 +229,24 @@ def test_results_at_any_allowed_address(vfa, d):
                              out=out)
     assert torch.equal(out, want) and torch.equal(lse, lse2)
     assert (flat[:8] == 7.0).all() and (flat[-8:] == 7.0).all()
+
+
+@pytest.mark.parametrize("sinks", [0, 4])
+def test_backward_calls_in_a_row_share_a_workspace(vfa, sinks):
+    """Each call's first kernels start behind all of the call before, which reads the same scratch."""
+    cases = []
+    for seed, lens in ((31, [700, 300]), (32, [64, 0, 900])):
+        c = _case(lens, lens, 4, 2, 64, seed)
+        q, k, v, cq, ck = _dev(c)
+        out, lse = vfa.varlen_fwd(q, k, v, cq, ck, c.max_seqlen_q, c.softmax_scale, 1, window_left=100,
+                                  sink_tokens=sinks)
+        cases.append((q, k, v, out, torch.randn_like(q), lse, cq, ck, c.softmax_scale, 1))
+    want = [vfa.varlen_bwd(*a, window_left=100, sink_tokens=sinks)[:3] for a in cases]
+    torch.cuda.synchronize()
+    ws = vfa.alloc_bwd_workspace(3, 1000, 4, 64, sink_tokens=sinks)
+    got = [[torch.empty_like(t) for t in w] for w in want]
+    for _ in range(20):
+        for a, g in zip(cases, got):
+            vfa.varlen_bwd(*a, window_left=100, sink_tokens=sinks, dq=g[0], dk=g[1], dv=g[2], workspace=ws)
+    assert vfa.read_status(ws) == 0
+    assert all(torch.equal(x, y) for w, g in zip(want, got) for x, y in zip(w, g))

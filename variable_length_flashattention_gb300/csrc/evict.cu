@@ -20,7 +20,8 @@
 //            of slots: ballots give the ranks of ties, free slots and movers, sums over
 //            warps and CTAs their starts.  Weights and positions are rewritten here.
 //            One CTA per row took 41 us for 64 sequences of 1056 tokens on 8 kv
-//            heads and 57 for 8 of 4000-32768, a cluster 21 and 34;
+//            heads and 57 for 8 of 4000-32768, a cluster 21 and 34, and 2 less with
+//            one barrier per sum (two buffers of sums in turn) instead of two;
 //   move     the rows of K and V by the lists, 16 bytes per thread, and the
 //            sequences' new state.
 // Bound: HBM, 8 D bytes per moved token and kv head, and 12 to 16 bytes per token for weights
@@ -93,15 +94,16 @@ __device__ __forceinline__ uint32_t order_of(float w)
 struct Shared {
     int bins[kBins];
     int warp[3][kSelWarps];
-    int sums[3][kMostCtas];             // of every CTA, by rank
+    int sums[2][3][kMostCtas];          // of every CTA, by rank; calls take the two in turn
     int digit, left, exact, bad;
 };
 
 // Sums ahead of this warp, in the order of ranks and warps, of N values per warp (its lane
-// 0's); total[i] gets the cluster's.  Everybody calls it.
+// 0's); total[i] gets the cluster's.  Everybody calls it, with a `call` that counts up: the
+// sums of a call are written where those of the one before the last were read.
 template <int N>
-__device__ __forceinline__ void warp_starts(cg::cluster_group &cluster, Shared &sh, const int (&v)[N],
-                                            int (&start)[N], int (&total)[N])
+__device__ __forceinline__ void warp_starts(cg::cluster_group &cluster, Shared &sh, int &call,
+                                            const int (&v)[N], int (&start)[N], int (&total)[N])
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
@@ -122,20 +124,20 @@ __device__ __forceinline__ void warp_starts(cg::cluster_group &cluster, Shared &
     }
     if (ctas == 1)
         return;
+    const int half = call++ & 1;
     if (threadIdx.x < ctas)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            cluster.map_shared_rank(&sh, threadIdx.x)->sums[i][rank] = total[i];
+            cluster.map_shared_rank(&sh, threadIdx.x)->sums[half][i][rank] = total[i];
     cluster.sync();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         total[i] = 0;
         for (int c = 0; c < ctas; ++c) {
-            start[i] += c < rank ? sh.sums[i][c] : 0;
-            total[i] += sh.sums[i][c];
+            start[i] += c < rank ? sh.sums[half][i][c] : 0;
+            total[i] += sh.sums[half][i][c];
         }
     }
-    cluster.sync();                     // the sums are read: they may be written again
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a)
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     uint32_t *bits = a.bits + static_cast<long long>(row) * ((a.capacity + 1) / 2);
     int32_t *to = a.lists + at, *from = to + static_cast<long long>(a.capacity) * (kPage / 2);
     auto position = [&](int j) { return p.position(j, j < p.known ? pos[j] : 0); };
-    int moves = 0;
+    int moves = 0, call = 0;
     if (p.b < p.n) {
         // Keys: in shared memory, or (long runs) where the lists will be.
         uint32_t *keys = c1 - c0 <= kSmemKeys / 32 ? s_keys - j0 : reinterpret_cast<uint32_t *>(to);
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
                 }
                 const int in_warp[1] = {__shfl_sync(0xffffffffu, x, 31)};
                 int start[1], total[1];
-                warp_starts<1>(cluster, sh, in_warp, start, total);
+                warp_starts<1>(cluster, sh, call, in_warp, start, total);
                 int before = start[0] + x - sum;
                 if (before < left && left <= before + sum) {
                     int digit = top, count = 0;
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
             const int j = i * 32 + lane;
             ties[0] += __popc(__ballot_sync(0xffffffffu, any && j < j1 && keys[j] == border));
         }
-        warp_starts<1>(cluster, sh, ties, rank_of, all);
+        warp_starts<1>(cluster, sh, call, ties, rank_of, all);
         int counts[2] = {0, 0}, start[2], total[2];         // free slots, movers
         for (int i = w0; i < w1; ++i) {
             const int j = i * 32 + lane;
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
             counts[1] += __popc(word & ~low);
         }
         // (behind this nobody of the cluster reads keys: the lists may be written)
-        warp_starts<2>(cluster, sh, counts, start, total);
+        warp_starts<2>(cluster, sh, call, counts, start, total);
         moves = total[0];
         int h = start[0], m = start[1];
         for (int i = w0; i < w1; ++i) {
@@ -329,7 +331,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
             m += __popc(mb);
         }
         // the lists are there for every CTA of the cluster
-        __threadfence();
         if (ctas > 1)
             cluster.sync();
         else
