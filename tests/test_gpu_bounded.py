@@ -244,6 +244,16 @@ def test_key_weights_of_many_blocks(vfa):
     _key_weights(vfa, _prompt([1500], [1500], 64, 8, 64, 2), 8, 1, -1, 0)
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-45, 1e-30, 1.0])
+@pytest.mark.parametrize("d,causal,window,sinks", [(64, 1, -1, 0), (128, 0, -1, 0), (128, 2, 31, 65),
+                                                   (256, 1, 40, 3)])
+def test_key_weights_scales(vfa, d, causal, window, sinks, scale):
+    """Also a scale of zero: every key that a query sees gets the same weight, hidden ones none."""
+    c = _prompt([257, 64, 5], [511, 64, 9], 4, 2, d, 11)
+    c.softmax_scale = scale
+    _key_weights(vfa, c, 2, causal, window, sinks)
+
+
 def test_key_weights_sum_to_the_queries(vfa):
     """With the forward's own lse every query spends a weight of one per head."""
     c = _prompt([700, 90], [700, 90], 8, 2, 128, 3)

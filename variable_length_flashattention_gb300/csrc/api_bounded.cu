@@ -219,7 +219,8 @@ vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse
     a.max_seqlen_q = max_seqlen_q;
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
-    a.scale_log2 = std::fmin(softmax_scale * 1.4426950408889634f, FLT_MAX);
+    // positive and finite, as in the forward: a masked -inf times it would be no number
+    a.scale_log2 = std::fmax(std::fmin(softmax_scale * 1.4426950408889634f, FLT_MAX), FLT_MIN);
     a.causal = causal;
     a.window_left = window_left < 0 ? -1 : window_left;
     a.sink_tokens = window_left < 0 ? 0 : sink_tokens;
