@@ -254,6 +254,30 @@ def test_key_weights_scales(vfa, d, causal, window, sinks, scale):
     _key_weights(vfa, c, 2, causal, window, sinks)
 
 
+def test_key_weights_of_hidden_queries_that_are_no_numbers(vfa):
+    """A query that is NaN, or whose lse is, changes the keys that it sees and no others."""
+    for d, bad_q, value in ((64, True, np.nan), (128, False, np.nan), (256, False, np.nan),
+                            (128, False, np.inf), (64, False, -np.inf)):
+        c = _prompt([300, 70], [300, 70], 2, 1, d, d)
+        cq = torch.from_numpy(c.cu_seqlens_q).cuda()
+        lse = torch.full((370, 2), 3.0, device="cuda")
+        q, k = c.q.cuda(), c.k.cuda()
+        call = lambda: vfa.varlen_key_weights(q, k, lse, cq, cq, 300, c.softmax_scale, 1,
+                                              torch.zeros(2, 1, 300, device="cuda"), window_left=40,
+                                              sink_tokens=3)
+        good = call()
+        if bad_q:
+            q[200] = value
+        else:
+            lse[200] = value
+        got = call()
+        sees = torch.zeros_like(good, dtype=torch.bool)
+        sees[0, 0, :3] = sees[0, 0, 160:201] = True
+        assert torch.equal(got[~sees], good[~sees])
+        if value != value:
+            assert got[sees].isnan().all()
+
+
 def test_key_weights_sum_to_the_queries(vfa):
     """With the forward's own lse every query spends a weight of one per head."""
     c = _prompt([700, 90], [700, 90], 8, 2, 128, 3)

@@ -140,9 +140,11 @@ struct KwUnit {
 };
 
 // Sums of this thread's key row over 32 columns: p = 2^(s scale_log2 + nl), nl of every
-// column from shared memory, all of them asked for before the first is used.
+// column from shared memory, all of them asked for before the first is used.  MASK: where
+// a column's bit of `see` is 0 p is 0, whatever the query's score and lse are.
+template <bool MASK>
 __device__ __forceinline__ void add_weights(const uint32_t (&sr)[32], float scale_log2, uint32_t stat,
-                                            float2 (&acc)[4])
+                                            float2 (&acc)[4], uint32_t see = 0xffffffffu)
 {
     uint4 nl[4];
     const float2 c2 = make_float2(scale_log2, scale_log2);
@@ -157,7 +159,12 @@ __device__ __forceinline__ void add_weights(const uint32_t (&sr)[32], float scal
         const float2 t = __ffma2_rn(
             make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2,
             make_float2(__uint_as_float(e & 2 ? q.z : q.x), __uint_as_float(e & 2 ? q.w : q.y)));
-        acc[e / 2 % 4] = __fadd2_rn(acc[e / 2 % 4], make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+        float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+        if (MASK) {
+            p.x = see >> e & 1u ? p.x : 0.f;
+            p.y = see >> (e + 1) & 1u ? p.y : 0.f;
+        }
+        acc[e / 2 % 4] = __fadd2_rn(acc[e / 2 % 4], p);
     }
 }
 
@@ -476,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
                     if constexpr (NH == 2) {
                         // the second chunk is on its way while the first is added up
                         tmem_ld32(addr + 32 * half * NH + 32, rb);
-                        add_weights(ra, a.scale_log2, stat + 128 * half * NH, acc);
+                        add_weights<false>(ra, a.scale_log2, stat + 128 * half * NH, acc);
                         tmem_wait_ld_r(rb);
                     }
                     tc_fence_before();
                     mbar_arrive(s_free(x, i));
-                    add_weights(NH == 2 ? rb : ra, a.scale_log2, stat + 128 * (half * NH + NH - 1), acc);
+                    add_weights<false>(NH == 2 ? rb : ra, a.scale_log2, stat + 128 * (half * NH + NH - 1), acc);
                 } else {
                     // little code for the few masked steps
 #pragma unroll 1
@@ -491,8 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
                         tmem_wait_ld_r(sr);
                         int lo, hi;
                         key_row_span(own, slo + 32 * c, w.lk, w.lq, a.causal, wl, off, &lo, &hi);
-                        hide(sr, below(hi) & ~below(lo));
-                        add_weights(sr, a.scale_log2, stat + 128 * c, acc);
+                        add_weights<true>(sr, a.scale_log2, stat + 128 * c, acc, below(hi) & ~below(lo));
                     }
                     tc_fence_before();
                     mbar_arrive(s_free(x, i));
