@@ -275,7 +275,8 @@ vfa_status vfa_varlen_schedule(const int32_t *cu_seqlens_q, const int32_t *cu_se
  *               the forward's results for these q, k, v).
  * k, v          device bf16 [total_k, num_kv_heads, head_dim].
  * lse           device f32 [total_q, num_heads], natural log (-FLT_MAX for
- *               rows without visible keys, which get dq = 0).
+ *               rows without visible keys, which get dq = 0; an infinity is
+ *               taken as well).
  * cu_seqlens_q/k, total_q/k, batch, num_heads, num_kv_heads, softmax_scale,
  * causal, window_left: as in vfa_varlen_fwd (softmax_scale must be > 0).
  * dq            device bf16 [total_q, num_heads, head_dim] (output).

@@ -250,3 +250,26 @@ def test_backward_calls_in_a_row_share_a_workspace(vfa, sinks):
             vfa.varlen_bwd(*a, window_left=100, sink_tokens=sinks, dq=g[0], dk=g[1], dv=g[2], workspace=ws)
     assert vfa.read_status(ws) == 0
     assert all(torch.equal(x, y) for w, g in zip(want, got) for x, y in zip(w, g))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal,window,sinks", [(2, -1, 0), (2, 30, 0), (2, 30, 3), (1, 30, 0), (0, -1, 0)])
+@pytest.mark.parametrize("value", [-float("inf"), float("inf")])
+def test_backward_of_rows_that_see_nothing(vfa, d, causal, window, sinks, value):
+    """What a logsumexp of nothing is elsewhere is no less than -FLT_MAX here: zero gradients."""
+    c = _case([300, 64, 40], [130, 64, 0], 4, 2, d, seed=d)
+    q, k, v, cq, ck = _dev(c)
+    out, lse = _forward(vfa, c, causal, window, sinks)
+    empty = lse == -FLT_MAX
+    assert empty.any() and not empty.all()
+    dout = W.upstream_grad(c, 5).cuda()
+
+    def grads(lse):
+        *g, ws = vfa.varlen_bwd(q, k, v, out, dout, lse, cq, ck, c.softmax_scale, causal, window_left=window,
+                                sink_tokens=sinks)
+        assert vfa.read_status(ws) == 0
+        return g
+
+    want, got = grads(lse), grads(torch.where(empty, value, lse))
+    assert all(t.isfinite().all() for t in want) and not want[0][empty].any()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))

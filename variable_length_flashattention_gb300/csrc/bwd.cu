@@ -281,10 +281,11 @@ __device__ __forceinline__ void query_row_span(long long i, long long j_base, in
     *hi = clamp_col(h);
 }
 
-// -lse log2(e); of a row without visible keys (lse = -FLT_MAX), whose scores are all hidden, 0
+// -lse log2(e); of a row without visible keys (lse = -FLT_MAX, or -inf from elsewhere), whose
+// scores are all hidden, 0
 __device__ __forceinline__ float neg_lse(float lse)
 {
-    return lse == -FLT_MAX ? 0.f : -lse * kLog2e;
+    return lse <= -FLT_MAX ? 0.f : -lse * kLog2e;
 }
 
 // P^T and dS^T of this thread's key row over its NC query columns: p =
