@@ -474,11 +474,9 @@ vfa_status vfa_paged_decode_finalize(const float *l, const float *o, int num_seq
  * workspace    device scratch of vfa_paged_decode_workspace_bytes() bytes,
  *              256-byte aligned, with the capacity (0: without key_weights).
  *              It must hold zeros before its first use; every call leaves what
- *              has to be zero that way.  A workspace made for num_seqs
- *              sequences and a capacity serves smaller ones with the same
- *              heads and head_dim too, and calls without key_weights; one made
- *              with capacity 0 is not for calls with them.  Calls sharing it
- *              must be stream-ordered.
+ *              has to be zero that way.  It serves every call with the same
+ *              heads and head_dim that asks for no more bytes, with and
+ *              without key_weights.  Calls sharing it must be stream-ordered.
  * Device-detected: a token count out of range or a page id outside [0,
  * num_blocks) among those it reads stores VFA_ERR_BAD_BLOCK in device_status
  * (nullable device int32 [1], the first error is kept) and leaves that

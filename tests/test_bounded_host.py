@@ -84,6 +84,17 @@ def test_paged_decode(vfa):
     assert size(4, 8, 2, 128, 3) - size(4, 8, 2, 128, 0) >= 4 * 8 * (8 + 3 * 16 * 4)
 
 
+def test_paged_decode_workspace_without_room_for_logits(vfa):
+    """A workspace made without key weights, however many sequences it is for, is too small with them."""
+    size = vfa.lib().vfa_paged_decode_workspace_bytes
+    for d in (64, 128, 256):
+        none = size(4096, 32, 8, d, 0)
+        assert none < size(1, 32, 8, d, 1)
+        good = [FAKE, FAKE, FAKE, 10, FAKE, 1, FAKE, 1, 32, 8, d, -1, 0, 0.1, FAKE, FAKE, FAKE, FAKE, NUL,
+                FAKE, none, NUL]
+        _calls(vfa, "vfa_paged_decode", good, [(20, none, vfa.VFA_ERR_INVALID_ARG, b"workspace too small")])
+
+
 def test_key_weights(vfa):
     bad, uns = vfa.VFA_ERR_INVALID_ARG, vfa.VFA_ERR_UNSUPPORTED
     good = [FAKE] * 5 + [4, 4, 4, 1, 2, 2, 128, 0.1, 1, 8, 4, FAKE, FAKE, 10, FAKE, 1 << 30, NUL]

@@ -143,6 +143,29 @@ def test_decode_of_many_and_of_long_sequences(vfa):
         assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+def test_decode_workspace_between_calls_of_all_kinds(vfa):
+    """One workspace for many short sequences, for few with long rows and key weights, and again: what
+    the one leaves there is never what the other counts with."""
+    cases = []
+    for lens, weights in (([400 + 7 * i for i in range(40)], False), ([5000], True), ([1300, 9], True),
+                          ([60] * 300, True), ([100] * 60, False)):
+        k, v, tables, rng = _cache(lens, 2, 64, seed=len(lens))
+        q = torch.from_numpy(rng.standard_normal((len(lens), 8, 64))).bfloat16()
+        cases.append(((q, k, v, tables), lens, weights))
+    size = max(vfa.alloc_paged_decode_workspace(len(lens), 8, 2, 64, c[3].shape[1] if weights else 0).numel()
+               for c, lens, weights in cases)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for (q, k, v, tables), lens, weights in cases + cases[::-1]:
+        args = (q.cuda(), k.cuda(), v.cuda(), _i32(tables), _i32(lens))
+        w = torch.zeros(len(lens), 2, 16 * tables.shape[1], device="cuda")
+        # (the bytes a call asks for, and all there are)
+        need = vfa.alloc_paged_decode_workspace(len(lens), 8, 2, 64, tables.shape[1] if weights else 0).numel()
+        for n in (need, size):
+            nan = torch.full_like(args[0], float("nan"))
+            got = vfa.paged_decode(*args, key_weights=w if weights else None, workspace=ws[:n], out=nan)
+            _check_decode((q, k, v, tables), lens, -1, 0, 0.0, got)
+
+
 @pytest.mark.parametrize("scale", [1e-30, 0.01, 1.0, 30.0])
 def test_decode_scales(vfa, scale):
     lens = [200, 31]

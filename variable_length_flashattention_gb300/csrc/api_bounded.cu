@@ -143,7 +143,7 @@ vfa_status vfa_paged_decode(const void *q, const void *k_pool, const void *v_poo
         1.4426950408889634;
     a.scale_log2 = scale_log2 > FLT_MAX ? FLT_MAX
                                         : (scale_log2 < FLT_MIN ? FLT_MIN : static_cast<float>(scale_log2));
-    return launched(vfa::launch_paged_decode(head_dim, a, workspace, workspace_bytes, sms,
+    return launched(vfa::launch_paged_decode(head_dim, a, workspace, sms,
                                              reinterpret_cast<cudaStream_t>(stream)),
                     "paged decode launch");
 }

@@ -321,7 +321,7 @@ struct PagedDecodeArgs {
     long long weight_stride;
     int32_t *status;                        // nullable
     float *part;                            // workspace: partial states
-    int32_t *tickets;                       // workspace: [num_seqs, head chunks], zero between calls
+    int32_t *tickets;                       // workspace: [head chunks, runs], zero between calls
     float2 *ml;                             // workspace: reference and sum, [num_seqs, num_q_heads]
     float *logits;                          // workspace: [num_seqs, num_kv_heads, max_pages, 16, group]
     int num_seqs, capacity, num_blocks, num_q_heads, num_kv_heads;
@@ -333,8 +333,8 @@ struct PagedDecodeArgs {
 // capacity > 0: with room for the logits of key weights.
 size_t paged_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                     int capacity);
-cudaError_t launch_paged_decode(int head_dim, PagedDecodeArgs &a, void *workspace,
-                                size_t workspace_bytes, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_decode(int head_dim, PagedDecodeArgs &a, void *workspace, int sm_count,
+                                cudaStream_t stream);
 
 // ------------------------------------------------------------ eviction
 

@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) paged_decode_kernel(co
             // runs with pages of this sequence
             const int p0 = seg.at + kSeqUnits;
             const int xa = p0 / run, parts = (p0 + v.pages - 1) / run - xa + 1;
-            int32_t *ticket = a.tickets + static_cast<long long>(s) * gridDim.y + blockIdx.y;
+            // (a run holds the first pages of one such sequence at most)
+            int32_t *ticket = a.tickets + static_cast<long long>(blockIdx.y) * gridDim.x + xa;
             __syncthreads();                        // every thread's part is written
             if (tid == 0) {
                 __threadfence();
@@ -789,26 +790,28 @@ int head_rows(int num_q_heads, int num_kv_heads)
     return num_kv_heads * ((num_q_heads / num_kv_heads + kTile - 1) / kTile);
 }
 
-// The workspace: partial states, tickets, then m and l of every row and the
-// logits.  Where the tickets start does not depend on the number of sequences.
-size_t part_bytes(int rows, int head_dim)
+// The workspace: a ticket per run, which has to be zero between calls; partial states, two
+// per run; m and l of every row, and the logits.  Where each starts depends on the heads
+// alone, so that no call's scores reach into the tickets of another, whatever their
+// sequences and capacities.
+size_t runs_of(int rows) { return rows > kMaxCtas ? rows : kMaxCtas; }      // in all rows
+
+size_t ticket_bytes(int rows)
 {
-    const size_t runs = rows > kMaxCtas ? rows : kMaxCtas;      // in all rows
-    return (runs * 2 * kTile * (head_dim + 4) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+    return (runs_of(rows) * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
 }
 
-// m and l of every row, and the logits.  They stand at the end of the workspace:
-// a smaller batch's do not reach into a larger one's tickets, which have to stay zero.
+size_t part_bytes(int rows, int head_dim)
+{
+    return (runs_of(rows) * 2 * kTile * (head_dim + 4) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+
+// m and l of every row, and the logits.
 size_t score_bytes(int num_seqs, int num_q_heads, int capacity)
 {
     return (static_cast<size_t>(num_seqs) * num_q_heads *
                 (sizeof(float2) + static_cast<size_t>(capacity) * kPage * sizeof(float)) +
             255) & ~static_cast<size_t>(255);
-}
-
-size_t ticket_bytes(int num_seqs, int rows)
-{
-    return (static_cast<size_t>(num_seqs) * rows * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
 }
 
 }  // namespace
@@ -817,22 +820,21 @@ size_t paged_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_he
                                     int capacity)
 {
     const int rows = head_rows(num_q_heads, num_kv_heads);
-    size_t n = part_bytes(rows, head_dim) + ticket_bytes(num_seqs, rows);
+    size_t n = ticket_bytes(rows) + part_bytes(rows, head_dim);
     if (capacity > 0)
         n += score_bytes(num_seqs, num_q_heads, capacity);
     return n;
 }
 
-cudaError_t launch_paged_decode(int head_dim, PagedDecodeArgs &a, void *workspace,
-                                size_t workspace_bytes, int sm_count, cudaStream_t stream)
+cudaError_t launch_paged_decode(int head_dim, PagedDecodeArgs &a, void *workspace, int sm_count,
+                                cudaStream_t stream)
 {
     const int rows = head_rows(a.num_q_heads, a.num_kv_heads);
     uint8_t *p = static_cast<uint8_t *>(workspace);
-    a.part = reinterpret_cast<float *>(p);
-    a.tickets = reinterpret_cast<int32_t *>(p + part_bytes(rows, head_dim));
+    a.tickets = reinterpret_cast<int32_t *>(p);
+    a.part = reinterpret_cast<float *>(p += ticket_bytes(rows));
     if (a.weights) {
-        p += (workspace_bytes - score_bytes(a.num_seqs, a.num_q_heads, a.capacity)) & ~static_cast<size_t>(255);
-        a.ml = reinterpret_cast<float2 *>(p);
+        a.ml = reinterpret_cast<float2 *>(p += part_bytes(rows, head_dim));
         a.logits = reinterpret_cast<float *>(p + static_cast<size_t>(a.num_seqs) * a.num_q_heads * sizeof(float2));
     }
     // pages a sequence reads at most
