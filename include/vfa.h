@@ -829,7 +829,9 @@ vfa_status vfa_pages_truncate(const int32_t *refcounts, int num_blocks, const in
  *              may be the same; entries past a sequence's keys are left as they
  *              were.  row_stride is at least the longest key length.
  * workspace    device scratch of vfa_varlen_key_weights_workspace_bytes()
- *              bytes, 256-byte aligned; its first int32 is the device status
+ *              bytes (at most 20 MB or 1 KB per key, and 8 bytes per key and
+ *              head), 256-byte aligned; one made for some sizes serves smaller
+ *              ones with as many heads.  Its first int32 is the device status
  *              word: VFA_ERR_BAD_SEQLENS (bad cu_seqlens, a q length above
  *              max_seqlen_q, more keys than row_stride; nothing is written) or
  *              VFA_ERR_TIMEOUT.  Calls sharing it must be stream-ordered.

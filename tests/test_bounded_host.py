@@ -84,6 +84,41 @@ def test_paged_decode(vfa):
     assert size(4, 8, 2, 128, 3) - size(4, 8, 2, 128, 0) >= 4 * 8 * (8 + 3 * 16 * 4)
 
 
+def _key_weight_partials(lq, lk, total_q, total_k, most_q, heads, kv_heads, step):
+    """Bytes of the partial sums of a batch, by the rule of its chunks' length."""
+    pairs = total_k // 256 + 1
+    chunks = max(128, 16 * 608 // pairs)
+    steps = -(-min(total_q, most_q) // 64) * heads
+    per = max(16 if heads * pairs < 608 else 128, -(-steps // chunks))
+    longest = max(-(-(-(-n // step) * (heads // kv_heads)) // per) for n in lq)
+    return 2 * longest * kv_heads * total_k * 4
+
+
+def test_key_weights_workspace_serves_smaller_calls(vfa):
+    """It covers the partial sums of every batch of its sizes and of smaller ones with as many heads, and
+    does not grow with the square of a prompt."""
+    import random
+    rng = random.Random(2)
+    size = vfa.lib().vfa_varlen_key_weights_workspace_bytes
+    assert size(1, 8192, 8192, 8192, 32) >= size(1, 4607, 4607, 4607, 32)
+    assert size(1, 4864, 4864, 4864, 32) >= size(1, 4863, 4863, 4863, 32)
+    for n in (1 << 17, 1 << 20):
+        assert size(1, n, n, n, 32) <= n * 8 * (128 + 32) + 4096        # 168 MB at 131072 tokens
+    assert size(2, 100, 50, 1 << 30, 4) == size(2, 100, 50, 100, 4)     # no query length is above all of them
+    for _ in range(3000):
+        heads = rng.choice([1, 2, 7, 8, 32, 64, 700])
+        kv_heads = rng.choice([h for h in range(1, heads + 1) if heads % h == 0])
+        n = rng.randint(1, 5)
+        lens = lambda: [int(2 ** rng.uniform(0, 20)) * rng.randint(0, 1) for _ in range(n)]
+        lq, lk = lens(), lens()
+        tq, tk, most = sum(lq), sum(lk), max(lq)
+        have = size(n, tq, tk, most, heads)
+        assert have - 8 * (n + 1) >= max(_key_weight_partials(lq, lk, tq, tk, most, heads, kv_heads, step)
+                                         for step in (64, 128))
+        bigger = [x + rng.choice([0, 1, 255, 5000, 1 << 18]) for x in (n, tq, tk, most)]
+        assert size(*bigger, heads) >= have
+
+
 def test_paged_decode_workspace_without_room_for_logits(vfa):
     """A workspace made without key weights, however many sequences it is for, is too small with them."""
     size = vfa.lib().vfa_paged_decode_workspace_bytes

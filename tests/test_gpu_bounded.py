@@ -313,6 +313,37 @@ def test_key_weights_sum_to_the_queries(vfa):
     assert np.allclose(_f64(w).sum(-1), [[2800, 2800], [360, 360]], rtol=1e-5)
 
 
+def test_key_weights_by_one_workspace(vfa):
+    """A workspace for the largest call, whose chunks are long ones, in smaller ones of either length of
+    chunk and of longer chunks still; none writes past the bytes it asks for.  Against sums over
+    every query in 64 bits, for some of the keys."""
+    hq, hkv, d, scale = 8, 2, 64, 0.125
+    calls = [([140000], [19700]), ([9000, 20000], [12000, 7700]), ([300, 5], [19456, 3]), ([140000], [700]),
+             ([2000], [2000]), ([17, 0, 129], [400, 3, 129])]
+    ws = vfa.alloc_key_weights_workspace(3, 140000, 19700, 140000, hq)
+    for i, (lq, lk) in enumerate(calls + calls[::-1]):
+        gen = torch.Generator(device="cuda").manual_seed(i)
+        q, k = (torch.randn(sum(n), h, d, device="cuda", generator=gen).bfloat16() for n, h in ((lq, hq), (lk, hkv)))
+        lse = 11.0 + torch.rand(sum(lq), hq, device="cuda", generator=gen)
+        cq, ck = W.cu_seqlens(lq), W.cu_seqlens(lk)
+        need = vfa.lib().vfa_varlen_key_weights_workspace_bytes(len(lq), sum(lq), sum(lk), max(lq), hq)
+        assert need <= ws.numel()
+        ws.fill_(0xff)
+        got = vfa.varlen_key_weights(q, k, lse, _i32(cq), _i32(ck), max(lq), scale, 0,
+                                     torch.zeros(len(lq), hkv, max(lk), device="cuda"), workspace=ws[:need])
+        assert vfa.read_status(ws) == 0 and (ws[need:] == 0xff).all()
+        for b in range(len(lq)):
+            at = torch.randint(0, lk[b], (40,), device="cuda", generator=gen)
+            for h in range(hkv):
+                qb = q[cq[b]:cq[b + 1], 4 * h:4 * h + 4].double().reshape(-1, d)
+                kb = k[ck[b] + at, h].double()
+                x = qb @ kb.T * scale
+                p = torch.exp(x - lse[cq[b]:cq[b + 1], 4 * h:4 * h + 4].double().reshape(-1, 1)).sum(0)
+                dx = (d + 16) * U * float((qb.abs() @ kb.abs().T).amax() if len(qb) else 0) * scale + 2.0 ** -22 * 12
+                bound = (np.expm1(dx) + (len(qb) + 2) * U + 2.0 ** -19) * p
+                assert ((got[b, h, at].double() - p).abs() <= bound).all()
+
+
 def test_key_weights_refuse_bad_lengths(vfa):
     c = _prompt([64, 64], [64, 64], 2, 2, 64, 1)
     q, k = c.q.cuda(), c.k.cuda()

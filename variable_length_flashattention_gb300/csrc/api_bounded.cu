@@ -153,7 +153,7 @@ size_t vfa_varlen_key_weights_workspace_bytes(int batch, int total_q, int total_
 {
     if (batch < 1 || total_q < 0 || total_k < 0 || max_seqlen_q < 0 || num_heads < 1)
         return 0;
-    return vfa::key_weights_workspace_bytes(batch, total_k, max_seqlen_q, num_heads);
+    return vfa::key_weights_workspace_bytes(batch, total_q, total_k, max_seqlen_q, num_heads);
 }
 
 vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse,
@@ -196,7 +196,7 @@ vfa_status vfa_varlen_key_weights(const void *q, const void *k, const float *lse
         return fail(VFA_ERR_UNSUPPORTED, "tensor too large");
     vfa_status st = check_workspace(
         workspace, workspace_bytes,
-        vfa::key_weights_workspace_bytes(batch, total_k, max_seqlen_q, num_heads));
+        vfa::key_weights_workspace_bytes(batch, total_q, total_k, max_seqlen_q, num_heads));
     if (st)
         return st;
     int sms;

@@ -304,7 +304,7 @@ struct KeyWeightArgs {
 // Queries of a step: the rows of a box of tm_q.
 __host__ __device__ constexpr int key_weights_rows(int head_dim) { return head_dim == 256 ? 64 : 128; }
 
-size_t key_weights_workspace_bytes(int batch, int total_k, int max_seqlen_q, int num_heads);
+size_t key_weights_workspace_bytes(int batch, int total_q, int total_k, int max_seqlen_q, int num_heads);
 cudaError_t launch_key_weights(int head_dim, KeyWeightArgs &a, void *workspace, int sm_count,
                                cudaStream_t stream);
 

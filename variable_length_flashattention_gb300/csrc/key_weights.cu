@@ -550,10 +550,44 @@ __global__ void __launch_bounds__(kTiles * kOwn) kw_sum_kernel(const KeyWeightAr
     }
 }
 
-// Steps of a unit: many, but where that leaves SMs without a unit.
-int chunk_steps_for(int total_k, int num_heads)
+// Steps of a unit: 128, or 16 where that leaves SMs without a unit; more where a prompt
+// would have over most_chunks() of them, since every chunk costs 8 bytes per key and kv head
+// (one prompt of 131072 tokens with 32 heads: 168 MB instead of 570).
+constexpr int kChunks = 128;                // of the longest prompt in all kv heads, where
+constexpr int kChunkPairs = 16 * kFewUnits; // this many (pair, chunk) are no fewer
+
+long long most_chunks(int total_k)
 {
-    return static_cast<long long>(num_heads) * (total_k / (kTiles * kOwn) + 1) < kFewUnits ? 16 : 128;
+    const long long pairs = total_k / (kTiles * kOwn) + 1;
+    return std::max<long long>(kChunks, kChunkPairs / pairs);
+}
+
+bool few_pairs(int total_k, int num_heads)
+{
+    return static_cast<long long>(num_heads) * (total_k / (kTiles * kOwn) + 1) < kFewUnits;
+}
+
+// Steps of the longest prompt in all heads, of 64 queries (the fewest a step has).
+long long steps_of(int total_q, int max_seqlen_q, int num_heads)
+{
+    return (static_cast<long long>(std::min(total_q, max_seqlen_q)) + 63) / 64 * num_heads;
+}
+
+int chunk_steps_for(int total_q, int total_k, int max_seqlen_q, int num_heads)
+{
+    const long long most = most_chunks(total_k);
+    const long long per = (steps_of(total_q, max_seqlen_q, num_heads) + most - 1) / most;
+    return static_cast<int>(std::max<long long>(few_pairs(total_k, num_heads) ? 16 : 128, per));
+}
+
+// Partial sums for chunks of `base` steps or more: each kv head has
+// steps / base or most_chunks() whole ones, and one that is not.  No less for a larger total_k.
+long long partials(long long steps, int base, int total_k, int num_heads)
+{
+    const double whole = std::min(static_cast<double>(steps / base) * total_k,
+                                  std::max(static_cast<double>(kChunks) * total_k,
+                                           static_cast<double>(kChunkPairs) * kTiles * kOwn));
+    return static_cast<long long>(whole) + static_cast<long long>(num_heads) * total_k;
 }
 
 template <int D>
@@ -588,13 +622,17 @@ size_t list_bytes(int batch)
 
 }  // namespace
 
-size_t key_weights_workspace_bytes(int batch, int total_k, int max_seqlen_q, int num_heads)
+size_t key_weights_workspace_bytes(int batch, int total_q, int total_k, int max_seqlen_q, int num_heads)
 {
-    // chunks of the longest sequence in all kv heads, whose steps are those of the
-    // query heads (of 64 queries at least): ceil(steps / per) in each kv head
-    const int per = chunk_steps_for(total_k, num_heads);
-    const long long steps = (static_cast<long long>(max_seqlen_q) + 63) / 64 * num_heads;
-    return list_bytes(batch) + 2 * static_cast<size_t>(steps / per + num_heads) * total_k * sizeof(float);
+    // room for long chunks, and for short ones of as many keys as have them: a
+    // workspace serves smaller calls too
+    const long long steps = steps_of(total_q, max_seqlen_q, num_heads);
+    const long long short_pairs = (kFewUnits - 1) / num_heads;         // few_pairs() up to here
+    const int short_k = static_cast<int>(std::min<long long>(total_k, short_pairs * kTiles * kOwn - 1));
+    long long most = partials(steps, 128, total_k, num_heads);
+    if (short_k > 0)
+        most = std::max(most, partials(steps, 16, short_k, num_heads));
+    return list_bytes(batch) + 2 * static_cast<size_t>(most) * sizeof(float);
 }
 
 cudaError_t launch_key_weights(int head_dim, KeyWeightArgs &a, void *workspace, int sm_count,
@@ -605,7 +643,7 @@ cudaError_t launch_key_weights(int head_dim, KeyWeightArgs &a, void *workspace, 
     a.pair_start = reinterpret_cast<int32_t *>(p + 256);
     a.unit_start = a.pair_start + a.batch + 1;
     a.part = reinterpret_cast<float *>(p + list_bytes(a.batch));
-    a.chunk_steps = chunk_steps_for(a.total_k, a.num_heads);
+    a.chunk_steps = chunk_steps_for(a.total_q, a.total_k, a.max_seqlen_q, a.num_heads);
     a.step = key_weights_rows(head_dim);
     switch (head_dim) {
     case 64: return launch_d<64>(a, sm_count, stream);
