@@ -161,9 +161,35 @@ def _need(t: torch.Tensor, dtype, name: str):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _plain(t: torch.Tensor, dtype) -> bool:
-    """What _need asks for, in one expression (it says what is wrong)."""
-    return t.is_cuda and t.dtype is dtype and t.is_contiguous()
+def _plain(t: torch.Tensor, dtype, dev: int) -> bool:
+    """What _dense asks for, in one expression (it says what is wrong)."""
+    return t.get_device() == dev and t.dtype is dtype and t.is_contiguous()
+
+
+def _packed_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k):
+    """(total_q, H, D, total_k, Hkv, batch) of packed q and k, v, checked against each other."""
+    qshape, kshape = q.shape, k.shape
+    if (len(qshape) != 3 or kshape != v.shape or len(kshape) != 3 or qshape[2] != kshape[2] or
+            kshape[1] == 0 or qshape[1] % kshape[1] != 0):
+        raise ValueError("q, k, v must be [tokens, heads, head_dim]; k/v heads must divide q heads")
+    batch = cu_seqlens_q.numel() - 1
+    if cu_seqlens_k.numel() != batch + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+    return (*qshape, kshape[0], kshape[1], batch)
+
+
+def _shaped(t: torch.Tensor, dtype, shape, name: str, dev: int):
+    """A caller's tensor that is read or written whole."""
+    if not _plain(t, dtype, dev):
+        _dense(t, dtype, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _scratch(t: torch.Tensor, dev: int):
+    """A caller's workspace: its bytes are counted, of any type."""
+    if t.get_device() != dev or not t.is_contiguous():
+        _dense(t, t.dtype, "workspace", dev)
 
 
 def _int32(n, name) -> int:
@@ -213,36 +239,30 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     (bottom-right); window_left >= 0 adds a sliding window (needs causal), past
     which the first sink_tokens keys stay visible (vfa_varlen_fwd_sinks)."""
     bf16, i32 = torch.bfloat16, torch.int32
-    if not (_plain(q, bf16) and _plain(k, bf16) and _plain(v, bf16) and _plain(cu_seqlens_q, i32) and
-            _plain(cu_seqlens_k, i32)):
+    dev = torch._C._cuda_getDevice()
+    if not (_plain(q, bf16, dev) and _plain(k, bf16, dev) and _plain(v, bf16, dev) and
+            _plain(cu_seqlens_q, i32, dev) and _plain(cu_seqlens_k, i32, dev)):
         for t, d, n in ((q, bf16, "q"), (k, bf16, "k"), (v, bf16, "v"),
                         (cu_seqlens_q, i32, "cu_seqlens_q"), (cu_seqlens_k, i32, "cu_seqlens_k")):
-            _need(t, d, n)
-    qshape, kshape = q.shape, k.shape
-    if (len(qshape) != 3 or kshape != v.shape or len(kshape) != 3 or qshape[2] != kshape[2] or
-            qshape[1] % kshape[1] != 0):
-        raise ValueError("q, k, v must be [tokens, heads, head_dim]; k/v heads must divide q heads")
-    total_q, H, D = qshape
-    total_k, Hkv, _ = kshape
-    batch = cu_seqlens_q.numel() - 1
-    if cu_seqlens_k.numel() != batch + 1:
-        raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+            _dense(t, d, n, dev)
+    total_q, H, D, total_k, Hkv, batch = _packed_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
     if out is None:
         out = torch.empty_like(q)
-    elif not _plain(out, bf16):
-        _need(out, bf16, "out")
+    else:
+        _shaped(out, bf16, q.shape, "out", dev)
     if lse is None:
         lse = torch.empty((total_q, H), dtype=torch.float32, device=q.device)
-    elif not _plain(lse, torch.float32):
-        _need(lse, torch.float32, "lse")
+    else:
+        _shaped(lse, torch.float32, (total_q, H), "lse", dev)
     if workspace is None:
         workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q.device)
+    else:
+        _scratch(workspace, dev)
     ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
            total_q, total_k, int(max_seqlen_q), batch, H, Hkv, D, float(softmax_scale), int(causal),
            int(window_left))
     outs = (out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-            torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None
-            else stream.cuda_stream)
+            _raw_stream(stream, dev))
     if sink_tokens != 0:
         st = (_lib or lib()).vfa_varlen_fwd_sinks(*ins, _int32(sink_tokens, "sink_tokens"), *outs)
     else:
@@ -259,24 +279,23 @@ def varlen_fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor,
                    workspace: Optional[torch.Tensor] = None, stream=None,
                    window_left: int = -1):
     """vfa_varlen_fwd_fp8: q8, k8 uint8 E4M3 codes [T, H(kv), 128], v bf16; returns (out, lse)."""
-    for t, n in ((q8, "q8"), (k8, "k8")):
-        _need(t, torch.uint8, n)
-    _need(v, torch.bfloat16, "v")
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
-    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k")
-    if (q8.dim() != 3 or k8.shape != v.shape or q8.shape[2] != k8.shape[2] or
-            q8.shape[1] % k8.shape[1] != 0):
-        raise ValueError("q8 [Tq, H, D], k8 and v [Tk, Hkv, D] with Hkv dividing H")
-    total_q, H, D = q8.shape
-    total_k, Hkv = k8.shape[0], k8.shape[1]
-    batch = cu_seqlens_q.numel() - 1
-    out = torch.empty(q8.shape, dtype=torch.bfloat16, device=q8.device) if out is None else out
+    dev = _device(q8, "q8")
+    for t, d, n in ((q8, _U8, "q8"), (k8, _U8, "k8"), (v, _BF16, "v"), (cu_seqlens_q, _I32, "cu_seqlens_q"),
+                    (cu_seqlens_k, _I32, "cu_seqlens_k")):
+        _dense(t, d, n, dev)
+    total_q, H, D, total_k, Hkv, batch = _packed_shapes(q8, k8, v, cu_seqlens_q, cu_seqlens_k)
+    if out is None:
+        out = torch.empty(q8.shape, dtype=torch.bfloat16, device=q8.device)
+    else:
+        _shaped(out, _BF16, q8.shape, "out", dev)
     if lse is None:
         lse = torch.empty((total_q, H), dtype=torch.float32, device=q8.device)
-    _need(out, torch.bfloat16, "out")
-    _need(lse, torch.float32, "lse")
+    else:
+        _shaped(lse, _F32, (total_q, H), "lse", dev)
     if workspace is None:
         workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q8.device)
+    else:
+        _scratch(workspace, dev)
     st = lib().vfa_varlen_fwd_fp8(_ptr(q8), _ptr(k8), _ptr(v), _ptr(cu_seqlens_q),
                                   _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q), batch,
                                   H, Hkv, D, float(softmax_scale), float(descale_q),
@@ -308,34 +327,39 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     """(dq, dk, dv) bf16 = gradients of varlen_fwd for upstream gradient dout (vfa_varlen_bwd;
     with sink_tokens vfa_varlen_bwd_sinks, and a workspace made for as many)."""
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    if not (_plain(q, bf16) and _plain(k, bf16) and _plain(v, bf16) and _plain(out, bf16) and
-            _plain(dout, bf16) and _plain(lse, f32) and _plain(cu_seqlens_q, i32) and
-            _plain(cu_seqlens_k, i32)):
+    dev = torch._C._cuda_getDevice()
+    if not (_plain(q, bf16, dev) and _plain(k, bf16, dev) and _plain(v, bf16, dev) and
+            _plain(out, bf16, dev) and _plain(dout, bf16, dev) and _plain(lse, f32, dev) and
+            _plain(cu_seqlens_q, i32, dev) and _plain(cu_seqlens_k, i32, dev)):
         for t, d, n in ((q, bf16, "q"), (k, bf16, "k"), (v, bf16, "v"), (out, bf16, "out"),
                         (dout, bf16, "dout"), (lse, f32, "lse"), (cu_seqlens_q, i32, "cu_seqlens_q"),
                         (cu_seqlens_k, i32, "cu_seqlens_k")):
-            _need(t, d, n)
-    if (q.dim() != 3 or k.shape != v.shape or out.shape != q.shape or dout.shape != q.shape or
-            q.shape[2] != k.shape[2] or q.shape[1] % k.shape[1] != 0):
-        raise ValueError("q, out, dout [Tq, H, D] and k, v [Tk, Hkv, D] with Hkv dividing H")
-    total_q, H, D = q.shape
-    total_k, Hkv = k.shape[0], k.shape[1]
-    batch = cu_seqlens_q.numel() - 1
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        if not _plain(t, bf16):
-            _need(t, bf16, n)
+            _dense(t, d, n, dev)
+    total_q, H, D, total_k, Hkv, batch = _packed_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    if out.shape != q.shape or dout.shape != q.shape or lse.shape != (total_q, H):
+        raise ValueError("out and dout must have q's shape [Tq, H, D] and lse [Tq, H]")
+    if dq is None:
+        dq = torch.empty_like(q)
+    else:
+        _shaped(dq, bf16, q.shape, "dq", dev)
+    if dk is None:
+        dk = torch.empty_like(k)
+    else:
+        _shaped(dk, bf16, k.shape, "dk", dev)
+    if dv is None:
+        dv = torch.empty_like(v)
+    else:
+        _shaped(dv, bf16, v.shape, "dv", dev)
     if workspace is None:
         workspace = alloc_bwd_workspace(batch, total_q, H, D, device=q.device,
                                         sink_tokens=max(sink_tokens, 0))
+    else:
+        _scratch(workspace, dev)
     ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
            cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), total_q, total_k, batch, H, Hkv, D,
            float(softmax_scale), int(causal), int(window_left))
     outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-            torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None
-            else stream.cuda_stream)
+            _raw_stream(stream, dev))
     if sink_tokens != 0:
         st = (_lib or lib()).vfa_varlen_bwd_sinks(*ins, _int32(sink_tokens, "sink_tokens"), *outs)
     else:
@@ -356,16 +380,18 @@ def varlen_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     inputs and outputs (allocated however it likes); the library allocates
     nothing.  Calls that can overlap on the GPU must not use it concurrently.
     """
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        _need(t, torch.bfloat16, n)
-    _need(lse, torch.float32, "lse")
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
-    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k")
-    total_q, H, D = q.shape
+    dev = _device(q, "q")
+    for t, d, n in ((q, _BF16, "q"), (k, _BF16, "k"), (v, _BF16, "v"), (cu_seqlens_q, _I32, "cu_seqlens_q"),
+                    (cu_seqlens_k, _I32, "cu_seqlens_k")):
+        _dense(t, d, n, dev)
+    total_q, H, D, total_k, Hkv, batch = _packed_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    _shaped(out, _BF16, q.shape, "out", dev)
+    _shaped(lse, _F32, (total_q, H), "lse", dev)
+    if device_status is not None:
+        _dense(device_status, _I32, "device_status", dev)
     st = lib().vfa_varlen_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
-                                      _ptr(cu_seqlens_k), total_q, k.shape[0], int(max_seqlen_q),
-                                      cu_seqlens_q.numel() - 1, H, k.shape[1], D,
-                                      float(softmax_scale),
+                                      _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q),
+                                      batch, H, Hkv, D, float(softmax_scale),
                                       int(causal), int(window_left), _ptr(out), _ptr(lse),
                                       _ptr(device_status),
                                       _stream(stream))
