@@ -28,3 +28,28 @@ def test_refused_lengths_with_any_workspace(vfa, d, fill):
         vfa.varlen_fwd(q, q, q, cq, ck, 128, 0.1, 1, out=out, workspace=ws, window_left=window)
         assert vfa.read_status(ws) == vfa.VFA_ERR_BAD_SEQLENS
         assert (out == 7.0).all()
+
+
+def test_workspaces_of_a_call_belong_to_its_stream(vfa, monkeypatch):
+    """A call on a stream of its own makes its workspace there: the block is handed out again behind
+    the kernels that still use it, not to what runs beside them."""
+    made = []
+    for name in ("alloc_workspace", "alloc_bwd_workspace"):
+        def alloc(*args, plain=getattr(vfa, name), **kw):
+            made.append(torch.cuda.current_stream())
+            return plain(*args, **kw)
+        monkeypatch.setattr(vfa, name, alloc)
+    q = torch.ones(70, 2, 64, device="cuda", dtype=torch.bfloat16)
+    q8 = torch.full((70, 2, 64), 0x30, device="cuda", dtype=torch.uint8)
+    cu = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, None):
+        want = [stream or torch.cuda.current_stream()]
+        out, lse = vfa.varlen_fwd(q, q, q, cu, cu, 70, 0.1, 1, stream=stream)
+        vfa.varlen_fwd_fp8(q8, q8, q, cu, cu, 70, 0.1, 1.0, 1.0, 1, stream=stream)
+        vfa.varlen_bwd(q, q, q, out, q, lse, cu, cu, 0.1, 1, stream=stream)
+        vfa.varlen_bwd(q, q, q, out, q, lse, cu, cu, 0.1, 1, window_left=9, sink_tokens=2, stream=stream)
+        assert made == 4 * want
+        made.clear()
+    torch.cuda.synchronize()

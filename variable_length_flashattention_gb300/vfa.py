@@ -255,7 +255,8 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     else:
         _shaped(lse, torch.float32, (total_q, H), "lse", dev)
     if workspace is None:
-        workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q.device)
+        with _of(stream):
+            workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q.device)
     else:
         _scratch(workspace, dev)
     ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
@@ -293,7 +294,8 @@ def varlen_fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor,
     else:
         _shaped(lse, _F32, (total_q, H), "lse", dev)
     if workspace is None:
-        workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q8.device)
+        with _of(stream):
+            workspace = alloc_workspace(batch, total_q, total_k, H, D, device=q8.device)
     else:
         _scratch(workspace, dev)
     st = lib().vfa_varlen_fwd_fp8(_ptr(q8), _ptr(k8), _ptr(v), _ptr(cu_seqlens_q),
@@ -351,8 +353,9 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     else:
         _shaped(dv, bf16, v.shape, "dv", dev)
     if workspace is None:
-        workspace = alloc_bwd_workspace(batch, total_q, H, D, device=q.device,
-                                        sink_tokens=max(sink_tokens, 0))
+        with _of(stream):
+            workspace = alloc_bwd_workspace(batch, total_q, H, D, device=q.device,
+                                            sink_tokens=max(sink_tokens, 0))
     else:
         _scratch(workspace, dev)
     ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
@@ -582,6 +585,12 @@ def _rows(t: torch.Tensor, shape, name: str, dev: int) -> int:
 
 def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _of(stream):
+    """Allocations belong to the stream the call's kernels run on: the block of a workspace that is
+    dropped on return is handed out again to work behind them, not beside them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -879,7 +888,7 @@ def kv4_decode(q: torch.Tensor, pool: torch.Tensor, tables: torch.Tensor,
     else:
         _dense(lse, _F32, "lse", dev)
     if workspace is None:
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _of(stream):
             workspace = alloc_kv4_decode_workspace(S, Hq, Hkv, D, device=q.device)
     else:
         _dense(workspace, _U8, "workspace", dev)
@@ -1154,7 +1163,7 @@ def paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, ta
     elif key_weights_out is not None:
         raise ValueError("key_weights_out needs key_weights")
     if workspace is None:
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _of(stream):
             workspace = alloc_paged_decode_workspace(S, Hq, Hkv, D, 0 if key_weights is None else cap,
                                                      device=q.device)
     else:
@@ -1213,7 +1222,7 @@ def varlen_key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
     _fits(Tq, Tk, H, D, batch)
     max_seqlen_q = _int32(max_seqlen_q, "max_seqlen_q")
     if workspace is None:
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _of(stream):
             workspace = alloc_key_weights_workspace(batch, Tq, Tk, max_seqlen_q, H, device=q.device)
     else:
         _dense(workspace, _U8, "workspace", dev)
