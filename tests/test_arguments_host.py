@@ -1,5 +1,6 @@
 """Arguments of the packed forward and backward that are refused before any work, without a GPU:
 the tensors here have shapes, types and a device, but no memory."""
+import types
 import warnings
 
 import pytest
@@ -9,6 +10,7 @@ from torch._subclasses.fake_tensor import FakeTensorMode
 from variable_length_flashattention_gb300 import vfa
 
 T, TK, H, HKV, D, B = 6, 8, 4, 2, 64, 2
+STREAM = types.SimpleNamespace(cuda_stream=0)
 
 
 @pytest.fixture(autouse=True)
@@ -16,11 +18,14 @@ def no_gpu(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
 
-    def never():
-        raise AssertionError("a call that should have been refused reached the library")
+    class Never:
+        def __getattr__(self, name):
+            def call(*args):
+                raise AssertionError(f"{name}: a call that should have been refused reached the library")
+            return call
 
-    monkeypatch.setattr(vfa, "_lib", None)
-    monkeypatch.setattr(vfa, "lib", never)
+    monkeypatch.setattr(vfa, "_lib", Never())
+    monkeypatch.setattr(vfa, "lib", Never)
     with warnings.catch_warnings():
         warnings.simplefilter("ignore")             # addresses of tensors without memory
         yield
@@ -40,18 +45,18 @@ def _inputs(fp8=False):
 def _fwd(qkv, cu, out=None, lse=None, workspace=None, most=T, causal=1, **kw):
     return vfa.varlen_fwd(*qkv, *cu, most, 0.1, causal, _t(T, H, D) if out is None else out,
                           _t(T, H, dtype=torch.float32) if lse is None else lse,
-                          _t(1 << 16, dtype=torch.uint8) if workspace is None else workspace, 0, **kw)
+                          _t(1 << 16, dtype=torch.uint8) if workspace is None else workspace, STREAM, **kw)
 
 
 def _fp8(qkv, cu, out=None, lse=None, workspace=None, most=T, causal=1, **kw):
     return vfa.varlen_fwd_fp8(*qkv, *cu, most, 0.1, 1.0, 1.0, causal, _t(T, H, D) if out is None else out,
                               _t(T, H, dtype=torch.float32) if lse is None else lse,
-                              _t(1 << 16, dtype=torch.uint8) if workspace is None else workspace, 0, **kw)
+                              _t(1 << 16, dtype=torch.uint8) if workspace is None else workspace, STREAM, **kw)
 
 
 def _noalloc(qkv, cu, out=None, lse=None, workspace=None, most=T, causal=1, **kw):
     return vfa.varlen_fwd_noalloc(*qkv, *cu, most, 0.1, causal, _t(T, H, D) if out is None else out,
-                                  _t(T, H, dtype=torch.float32) if lse is None else lse, workspace, 0, **kw)
+                                  _t(T, H, dtype=torch.float32) if lse is None else lse, workspace, STREAM, **kw)
 
 
 def _bwd(qkv, cu, out=None, lse=None, workspace=None, causal=1, dout=None, dq=None, dk=None, dv=None, **kw):
@@ -60,7 +65,7 @@ def _bwd(qkv, cu, out=None, lse=None, workspace=None, causal=1, dout=None, dq=No
                           _t(T, H, dtype=torch.float32) if lse is None else lse, *cu, 0.1, causal,
                           dq=give(dq, T, H, D), dk=give(dk, TK, HKV, D), dv=give(dv, TK, HKV, D),
                           workspace=_t(1 << 16, dtype=torch.uint8) if workspace is None else workspace,
-                          stream=0, **kw)
+                          stream=STREAM, **kw)
 
 
 CALLS = [(_fwd, False), (_fp8, True), (_noalloc, False), (_bwd, False)]
@@ -72,7 +77,8 @@ def test_tensors_that_do_not_fit_each_other(call, fp8):
     x = qkv[0].dtype
     f32, i32 = torch.float32, torch.int32
     for word, change in (
-            ("out", dict(out=_t(T - 1, H, D))), ("out", dict(out=_t(T, D, H))), ("out", dict(out=_t(T, H, D, dtype=f32))),
+            ("out", dict(out=_t(T - 1, H, D))), ("out", dict(out=_t(T, D, H))),
+            ("out", dict(out=_t(T, H, D, dtype=f32))),
             ("lse", dict(lse=_t(T, H - 1, dtype=f32))), ("lse", dict(lse=_t(T * H, dtype=f32))),
             ("lse", dict(lse=_t(T, H))), ("CUDA", dict(lse=_t(T, H, dtype=f32, device="cpu"))),
             ("CUDA", dict(out=_t(T, H, D, device="cpu")))):
@@ -120,3 +126,24 @@ def test_gradients_that_do_not_fit():
                          ("dv", dict(dv=_t(TK, HKV))), ("dout", dict(dout=_t(T + 1, H, D)))):
         with pytest.raises(ValueError, match=word):
             _bwd(qkv, cu, **change)
+
+
+@pytest.mark.parametrize("call,fp8", CALLS)
+def test_numbers_past_32_bits(call, fp8):
+    """A window larger than anything is refused, not cut to the 0 that its low bits are."""
+    qkv, cu = _inputs(fp8)
+    changes = [dict(window_left=1 << 32), dict(window_left=(1 << 32) - 1), dict(window_left=-(1 << 32)),
+               dict(causal=(1 << 32) + 1)]
+    changes += [dict(most=(1 << 32) + T)] if call is not _bwd else []
+    changes += [dict(sink_tokens=1 << 32)] if call in (_fwd, _bwd) else []
+    for change in changes:
+        with pytest.raises(ValueError, match="32 bits"):
+            call(qkv, cu, **change)
+
+
+@pytest.mark.parametrize("call,fp8", CALLS)
+def test_sizes_past_32_bits(call, fp8):
+    qkv, cu = _inputs(fp8)
+    qkv[0] = _t((1 << 32) + T, H, D, dtype=qkv[0].dtype)
+    with pytest.raises(ValueError, match="32 bits"):
+        call(qkv, cu)

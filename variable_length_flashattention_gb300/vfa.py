@@ -175,6 +175,7 @@ def _packed_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k):
     batch = cu_seqlens_q.numel() - 1
     if cu_seqlens_k.numel() != batch + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+    _fits(*qshape, kshape[0], batch)
     return (*qshape, kshape[0], kshape[1], batch)
 
 
@@ -260,12 +261,13 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     else:
         _scratch(workspace, dev)
     ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
-           total_q, total_k, int(max_seqlen_q), batch, H, Hkv, D, float(softmax_scale), int(causal),
-           int(window_left))
+           total_q, total_k, _int32(max_seqlen_q, "max_seqlen_q"), batch, H, Hkv, D, float(softmax_scale),
+           _int32(causal, "causal"), _int32(window_left, "window_left"))
     outs = (out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
             _raw_stream(stream, dev))
     if sink_tokens != 0:
-        st = (_lib or lib()).vfa_varlen_fwd_sinks(*ins, _int32(sink_tokens, "sink_tokens"), *outs)
+        sinks = _int32(sink_tokens, "sink_tokens")
+        st = (_lib or lib()).vfa_varlen_fwd_sinks(*ins, sinks, *outs)
     else:
         st = (_lib or lib()).vfa_varlen_fwd(*ins, *outs)
     if st:
@@ -299,10 +301,11 @@ def varlen_fwd_fp8(q8: torch.Tensor, k8: torch.Tensor, v: torch.Tensor,
     else:
         _scratch(workspace, dev)
     st = lib().vfa_varlen_fwd_fp8(_ptr(q8), _ptr(k8), _ptr(v), _ptr(cu_seqlens_q),
-                                  _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q), batch,
-                                  H, Hkv, D, float(softmax_scale), float(descale_q),
-                                  float(descale_k), int(causal), int(window_left), _ptr(out),
-                                  _ptr(lse), _ptr(workspace),
+                                  _ptr(cu_seqlens_k), total_q, total_k,
+                                  _int32(max_seqlen_q, "max_seqlen_q"), batch, H, Hkv, D,
+                                  float(softmax_scale), float(descale_q), float(descale_k),
+                                  _int32(causal, "causal"), _int32(window_left, "window_left"),
+                                  _ptr(out), _ptr(lse), _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st)
     return out, lse
@@ -360,11 +363,12 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
         _scratch(workspace, dev)
     ins = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
            cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), total_q, total_k, batch, H, Hkv, D,
-           float(softmax_scale), int(causal), int(window_left))
+           float(softmax_scale), _int32(causal, "causal"), _int32(window_left, "window_left"))
     outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.nbytes,
             _raw_stream(stream, dev))
     if sink_tokens != 0:
-        st = (_lib or lib()).vfa_varlen_bwd_sinks(*ins, _int32(sink_tokens, "sink_tokens"), *outs)
+        sinks = _int32(sink_tokens, "sink_tokens")
+        st = (_lib or lib()).vfa_varlen_bwd_sinks(*ins, sinks, *outs)
     else:
         st = (_lib or lib()).vfa_varlen_bwd(*ins, *outs)
     if st:
@@ -393,9 +397,10 @@ def varlen_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if device_status is not None:
         _dense(device_status, _I32, "device_status", dev)
     st = lib().vfa_varlen_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
-                                      _ptr(cu_seqlens_k), total_q, total_k, int(max_seqlen_q),
-                                      batch, H, Hkv, D, float(softmax_scale),
-                                      int(causal), int(window_left), _ptr(out), _ptr(lse),
+                                      _ptr(cu_seqlens_k), total_q, total_k,
+                                      _int32(max_seqlen_q, "max_seqlen_q"), batch, H, Hkv, D,
+                                      float(softmax_scale), _int32(causal, "causal"),
+                                      _int32(window_left, "window_left"), _ptr(out), _ptr(lse),
                                       _ptr(device_status),
                                       _stream(stream))
     _check(st)
@@ -416,8 +421,9 @@ def schedule(cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, total_q: in
     nbytes = workspace_bytes(batch, total_q, total_k, num_heads, 128)
     scratch = torch.empty((nbytes + 3) // 4, dtype=torch.int32, device=dev)
     st = lib().vfa_varlen_schedule(_ptr(cu_seqlens_q), _ptr(cu_seqlens_k), total_q, total_k,
-                                   int(max_seqlen_q), batch, num_heads, block_q, block_k,
-                                   int(causal), int(window_left), int(bool(pair)), _ptr(items),
+                                   _int32(max_seqlen_q, "max_seqlen_q"), batch, num_heads, block_q,
+                                   block_k, _int32(causal, "causal"),
+                                   _int32(window_left, "window_left"), int(bool(pair)), _ptr(items),
                                    cap,
                                    _ptr(n_items), _ptr(status), _ptr(scratch), scratch.numel() * 4,
                                    _stream(stream))
@@ -1228,8 +1234,8 @@ def varlen_key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
         _dense(workspace, _U8, "workspace", dev)
     st = (_lib or lib()).vfa_varlen_key_weights(
         q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(),
-        cu_seqlens_k.data_ptr(), Tq, Tk, max_seqlen_q, batch, H, Hkv, D, softmax_scale, int(causal),
-        _int32(window_left, "window_left"), _int32(sink_tokens, "sink_tokens"),
+        cu_seqlens_k.data_ptr(), Tq, Tk, max_seqlen_q, batch, H, Hkv, D, softmax_scale,
+        _int32(causal, "causal"), _int32(window_left, "window_left"), _int32(sink_tokens, "sink_tokens"),
         key_weights.data_ptr(), key_weights_out.data_ptr(), key_weights.shape[2],
         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if st:
