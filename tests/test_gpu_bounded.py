@@ -143,6 +143,19 @@ def test_decode_of_many_and_of_long_sequences(vfa):
         assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("group", [65, 72, 130])
+def test_decode_weights_of_many_query_heads(vfa, group):
+    """More query heads of a kv head than their sums wait in shared memory for."""
+    lens = [100, 1, 33]
+    k, v, tables, rng = _cache(lens, 2, 64, seed=group)
+    q = torch.from_numpy(rng.standard_normal((3, 2 * group, 64))).bfloat16()
+    w = torch.rand(3, 2, 16 * tables.shape[1], device="cuda")
+    old, w_out = torch.full_like(w, 3.0), torch.full_like(w, 3.0)
+    got = vfa.paged_decode(q.cuda(), k.cuda(), v.cuda(), _i32(tables), _i32(lens), 60, 3, key_weights=w,
+                           key_weights_out=w_out)
+    _check_decode((q, k, v, tables), lens, 60, 3, 0.0, got, (w, w_out, old))
+
+
 def test_decode_workspace_between_calls_of_all_kinds(vfa):
     """One workspace for many short sequences, for few with long rows and key weights, and again: what
     the one leaves there is never what the other counts with."""
@@ -433,6 +446,14 @@ def test_evict_again(vfa, in_place):
 def test_evict_long_rows(vfa):
     lens = [5000, 2049, 1024]
     _check_evict(vfa, _evict_case(lens, 2, 64, 4), lens, [1000, 2048, 100], 4, 64, True)
+
+
+@pytest.mark.parametrize("budgets", [[20000, 10000, 60000], [32999, 30001, 35001], [1, 0, 40000]])
+def test_evict_rows_past_shared_memory(vfa, budgets):
+    """More slots than the CTAs of a cluster keep the keys of: they wait where the lists of moves go."""
+    lens = [33000, 40000, 70001]
+    case = _evict_case(lens, 1, 64, 8, known=[0, 39000, 500], gone=[0, 5, 77])
+    _check_evict(vfa, case, lens, budgets, 4, 100, True)
 
 
 def test_evict_orders_every_float(vfa):
