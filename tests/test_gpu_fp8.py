@@ -142,3 +142,26 @@ def test_cross_attention_d64(vfa, oracle_mod, seed):
                                           f8.descale_q, f8.descale_k, 0)
     assert_out_close(out, ro, f"fp8 cross-d64 seed {seed}")
     assert_lse_close(lse, rl, f"fp8 cross-d64 seed {seed}")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal,window", [(0, -1), (1, -1), (1, 40)])
+def test_results_at_any_allowed_address(vfa, d, causal, window):
+    """Whole and ragged tiles to an output at a multiple of 16 bytes that is none of 32: the same bits,
+    and nothing around it or in tokens of no sequence's tile."""
+    lens = [200, 0, 129, 128, 1]
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    q, k, v = (torch.randn(sum(lens), h, d, device="cuda", generator=gen) for h in (4, 2, 2))
+    q8, k8 = ((x * 16).to(torch.float8_e4m3fn).view(torch.uint8) for x in (q, k))
+    cu = torch.tensor([0, 200, 200, 329, 457, 458], dtype=torch.int32, device="cuda")
+    args = (q8, k8, v.bfloat16(), cu, cu, 200, d ** -0.5, 1 / 16, 1 / 16, causal)
+    want, lse = vfa.varlen_fwd_fp8(*args, window_left=window)
+    flat = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:-8].view(q.shape)
+    assert want.data_ptr() % 32 == 0 and out.data_ptr() % 32 == 16
+    for _ in range(3):
+        out.fill_(7.0)
+        _, lse2 = vfa.varlen_fwd_fp8(*args, window_left=window, out=out)
+        assert torch.equal(out, want) and torch.equal(lse, lse2)
+        assert (flat[:8] == 7.0).all() and (flat[-8:] == 7.0).all()
+    assert want.isfinite().all()

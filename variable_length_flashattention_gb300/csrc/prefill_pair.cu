@@ -43,7 +43,10 @@
 //     stores, whose stages have to be read before they are written again, the
 //     epilogue took 3000 cycles of an item's 37000 (window of 1024), in which
 //     the tensor core had nothing to do: the long-tailed batch ran at 1451
-//     TFLOP/s, 1487 now;
+//     TFLOP/s, 1487 now.  With FP8 Q and K at head_dim 64 and no window the stages are
+//     the faster way (4 of 8192, causal, 16 heads: 606 us, 616 from the registers;
+//     64 single queries on up to 8000 keys: 261, 268; 16 causal of up to 2048: 96.7, 96.0)
+//     and stay;
 //   * TMEM: O_a, O_b (D columns each), S/P_a, S/P_b (128 columns each);
 //   * with a window, sinks (first keys that stay visible) are key tiles of
 //     their own ahead of the window's: an item's tiles are [0, sinks) and
@@ -88,8 +91,9 @@ struct PairCfg {
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 2 * D;              // S_x at S_COL + x * BK; O_x at x * D
     static constexpr int NUM_BARS = 4 + 4 * NS + 15;
+    static constexpr uint32_t WARP_STAGE = F8 && D == 64 ? 32 * 64 : 0;   // a warp's 32 rows x 32 outputs
     static constexpr size_t SMEM = 1024 + 2 * Q_BYTES + NS * (K_BYTES + KV_BYTES) +
-                                   NUM_BARS * 8 + 64;
+                                   8 * WARP_STAGE + NUM_BARS * 8 + 64;
     static constexpr uint32_t IDESC_QK =
         F8 ? idesc_e4m3_f32(BQ, BK) : idesc_bf16_f32(BQ, BK, false, false);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(BQ, D, false, true);
@@ -261,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sQ = base;                           // Q_a, Q_b
     const uint32_t sK = sQ + 2 * C::Q_BYTES;
     const uint32_t sV = sK + NS * C::K_BYTES;
-    const uint32_t bars = sV + NS * C::KV_BYTES;
+    const uint32_t sO = sV + NS * C::KV_BYTES;          // output staging, where there is one
+    const uint32_t bars = sO + 8 * C::WARP_STAGE;
     auto q_full = [&](int x) { return bars + 8u * x; };
     auto q_empty = [&](int x) { return bars + 8u * (2 + x); };
     auto k_full = [&](int i) { return bars + 8u * (4 + i); };
@@ -613,6 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t g = 0;                               // this slot's tiles so far
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
         const bool sectors = reinterpret_cast<uintptr_t>(out) % 32 == 0;
+        constexpr bool STAGED = F8 && D == 64 && WIN == 0;
+        const uint32_t wstage = sO + (warp - kFirstMathWarp) * C::WARP_STAGE;
         // A tile masked in place where it needs it, or (head_dim 64 without a window)
         // a plain and a masked form of it.
         constexpr bool IN_PLACE = D == 128 || WIN > 0;
@@ -814,37 +821,98 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv_l = l > 0.f ? 1.f / l : 0.f;
             if (row_valid)
                 p.lse[tok * H + h] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -FLT_MAX;
-            // O / l -> bf16: a thread's row, whole 32-byte sectors at a time (halves where
-            // `out` is not aligned to them).
-            uint32_t pk[D / 2];
+            if constexpr (STAGED) {
+                // 32 columns at a time through this warp's stage: each thread writes its row
+                // segment (swizzled as the 64-byte TMA swizzle lays it out, conflict-free).  A
+                // warp whose 32 rows all belong to the sequence then hands the chunk to a TMA
+                // tile store; otherwise (the sequence's last tile: rows past it belong to the
+                // next sequence) every store instruction writes eight whole 64-byte row
+                // segments of the rows that exist.
+                const int tile_rows = min(BQ, lq - i * BQ);
+                const bool warp_rows = quarter * 32 + 32 <= tile_rows;   // warp-uniform
+                __nv_bfloat16 *out_tile = out + ((static_cast<long long>(q0) + i * BQ) * H + h) * D;
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                uint32_t ra[32], rb[32];
-                tmem_ld32(o_addr + 64 * half, ra);
-                tmem_ld32(o_addr + 64 * half + 32, rb);
-                tmem_wait_ld_r(ra);
-                tmem_bind_r(rb);
+                for (int cb = 0; cb < D / 32; ++cb) {
+                    uint32_t rr[32];
+                    tmem_ld32(o_addr + cb * 32, rr);
+                    tmem_wait_ld_r(rr);
+                    // the stage's previous tile store has read it
+                    if (lane == 0)
+                        bulk_wait_group_read0();
+                    __syncwarp();
+                    const uint32_t row = wstage + lane * 64;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    pk[32 * half + e] = pack_bf16x2(__uint_as_float(ra[2 * e]) * inv_l,
-                                                    __uint_as_float(ra[2 * e + 1]) * inv_l);
-                    pk[32 * half + 16 + e] = pack_bf16x2(__uint_as_float(rb[2 * e]) * inv_l,
-                                                         __uint_as_float(rb[2 * e + 1]) * inv_l);
+                    for (int c = 0; c < 4; ++c)
+                        st_shared_v4(row + ((c ^ ((lane >> 1) & 3)) << 4),
+                                     pack_bf16x2(__uint_as_float(rr[8 * c + 0]) * inv_l,
+                                                 __uint_as_float(rr[8 * c + 1]) * inv_l),
+                                     pack_bf16x2(__uint_as_float(rr[8 * c + 2]) * inv_l,
+                                                 __uint_as_float(rr[8 * c + 3]) * inv_l),
+                                     pack_bf16x2(__uint_as_float(rr[8 * c + 4]) * inv_l,
+                                                 __uint_as_float(rr[8 * c + 5]) * inv_l),
+                                     pack_bf16x2(__uint_as_float(rr[8 * c + 6]) * inv_l,
+                                                 __uint_as_float(rr[8 * c + 7]) * inv_l));
+                    if (warp_rows) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&p.tm_o, wstage, cb * 32, h, q0 + i * BQ + quarter * 32);
+                            bulk_commit_group();
+                        }
+                    } else {
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int rw = 8 * k + (lane >> 2), ch = lane & 3;
+                            const int rt = quarter * 32 + rw;          // row within the tile
+                            const uint4 v =
+                                ld_shared_v4(wstage + rw * 64 + ((ch ^ ((rw >> 1) & 3)) << 4));
+                            if (rt < tile_rows)
+                                *reinterpret_cast<uint4 *>(out_tile + static_cast<long long>(rt) * H * D +
+                                                           cb * 32 + ch * 8) = v;
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else {
+                // O / l -> bf16: a thread's row, whole 32-byte sectors at a time (halves where
+                // `out` is not aligned to them).
+                uint32_t pk[D / 2];
+#pragma unroll
+                for (int half = 0; half < D / 64; ++half) {
+                    uint32_t ra[32], rb[32];
+                    tmem_ld32(o_addr + 64 * half, ra);
+                    tmem_ld32(o_addr + 64 * half + 32, rb);
+                    tmem_wait_ld_r(ra);
+                    tmem_bind_r(rb);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        pk[32 * half + e] = pack_bf16x2(__uint_as_float(ra[2 * e]) * inv_l,
+                                                        __uint_as_float(ra[2 * e + 1]) * inv_l);
+                        pk[32 * half + 16 + e] = pack_bf16x2(__uint_as_float(rb[2 * e]) * inv_l,
+                                                             __uint_as_float(rb[2 * e + 1]) * inv_l);
+                    }
+                }
+                if (row_valid) {
+                    __nv_bfloat16 *dst = out + (tok * H + h) * D;
+                    if (sectors) {
+#pragma unroll
+                        for (int e = 0; e < D / 2; e += 8)
+                            st_global_v8(dst + 2 * e, pk + e);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < D / 2; e += 4)
+                            *reinterpret_cast<uint4 *>(dst + 2 * e) =
+                                make_uint4(pk[e], pk[e + 1], pk[e + 2], pk[e + 3]);
+                    }
                 }
             }
-            if (row_valid) {
-                __nv_bfloat16 *dst = out + (tok * H + h) * D;
-                if (sectors) {
-#pragma unroll
-                    for (int e = 0; e < D / 2; e += 8)
-                        st_global_v8(dst + 2 * e, pk + e);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < D / 2; e += 4)
-                        *reinterpret_cast<uint4 *>(dst + 2 * e) =
-                            make_uint4(pk[e], pk[e + 1], pk[e + 2], pk[e + 3]);
-                }
-            }
+        }
+        if (STAGED) {
+            // every tile store of this warp has completed before the CTA exits
+            if (lane == 0)
+                bulk_wait_group0();
+            __syncwarp();
         }
     }
 
