@@ -147,3 +147,16 @@ def test_sizes_past_32_bits(call, fp8):
     qkv[0] = _t((1 << 32) + T, H, D, dtype=qkv[0].dtype)
     with pytest.raises(ValueError, match="32 bits"):
         call(qkv, cu)
+
+
+@pytest.mark.parametrize("call,fp8", CALLS)
+def test_tensors_of_a_machine_without_a_gpu(monkeypatch, call, fp8):
+    def none():
+        raise RuntimeError("no driver")
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", none)
+    monkeypatch.setattr(torch.cuda, "current_device", none)
+    qkv, cu = _inputs(fp8)
+    qkv[0] = _t(T, H, D, dtype=qkv[0].dtype, device="cpu")
+    with pytest.raises(ValueError, match="q8? must be a CUDA tensor"):
+        call(qkv, cu)

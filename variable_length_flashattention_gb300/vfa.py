@@ -240,7 +240,7 @@ def varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     (bottom-right); window_left >= 0 adds a sliding window (needs causal), past
     which the first sink_tokens keys stay visible (vfa_varlen_fwd_sinks)."""
     bf16, i32 = torch.bfloat16, torch.int32
-    dev = torch._C._cuda_getDevice()
+    dev = _device(q, "q")
     if not (_plain(q, bf16, dev) and _plain(k, bf16, dev) and _plain(v, bf16, dev) and
             _plain(cu_seqlens_q, i32, dev) and _plain(cu_seqlens_k, i32, dev)):
         for t, d, n in ((q, bf16, "q"), (k, bf16, "k"), (v, bf16, "v"),
@@ -332,7 +332,7 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     """(dq, dk, dv) bf16 = gradients of varlen_fwd for upstream gradient dout (vfa_varlen_bwd;
     with sink_tokens vfa_varlen_bwd_sinks, and a workspace made for as many)."""
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    dev = torch._C._cuda_getDevice()
+    dev = _device(q, "q")
     if not (_plain(q, bf16, dev) and _plain(k, bf16, dev) and _plain(v, bf16, dev) and
             _plain(out, bf16, dev) and _plain(dout, bf16, dev) and _plain(lse, f32, dev) and
             _plain(cu_seqlens_q, i32, dev) and _plain(cu_seqlens_k, i32, dev)):
