@@ -19,9 +19,15 @@
 //            of a cluster adds up its share of the counts.  Then every warp takes a run
 //            of slots: ballots give the ranks of ties, free slots and movers, sums over
 //            warps and CTAs their starts.  Weights and positions are rewritten here.
-//            One CTA per row took 41 us for 64 sequences of 1056 tokens on 8 kv
-//            heads and 57 for 8 of 4000-32768, a cluster 21 and 34, and 2 less with
-//            one barrier per sum (two buffers of sums in turn) instead of two;
+//            One CTA per row whose keys were formed anew from the weights for every
+//            count took 41 us for 64 sequences of 1056 tokens on 8 kv heads and 57 for 8 of
+//            4000-32768.  Keys in shared memory, loads in batches and the scan by all
+//            threads brought the first, whose rows have one CTA still, to 21, those and
+//            clusters the second to 34, and one barrier per sum (two buffers of sums in
+//            turn) instead of two that to 32.  The CTAs of a row go by the table's
+//            width, which the host knows, not by the row's tokens, which it does not:
+//            the 64 sequences take 19 us with their moves in tables of 128 pages, 39 in
+//            256, 116 in 2048 (clusters of eight CTAs, four or five words of slots each);
 //   move     the rows of K and V by the lists, 16 bytes per thread, and the
 //            sequences' new state.
 // Bound: HBM, 8 D bytes per moved token and kv head, and 12 to 16 bytes per token for weights
